@@ -1,6 +1,8 @@
 /*
  * poetx.h -- C ABI of libpoetx.so: forward and backward pass of one POET-X
- * reparameterized linear layer on AMD Instinct MI355X (gfx950).
+ * reparameterized linear layer on AMD Instinct MI355X (gfx950), and of the
+ * operators of an attention block around such layers (rotary positions,
+ * attention, dropout; last part of this file).
  *
  * The layer ("Reparameterized LLM Training via Orthogonal Equivalence
  * Transformation", Abstract) computes y = x W^T with W = R W0 P, where W0 is
@@ -376,6 +378,148 @@ size_t poetx_workspace_bytes(const poetx_shape* sh, int32_t which);
 
 /* Bytes of the saved-activation buffer; 0 on bad arguments. */
 size_t poetx_saved_bytes(const poetx_shape* sh);
+
+/*
+ * The operators of an attention block around POET-X projections: rotary
+ * positions, attention, dropout with the residual sum.  They share the
+ * conventions above.  Activations (q, k, v, o, x, y and their gradients) are
+ * of type `act`; rows may have a pitch: a tensor of T rows of H heads of D
+ * values has head h of row t at t * ld + h * D, so q, k and v may be column
+ * ranges of one projection's output.  Pitches count elements, are at least
+ * H * D and multiples of 8 (16 bytes for bf16, 32 for float32); the rows of
+ * an output must not overlap each other or an input, except where stated.
+ */
+
+/*
+ * poetx_rope -- rotary positions for q and k in one launch (the gradient is
+ * the same call with inverse = 1 on dq, dk).  For token t, row p = pos[t] of
+ * the table holds (c_i, s_i), i < rot/2; of every head the pairs
+ *   interleaved = 0: (x_i, x_{i + rot/2}),  1: (x_{2i}, x_{2i+1})
+ * become (a c - b s, a s + b c) (s negated when inverse), and elements from
+ * rot to D are copied.  Scaled or stretched frequencies, and a magnitude,
+ * are properties of the table.
+ *   q [T][Hq][D] -> qo, k [T][Hk][D] -> ko (Hk = 0: k, ko NULL); qo = q and
+ *   ko = k (same pitch) turn in place.
+ *   pos [T] int32; table [P][rot/2][2] float32.  A position outside [0, P)
+ *   reads nothing and writes NaN to the turned part of its row.
+ * D a multiple of 8 up to 512, rot even, 2 <= rot <= D; T = 0 does nothing.
+ * Errors: ERR_ARG, ERR_DEVICE.
+ */
+typedef struct {
+  int32_t T, Hq, Hk, D, rot, P, act, interleaved, inverse;
+  int64_t ldq, ldk, ldqo, ldko;
+} poetx_rope_shape;
+int32_t poetx_rope(const poetx_rope_shape* sh, const void* q, const void* k, const int32_t* pos,
+                   const float* table, void* qo, void* ko, poetx_stream_t stream);
+
+/*
+ * poetx_dropout_fwd / poetx_dropout_bwd -- dropout whose mask is never
+ * stored, with the residual sum:
+ *   y[i] = residual[i] + (keep(i) ? x[i] * g : 0),   dx[i] = keep(i) ? dy[i] * g : 0
+ * (residual NULL: 0; its gradient is dy itself).  keep(i): the 16-bit lane
+ * (e mod 8) of Philox 4x32-10 (Salmon et al., "Parallel random numbers: as
+ * easy as 1, 2, 3", 2011) with key `seed` and counter e / 8, e = offset + i,
+ * is at least t = round(p * 65536); lane 2w is the low half of word w,
+ * 2w + 1 its high half.  g = 65536 / (65536 - t), so E[y] = residual + x
+ * for the probability t / 65536 in effect; t = 65536 drops everything.  A
+ * dropped x is not read into the sum: NaN or infinity there leaves no trace.
+ *   n >= 0 contiguous elements of type act; 0 <= p <= 1; offset a multiple
+ *   of 8 (a caller advances it by n rounded up to 8 per call).
+ *   offset_dev: NULL, or a device uint64 (a multiple of 8) added to offset,
+ *   so that a captured graph draws a new mask each replay.
+ * y may be x or residual, dx may be dy.
+ * Errors: ERR_ARG, ERR_DEVICE.
+ */
+int32_t poetx_dropout_fwd(int64_t n, int32_t act, const void* x, const void* residual, void* y,
+                          double p, uint64_t seed, uint64_t offset, const uint64_t* offset_dev,
+                          poetx_stream_t stream);
+int32_t poetx_dropout_bwd(int64_t n, int32_t act, const void* dy, void* dx, double p, uint64_t seed,
+                          uint64_t offset, const uint64_t* offset_dev, poetx_stream_t stream);
+
+/*
+ * Attention over packed documents.  Tq query rows and Tk key rows hold ndoc
+ * documents one after the other: document d has query rows [cu_q[d],
+ * cu_q[d+1]) and key rows [cu_k[d], cu_k[d+1]) (lengths may differ and be
+ * 0); rows before cu[0] and from cu[ndoc] on belong to none.  Query i (of Lq)
+ * of a document stands at key position i + Lk - Lq (the ends are aligned);
+ * it sees every key of its document, with causal != 0 only those at j <= its
+ * position or j < prefix[d] (prefix NULL: 0).  Head h reads key head
+ * h / (Hq / Hkv).  With x = scale * q.k,
+ *   s = cap > 0 ? cap * tanh(x / cap) : x,   s -= slopes[h] * |position - j|,
+ *   p = exp(s - lse),  lse = log sum_j exp(s),  o = sum_j p v_j
+ * over the keys seen.  A query that sees none has o = 0, lse = -inf and
+ * takes no part in any gradient.  Keys and values that a query does not see
+ * have no influence on it, whatever they hold (NaN included).
+ * Backward: delta = do.o;  dl = p (do.v - delta);  ds = dl (1 - tanh^2) scale;
+ *   dq = sum ds k;  dk, dv sum over the query heads that share a key head.
+ * slopes are constants (no gradient).  The bf16 path rounds p and ds to bf16
+ * as matrix operands; sums, lse and delta are float32.  Results are
+ * deterministic (no atomics).
+ *   scale <= 0 selects 1 / sqrt(D); cap = 0: no cap; slopes [Hq] or NULL.
+ *   D a multiple of 8 up to 128; Hq a multiple of Hkv.
+ *   ldq, ldk, ldv, ldo: pitches of q, k, v, o; lddo, lddq, lddk, lddv of dout
+ *   and the gradients.
+ */
+typedef struct {
+  int32_t Tq, Tk, ndoc, Hq, Hkv, D, act, causal;
+  float scale, cap;
+  int64_t ldq, ldk, ldv, ldo, lddo, lddq, lddk, lddv;
+} poetx_attn_shape;
+
+/* Bytes of a plan (0 on bad arguments), and of the workspace of
+ * poetx_attn_fwd (which = 0) or poetx_attn_bwd (1). */
+size_t poetx_attn_plan_bytes(const poetx_attn_shape* sh);
+size_t poetx_attn_workspace_bytes(const poetx_attn_shape* sh, int32_t which);
+
+/*
+ * poetx_attn_plan -- the mask of a packed batch as intervals: the keys each
+ * query row sees and the queries that see each key row.  One plan serves
+ * every layer, head and direction of that batch.  It depends on Tq, Tk, ndoc
+ * and causal only.
+ *   cu_q, cu_k [ndoc+1] int32, prefix [ndoc] int32 or NULL; plan
+ *   poetx_attn_plan_bytes(sh) bytes.  Offsets that decrease or leave [0, T]
+ *   are clamped: they give some mask, never an access out of range.
+ * Errors: ERR_ARG, ERR_WORKSPACE (plan_bytes too small), ERR_DEVICE.
+ */
+int32_t poetx_attn_plan(const poetx_attn_shape* sh, const int32_t* cu_q, const int32_t* cu_k,
+                        const int32_t* prefix, void* plan, size_t plan_bytes,
+                        poetx_stream_t stream);
+
+/*
+ * poetx_attn_fwd / poetx_attn_bwd.
+ *   q [Tq][Hq][D], k, v [Tk][Hkv][D], o, dout, dq like q, dk, dv like k (act);
+ *   lse [Hq][Tq] float32 (written by fwd, read by bwd); plan from
+ *   poetx_attn_plan; ws poetx_attn_workspace_bytes(sh, 0 | 1) bytes.
+ * Errors: ERR_ARG, ERR_WORKSPACE, ERR_DEVICE.
+ */
+int32_t poetx_attn_fwd(const poetx_attn_shape* sh, const void* q, const void* k, const void* v,
+                       const float* slopes, const void* plan, void* o, float* lse, void* ws,
+                       size_t ws_bytes, poetx_stream_t stream);
+int32_t poetx_attn_bwd(const poetx_attn_shape* sh, const void* dout, const void* q, const void* k,
+                       const void* v, const void* o, const float* lse, const float* slopes,
+                       const void* plan, void* dq, void* dk, void* dv, void* ws, size_t ws_bytes,
+                       poetx_stream_t stream);
+
+/*
+ * poetx_attn_decode -- the single-token form: one query row per sequence over
+ * a cache, same scores as above.  Sequence b sees cache rows [start[b],
+ * len[b]) (start NULL: 0; both clamped to [0, rows]); its query stands at
+ * position len[b] - 1.  An empty range gives o = 0.
+ *   q, o [B][Hq][D] (pitches ldq, ldo); row j of sequence b of the caches
+ *   at b * bsk + j * ldk, b * bsv + j * ldv (offsets are 64-bit), heads of
+ *   D values side by side; rows: cache capacity per sequence.
+ *   ws poetx_attn_decode_workspace_bytes(sh) bytes.
+ * Errors: ERR_ARG, ERR_WORKSPACE, ERR_DEVICE.
+ */
+typedef struct {
+  int32_t B, Hq, Hkv, D, act, rows;
+  float scale, cap;
+  int64_t ldq, ldo, ldk, ldv, bsk, bsv;
+} poetx_decode_shape;
+size_t poetx_attn_decode_workspace_bytes(const poetx_decode_shape* sh);
+int32_t poetx_attn_decode(const poetx_decode_shape* sh, const void* q, const void* k, const void* v,
+                          const int32_t* start, const int32_t* len, const float* slopes, void* o,
+                          void* ws, size_t ws_bytes, poetx_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -17,6 +17,7 @@ STATUS = {0: "POETX_OK", 1: "POETX_ERR_ARG", 2: "POETX_ERR_UNSUPPORTED",
 
 # every symbol include/poetx.h declares, with its ctypes signature
 _p, _i, _sz = C.c_void_p, C.c_int32, C.c_size_t
+_i64, _u64, _d = C.c_int64, C.c_uint64, C.c_double
 SIGNATURES = {
     "poetx_abi_version": (_i, []),
     "poetx_status_str": (C.c_char_p, [_i]),
@@ -43,6 +44,16 @@ SIGNATURES = {
     "poetx_dequant": (_i, [_i, _i, _p, _p, _i, _p, _p]),
     "poetx_set_stage_events": (_i, [_p, _i]),
     "poetx_set_fused_gather": (_i, [_i]),
+    "poetx_rope": (_i, [_p, _p, _p, _p, _p, _p, _p, _p]),
+    "poetx_dropout_fwd": (_i, [_i64, _i, _p, _p, _p, _d, _u64, _u64, _p, _p]),
+    "poetx_dropout_bwd": (_i, [_i64, _i, _p, _p, _d, _u64, _u64, _p, _p]),
+    "poetx_attn_plan_bytes": (_sz, [_p]),
+    "poetx_attn_workspace_bytes": (_sz, [_p, _i]),
+    "poetx_attn_plan": (_i, [_p, _p, _p, _p, _p, _sz, _p]),
+    "poetx_attn_fwd": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _p, _sz, _p]),
+    "poetx_attn_bwd": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _sz, _p]),
+    "poetx_attn_decode_workspace_bytes": (_sz, [_p]),
+    "poetx_attn_decode": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _p, _sz, _p]),
 }
 
 
@@ -53,6 +64,20 @@ ABI_VERSION = 2                   # POETX_ABI_VERSION
 class Shape(C.Structure):
     _fields_ = [("m", C.c_int32), ("n", C.c_int32), ("b", C.c_int32), ("k", C.c_int32),
                 ("T", C.c_int32), ("act", C.c_int32)]
+
+
+def _struct(name: str, ints: str, floats: str, longs: str):
+    fields = ([(f, C.c_int32) for f in ints.split()] + [(f, C.c_float) for f in floats.split()]
+              + [(f, C.c_int64) for f in longs.split()])
+    return type(name, (C.Structure,), {"_fields_": fields})
+
+
+RopeShape = _struct("RopeShape", "T Hq Hk D rot P act interleaved inverse", "",
+                    "ldq ldk ldqo ldko")
+AttnShape = _struct("AttnShape", "Tq Tk ndoc Hq Hkv D act causal", "scale cap",
+                    "ldq ldk ldv ldo lddo lddq lddk lddv")
+DecodeShape = _struct("DecodeShape", "B Hq Hkv D act rows", "scale cap",
+                      "ldq ldo ldk ldv bsk bsv")
 
 
 class PoetxError(RuntimeError):

@@ -10,6 +10,7 @@
 #include <tuple>
 
 #include "../../include/poetx.h"
+#include "api_util.h"
 #include "kernels.h"
 
 namespace poetx {
@@ -30,12 +31,6 @@ hipError_t lds_opt_in(const void* kern, int bytes) {
   return e;
 }
 
-}  // namespace poetx
-
-using namespace poetx;
-
-namespace {
-
 thread_local char g_err[512] = "";
 
 int32_t fail(int32_t st, const char* fmt, ...) {
@@ -55,18 +50,11 @@ int32_t dev_fail(hipError_t e, const char* where) {
   return fail(POETX_ERR_DEVICE, "%s: %s", where, hipGetErrorString(e));
 }
 
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+}  // namespace poetx
 
-#define NEED_PTR(p)                                                                  \
-  do {                                                                               \
-    if (!(p)) return fail(POETX_ERR_ARG, "%s: null pointer '%s'", fn, #p);           \
-    if (!aligned16(p)) return fail(POETX_ERR_ARG, "%s: '%s' not 16-byte aligned", fn, #p); \
-  } while (0)
-#define OPT_PTR(p)                                                                   \
-  do {                                                                               \
-    if ((p) && !aligned16(p))                                                        \
-      return fail(POETX_ERR_ARG, "%s: '%s' not 16-byte aligned", fn, #p);            \
-  } while (0)
+using namespace poetx;
+
+namespace {
 
 bool b_supported(int b) {
   return b == 8 || b == 16 || b == 32 || b == 64 || b == 128 || b == 256 || b == 512;
@@ -74,10 +62,6 @@ bool b_supported(int b) {
 
 constexpr int K_MAX = 8;
 constexpr int SMALL_B_MAX = 64;  // LDS-resident fp32 Cayley-Neumann kernels
-
-size_t es_of(int act) { return act == POETX_BF16 ? 2 : 4; }
-
-size_t align_up(size_t x) { return (x + 255) & ~size_t(255); }
 
 // the MFMA Cayley-Neumann panels run for bf16 blocks of 64..512
 bool cnp_uses_panel(int b, int act) { return act == POETX_BF16 && b >= 64; }

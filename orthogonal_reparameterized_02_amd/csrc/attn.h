@@ -1,0 +1,70 @@
+// Host-side launchers and argument blocks of the attention-block operators
+// (internal to libpoetx.so).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "common.h"
+
+namespace poetx {
+
+// ---- rotary positions (rope.hip) -------------------------------------------
+struct RopeArgs {
+  int T, Hq, Hk, D, rot, P, interleaved;
+  float sgn;  // -1: inverse
+  long ldq, ldk, ldqo, ldko;
+  const int* pos;
+  const float* table;
+};
+template <typename TS>
+hipError_t launch_rope(const RopeArgs& a, const TS* q, const TS* k, TS* qo, TS* ko, hipStream_t s);
+
+// ---- dropout (dropout.hip) --------------------------------------------------
+// out[i] = (res ? res[i] : 0) + (keep(i) ? x[i] * gain : 0)
+template <typename TS>
+hipError_t launch_dropout(long n, const TS* x, const TS* res, TS* out, uint32_t cut, uint64_t seed,
+                          uint64_t offset, const uint64_t* offset_dev, hipStream_t s);
+
+// ---- attention (attn_*.hip) -------------------------------------------------
+// The mask as intervals: query row t sees keys [row_lo, row_hi), stands at
+// key position row_pos; key row j is seen by queries [key_lo, key_hi).
+// Within a document both bounds grow with the row, so the rows of any tile
+// see one interval's worth of keys.
+struct AttnPlan {
+  int *row_lo, *row_hi, *row_pos;  // [Tq]
+  int *key_lo, *key_hi;            // [Tk]
+};
+
+struct AttnArgs {
+  int Tq, Tk, Hq, Hkv, group, D;
+  float scale, cap;
+  const float* slopes;  // or null
+  long ldq, ldk, ldv, ldo, lddo, lddq, lddk, lddv;
+  const void *q, *k, *v;
+  void* o;
+  float* lse;
+  // backward
+  const void* dout;
+  void *dq, *dk, *dv;
+  float* delta;  // [Hq][Tq]
+  AttnPlan pl;
+};
+
+hipError_t launch_attn_plan(int Tq, int Tk, int ndoc, int causal, const int* cu_q, const int* cu_k,
+                            const int* prefix, const AttnPlan& pl, hipStream_t s);
+template <typename TS> hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t s);
+template <typename TS> hipError_t launch_attn_bwd(const AttnArgs& a, hipStream_t s);
+
+struct DecodeArgs {
+  int B, Hq, Hkv, group, D, rows;
+  float scale, cap;
+  const float* slopes;
+  long ldq, ldo, ldk, ldv, bsk, bsv;
+  const void *q, *k, *v;
+  void* o;
+  const int *start, *len;
+};
+template <typename TS> hipError_t launch_attn_decode(const DecodeArgs& a, hipStream_t s);
+
+}  // namespace poetx

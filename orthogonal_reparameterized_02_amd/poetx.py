@@ -13,7 +13,8 @@ from typing import Optional
 
 import torch
 
-from ._lib import BF16, F32, I8, PoetxError, Shape, check, lib  # noqa: F401
+from ._lib import (AttnShape, BF16, DecodeShape, F32, I8, PoetxError, RopeShape, Shape,  # noqa: F401
+                   check, lib)
 
 _DT = {F32: torch.float32, BF16: torch.bfloat16}
 
@@ -269,3 +270,184 @@ def poetx_dequant(q, scale, per_row: bool, out, stream=None) -> None:
         rows, cols, _dev(q, "q", torch.int8, rows * cols),
         _dev(scale, "scale", torch.float32, rows if per_row else cols), int(bool(per_row)),
         _dev(out, "out", torch.bfloat16, rows * cols), _stream(stream)))
+
+
+# ---- attention-block operators ------------------------------------------------
+
+
+def _rows(t: Optional[torch.Tensor], name: str, shape, dtype):
+    """Pointer and row pitch of a [rows][H][D] tensor whose heads lie side by
+    side (a column range of a wider tensor is fine)."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    T, H, D = shape
+    st = t.stride()
+    if t.numel() and ((D > 1 and st[2] != 1) or (H > 1 and st[1] != D)):
+        raise ValueError(f"{name}: heads must lie side by side in a row (strides {st})")
+    return C.c_void_p(t.data_ptr()), (st[0] if T > 1 else max(H * D, 8))
+
+
+def _vec(t: Optional[torch.Tensor], name: str, dtype, numel: int, optional=False):
+    """Pointer of a contiguous vector of at least numel values."""
+    return _dev(t, name, dtype, numel, optional)
+
+
+def poetx_rope(q, k, pos, table, qo, ko, interleaved: bool = False, inverse: bool = False,
+               stream=None) -> None:
+    """Turn q [T][Hq][D] and k [T][Hk][D] (k, ko may be None) by the angles
+    of table [P][rot/2][2] (cos, sin) at pos [T]."""
+    T, Hq, D = q.shape
+    if table.dim() != 3 or table.shape[2] != 2:
+        raise ValueError(f"table has shape {tuple(table.shape)}, expected [P][rot/2][2]")
+    Hk = 0 if k is None else k.shape[1]
+    qp, ldq = _rows(q, "q", (T, Hq, D), q.dtype)
+    qop, ldqo = _rows(qo, "qo", (T, Hq, D), q.dtype)
+    kp, ldk = (None, 0) if k is None else _rows(k, "k", (T, Hk, D), q.dtype)
+    kop, ldko = (None, 0) if k is None else _rows(ko, "ko", (T, Hk, D), q.dtype)
+    sh = RopeShape(T, Hq, Hk, D, 2 * table.shape[1], table.shape[0], act_of(q.dtype),
+                   int(interleaved), int(inverse), ldq, ldk, ldqo, ldko)
+    check("poetx_rope", lib().poetx_rope(
+        C.byref(sh), qp, kp, _vec(pos, "pos", torch.int32, T),
+        _vec(table, "table", torch.float32, table.numel()), qop, kop, _stream(stream)))
+
+
+def poetx_dropout_fwd(x, residual, y, p: float, seed: int, offset: int = 0, offset_dev=None,
+                      stream=None) -> None:
+    """y = residual + dropout(x); residual may be None."""
+    n = x.numel()
+    check("poetx_dropout_fwd", lib().poetx_dropout_fwd(
+        n, act_of(x.dtype), _dev(x, "x"), _dev(residual, "residual", x.dtype, n, optional=True),
+        _dev(y, "y", x.dtype, n), p, seed, offset,
+        _dev(offset_dev, "offset_dev", torch.int64, 1, optional=True), _stream(stream)))
+
+
+def poetx_dropout_bwd(dy, dx, p: float, seed: int, offset: int = 0, offset_dev=None,
+                      stream=None) -> None:
+    """dx of the forward call with the same p, seed and offset."""
+    n = dy.numel()
+    check("poetx_dropout_bwd", lib().poetx_dropout_bwd(
+        n, act_of(dy.dtype), _dev(dy, "dy"), _dev(dx, "dx", dy.dtype, n), p, seed, offset,
+        _dev(offset_dev, "offset_dev", torch.int64, 1, optional=True), _stream(stream)))
+
+
+def attn_shape(q, k, v, ndoc: int, causal: bool = True, scale: float = 0.0,
+               cap: float = 0.0) -> AttnShape:
+    """Shape of attention over q [Tq][Hq][D], k, v [Tk][Hkv][D]; pitches of
+    outputs and gradients are set by the calls."""
+    Tq, Hq, D = q.shape
+    Tk, Hkv, _ = k.shape
+    wq, wk = Hq * D, Hkv * D
+    return AttnShape(Tq, Tk, ndoc, Hq, Hkv, D, act_of(q.dtype), int(causal), scale, cap, wq, wk, wk,
+                     wq, wq, wq, wk, wk)
+
+
+def poetx_attn_plan_bytes(sh: AttnShape) -> int:
+    return lib().poetx_attn_plan_bytes(C.byref(sh))
+
+
+def poetx_attn_workspace_bytes(sh: AttnShape, which: int) -> int:
+    return lib().poetx_attn_workspace_bytes(C.byref(sh), which)
+
+
+def poetx_attn_plan(sh: AttnShape, cu_q, cu_k, plan, prefix=None, stream=None) -> None:
+    """The mask of a packed batch (offsets cu_q, cu_k [ndoc+1], prefix [ndoc])."""
+    check("poetx_attn_plan", lib().poetx_attn_plan(
+        C.byref(sh), _vec(cu_q, "cu_q", torch.int32, sh.ndoc + 1),
+        _vec(cu_k, "cu_k", torch.int32, sh.ndoc + 1),
+        _vec(prefix, "prefix", torch.int32, sh.ndoc, optional=True), _dev(plan, "plan"),
+        plan.numel() * plan.element_size(), _stream(stream)))
+
+
+def poetx_attn_fwd(sh: AttnShape, q, k, v, plan, o, lse, ws=None, slopes=None, stream=None) -> None:
+    sh = AttnShape.from_buffer_copy(sh)
+    dt = _DT[sh.act]
+    fq, fk = (sh.Tq, sh.Hq, sh.D), (sh.Tk, sh.Hkv, sh.D)
+    qp, sh.ldq = _rows(q, "q", fq, dt)
+    kp, sh.ldk = _rows(k, "k", fk, dt)
+    vp, sh.ldv = _rows(v, "v", fk, dt)
+    op, sh.ldo = _rows(o, "o", fq, dt)
+    wp, wb = _ws(ws, poetx_attn_workspace_bytes(sh, 0))
+    check("poetx_attn_fwd", lib().poetx_attn_fwd(
+        C.byref(sh), qp, kp, vp, _vec(slopes, "slopes", torch.float32, sh.Hq, optional=True),
+        _plan(sh, plan), op, _vec(lse, "lse", torch.float32, sh.Hq * sh.Tq), wp, wb,
+        _stream(stream)))
+
+
+def _plan(sh: AttnShape, plan):
+    p = _dev(plan, "plan")
+    need = poetx_attn_plan_bytes(sh)
+    if plan.numel() * plan.element_size() < need:
+        raise ValueError(f"plan: {need} bytes required")
+    return p
+
+
+def poetx_attn_bwd(sh: AttnShape, dout, q, k, v, o, lse, plan, dq, dk, dv, ws, slopes=None,
+                   stream=None) -> None:
+    sh = AttnShape.from_buffer_copy(sh)
+    dt = _DT[sh.act]
+    fq, fk = (sh.Tq, sh.Hq, sh.D), (sh.Tk, sh.Hkv, sh.D)
+    qp, sh.ldq = _rows(q, "q", fq, dt)
+    kp, sh.ldk = _rows(k, "k", fk, dt)
+    vp, sh.ldv = _rows(v, "v", fk, dt)
+    op, sh.ldo = _rows(o, "o", fq, dt)
+    dop, sh.lddo = _rows(dout, "dout", fq, dt)
+    dqp, sh.lddq = _rows(dq, "dq", fq, dt)
+    dkp, sh.lddk = _rows(dk, "dk", fk, dt)
+    dvp, sh.lddv = _rows(dv, "dv", fk, dt)
+    wp, wb = _ws(ws, poetx_attn_workspace_bytes(sh, 1))
+    check("poetx_attn_bwd", lib().poetx_attn_bwd(
+        C.byref(sh), dop, qp, kp, vp, op, _vec(lse, "lse", torch.float32, sh.Hq * sh.Tq),
+        _vec(slopes, "slopes", torch.float32, sh.Hq, optional=True), _plan(sh, plan), dqp, dkp, dvp,
+        wp, wb, _stream(stream)))
+
+
+def decode_shape(q, k, v, scale: float = 0.0, cap: float = 0.0) -> DecodeShape:
+    """Shape of a decode call: q [B][Hq][D], caches [B][rows][Hkv][D]; the
+    pitches are set by the call."""
+    B, Hq, D = q.shape
+    _, rows, Hkv, _ = k.shape
+    wq, wk = Hq * D, Hkv * D
+    return DecodeShape(B, Hq, Hkv, D, act_of(q.dtype), rows, scale, cap, wq, wq, wk, wk, rows * wk,
+                       rows * wk)
+
+
+def poetx_attn_decode_workspace_bytes(sh: DecodeShape) -> int:
+    return lib().poetx_attn_decode_workspace_bytes(C.byref(sh))
+
+
+def _cache(t: torch.Tensor, name: str, sh: DecodeShape):
+    """Pointer, row pitch and sequence pitch of a [B][rows][Hkv][D] cache."""
+    dt, want = _DT[sh.act], (sh.B, sh.rows, sh.Hkv, sh.D)
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dtype != dt:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dt}")
+    if tuple(t.shape) != want:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {want}")
+    st, w = t.stride(), sh.Hkv * sh.D
+    if t.numel() and (st[3] != 1 or (sh.Hkv > 1 and st[2] != sh.D)):
+        raise ValueError(f"{name}: heads must lie side by side in a row (strides {st})")
+    return C.c_void_p(t.data_ptr()), (st[1] if sh.rows > 1 else w), (st[0] if sh.B > 1 else 0)
+
+
+def poetx_attn_decode(sh: DecodeShape, q, k, v, length, o, ws, start=None, slopes=None,
+                      stream=None) -> None:
+    """One query row per sequence over cache rows [start[b], length[b])."""
+    sh = DecodeShape.from_buffer_copy(sh)
+    dt = _DT[sh.act]
+    fq = (sh.B, sh.Hq, sh.D)
+    qp, sh.ldq = _rows(q, "q", fq, dt)
+    op, sh.ldo = _rows(o, "o", fq, dt)
+    kp, sh.ldk, sh.bsk = _cache(k, "k", sh)
+    vp, sh.ldv, sh.bsv = _cache(v, "v", sh)
+    wp, wb = _ws(ws, poetx_attn_decode_workspace_bytes(sh))
+    check("poetx_attn_decode", lib().poetx_attn_decode(
+        C.byref(sh), qp, kp, vp, _vec(start, "start", torch.int32, sh.B, optional=True),
+        _vec(length, "length", torch.int32, sh.B),
+        _vec(slopes, "slopes", torch.float32, sh.Hq, optional=True), op, wp, wb, _stream(stream)))

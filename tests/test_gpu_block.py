@@ -1,0 +1,436 @@
+"""GPU parity of the attention-block operators (rotary positions, dropout,
+attention over packed documents, attention over a cache) against the float64
+oracle on the same seeded inputs.
+
+Tolerances.  float32: 1e-5 relative (2-norm) as for the layer.  bf16: the
+inputs are exact in the oracle; p and ds are rounded to bf16 once as matrix
+operands and each output once, every rounding at most 2^-9 relative and
+independent, so the 2-norm error is below 3 * 2^-9 = 5.9e-3; the largest
+difference is bounded by 2e-2 of the largest value.  lse is a float32 sum of
+float32 exponentials: 5e-5 absolute."""
+import math
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from gpu_util import bits, to_dev, to_f64
+from orthogonal_reparameterized_02_amd import poetx as P
+from oracle import block_oracle as B
+
+pytestmark = pytest.mark.gpu
+
+FRO = {"f32": 1e-5, "bf16": 3 * 2.0 ** -9}
+MAX = {"f32": 1e-4, "bf16": 2e-2}
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    P.lib()
+
+
+def say(*a):
+    print(*a, file=sys.stderr, flush=True)
+
+
+def normal(rng, shape, dt, scale=1.0):
+    return torch.from_numpy((rng.standard_normal(shape) * scale).astype(np.float32)).to(DT[dt]).cuda()
+
+
+def close(name, got, ref, dt):
+    """2-norm and largest difference, with equal NaN and infinity patterns."""
+    got, ref = to_f64(got) if torch.is_tensor(got) else got, np.asarray(ref, np.float64)
+    fin = np.isfinite(ref)
+    np.testing.assert_array_equal(np.isfinite(got), fin, err_msg=name)
+    np.testing.assert_array_equal(got[np.isinf(ref)], ref[np.isinf(ref)], err_msg=name)
+    g, r = got[fin], ref[fin]
+    if not r.size or not np.abs(r).max():
+        assert not g.size or np.abs(g).max() <= FRO[dt], name
+        return
+    fro, mx = np.linalg.norm(g - r) / np.linalg.norm(r), np.abs(g - r).max() / np.abs(r).max()
+    say(f"  {name}: fro={fro:.2e} max={mx:.2e}")
+    assert fro <= FRO[dt] and mx <= MAX[dt], (name, fro, mx)
+
+
+# ---- rotary positions -----------------------------------------------------------
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("T,Hq,Hk,D,rot,pairs", [
+    (1, 4, 1, 64, 64, False), (7, 3, 0, 128, 128, True), (65, 5, 5, 104, 40, True), (33, 2, 1, 40, 12, False),
+    (130, 8, 2, 128, 64, False), (9, 1, 1, 8, 2, False), (5, 2, 2, 24, 6, True), (300, 4, 4, 256, 96, False)])
+def test_rope(dt, T, Hq, Hk, D, rot, pairs):
+    rng = np.random.default_rng(T + D)
+    q, k = normal(rng, (T, Hq, D), dt), normal(rng, (T, max(Hk, 1), D), dt)
+    ang = rng.uniform(-9, 9, (50, rot // 2))
+    table = np.stack([np.cos(ang), np.sin(ang)], -1).astype(np.float32)
+    pos = rng.integers(0, 50, T).astype(np.int32)
+    for inverse in (False, True):
+        qo, ko = torch.empty_like(q), torch.empty_like(k)
+        P.poetx_rope(q, k if Hk else None, to_dev(pos), to_dev(table), qo, ko if Hk else None, pairs, inverse)
+        # one rounding to the output type of a float32 expression of two products
+        tol = dict(rtol=0, atol=1e-5) if dt == "f32" else dict(rtol=2.0 ** -8, atol=1e-6)
+        np.testing.assert_allclose(to_f64(qo), B.rope(to_f64(q), pos, table, pairs, inverse), **tol)
+        if Hk:
+            np.testing.assert_allclose(to_f64(ko), B.rope(to_f64(k), pos, table, pairs, inverse), **tol)
+        np.testing.assert_array_equal(bits(qo[..., rot:]), bits(q[..., rot:]))
+
+
+def test_rope_in_place_strided_and_bad_positions():
+    rng = np.random.default_rng(1)
+    T, H, D = 37, 4, 64
+    wide = normal(rng, (T, 3 * H * D), "bf16")
+    keep = wide.clone()
+    q, k = wide[:, :H * D].view(T, H, D), wide[:, H * D:2 * H * D].view(T, H, D)
+    ang = rng.uniform(-3, 3, (20, D // 2))
+    table, pos = np.stack([np.cos(ang), np.sin(ang)], -1).astype(np.float32), rng.integers(0, 20, T).astype(np.int32)
+    want = torch.empty(T, H, D, dtype=torch.bfloat16, device="cuda"), torch.empty(T, H, D, dtype=torch.bfloat16, device="cuda")
+    P.poetx_rope(q, k, to_dev(pos), to_dev(table), *want)
+    P.poetx_rope(q, k, to_dev(pos), to_dev(table), q, k)
+    np.testing.assert_array_equal(bits(q.contiguous()), bits(want[0]))
+    np.testing.assert_array_equal(bits(k.contiguous()), bits(want[1]))
+    np.testing.assert_array_equal(bits(wide[:, 2 * H * D:].contiguous()), bits(keep[:, 2 * H * D:].contiguous()))
+    # positions outside the table: NaN in that row, the others untouched by it
+    pos[3], pos[5] = -1, 20
+    P.poetx_rope(want[0], None, to_dev(pos), to_dev(table), want[1], None)
+    bad = torch.isnan(want[1]).flatten(1).all(1).cpu().numpy()
+    assert bad[3] and bad[5] and bad.sum() == 2 and not torch.isnan(want[1][[0, 4, 6]]).any()
+
+
+# ---- dropout ----------------------------------------------------------------------
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("n,p,seed,offset", [(1, 0.5, 1, 0), (7, 0.1, 2 ** 63 + 5, 8), (4099, 0.3, 9, 2 ** 34 + 16),
+                                             (2048, 0.0, 3, 0), (513, 1.0, 3, 0), (6000, 0.999, 4, 2 ** 35 - 64)])
+def test_dropout(dt, n, p, seed, offset):
+    rng = np.random.default_rng(n)
+    x, r = normal(rng, (n,), dt), normal(rng, (n,), dt)
+    x[::5] = float("nan")
+    ref_keep = B.keep(n, p, seed, offset)
+    y, y0, dx = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x)
+    P.poetx_dropout_fwd(x, r, y, p, seed, offset)
+    P.poetx_dropout_fwd(x, None, y0, p, seed, offset)
+    P.poetx_dropout_bwd(r, dx, p, seed, offset)
+    # one or two float32 roundings, then one to the output type
+    tol = dict(rtol=2.0 ** -22, atol=1e-6) if dt == "f32" else dict(rtol=2.0 ** -8, atol=1e-6)
+    np.testing.assert_allclose(to_f64(y), B.dropout(to_f64(x), to_f64(r), p, seed, offset), **tol)
+    np.testing.assert_allclose(to_f64(y0), B.dropout(to_f64(x), None, p, seed, offset), **tol)
+    np.testing.assert_allclose(to_f64(dx), B.dropout(to_f64(r), None, p, seed, offset), **tol)
+    # the mask itself
+    one = torch.ones_like(x)
+    P.poetx_dropout_fwd(one, None, y0, p, seed, offset)
+    np.testing.assert_array_equal(to_f64(y0) != 0, ref_keep)
+    # in place, over the residual, and the offset taken from the device
+    old = r.clone()
+    P.poetx_dropout_fwd(one, r, r, p, seed, 0, torch.tensor([offset], dtype=torch.int64, device="cuda"))
+    np.testing.assert_array_equal(bits(r)[~ref_keep], bits(old)[~ref_keep])
+    np.testing.assert_allclose(to_f64(r), B.dropout(np.ones(n), to_f64(old), p, seed, offset), **tol)
+    P.poetx_dropout_fwd(one, None, one, p, seed, 8, torch.tensor([offset - 8], dtype=torch.int64, device="cuda"))
+    np.testing.assert_array_equal(to_f64(one) != 0, ref_keep)
+
+
+def test_dropout_past_32_bits():
+    n = 2 ** 32 + 24
+    x = torch.ones(n, dtype=torch.bfloat16, device="cuda")
+    P.poetx_dropout_bwd(x, x, 0.5, 11, 8)
+    tail = B.keep(56, 0.5, 11, 8 + n - 56)
+    np.testing.assert_array_equal(to_f64(x[-56:]) != 0, tail)
+
+
+# ---- attention ----------------------------------------------------------------------
+CASES = [  # q lengths, k lengths, rows before and after the documents, Hq, Hkv, D, causal, prefix, cap, bias
+    dict(q=[1], k=[1], Hq=1, Hkv=1, D=64),
+    dict(q=[64], k=[64], Hq=4, Hkv=4, D=64),
+    dict(q=[33, 1, 0, 95], k=[33, 1, 0, 95], Hq=4, Hkv=2, D=128),
+    dict(q=[129], k=[129], Hq=2, Hkv=1, D=128, causal=False),
+    dict(q=[100, 157], k=[100, 157], pad=(3, 9), Hq=3, Hkv=3, D=128, prefix=[40, 200]),
+    dict(q=[70, 60], k=[70, 60], Hq=4, Hkv=1, D=40, cap=5.0),
+    dict(q=[65, 31], k=[65, 31], Hq=4, Hkv=2, D=104, bias=True),
+    dict(q=[40, 20], k=[300, 7], Hq=4, Hkv=2, D=128, cap=3.0, bias=True),   # chunk of a prompt; rows that see nothing
+    dict(q=[50], k=[10], Hq=2, Hkv=2, D=8, causal=False, bias=True),
+    dict(q=[5, 200, 3, 47], k=[64, 200, 0, 1], pad=(0, 70), Hq=5, Hkv=5, D=72, prefix=[0, 64, 1, 1]),
+    dict(q=[257], k=[257], Hq=8, Hkv=1, D=64, bias=True, prefix=[100]),
+    dict(q=[300], k=[300], Hq=2, Hkv=2, D=128, cap=30.0),
+]
+
+
+def setup(c, dt, seed=0, scale=1.5):
+    rng = np.random.default_rng(seed + sum(c["q"]) + c["D"])
+    a, b = c.get("pad", (0, 0))
+    cu_q, cu_k = (np.concatenate([[0], np.cumsum(c[n])]).astype(np.int32) + a for n in "qk")
+    Tq, Tk = int(cu_q[-1]) + b, int(cu_k[-1]) + b
+    Hq, Hkv, D = c["Hq"], c["Hkv"], c["D"]
+    st = dict(q=normal(rng, (Tq, Hq, D), dt, scale), k=normal(rng, (Tk, Hkv, D), dt), v=normal(rng, (Tk, Hkv, D), dt),
+              dout=normal(rng, (Tq, Hq, D), dt), cu_q=cu_q, cu_k=cu_k, prefix=c.get("prefix"),
+              slopes=(2.0 ** -np.arange(1, Hq + 1)).astype(np.float32) if c.get("bias") else None,
+              causal=c.get("causal", True), cap=c.get("cap", 0.0), ndoc=len(c["q"]))
+    return st
+
+
+def run(st, stream=None, scale=0.0):
+    sh = P.attn_shape(st["q"], st["k"], st["v"], st["ndoc"], st["causal"], scale, st["cap"])
+    e = lambda t: torch.full(t.shape, 7.0, dtype=t.dtype, device="cuda")
+    plan = torch.empty(P.poetx_attn_plan_bytes(sh), dtype=torch.uint8, device="cuda")
+    ws = [torch.empty(max(16, P.poetx_attn_workspace_bytes(sh, w)), dtype=torch.uint8, device="cuda") for w in (0, 1)]
+    slopes = None if st["slopes"] is None else to_dev(st["slopes"])
+    pre = None if st["prefix"] is None else to_dev(np.asarray(st["prefix"], np.int32))
+    out = {"o": e(st["q"]), "dq": e(st["q"]), "dk": e(st["k"]), "dv": e(st["v"]),
+           "lse": torch.full((sh.Hq, sh.Tq), 7.0, device="cuda")}
+    P.poetx_attn_plan(sh, to_dev(st["cu_q"]), to_dev(st["cu_k"]), plan, pre)
+    P.poetx_attn_fwd(sh, st["q"], st["k"], st["v"], plan, out["o"], out["lse"], ws[0], slopes)
+    P.poetx_attn_bwd(sh, st["dout"], st["q"], st["k"], st["v"], out["o"], out["lse"], plan, out["dq"], out["dk"],
+                     out["dv"], ws[1], slopes)
+    torch.cuda.synchronize()
+    return out
+
+
+def reference(st, scale=None):
+    seen, pos = B.mask(st["q"].shape[0], st["k"].shape[0], st["cu_q"], st["cu_k"], st["prefix"], st["causal"])
+    with np.errstate(invalid="ignore"):
+        return B.attention(to_f64(st["q"]), to_f64(st["k"]), to_f64(st["v"]), seen, pos, scale, st["cap"],
+                           st["slopes"], to_f64(st["dout"])), seen
+
+
+def check(out, ref, dt):
+    for n in ("o", "dq", "dk", "dv"):
+        close(n, out[n], ref[n], dt)
+    lse, want = to_f64(out["lse"]), ref["lse"]
+    np.testing.assert_array_equal(np.isneginf(lse), np.isneginf(want))
+    fin = np.isfinite(want)
+    assert np.abs(lse[fin] - want[fin]).max(initial=0.0) <= 5e-5
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("i", range(len(CASES)))
+def test_attention(i, dt):
+    say(f"attention {dt} {CASES[i]}")
+    st = setup(CASES[i], dt)
+    out = run(st)
+    ref, seen = reference(st)
+    check(out, ref, dt)
+    empty = ~seen.any(1)
+    assert not to_f64(out["o"])[empty].any() and not to_f64(out["dq"])[empty].any()
+    hidden = ~seen.any(0)
+    assert not to_f64(out["dk"])[hidden].any() and not to_f64(out["dv"])[hidden].any()
+    again = run(st)
+    for n in out:
+        np.testing.assert_array_equal(bits(out[n]), bits(again[n]))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_attention_padding_may_hold_anything(dt):
+    """Rows of no document hold NaN and infinity in every input."""
+    st = setup(CASES[4], dt)
+    clean = run(st)
+    a, b = CASES[4]["pad"]
+    for n in ("q", "k", "v", "dout"):
+        st[n][:a] = float("nan")
+        st[n][-b:] = float("inf")
+    out = run(st)
+    for n in out:
+        np.testing.assert_array_equal(bits(out[n]), bits(clean[n]), err_msg=n)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("where,value", [("k", "nan"), ("v", "nan"), ("q", "nan"), ("dout", "nan"), ("v", "inf"),
+                                         ("k", "inf"), ("dout", "-inf")])
+def test_attention_non_finite_reaches_only_who_sees_it(dt, where, value):
+    """One row of one document is not finite: earlier rows (causal) and other
+    documents are those of the oracle, which never multiplies a hidden pair."""
+    st = setup(dict(q=[70, 90], k=[70, 90], Hq=4, Hkv=2, D=64), dt)
+    st[where][70 + 40, 0] = float(value)
+    out = run(st)
+    ref, _ = reference(st)
+    # outside the document and before the row everything is finite and right
+    head = slice(0, 2) if where in "kv" else slice(0, 1)
+    for n in ("o", "dq"):
+        close(n + " other document", out[n][:70], ref[n][:70], dt)
+        close(n + " other heads", out[n][:, 2:], ref[n][:, 2:], dt)
+        close(n + " earlier rows", out[n][:110], ref[n][:110], dt)
+    for n in ("dk", "dv"):
+        close(n + " other document", out[n][:70], ref[n][:70], dt)
+        close(n + " other heads", out[n][:, 1:], ref[n][:, 1:], dt)
+        close(n + " later keys", out[n][111:], ref[n][111:], dt)
+    if where in ("q", "dout"):  # rows after it do not depend on it
+        close("dq later rows", out["dq"][111:], ref["dq"][111:], dt)
+    for n in ("dq", "dk", "dv", "o"):
+        np.testing.assert_array_equal(np.isfinite(to_f64(out[n])), np.isfinite(ref[n]), err_msg=n)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_attention_large_scores(dt):
+    """Scores far apart: the running maximum keeps every exponential in range."""
+    st = setup(dict(q=[90], k=[90], Hq=2, Hkv=1, D=64), dt, scale=60.0)
+    st["k"][80] *= 4
+    out = run(st)
+    ref, _ = reference(st)
+    close("o", out["o"], ref["o"], dt)
+    assert all(torch.isfinite(out[n]).all() for n in out)
+
+
+def test_attention_strides_stream_and_scale():
+    """q, k, v as column ranges of one fused projection, outputs into another,
+    on a side stream, with a scale of its own: bitwise the plain layout."""
+    c = CASES[6]
+    st = setup(c, "bf16")
+    T, Hq, Hkv, D = st["q"].shape[0], c["Hq"], c["Hkv"], c["D"]
+    want = run(st, scale=0.2)
+    ref, _ = reference(st, scale=0.2)
+    check(want, ref, "bf16")
+    w = (Hq + 2 * Hkv) * D
+    fused, grads = torch.zeros(T, w + 8, dtype=torch.bfloat16, device="cuda"), torch.zeros(T, w + 16, dtype=torch.bfloat16, device="cuda")
+    cut = lambda t: (t[:, :Hq * D].view(T, Hq, D), t[:, Hq * D:(Hq + Hkv) * D].view(T, Hkv, D),
+                     t[:, (Hq + Hkv) * D:w].view(T, Hkv, D))
+    for dst, n in zip(cut(fused), "qkv"):
+        dst.copy_(st[n])
+    q, k, v = cut(fused)
+    dq, dk, dv = cut(grads)
+    o, do = (torch.zeros(T, Hq * D + 24, dtype=torch.bfloat16, device="cuda")[:, :Hq * D].view(T, Hq, D) for _ in range(2))
+    do.copy_(st["dout"])
+    lse = torch.empty(Hq, T, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        sh = P.attn_shape(q, k, v, st["ndoc"], True, 0.2)
+        plan = torch.empty(P.poetx_attn_plan_bytes(sh), dtype=torch.uint8, device="cuda")
+        ws = torch.empty(P.poetx_attn_workspace_bytes(sh, 0) + P.poetx_attn_workspace_bytes(sh, 1), dtype=torch.uint8, device="cuda")
+        P.poetx_attn_plan(sh, to_dev(st["cu_q"]), to_dev(st["cu_k"]), plan)
+        P.poetx_attn_fwd(sh, q, k, v, plan, o, lse, ws, to_dev(st["slopes"]))
+        P.poetx_attn_bwd(sh, do, q, k, v, o, lse, plan, dq, dk, dv, ws, to_dev(st["slopes"]))
+    s.synchronize()
+    for n, t in (("o", o), ("dq", dq), ("dk", dk), ("dv", dv), ("lse", lse)):
+        np.testing.assert_array_equal(bits(t.contiguous()), bits(want[n]), err_msg=n)
+    assert not to_f64(grads[:, w:].contiguous()).any() and not to_f64(fused[:, w:].contiguous()).any()
+
+
+def test_attention_rows_past_32_bits():
+    """Key rows whose byte offset passes 2^32 (a wide pitch)."""
+    Tk, ld = 70000, 65536
+    wide = torch.empty(Tk, ld, dtype=torch.bfloat16, device="cuda")
+    st = setup(dict(q=[50], k=[100], Hq=2, Hkv=1, D=64), "bf16")
+    want = run(st)
+    k, v = wide[:, 64:128].view(Tk, 1, 64), wide[:, 256:320].view(Tk, 1, 64)
+    k[-100:], v[-100:] = st["k"], st["v"]
+    st["k"], st["v"], st["cu_k"] = k, v, st["cu_k"] + (Tk - 100)
+    out = run(st)
+    for n in ("o", "dq", "lse"):
+        np.testing.assert_array_equal(bits(out[n]), bits(want[n]), err_msg=n)
+    for n in ("dk", "dv"):
+        np.testing.assert_array_equal(bits(out[n][-100:]), bits(want[n]), err_msg=n)
+        assert not out[n][:-100].any()
+
+
+def test_plan_of_decreasing_offsets_stays_in_range():
+    sh = P.attn_shape(torch.empty(40, 1, 64, device="cuda"), torch.empty(30, 1, 64, device="cuda"), torch.empty(30, 1, 64, device="cuda"), 4)
+    plan = torch.empty(P.poetx_attn_plan_bytes(sh), dtype=torch.uint8, device="cuda")
+    bad = torch.tensor([5, -7, 900, 3, 2 ** 31 - 1], dtype=torch.int32, device="cuda")
+    P.poetx_attn_plan(sh, bad, bad.flip(0).contiguous(), plan, torch.tensor([-5, 2 ** 31 - 1, 3, 0], dtype=torch.int32, device="cuda"))
+    a = plan.view(torch.int32).cpu().numpy()
+    for base, n, top in ((0, 40, 30), (64, 40, 30), (192, 30, 40), (256, 30, 40)):
+        part = a[base:base + n]
+        assert (part >= 0).all() and (part <= top).all()
+
+
+# ---- single tokens over a cache --------------------------------------------------------
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("B_,Hq,Hkv,D,rows,lens,start,cap,bias", [
+    (1, 8, 8, 64, 64, [1], None, 0.0, False),
+    (4, 8, 2, 128, 300, [0, 300, 1, 129], None, 0.0, False),
+    (3, 5, 1, 128, 700, [700, 65, 64], [0, 64, 64], 4.0, False),
+    (2, 32, 8, 128, 1100, [1033, 257], [100, 0], 0.0, True),
+    (2, 40, 1, 72, 200, [200, 63], None, 8.0, True),
+    (1, 4, 4, 8, 5000, [4999], [1], 0.0, True),
+    (2, 2, 1, 128, 40, [90, -3], None, 0.0, False),       # lengths outside the cache are clamped
+])
+def test_decode(dt, B_, Hq, Hkv, D, rows, lens, start, cap, bias):
+    say(f"decode {dt} B={B_} H={Hq}/{Hkv} D={D} rows={rows} lens={lens}")
+    rng = np.random.default_rng(rows + D)
+    q, k, v = normal(rng, (B_, Hq, D), dt, 1.5), normal(rng, (B_, rows, Hkv, D), dt), normal(rng, (B_, rows, Hkv, D), dt)
+    slopes = (2.0 ** -np.arange(1, Hq + 1)).astype(np.float32) if bias else None
+    cl = np.clip(lens, 0, rows)
+    ref = B.decode(to_f64(q), to_f64(k), to_f64(v), start, cl, None, cap, slopes)
+    for b in range(B_):  # what is outside the range may hold anything
+        k[b, cl[b]:], v[b, cl[b]:] = float("nan"), float("inf")
+        if start:
+            k[b, :start[b]], v[b, :start[b]] = float("inf"), float("nan")
+    sh = P.decode_shape(q, k, v, cap=cap)
+    ws = torch.empty(P.poetx_attn_decode_workspace_bytes(sh), dtype=torch.uint8, device="cuda")
+    o = torch.full_like(q, 7.0)
+    args = dict(start=None if start is None else to_dev(np.asarray(start, np.int32)), slopes=None if slopes is None else to_dev(slopes))
+    P.poetx_attn_decode(sh, q, k, v, to_dev(np.asarray(lens, np.int32)), o, ws, **args)
+    close("o", o, ref, dt)
+    o2 = torch.empty_like(q)
+    P.poetx_attn_decode(sh, q, k, v, to_dev(np.asarray(lens, np.int32)), o2, ws, **args)
+    np.testing.assert_array_equal(bits(o), bits(o2))
+
+
+def test_decode_cache_past_32_bits_and_layouts():
+    """A cache [rows][B] (sequence pitch below the row pitch) whose offsets
+    pass 2^32 bytes."""
+    rows, Hkv, D = 2_200_000, 8, 128
+    rng = np.random.default_rng(0)
+    k, v = (torch.empty(rows, 1, Hkv, D, dtype=torch.bfloat16, device="cuda").transpose(0, 1) for _ in range(2))
+    q = normal(rng, (1, 16, D), "bf16")
+    k[0, -333:], v[0, -333:] = normal(rng, (333, Hkv, D), "bf16"), normal(rng, (333, Hkv, D), "bf16")
+    sh = P.decode_shape(q, k, v)
+    ws = torch.empty(P.poetx_attn_decode_workspace_bytes(sh), dtype=torch.uint8, device="cuda")
+    o = torch.empty_like(q)
+    i32 = lambda x: torch.tensor([x], dtype=torch.int32, device="cuda")
+    P.poetx_attn_decode(sh, q, k, v, i32(rows), o, ws, start=i32(rows - 333))
+    close("o", o, B.decode(to_f64(q), to_f64(k[:, -333:].contiguous()), to_f64(v[:, -333:].contiguous()), None, [333]), "bf16")
+    # two sequences interleaved row by row
+    k2, v2 = (normal(rng, (70, 2, Hkv, D), "bf16").transpose(0, 1) for _ in range(2))
+    q2 = normal(rng, (2, 16, D), "bf16")
+    sh = P.decode_shape(q2, k2, v2)
+    ws = torch.empty(P.poetx_attn_decode_workspace_bytes(sh), dtype=torch.uint8, device="cuda")
+    o = torch.empty_like(q2)
+    P.poetx_attn_decode(sh, q2, k2, v2, torch.tensor([70, 41], dtype=torch.int32, device="cuda"), o, ws)
+    close("o", o, B.decode(to_f64(q2), to_f64(k2.contiguous()), to_f64(v2.contiguous()), None, [70, 41]), "bf16")
+
+
+# ---- graphs -----------------------------------------------------------------------------
+def test_block_operators_in_a_captured_graph():
+    """Rotary positions, attention both ways and dropout captured once; every
+    replay, with other work between them, equals the eager calls; the dropout
+    offset on the device gives each replay its own mask."""
+    rng = np.random.default_rng(5)
+    T, Hq, Hkv, D = 200, 4, 2, 64
+    x = {n: normal(rng, (T, h, D), "bf16") for n, h in (("q", Hq), ("k", Hkv), ("v", Hkv), ("do", Hq))}
+    ang = rng.uniform(-3, 3, (T, D // 2))
+    table, pos = to_dev(np.stack([np.cos(ang), np.sin(ang)], -1).astype(np.float32)), torch.arange(T, dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 77, T], dtype=torch.int32, device="cuda")
+    sh = P.attn_shape(x["q"], x["k"], x["v"], 2)
+    new = lambda: {n: torch.empty_like(x[m]) for n, m in (("qr", "q"), ("kr", "k"), ("o", "q"), ("y", "q"), ("dq", "q"), ("dk", "k"), ("dv", "v"))}
+    plan = torch.empty(P.poetx_attn_plan_bytes(sh), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(max(P.poetx_attn_workspace_bytes(sh, w) for w in (0, 1)) + 16, dtype=torch.uint8, device="cuda")
+    lse = torch.empty(Hq, T, device="cuda")
+    off = torch.zeros(1, dtype=torch.int64, device="cuda")
+
+    def step(t):
+        P.poetx_rope(x["q"], x["k"], pos, table, t["qr"], t["kr"])
+        P.poetx_attn_plan(sh, cu, cu, plan)
+        P.poetx_attn_fwd(sh, t["qr"], t["kr"], x["v"], plan, t["o"], lse, ws)
+        P.poetx_dropout_fwd(t["o"], x["q"], t["y"], 0.25, 3, 0, off)
+        P.poetx_attn_bwd(sh, x["do"], t["qr"], t["kr"], x["v"], t["o"], lse, plan, t["dq"], t["dk"], t["dv"], ws)
+
+    eager, graph = new(), new()
+    step(graph)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(graph)
+    last = None
+    for i in range(4):
+        off.fill_(8 * T * i)
+        x["q"].add_(0.125)
+        step(eager)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        for n in eager:
+            np.testing.assert_array_equal(bits(eager[n]), bits(graph[n]), err_msg=f"{n} {i}")
+        mask = bits(graph["y"] - x["q"])
+        assert last is None or (mask != last).any()
+        last = mask
