@@ -386,7 +386,7 @@ size_t poetx_saved_bytes(const poetx_shape* sh);
  * of type `act`; rows may have a pitch: a tensor of T rows of H heads of D
  * values has head h of row t at t * ld + h * D, so q, k and v may be column
  * ranges of one projection's output.  Pitches count elements, are at least
- * H * D and multiples of 8 (16 bytes for bf16, 32 for float32); the rows of
+ * H * D, at most 2^20 and multiples of 8 (16 bytes for bf16, 32 for float32); the rows of
  * an output must not overlap each other or an input, except where stated.
  */
 

@@ -24,8 +24,8 @@ int32_t check_act(const char* fn, int32_t act) {
 int32_t check_ld(const char* fn, const char* name, int64_t ld, int64_t width) {
   if (ld < width) return fail(POETX_ERR_ARG, "%s: %s=%lld < %lld", fn, name, (long long)ld, (long long)width);
   if (ld % 8) return fail(POETX_ERR_ARG, "%s: %s=%lld is not a multiple of 8", fn, name, (long long)ld);
-  if (ld > (int64_t)1 << 24)
-    return fail(POETX_ERR_ARG, "%s: %s=%lld above 2^24", fn, name, (long long)ld);
+  if (ld > (int64_t)1 << 20)
+    return fail(POETX_ERR_ARG, "%s: %s=%lld above 2^20", fn, name, (long long)ld);
   return POETX_OK;
 }
 

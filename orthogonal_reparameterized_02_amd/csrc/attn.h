@@ -51,6 +51,9 @@ struct AttnArgs {
   AttnPlan pl;
 };
 
+// (api.hip) LDS above 64 KB for a kernel on the current device
+hipError_t lds_opt_in(const void* kern, int bytes);
+
 hipError_t launch_attn_plan(int Tq, int Tk, int ndoc, int causal, const int* cu_q, const int* cu_k,
                             const int* prefix, const AttnPlan& pl, hipStream_t s);
 template <typename TS> hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t s);

@@ -8,22 +8,6 @@ namespace {
 constexpr int NTH = 256;
 
 template <typename TS>
-__global__ __launch_bounds__(NTH) void k_attn_fwd_rows(AttnArgs a) {
-  const int lane = threadIdx.x % 64, h = blockIdx.y;
-  const int t = blockIdx.x * (NTH / 64) + threadIdx.x / 64;
-  if (t >= a.Tq) return;
-  const int hk = h / a.group;
-  float lse;
-  const float2 o = attn_row<TS>((const TS*)a.q + (long)t * a.ldq + (long)h * a.D,
-                                (const TS*)a.k + (long)hk * a.D, a.ldk,
-                                (const TS*)a.v + (long)hk * a.D, a.ldv, a.pl.row_lo[t],
-                                a.pl.row_hi[t], a.pl.row_pos[t], a.D, a.scale, a.cap,
-                                a.slopes ? a.slopes[h] : 0.0f, lane, lse);
-  st2((TS*)a.o + (long)t * a.ldo + (long)h * a.D, lane, a.D, o);
-  if (lane == 0) a.lse[(long)h * a.Tq + t] = lse;
-}
-
-template <typename TS>
 __global__ __launch_bounds__(NTH) void k_attn_dq_rows(AttnArgs a) {
   const int lane = threadIdx.x % 64, h = blockIdx.y;
   const int t = blockIdx.x * (NTH / 64) + threadIdx.x / 64;
@@ -71,11 +55,6 @@ constexpr int ROWS = NTH / 64;
 
 }  // namespace
 
-template <typename TS> hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t s) {
-  k_attn_fwd_rows<TS><<<dim3((a.Tq + ROWS - 1) / ROWS, a.Hq), NTH, 0, s>>>(a);
-  return hipGetLastError();
-}
-
 template <typename TS> hipError_t launch_attn_bwd(const AttnArgs& a, hipStream_t s) {
   k_attn_dq_rows<TS><<<dim3((a.Tq + ROWS - 1) / ROWS, a.Hq), NTH, 0, s>>>(a);
   const hipError_t e = hipGetLastError();
@@ -89,8 +68,6 @@ template <typename TS> hipError_t launch_attn_decode(const DecodeArgs& a, hipStr
   return hipGetLastError();
 }
 
-template hipError_t launch_attn_fwd<bf16>(const AttnArgs&, hipStream_t);
-template hipError_t launch_attn_fwd<float>(const AttnArgs&, hipStream_t);
 template hipError_t launch_attn_bwd<bf16>(const AttnArgs&, hipStream_t);
 template hipError_t launch_attn_bwd<float>(const AttnArgs&, hipStream_t);
 template hipError_t launch_attn_decode<bf16>(const DecodeArgs&, hipStream_t);

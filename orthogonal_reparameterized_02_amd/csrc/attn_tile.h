@@ -1,0 +1,306 @@
+// Tiles, operand fragments and scores of the MFMA attention kernels.
+//
+// Products run on 32 x 32 MFMA tiles.  An operand fragment is 16 bytes a
+// lane: lane l holds row l % 32, and of every 32-byte chunk of that row the
+// half l / 32 (bf16: one v_mfma_f32_32x32x16_bf16 a chunk; float32: four
+// v_mfma_f32_32x32x2_f32).  A and B are read alike, so the order of the
+// elements within a chunk does not matter.  The accumulator holds
+// D[8 (i/4) + 4 (l/32) + i % 4][l % 32] in register i: a lane owns one
+// column, the four rows of a quad are consecutive.
+// Scores are formed as D[key][query] where queries are what a wave owns (the
+// forward pass, dq), or D[query][key] where keys are (dk, dv): the running
+// maximum and sum, the mask and the next product's B operand then stay in the
+// lane, for the quads of a 32-row score tile are exactly a B fragment whose
+// K order is 8 g + 4 (l/32) + 0..3; the A fragment of the transposed tile
+// (rows of V, K, Q or dO read down their columns) takes the same K order.
+#pragma once
+
+#include "attn.h"
+
+namespace poetx {
+
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef short s16x8_t __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
+
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// ---- fragments ----------------------------------------------------------------
+__device__ __forceinline__ f32x16_t mma16(const bf16*, uint4 a, uint4 b, f32x16_t c) {
+  return mfma32x32x16(as_bf16x8(a), as_bf16x8(b), c);
+}
+__device__ __forceinline__ f32x16_t mma16(const float*, uint4 a, uint4 b, f32x16_t c) {
+  c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a.x), __uint_as_float(b.x), c, 0, 0, 0);
+  c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a.y), __uint_as_float(b.y), c, 0, 0, 0);
+  c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a.z), __uint_as_float(b.z), c, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a.w), __uint_as_float(b.w), c, 0, 0, 0);
+}
+
+// ---- tiles in LDS ---------------------------------------------------------------
+// Rows of DP elements (DP = 64 or 128, the head width rounded up; elements
+// past the head are zero), 16-byte chunk c of row r at position c ^ key(r).
+// The keys keep two access patterns off each other's banks: a row fragment
+// (16 rows, one chunk) and a column fragment (bf16: ds_read_b64_tr_b16, 4
+// rows x 64 bytes; float32: two rows four apart, 128 bytes each).
+template <typename T, int DP> struct Tile {
+  static constexpr int ES = sizeof(T);
+  static constexpr int RB = DP * ES;        // bytes a row
+  static constexpr int LPR = RB / 16;       // lanes (chunks) a row
+  static constexpr int RPL = 64 / LPR;      // rows one wave's load fills
+  static constexpr int KS = RB / 32;        // row fragments a row
+  static constexpr int NT = DP / 32;        // 32-wide column tiles
+
+  static __device__ __forceinline__ int key(int r) {
+    if constexpr (ES == 4) return (r & 3) | ((r & 8) >> 1) | ((r & 4) << 1);
+    else if constexpr (RB == 256) return ((r & 3) << 2) | ((r >> 2) & 3);
+    else return ((r & 2) << 1) | ((r >> 2) & 3);
+  }
+  // row fragment ks of rows r0 .. r0 + 31 (r0 a multiple of 32)
+  static __device__ __forceinline__ uint4 row_frag(const char* tile, int r0, int ks, int lane) {
+    const int r = r0 + (lane & 31), c = 2 * ks + (lane >> 5);
+    return *reinterpret_cast<const uint4*>(tile + r * RB + ((c ^ key(r)) << 4));
+  }
+  // column fragment: columns 32 ct + 0..31 as rows of the operand, K = the
+  // tile rows of score quads: bf16 quads 2t, 2t+1 (16 rows), float32 quad t
+  // (8 rows) of the 32 rows from r0
+  static __device__ __forceinline__ uint4 col_frag(const char* tile, int r0, int t, int ct, int lane) {
+    if constexpr (ES == 2) {
+      const int r = r0 + 16 * t + 4 * (lane >> 5) + ((lane & 15) >> 2);
+      const int col = 32 * ct + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+      const int c = col >> 3, b = (col & 7) * 2;
+      const char* p0 = tile + r * RB + ((c ^ key(r)) << 4) + b;
+      const char* p1 = tile + (r + 8) * RB + ((c ^ key(r + 8)) << 4) + b;
+      const s16x4_t h0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(const_cast<char*>(p0)));
+      const s16x4_t h1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(const_cast<char*>(p1)));
+      return __builtin_bit_cast(uint4, __builtin_shufflevector(h0, h1, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+      const int col = 32 * ct + (lane & 31), c = col >> 2, b = (col & 3) * 4;
+      const int r = r0 + 8 * t + 4 * (lane >> 5);
+      uint32_t u[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        u[e] = *reinterpret_cast<const uint32_t*>(tile + (r + e) * RB + ((c ^ key(r + e)) << 4) + b);
+      return make_uint4(u[0], u[1], u[2], u[3]);
+    }
+  }
+  static constexpr int CSTEP = 32 * ES / 64 == 1 ? 2 : 4;  // column fragments per 32 tile rows
+
+  // the B fragment of score quads (see col_frag) of one 32-row score tile
+  static __device__ __forceinline__ uint4 score_frag(const f32x16_t& p, int t) {
+    if constexpr (ES == 2)
+      return make_uint4(pack2bf(p[8 * t], p[8 * t + 1]), pack2bf(p[8 * t + 2], p[8 * t + 3]),
+                        pack2bf(p[8 * t + 4], p[8 * t + 5]), pack2bf(p[8 * t + 6], p[8 * t + 7]));
+    else
+      return make_uint4(__float_as_uint(p[4 * t]), __float_as_uint(p[4 * t + 1]),
+                        __float_as_uint(p[4 * t + 2]), __float_as_uint(p[4 * t + 3]));
+  }
+};
+
+// Loads of a tile straight into LDS (buffer_load_dwordx4 ... lds: a wave
+// fills 1 KB).  Lane l lands at byte 16 l of the wave's part, so it fetches
+// the chunk that belongs there.  The buffer range ends with the last row
+// that counts: rows past it, and chunks past the head (whose offset is put
+// out of range), arrive as zeros.  Completion is tracked by vmcnt.
+template <typename T, int DP, int ROWS, int NW> struct Loader {
+  using L = Tile<T, DP>;
+  static constexpr int STEP = NW * L::RPL;        // rows one load of all waves fills
+  static constexpr int N = ROWS / STEP;           // loads a wave
+  static constexpr int VAR = STEP % 16 ? 2 : 1;   // lane offsets repeat every 16 rows
+  static_assert(ROWS % STEP == 0 && STEP * VAR % 16 == 0, "tile split");
+  int vo[VAR];
+  int ldb;      // pitch in bytes
+  int headb;    // head bytes
+  int wave;
+
+  __device__ __forceinline__ void init(long ld, int D, int wave_, int lane) {
+    ldb = (int)ld * L::ES;
+    headb = D * L::ES;
+    wave = wave_;
+#pragma unroll
+    for (int u = 0; u < VAR; ++u) {
+      const int r = (u * NW + wave) * L::RPL + lane / L::LPR;
+      const int c = (lane % L::LPR) ^ L::key(r);
+      vo[u] = c * 16 < headb ? r * ldb + c * 16 : 0x60000000;
+    }
+  }
+  // rows [row0, row0 + ROWS) of base (a head's first element in row 0), of
+  // which those below `end` count, into LDS at byte offset lds
+  __device__ __forceinline__ void load(const T* base, long ld, int row0, int end, uint32_t lds) const {
+    const int rows = min(max(end - row0, 0), ROWS);
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(base + (long)row0 * ld), (short)0, rows > 0 ? (rows - 1) * ldb + headb : 0, 0x00020000);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const uint32_t m0v = __builtin_amdgcn_readfirstlane(lds + (j * NW + wave) * 1024);
+      asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(m0v),
+                   "v"(vo[j % VAR] + (j - j % VAR) * STEP * ldb), "s"(rs)
+                   : "memory");
+    }
+  }
+};
+
+// A wave's 32 rows as row fragments in registers, straight from memory: rows
+// from `end` on and elements past the head are zero.
+template <typename T, int KS>
+__device__ __forceinline__ void rows_to_regs(uint4 (&f)[KS], const T* base, long ld,
+                                             int row0, int end, int D, int lane) {
+  const int r = row0 + (lane & 31);
+  const T* p = base + (long)r * ld;
+#pragma unroll
+  for (int ks = 0; ks < KS; ++ks) {
+    const int e = (32 * ks + 16 * (lane >> 5)) / (int)sizeof(T);
+    f[ks] = r < end && e < D ? *reinterpret_cast<const uint4*>(p + e) : make_uint4(0, 0, 0, 0);
+  }
+}
+
+// acc (transposed: D[element][row], NT tiles of 32 elements) * mul to the
+// wave's rows in memory: halves of lanes l and l + 32 are joined so that a
+// lane stores eight consecutive elements.
+template <int NT>
+__device__ __forceinline__ void store_rowsT(bf16* p, const f32x16_t (&acc)[NT], float mul, int D,
+                                            bool live, int lane) {
+  const int h = lane >> 5;
+#pragma unroll
+  for (int ct = 0; ct < NT; ++ct)
+#pragma unroll
+    for (int g = 0; g < 4; g += 2) {
+      uint32_t a0 = pack2bf(acc[ct][4 * g] * mul, acc[ct][4 * g + 1] * mul);
+      uint32_t a1 = pack2bf(acc[ct][4 * g + 2] * mul, acc[ct][4 * g + 3] * mul);
+      uint32_t b0 = pack2bf(acc[ct][4 * g + 4] * mul, acc[ct][4 * g + 5] * mul);
+      uint32_t b1 = pack2bf(acc[ct][4 * g + 6] * mul, acc[ct][4 * g + 7] * mul);
+      // upper half of a <-> lower half of b: lane half h then holds quad
+      // g + h of both halves, elements 8 (g + h) + 0..7
+      const auto s0 = __builtin_amdgcn_permlane32_swap(a0, b0, false, false);
+      const auto s1 = __builtin_amdgcn_permlane32_swap(a1, b1, false, false);
+      const int e = 32 * ct + 8 * (g + h);
+      if (live && e < D) *reinterpret_cast<uint4*>(p + e) = make_uint4(s0[0], s1[0], s0[1], s1[1]);
+    }
+}
+template <int NT>
+__device__ __forceinline__ void store_rowsT(float* p, const f32x16_t (&acc)[NT], float mul, int D,
+                                            bool live, int lane) {
+  const int h = lane >> 5;
+#pragma unroll
+  for (int ct = 0; ct < NT; ++ct)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int e = 32 * ct + 8 * g + 4 * h;
+      if (live && e < D)
+        *reinterpret_cast<float4*>(p + e) = make_float4(acc[ct][4 * g] * mul, acc[ct][4 * g + 1] * mul,
+                                                        acc[ct][4 * g + 2] * mul, acc[ct][4 * g + 3] * mul);
+    }
+}
+
+// 0 if every value is finite, NaN otherwise
+template <int NT> __device__ __forceinline__ float finite_probe(const f32x16_t (&acc)[NT]) {
+  float c = 0.0f;
+#pragma unroll
+  for (int ct = 0; ct < NT; ++ct)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) c = fmaf(acc[ct][i], 0.0f, c);
+  return c;
+}
+
+// sum or maximum over the two lanes that share a column
+__device__ __forceinline__ float other_half(float x) {
+  const uint32_t u = __float_as_uint(x);
+  const auto s = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return __uint_as_float((threadIdx.x & 32) ? s[0] : s[1]);
+}
+
+// ---- scores ----------------------------------------------------------------------
+// MODE 0: scale only; 1: capped; 2: distance bias, capped or not.
+// In units of log2: s2 = log2(e) * score.
+template <typename T> __device__ __forceinline__ float tanh_fast(float x) {
+  // 1 - 2 / (e^2x + 1): absolute error of one unit in 2^-23, enough next to
+  // bf16 operands.  float32 near 0 takes an odd polynomial (least squares on
+  // [0, 0.65], relative error 8e-8): the difference would cancel there and the
+  // cap multiplies what is lost.
+  const float big = 1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + exp2_hw(x * (2.0f * LOG2E)));
+  if constexpr (sizeof(T) == 2) return big;
+  const float u = x * x;
+  float p = -0.005514524877071381f;
+  p = fmaf(p, u, 0.020468397065997124f);
+  p = fmaf(p, u, -0.05368747189640999f);
+  p = fmaf(p, u, 0.13330818712711334f);
+  p = fmaf(p, u, -0.3333325982093811f);
+  return fabsf(x) < 0.65f ? fmaf(x * u, p, x) : big;
+}
+
+struct ScoreArgs {
+  float c;      // MODE 0, 2: scale log2e; capped: scale / cap
+  float capl;   // cap log2e, 0: no cap
+  float slope;  // slope log2e
+};
+
+__device__ __forceinline__ ScoreArgs score_args(const AttnArgs& a, int h) {
+  ScoreArgs s;
+  s.c = a.cap > 0.0f ? a.scale / a.cap : a.scale * LOG2E;
+  s.capl = a.cap * LOG2E;
+  s.slope = a.slopes ? a.slopes[h] * LOG2E : 0.0f;
+  return s;
+}
+
+// s2 of q.k; t: tanh of the capped score (0 without a cap); dist: query
+// position - key
+template <typename T, int MODE>
+__device__ __forceinline__ float score2(float qk, const ScoreArgs& s, float dist, float& t) {
+  t = 0.0f;
+  if constexpr (MODE == 0) return qk * s.c;
+  if constexpr (MODE == 1) {
+    t = tanh_fast<T>(qk * s.c);
+    return s.capl * t;
+  }
+  float x = qk * s.c;
+  if (s.capl > 0.0f) {
+    t = tanh_fast<T>(x);
+    x = s.capl * t;
+  }
+  return fmaf(-s.slope, fabsf(dist), x);
+}
+
+// ---- a wave's or workgroup's interval of visible rows ------------------------------
+// Bounds of up to 64 rows per call, one a lane; intervals that are not empty
+// grow with the row, so the first and the last of them give the bounds.
+struct Span {
+  int lo, hi;          // union of the intervals (lo >= hi: none)
+  int all_lo, all_hi;  // intersection
+};
+__device__ __forceinline__ Span span_of(int lo, int hi) {
+  const uint64_t some = __ballot(lo < hi);
+  Span s = {0, 0, 0, 0};
+  if (some) {
+    const int first = __builtin_ctzll(some), last = 63 - __builtin_clzll(some);
+    s.lo = __builtin_amdgcn_readlane(lo, first);
+    s.hi = __builtin_amdgcn_readlane(hi, last);
+    s.all_lo = __builtin_amdgcn_readlane(lo, last);
+    s.all_hi = __builtin_amdgcn_readlane(hi, first);
+  }
+  return s;
+}
+// union of the intervals of rows [r0, r0 + n) of an array pair of `rows`
+__device__ __forceinline__ void span_rows(const int* los, const int* his, int r0, int n, int rows,
+                                          int lane, int& lo, int& hi) {
+  lo = hi = 0;
+  for (int b = 0; b < n; b += 64) {
+    const int r = r0 + b + lane;
+    const bool in = b + lane < n && r < rows;
+    const Span s = span_of(in ? los[r] : 0, in ? his[r] : 0);
+    if (s.lo < s.hi) {
+      if (lo >= hi) lo = s.lo;
+      hi = s.hi;
+    }
+  }
+}
+
+// Consecutive workgroups are dealt round-robin over the 8 XCDs; renumbered so
+// that each XCD walks a contiguous range (the tiles of a head share its keys
+// and values in that XCD's L2).
+__device__ __forceinline__ int xcd_order(int id, int n) {
+  return n % 8 == 0 ? (id % 8) * (n / 8) + id / 8 : id;
+}
+
+}  // namespace poetx
