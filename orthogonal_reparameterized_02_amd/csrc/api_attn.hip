@@ -88,7 +88,7 @@ AttnPlan plan_at(const poetx_attn_shape* sh, const void* plan) {
 }
 
 size_t attn_ws(const poetx_attn_shape* sh, int which) {
-  return which == 0 ? 0 : align_up((size_t)sh->Hq * sh->Tq * 4);  // delta
+  return which == 0 ? 0 : 2 * align_up((size_t)sh->Hq * sh->Tq * 4);  // delta, lse2
 }
 
 AttnArgs args_of(const poetx_attn_shape* sh, const void* q, const void* k, const void* v,
@@ -296,6 +296,7 @@ int32_t poetx_attn_bwd(const poetx_attn_shape* sh, const void* dout, const void*
   a.dout = dout;
   a.dq = dq, a.dk = dk, a.dv = dv;
   a.delta = (float*)ws;
+  a.lse2 = (float*)((char*)ws + align_up((size_t)sh->Hq * sh->Tq * 4));
   const hipStream_t s = (hipStream_t)stream;
   return launched(sh->act == POETX_BF16 ? launch_attn_bwd<bf16>(a, s) : launch_attn_bwd<float>(a, s), fn);
 }

@@ -47,7 +47,7 @@ struct AttnArgs {
   // backward
   const void* dout;
   void *dq, *dk, *dv;
-  float* delta;  // [Hq][Tq]
+  float *delta, *lse2;  // [Hq][Tq] each
   AttnPlan pl;
 };
 

@@ -1,0 +1,358 @@
+// Attention backward on MFMA tiles, in two passes without atomics: dq (a
+// wave owns 32 queries and walks their keys), then dk and dv (a wave owns 32
+// keys and walks the queries that see them, every query head of the group in
+// turn).  Both form the scores again from q, k and lse.  The second forming
+// costs two products in seven; adding dq tiles from the second pass into
+// memory instead would need atomics, whose order changes the sums.
+//   p = exp2(s2 - lse2),  ds = p (dp - delta) (1 - t^2),
+//   dq = scale ds k,  dk = scale ds^T q,  dv = p^T dout
+// -delta is the initial value of the dp accumulators; scale multiplies the
+// finished sums.
+#include "attn_rows.h"
+#include "attn_tile.h"
+
+namespace poetx {
+
+namespace {
+
+constexpr int NW = 4;         // waves
+constexpr int BM = 32 * NW;   // rows a workgroup owns
+
+template <typename T, int DP> struct BwdCfg {
+  static constexpr int BN = sizeof(T) == 2 ? 64 : 32;  // rows of a streamed tile
+  static constexpr int TILE = BN * Tile<T, DP>::RB;
+  static constexpr int VS = 64;                        // a wave's load fills 64 values
+  static constexpr int ROWV = 3 * VS * 4;              // lse2, delta, position of a tile's queries
+  static constexpr int LDS_DQ = 4 * TILE;
+  static constexpr int LDS_DKV = 4 * TILE + 2 * ROWV;
+  static constexpr int OCC = sizeof(T) == 2 || DP == 64 ? 2 : 1;  // waves a SIMD: by registers
+};
+
+__device__ __forceinline__ float dot8(const bf16*, uint4 a, uint4 b) {
+  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), s);
+    s = fmaf(__uint_as_float(x[i] & 0xffff0000u), __uint_as_float(y[i] & 0xffff0000u), s);
+  }
+  return s;
+}
+__device__ __forceinline__ float dot8(const float*, uint4 a, uint4 b) {
+  float s = __uint_as_float(a.x) * __uint_as_float(b.x);
+  s = fmaf(__uint_as_float(a.y), __uint_as_float(b.y), s);
+  s = fmaf(__uint_as_float(a.z), __uint_as_float(b.z), s);
+  return fmaf(__uint_as_float(a.w), __uint_as_float(b.w), s);
+}
+
+// dq, and for the second pass delta = dout . o and lse2 = lse log2e of every
+// query (lse2 = +inf where lse = -inf: such a query's p is 0)
+template <typename T, int DP, int MODE>
+__global__ __launch_bounds__(64 * NW, (BwdCfg<T, DP>::OCC)) void k_attn_dq(AttnArgs a, int tiles) {
+  using L = Tile<T, DP>;
+  using C = BwdCfg<T, DP>;
+  constexpr int BN = C::BN, NS = BN / 32;
+  extern __shared__ __align__(16) char smem[];
+  const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int w = xcd_order(blockIdx.x, gridDim.x);
+  const int h = w / tiles, q0 = (tiles - 1 - w % tiles) * BM;  // long rows (causal) first
+  const int hk = h / a.group, r0 = q0 + 32 * wave;
+  const T* qp = (const T*)a.q + (long)h * a.D;
+  const T* kp = (const T*)a.k + (long)hk * a.D;
+  const T* vp = (const T*)a.v + (long)hk * a.D;
+  const T* dop = (const T*)a.dout + (long)h * a.D;
+  const T* op = (const T*)a.o + (long)h * a.D;
+
+  const int t = r0 + (lane & 31);
+  const bool in = t < a.Tq;
+  const int lo = in ? a.pl.row_lo[t] : 0, hi = in ? a.pl.row_hi[t] : 0;
+  const float pos = MODE == 2 && in ? (float)a.pl.row_pos[t] : 0.0f;
+  const Span sp = span_of(lo, hi);
+  int klo, khi;
+  span_rows(a.pl.row_lo, a.pl.row_hi, q0, BM, a.Tq, lane, klo, khi);
+
+  Loader<T, DP, BN, NW> lk, lv;
+  lk.init(a.ldk, a.D, wave, lane);
+  lv.init(a.ldv, a.D, wave, lane);
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
+
+  uint4 qf[L::KS], dof[L::KS];
+  rows_to_regs<T>(dof, dop, a.lddo, r0, a.Tq, a.D, lane);
+  float delta = 0.0f;
+  {
+    uint4 of[L::KS];
+    rows_to_regs<T>(of, op, a.ldo, r0, a.Tq, a.D, lane);
+#pragma unroll
+    for (int ks = 0; ks < L::KS; ++ks) delta += dot8((const T*)nullptr, dof[ks], of[ks]);
+  }
+  delta += other_half(delta);
+  const float lse = in ? a.lse[(long)h * a.Tq + t] : 0.0f;
+  const float lse2 = lse == -INFINITY ? INFINITY : lse * LOG2E;
+  if (in && lane < 32) {
+    a.delta[(long)h * a.Tq + t] = delta;
+    a.lse2[(long)h * a.Tq + t] = lse2;
+  }
+  rows_to_regs<T>(qf, qp, a.ldq, r0, a.Tq, a.D, lane);
+
+  const ScoreArgs sa = score_args(a, h);
+  f32x16_t dq[L::NT];
+#pragma unroll
+  for (int i = 0; i < L::NT; ++i) dq[i] = (f32x16_t){};
+
+  if (klo < khi) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    lk.load(kp, a.ldk, klo, khi, lds0);
+    lv.load(vp, a.ldv, klo, khi, lds0 + 2 * C::TILE);
+  }
+  int buf = 0;
+  for (int j0 = klo; j0 < khi; j0 += BN, buf ^= 1) {
+    // this tile has landed, and every wave has left the other buffer
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (j0 + BN < khi) {
+      lk.load(kp, a.ldk, j0 + BN, khi, lds0 + (buf ^ 1) * C::TILE);
+      lv.load(vp, a.ldv, j0 + BN, khi, lds0 + (2 + (buf ^ 1)) * C::TILE);
+    }
+    const char* kt = smem + buf * C::TILE;
+    const char* vt = smem + (2 + buf) * C::TILE;
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+      const int jn = j0 + 32 * n;
+      if (sp.lo >= jn + 32 || sp.hi <= jn) continue;  // nothing here for this wave
+      f32x16_t s = {}, dp;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) dp[i] = -delta;
+#pragma unroll
+      for (int ks = 0; ks < L::KS; ++ks)
+        s = mma16((const T*)nullptr, L::row_frag(kt, 32 * n, ks, lane), qf[ks], s);
+#pragma unroll
+      for (int ks = 0; ks < L::KS; ++ks)
+        dp = mma16((const T*)nullptr, L::row_frag(vt, 32 * n, ks, lane), dof[ks], dp);
+      const int jl = jn + 4 * (lane >> 5);  // key of register 0
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float tt;
+        if constexpr (MODE == 0) {
+          s[i] = exp2_hw(fmaf(s[i], sa.c, -lse2)) * dp[i];
+        } else {
+          const float x = score2<T, MODE>(s[i], sa, pos - (float)(jl + 8 * (i / 4) + i % 4), tt);
+          s[i] = exp2_hw(x - lse2) * dp[i];
+          s[i] = fmaf(-s[i] * tt, tt, s[i]);
+        }
+      }
+      if (sp.all_lo > jn || sp.all_hi < jn + 32) {  // some pair is hidden
+        const uint32_t width = (uint32_t)(hi - lo);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          s[i] = (uint32_t)(jl - lo + 8 * (i / 4) + i % 4) < width ? s[i] : 0.0f;
+      }
+#pragma unroll
+      for (int u = 0; u < L::CSTEP; ++u) {
+        const uint4 p = L::score_frag(s, u);
+#pragma unroll
+        for (int ct = 0; ct < L::NT; ++ct)
+          dq[ct] = mma16((const T*)nullptr, L::col_frag(kt, 32 * n, u, ct, lane), p, dq[ct]);
+      }
+    }
+  }
+
+  // as in the forward pass: what is not finite is formed again row by row
+  const bool empty = lo >= hi;
+  const float probe = empty ? 0.0f : finite_probe<L::NT>(dq);
+  if (__any(probe != 0.0f)) {
+    for (int r = 0; r < 32; ++r) {
+      const int tr = r0 + r;
+      if (tr >= a.Tq) break;
+      float unused;
+      const float2 g = attn_row_dq<T>(qp + (long)tr * a.ldq, dop + (long)tr * a.lddo,
+                                      op + (long)tr * a.ldo, kp, a.ldk, vp, a.ldv, a.pl.row_lo[tr],
+                                      a.pl.row_hi[tr], a.pl.row_pos[tr], a.D, a.scale, a.cap,
+                                      a.slopes ? a.slopes[h] : 0.0f, a.lse[(long)h * a.Tq + tr], lane, unused);
+      st2((T*)a.dq + (long)tr * a.lddq + (long)h * a.D, lane, a.D, g);
+    }
+    return;
+  }
+  if (empty) {
+#pragma unroll
+    for (int i = 0; i < L::NT; ++i) dq[i] = (f32x16_t){};
+  }
+  store_rowsT<L::NT>((T*)a.dq + (long)(in ? t : 0) * a.lddq + (long)h * a.D, dq, a.scale, a.D, in, lane);
+}
+
+// dk and dv
+template <typename T, int DP, int MODE>
+__global__ __launch_bounds__(64 * NW, (BwdCfg<T, DP>::OCC)) void k_attn_dkv(AttnArgs a, int tiles) {
+  using L = Tile<T, DP>;
+  using C = BwdCfg<T, DP>;
+  constexpr int BN = C::BN, NS = BN / 32;
+  extern __shared__ __align__(16) char smem[];
+  const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int w = xcd_order(blockIdx.x, gridDim.x);
+  const int hk = w / tiles, k0 = (w % tiles) * BM;  // keys seen by many (causal) first
+  const int r0 = k0 + 32 * wave;
+  const T* kp = (const T*)a.k + (long)hk * a.D;
+  const T* vp = (const T*)a.v + (long)hk * a.D;
+
+  const int t = r0 + (lane & 31);
+  const bool in = t < a.Tk;
+  const int lo = in ? a.pl.key_lo[t] : 0, hi = in ? a.pl.key_hi[t] : 0;
+  const Span sp = span_of(lo, hi);
+  int qlo, qhi;
+  span_rows(a.pl.key_lo, a.pl.key_hi, k0, BM, a.Tk, lane, qlo, qhi);
+
+  Loader<T, DP, BN, NW> lq, lo_;
+  lq.init(a.ldq, a.D, wave, lane);
+  lo_.init(a.lddo, a.D, wave, lane);
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
+  // tile n: query head n / per of the group, query rows from qlo + BN (n % per)
+  const int per = (qhi - qlo + BN - 1) / BN, total = per * a.group;
+  auto load = [&](int n, int buf) {
+    const int h = hk * a.group + n / per, i0 = qlo + (n % per) * BN;
+    lq.load((const T*)a.q + (long)h * a.D, a.ldq, i0, qhi, lds0 + buf * C::TILE);
+    lo_.load((const T*)a.dout + (long)h * a.D, a.lddo, i0, qhi, lds0 + (2 + buf) * C::TILE);
+    // one value a query: a dword a lane, wave by wave
+    if (wave < (MODE == 2 ? 3 : 2)) {
+      const float* src = wave == 0 ? a.lse2 + (long)h * a.Tq : wave == 1 ? a.delta + (long)h * a.Tq
+                                                                         : (const float*)a.pl.row_pos;
+      const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)(src + i0), (short)0, min(qhi - i0, BN) * 4, 0x00020000);
+      const uint32_t m0v = __builtin_amdgcn_readfirstlane(lds0 + 4 * C::TILE + buf * C::ROWV + wave * C::VS * 4);
+      asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(m0v),
+                   "v"(lane < BN ? lane * 4 : 0x60000000), "s"(rs)
+                   : "memory");
+    }
+  };
+
+  uint4 kf[L::KS], vf[L::KS];
+  rows_to_regs<T>(kf, kp, a.ldk, r0, a.Tk, a.D, lane);
+  rows_to_regs<T>(vf, vp, a.ldv, r0, a.Tk, a.D, lane);
+  f32x16_t dk[L::NT], dv[L::NT];
+#pragma unroll
+  for (int i = 0; i < L::NT; ++i) dk[i] = dv[i] = (f32x16_t){};
+
+  if (total > 0) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    load(0, 0);
+  }
+  int buf = 0;
+  for (int n = 0; n < total; ++n, buf ^= 1) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (n + 1 < total) load(n + 1, buf ^ 1);
+    const int i0 = qlo + (n % per) * BN;
+    const ScoreArgs sa = score_args(a, hk * a.group + n / per);
+    const char* qt = smem + buf * C::TILE;
+    const char* ot = smem + (2 + buf) * C::TILE;
+    const float* rv = reinterpret_cast<const float*>(smem + 4 * C::TILE + buf * C::ROWV);
+#pragma unroll 1
+    for (int u = 0; u < NS; ++u) {
+      const int in0 = i0 + 32 * u;
+      if (sp.lo >= in0 + 32 || sp.hi <= in0) continue;  // nothing here for this wave
+      const float* row = rv + 32 * u + 4 * (lane >> 5);  // quad g: row[8 g .. 8 g + 3]
+      f32x16_t s = {}, dp, p;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const float4 d = *reinterpret_cast<const float4*>(row + C::VS + 8 * g);
+        dp[4 * g] = -d.x, dp[4 * g + 1] = -d.y, dp[4 * g + 2] = -d.z, dp[4 * g + 3] = -d.w;
+      }
+#pragma unroll
+      for (int ks = 0; ks < L::KS; ++ks)
+        s = mma16((const T*)nullptr, L::row_frag(qt, 32 * u, ks, lane), kf[ks], s);
+#pragma unroll
+      for (int ks = 0; ks < L::KS; ++ks)
+        dp = mma16((const T*)nullptr, L::row_frag(ot, 32 * u, ks, lane), vf[ks], dp);
+      const int il = in0 + 4 * (lane >> 5);  // query of register 0
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const float4 e4 = *reinterpret_cast<const float4*>(row + 8 * g);
+        const float e[4] = {e4.x, e4.y, e4.z, e4.w};
+        int4 pq = make_int4(0, 0, 0, 0);
+        if constexpr (MODE == 2) pq = *reinterpret_cast<const int4*>(row + 2 * C::VS + 8 * g);
+        const int ps[4] = {pq.x, pq.y, pq.z, pq.w};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int i = 4 * g + x;
+          if constexpr (MODE == 0) {
+            p[i] = exp2_hw(fmaf(s[i], sa.c, -e[x]));
+            s[i] = p[i] * dp[i];
+          } else {
+            float tt;
+            p[i] = exp2_hw(score2<T, MODE>(s[i], sa, (float)(ps[x] - t), tt) - e[x]);
+            s[i] = p[i] * dp[i];
+            s[i] = fmaf(-s[i] * tt, tt, s[i]);
+          }
+        }
+      }
+      if (sp.all_lo > in0 || sp.all_hi < in0 + 32) {  // some pair is hidden
+        const uint32_t width = (uint32_t)(hi - lo);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const bool seen = (uint32_t)(il - lo + 8 * (i / 4) + i % 4) < width;
+          p[i] = seen ? p[i] : 0.0f;
+          s[i] = seen ? s[i] : 0.0f;
+        }
+      }
+#pragma unroll
+      for (int v = 0; v < L::CSTEP; ++v) {
+        const uint4 pf = L::score_frag(p, v), sf = L::score_frag(s, v);
+#pragma unroll
+        for (int ct = 0; ct < L::NT; ++ct) {
+          dv[ct] = mma16((const T*)nullptr, L::col_frag(ot, 32 * u, v, ct, lane), pf, dv[ct]);
+          dk[ct] = mma16((const T*)nullptr, L::col_frag(qt, 32 * u, v, ct, lane), sf, dk[ct]);
+        }
+      }
+    }
+  }
+
+  const bool empty = lo >= hi;
+  const float probe = empty ? 0.0f : finite_probe<L::NT>(dk) + finite_probe<L::NT>(dv);
+  if (__any(probe != 0.0f)) {
+    for (int r = 0; r < 32; ++r) {
+      const int tr = r0 + r;
+      if (tr >= a.Tk) break;
+      float2 gk, gv;
+      attn_row_dkv<T>(a, hk, tr, lane, gk, gv);
+      st2((T*)a.dk + (long)tr * a.lddk + (long)hk * a.D, lane, a.D, gk);
+      st2((T*)a.dv + (long)tr * a.lddv + (long)hk * a.D, lane, a.D, gv);
+    }
+    return;
+  }
+  if (empty) {
+#pragma unroll
+    for (int i = 0; i < L::NT; ++i) dk[i] = dv[i] = (f32x16_t){};
+  }
+  const long tt = in ? t : 0;
+  store_rowsT<L::NT>((T*)a.dk + tt * a.lddk + (long)hk * a.D, dk, a.scale, a.D, in, lane);
+  store_rowsT<L::NT>((T*)a.dv + tt * a.lddv + (long)hk * a.D, dv, 1.0f, a.D, in, lane);
+}
+
+template <typename T, int DP, int MODE> hipError_t bwd(const AttnArgs& a, hipStream_t s) {
+  using C = BwdCfg<T, DP>;
+  hipError_t e = lds_opt_in((const void*)k_attn_dq<T, DP, MODE>, C::LDS_DQ);
+  if (e == hipSuccess) e = lds_opt_in((const void*)k_attn_dkv<T, DP, MODE>, C::LDS_DKV);
+  if (e != hipSuccess) return e;
+  const int tq = (a.Tq + BM - 1) / BM, tk = (a.Tk + BM - 1) / BM;
+  if (tq) {
+    k_attn_dq<T, DP, MODE><<<dim3((unsigned)tq * a.Hq), 64 * NW, C::LDS_DQ, s>>>(a, tq);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (tk) k_attn_dkv<T, DP, MODE><<<dim3((unsigned)tk * a.Hkv), 64 * NW, C::LDS_DKV, s>>>(a, tk);
+  return hipGetLastError();
+}
+
+template <typename T, int DP> hipError_t bwd_mode(const AttnArgs& a, hipStream_t s) {
+  if (a.slopes) return bwd<T, DP, 2>(a, s);
+  return a.cap > 0.0f ? bwd<T, DP, 1>(a, s) : bwd<T, DP, 0>(a, s);
+}
+
+}  // namespace
+
+template <typename T> hipError_t launch_attn_bwd(const AttnArgs& a, hipStream_t s) {
+  return a.D <= 64 ? bwd_mode<T, 64>(a, s) : bwd_mode<T, 128>(a, s);
+}
+
+template hipError_t launch_attn_bwd<bf16>(const AttnArgs&, hipStream_t);
+template hipError_t launch_attn_bwd<float>(const AttnArgs&, hipStream_t);
+
+}  // namespace poetx
