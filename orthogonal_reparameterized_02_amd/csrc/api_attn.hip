@@ -124,7 +124,18 @@ int32_t check_decode(const char* fn, const poetx_decode_shape* sh) {
   return POETX_OK;
 }
 
-size_t decode_ws(const poetx_decode_shape* sh) { return 256; }
+DecodeArgs decode_args(const poetx_decode_shape* sh) {
+  DecodeArgs a = {};
+  a.B = sh->B, a.Hq = sh->Hq, a.Hkv = sh->Hkv, a.group = sh->Hq / sh->Hkv, a.D = sh->D, a.rows = sh->rows;
+  a.scale = sh->scale > 0.0f ? sh->scale : 1.0f / sqrtf((float)sh->D);
+  a.cap = sh->cap;
+  a.ldq = sh->ldq, a.ldo = sh->ldo, a.ldk = sh->ldk, a.ldv = sh->ldv, a.bsk = sh->bsk, a.bsv = sh->bsv;
+  return a;
+}
+
+size_t decode_ws(const poetx_decode_shape* sh) {
+  return sh->B ? align_up(attn_decode_ws_bytes(decode_args(sh))) : 256;
+}
 
 int32_t check_dropout(const char* fn, int64_t n, int32_t act, double p, uint64_t offset,
                       const uint64_t* offset_dev) {
@@ -323,11 +334,13 @@ int32_t poetx_attn_decode(const poetx_decode_shape* sh, const void* q, const voi
   NEED_PTR(ws);
   const size_t need = decode_ws(sh);
   if (ws_bytes < need) return fail(POETX_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, ws_bytes, need);
-  const DecodeArgs a = {sh->B, sh->Hq, sh->Hkv, sh->Hq / sh->Hkv, sh->D, sh->rows,
-                        sh->scale > 0.0f ? sh->scale : 1.0f / sqrtf((float)sh->D), sh->cap, slopes,
-                        sh->ldq, sh->ldo, sh->ldk, sh->ldv, sh->bsk, sh->bsv, q, k, v, o, start, len};
+  DecodeArgs a = decode_args(sh);
+  a.q = q, a.k = k, a.v = v, a.o = o;
+  a.slopes = slopes;
+  a.start = start, a.len = len;
   const hipStream_t s = (hipStream_t)stream;
-  return launched(sh->act == POETX_BF16 ? launch_attn_decode<bf16>(a, s) : launch_attn_decode<float>(a, s), fn);
+  return launched(sh->act == POETX_BF16 ? launch_attn_decode<bf16>(a, (float*)ws, s)
+                                               : launch_attn_decode<float>(a, (float*)ws, s), fn);
 }
 
 }  // extern "C"

@@ -68,6 +68,8 @@ struct DecodeArgs {
   void* o;
   const int *start, *len;
 };
-template <typename TS> hipError_t launch_attn_decode(const DecodeArgs& a, hipStream_t s);
+// ws: attn_decode_ws_bytes(a) bytes for the pieces' partial results
+size_t attn_decode_ws_bytes(const DecodeArgs& a);
+template <typename TS> hipError_t launch_attn_decode(const DecodeArgs& a, float* ws, hipStream_t s);
 
 }  // namespace poetx

@@ -30,7 +30,7 @@ template <typename T, int DP> struct FwdCfg {
 };
 
 template <typename T, int DP, int MODE>
-__global__ __launch_bounds__(64 * NW, 2) void k_attn_fwd(AttnArgs a, int tiles) {
+__global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void k_attn_fwd(AttnArgs a, int tiles) {
   using L = Tile<T, DP>;
   using C = FwdCfg<T, DP>;
   constexpr int BN = C::BN, NS = BN / 32;

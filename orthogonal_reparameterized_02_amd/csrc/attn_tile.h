@@ -108,7 +108,7 @@ template <typename T, int DP, int ROWS, int NW> struct Loader {
   using L = Tile<T, DP>;
   static constexpr int STEP = NW * L::RPL;        // rows one load of all waves fills
   static constexpr int N = ROWS / STEP;           // loads a wave
-  static constexpr int VAR = STEP % 16 ? 2 : 1;   // lane offsets repeat every 16 rows
+  static constexpr int VAR = STEP < 16 ? 16 / STEP : 1;  // lane offsets repeat every 16 rows
   static_assert(ROWS % STEP == 0 && STEP * VAR % 16 == 0, "tile split");
   int vo[VAR];
   int ldb;      // pitch in bytes
