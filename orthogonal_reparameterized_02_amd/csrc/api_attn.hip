@@ -87,10 +87,6 @@ AttnPlan plan_at(const poetx_attn_shape* sh, const void* plan) {
   return pl;
 }
 
-size_t attn_ws(const poetx_attn_shape* sh, int which) {
-  return which == 0 ? 0 : 2 * align_up((size_t)sh->Hq * sh->Tq * 4);  // delta, lse2
-}
-
 AttnArgs args_of(const poetx_attn_shape* sh, const void* q, const void* k, const void* v,
                  const float* slopes, const void* plan) {
   AttnArgs a = {};
@@ -103,7 +99,15 @@ AttnArgs args_of(const poetx_attn_shape* sh, const void* q, const void* k, const
   a.lddo = sh->lddo, a.lddq = sh->lddq, a.lddk = sh->lddk, a.lddv = sh->lddv;
   a.q = q, a.k = k, a.v = v;
   a.pl = plan_at(sh, plan);
+  a.ndoc = sh->ndoc;
   return a;
+}
+
+// backward: delta and lse2, [Hq][Tq] float32 each; then partial sums
+size_t row_bytes(const poetx_attn_shape* sh) { return align_up((size_t)sh->Hq * sh->Tq * 4); }
+size_t attn_ws(const poetx_attn_shape* sh, int which) {
+  const AttnArgs a = args_of(sh, nullptr, nullptr, nullptr, nullptr, nullptr);
+  return which == 0 ? align_up(attn_fwd_part_bytes(a)) : 2 * row_bytes(sh) + align_up(attn_bwd_part_bytes(a));
 }
 
 int32_t check_decode(const char* fn, const poetx_decode_shape* sh) {
@@ -272,6 +276,7 @@ int32_t poetx_attn_fwd(const poetx_attn_shape* sh, const void* q, const void* k,
   AttnArgs a = args_of(sh, q, k, v, slopes, plan);
   a.o = o;
   a.lse = lse;
+  a.part = (float*)ws;
   const hipStream_t s = (hipStream_t)stream;
   return launched(sh->act == POETX_BF16 ? launch_attn_fwd<bf16>(a, s) : launch_attn_fwd<float>(a, s), fn);
 }
@@ -307,7 +312,8 @@ int32_t poetx_attn_bwd(const poetx_attn_shape* sh, const void* dout, const void*
   a.dout = dout;
   a.dq = dq, a.dk = dk, a.dv = dv;
   a.delta = (float*)ws;
-  a.lse2 = (float*)((char*)ws + align_up((size_t)sh->Hq * sh->Tq * 4));
+  a.lse2 = (float*)((char*)ws + row_bytes(sh));
+  a.part = (float*)((char*)ws + 2 * row_bytes(sh));
   const hipStream_t s = (hipStream_t)stream;
   return launched(sh->act == POETX_BF16 ? launch_attn_bwd<bf16>(a, s) : launch_attn_bwd<float>(a, s), fn);
 }

@@ -27,6 +27,15 @@ hipError_t launch_dropout(long n, const TS* x, const TS* res, TS* out, uint32_t 
                           uint64_t offset, const uint64_t* offset_dev, hipStream_t s);
 
 // ---- attention (attn_*.hip) -------------------------------------------------
+// Parts that a loop of about `steps` tiles is cut into where `groups`
+// workgroups run it: none from one workgroup a CU on (256), else up to two
+// workgroups a CU, four steps a part at least, 16 parts at most.
+inline int parts_for(long groups, int steps) {
+  if (groups >= 256 || groups < 1) return 1;
+  const int want = (int)(512 / groups), most = steps / 4 < 16 ? steps / 4 : 16;
+  return want < most ? want : most > 1 ? most : 1;
+}
+
 // The mask as intervals: query row t sees keys [row_lo, row_hi), stands at
 // key position row_pos; key row j is seen by queries [key_lo, key_hi).
 // Within a document both bounds grow with the row, so the rows of any tile
@@ -48,6 +57,8 @@ struct AttnArgs {
   const void* dout;
   void *dq, *dk, *dv;
   float *delta, *lse2;  // [Hq][Tq] each
+  float* part;          // partial sums (attn_ws_bytes)
+  int ndoc;
   AttnPlan pl;
 };
 
@@ -56,6 +67,9 @@ hipError_t lds_opt_in(const void* kern, int bytes);
 
 hipError_t launch_attn_plan(int Tq, int Tk, int ndoc, int causal, const int* cu_q, const int* cu_k,
                             const int* prefix, const AttnPlan& pl, hipStream_t s);
+// bytes of a.part for the forward and the backward pass
+size_t attn_fwd_part_bytes(const AttnArgs& a);
+size_t attn_bwd_part_bytes(const AttnArgs& a);
 template <typename TS> hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t s);
 template <typename TS> hipError_t launch_attn_bwd(const AttnArgs& a, hipStream_t s);
 

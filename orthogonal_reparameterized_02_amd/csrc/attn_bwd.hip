@@ -8,6 +8,8 @@
 //   dq = scale ds k,  dk = scale ds^T q,  dv = p^T dout
 // -delta is the initial value of the dp accumulators; scale multiplies the
 // finished sums.
+#include <algorithm>
+
 #include "attn_rows.h"
 #include "attn_tile.h"
 
@@ -48,15 +50,16 @@ __device__ __forceinline__ float dot8(const float*, uint4 a, uint4 b) {
 // dq, and for the second pass delta = dout . o and lse2 = lse log2e of every
 // query (lse2 = +inf where lse = -inf: such a query's p is 0)
 template <typename T, int DP, int MODE>
-__global__ __launch_bounds__(64 * NW, (BwdCfg<T, DP>::OCC)) void k_attn_dq(AttnArgs a, int tiles) {
+__global__ __launch_bounds__(64 * NW, (BwdCfg<T, DP>::OCC)) void k_attn_dq(AttnArgs a, int tiles, int parts) {
   using L = Tile<T, DP>;
   using C = BwdCfg<T, DP>;
   constexpr int BN = C::BN, NS = BN / 32;
   extern __shared__ __align__(16) char smem[];
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  const int w = xcd_order(blockIdx.x, gridDim.x);
-  const int h = w / tiles, q0 = (tiles - 1 - w % tiles) * BM;  // long rows (causal) first
-  const int hk = h / a.group, r0 = q0 + 32 * wave;
+  int h, tile;
+  work_of(blockIdx.x, a.Hq, h, tile);
+  const int q0 = (tiles - 1 - tile) * BM;  // long rows (causal) first
+  const int hk = h / a.group, r0 = q0 + 32 * wave, part = blockIdx.y;
   const T* qp = (const T*)a.q + (long)h * a.D;
   const T* kp = (const T*)a.k + (long)hk * a.D;
   const T* vp = (const T*)a.v + (long)hk * a.D;
@@ -70,6 +73,10 @@ __global__ __launch_bounds__(64 * NW, (BwdCfg<T, DP>::OCC)) void k_attn_dq(AttnA
   const Span sp = span_of(lo, hi);
   int klo, khi;
   span_rows(a.pl.row_lo, a.pl.row_hi, q0, BM, a.Tq, lane, klo, khi);
+  int jb, je;  // this part's keys
+  part_of((khi - klo + BN - 1) / BN, parts, part, jb, je);
+  jb = klo + jb * BN;
+  je = min(klo + je * BN, khi);
 
   Loader<T, DP, BN, NW> lk, lv;
   lk.init(a.ldk, a.D, wave, lane);
@@ -88,7 +95,7 @@ __global__ __launch_bounds__(64 * NW, (BwdCfg<T, DP>::OCC)) void k_attn_dq(AttnA
   delta += other_half(delta);
   const float lse = in ? a.lse[(long)h * a.Tq + t] : 0.0f;
   const float lse2 = lse == -INFINITY ? INFINITY : lse * LOG2E;
-  if (in && lane < 32) {
+  if (in && lane < 32 && part == 0) {
     a.delta[(long)h * a.Tq + t] = delta;
     a.lse2[(long)h * a.Tq + t] = lse2;
   }
@@ -99,19 +106,19 @@ __global__ __launch_bounds__(64 * NW, (BwdCfg<T, DP>::OCC)) void k_attn_dq(AttnA
 #pragma unroll
   for (int i = 0; i < L::NT; ++i) dq[i] = (f32x16_t){};
 
-  if (klo < khi) {
+  if (jb < je) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    lk.load(kp, a.ldk, klo, khi, lds0);
-    lv.load(vp, a.ldv, klo, khi, lds0 + 2 * C::TILE);
+    lk.load(kp, a.ldk, jb, je, lds0);
+    lv.load(vp, a.ldv, jb, je, lds0 + 2 * C::TILE);
   }
   int buf = 0;
-  for (int j0 = klo; j0 < khi; j0 += BN, buf ^= 1) {
+  for (int j0 = jb; j0 < je; j0 += BN, buf ^= 1) {
     // this tile has landed, and every wave has left the other buffer
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    if (j0 + BN < khi) {
-      lk.load(kp, a.ldk, j0 + BN, khi, lds0 + (buf ^ 1) * C::TILE);
-      lv.load(vp, a.ldv, j0 + BN, khi, lds0 + (2 + (buf ^ 1)) * C::TILE);
+    if (j0 + BN < je) {
+      lk.load(kp, a.ldk, j0 + BN, je, lds0 + (buf ^ 1) * C::TILE);
+      lv.load(vp, a.ldv, j0 + BN, je, lds0 + (2 + (buf ^ 1)) * C::TILE);
     }
     const char* kt = smem + buf * C::TILE;
     const char* vt = smem + (2 + buf) * C::TILE;
@@ -156,40 +163,45 @@ __global__ __launch_bounds__(64 * NW, (BwdCfg<T, DP>::OCC)) void k_attn_dq(AttnA
     }
   }
 
-  // as in the forward pass: what is not finite is formed again row by row
   const bool empty = lo >= hi;
-  const float probe = empty ? 0.0f : finite_probe<L::NT>(dq);
-  if (__any(probe != 0.0f)) {
-    for (int r = 0; r < 32; ++r) {
-      const int tr = r0 + r;
-      if (tr >= a.Tq) break;
-      float unused;
-      const float2 g = attn_row_dq<T>(qp + (long)tr * a.ldq, dop + (long)tr * a.lddo,
-                                      op + (long)tr * a.ldo, kp, a.ldk, vp, a.ldv, a.pl.row_lo[tr],
-                                      a.pl.row_hi[tr], a.pl.row_pos[tr], a.D, a.scale, a.cap,
-                                      a.slopes ? a.slopes[h] : 0.0f, a.lse[(long)h * a.Tq + tr], lane, unused);
-      st2((T*)a.dq + (long)tr * a.lddq + (long)h * a.D, lane, a.D, g);
-    }
-    return;
-  }
-  if (empty) {
+  if (empty) {  // beside rows that see a whole tile it has sums of its own
 #pragma unroll
     for (int i = 0; i < L::NT; ++i) dq[i] = (f32x16_t){};
   }
-  store_rowsT<L::NT>((T*)a.dq + (long)(in ? t : 0) * a.lddq + (long)h * a.D, dq, a.scale, a.D, in, lane);
+  float* pq = a.part + (long)part * a.Tq * a.Hq * a.D + (long)h * a.D;
+  const long ldp = (long)a.Hq * a.D;
+  // as in the forward pass: what is not finite is formed again row by row
+  if (__any(finite_probe<L::NT>(dq) != 0.0f)) {
+    for (int r = 0; r < 32; ++r) {
+      const int tr = r0 + r;
+      if (tr >= a.Tq) break;
+      const float2 x = ld2(dop + (long)tr * a.lddo, lane, a.D), y = ld2(op + (long)tr * a.ldo, lane, a.D);
+      const float2 g = attn_row_dq<T>(qp + (long)tr * a.ldq, dop + (long)tr * a.lddo, kp, a.ldk, vp, a.ldv,
+                                      max(a.pl.row_lo[tr], jb), min(a.pl.row_hi[tr], je), a.pl.row_pos[tr],
+                                      a.D, a.scale, a.cap, a.slopes ? a.slopes[h] : 0.0f,
+                                      a.lse[(long)h * a.Tq + tr], wave_sum(x.x * y.x + x.y * y.y), lane);
+      if (parts > 1) st2(pq + tr * ldp, lane, a.D, g);
+      else st2((T*)a.dq + (long)tr * a.lddq + (long)h * a.D, lane, a.D, make_float2(g.x * a.scale, g.y * a.scale));
+    }
+    return;
+  }
+  const long tt = in ? t : 0;
+  if (parts > 1) store_rowsT<L::NT>(pq + tt * ldp, dq, 1.0f, a.D, in, lane);
+  else store_rowsT<L::NT>((T*)a.dq + tt * a.lddq + (long)h * a.D, dq, a.scale, a.D, in, lane);
 }
 
 // dk and dv
 template <typename T, int DP, int MODE>
-__global__ __launch_bounds__(64 * NW, (BwdCfg<T, DP>::OCC)) void k_attn_dkv(AttnArgs a, int tiles) {
+__global__ __launch_bounds__(64 * NW, DP == 128 ? 1 : 2) void k_attn_dkv(AttnArgs a, int parts) {
   using L = Tile<T, DP>;
   using C = BwdCfg<T, DP>;
   constexpr int BN = C::BN, NS = BN / 32;
   extern __shared__ __align__(16) char smem[];
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  const int w = xcd_order(blockIdx.x, gridDim.x);
-  const int hk = w / tiles, k0 = (w % tiles) * BM;  // keys seen by many (causal) first
-  const int r0 = k0 + 32 * wave;
+  int hk, tile;
+  work_of(blockIdx.x, a.Hkv, hk, tile);
+  const int k0 = tile * BM;  // keys seen by many (causal) first
+  const int r0 = k0 + 32 * wave, part = blockIdx.y;
   const T* kp = (const T*)a.k + (long)hk * a.D;
   const T* vp = (const T*)a.v + (long)hk * a.D;
 
@@ -205,7 +217,9 @@ __global__ __launch_bounds__(64 * NW, (BwdCfg<T, DP>::OCC)) void k_attn_dkv(Attn
   lo_.init(a.lddo, a.D, wave, lane);
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
   // tile n: query head n / per of the group, query rows from qlo + BN (n % per)
-  const int per = (qhi - qlo + BN - 1) / BN, total = per * a.group;
+  const int per = (qhi - qlo + BN - 1) / BN;
+  int nb, ne;  // this part's tiles
+  part_of(per * a.group, parts, part, nb, ne);
   auto load = [&](int n, int buf) {
     const int h = hk * a.group + n / per, i0 = qlo + (n % per) * BN;
     lq.load((const T*)a.q + (long)h * a.D, a.ldq, i0, qhi, lds0 + buf * C::TILE);
@@ -230,21 +244,21 @@ __global__ __launch_bounds__(64 * NW, (BwdCfg<T, DP>::OCC)) void k_attn_dkv(Attn
 #pragma unroll
   for (int i = 0; i < L::NT; ++i) dk[i] = dv[i] = (f32x16_t){};
 
-  if (total > 0) {
+  if (nb < ne) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    load(0, 0);
+    load(nb, 0);
   }
   int buf = 0;
-  for (int n = 0; n < total; ++n, buf ^= 1) {
+  for (int n = nb; n < ne; ++n, buf ^= 1) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    if (n + 1 < total) load(n + 1, buf ^ 1);
+    if (n + 1 < ne) load(n + 1, buf ^ 1);
     const int i0 = qlo + (n % per) * BN;
     const ScoreArgs sa = score_args(a, hk * a.group + n / per);
     const char* qt = smem + buf * C::TILE;
     const char* ot = smem + (2 + buf) * C::TILE;
     const float* rv = reinterpret_cast<const float*>(smem + 4 * C::TILE + buf * C::ROWV);
-#pragma unroll 1
+#pragma unroll
     for (int u = 0; u < NS; ++u) {
       const int in0 = i0 + 32 * u;
       if (sp.lo >= in0 + 32 || sp.hi <= in0) continue;  // nothing here for this wave
@@ -305,25 +319,75 @@ __global__ __launch_bounds__(64 * NW, (BwdCfg<T, DP>::OCC)) void k_attn_dkv(Attn
   }
 
   const bool empty = lo >= hi;
-  const float probe = empty ? 0.0f : finite_probe<L::NT>(dk) + finite_probe<L::NT>(dv);
-  if (__any(probe != 0.0f)) {
-    for (int r = 0; r < 32; ++r) {
-      const int tr = r0 + r;
-      if (tr >= a.Tk) break;
-      float2 gk, gv;
-      attn_row_dkv<T>(a, hk, tr, lane, gk, gv);
-      st2((T*)a.dk + (long)tr * a.lddk + (long)hk * a.D, lane, a.D, gk);
-      st2((T*)a.dv + (long)tr * a.lddv + (long)hk * a.D, lane, a.D, gv);
-    }
-    return;
-  }
-  if (empty) {
+  if (empty) {  // beside rows that see a whole tile it has sums of its own
 #pragma unroll
     for (int i = 0; i < L::NT; ++i) dk[i] = dv[i] = (f32x16_t){};
   }
+  const long ldp = (long)a.Hkv * a.D;
+  float* pk = a.part + (long)part * 2 * a.Tk * ldp + (long)hk * a.D;
+  float* pv = pk + a.Tk * ldp;
+  T* gk = (T*)a.dk + (long)hk * a.D;
+  T* gv = (T*)a.dv + (long)hk * a.D;
+  if (__any(finite_probe<L::NT>(dk) + finite_probe<L::NT>(dv) != 0.0f)) {
+    for (int r = 0; r < 32; ++r) {
+      const int tr = r0 + r;
+      if (tr >= a.Tk) break;
+      float2 xk = make_float2(0.0f, 0.0f), xv = xk;
+      for (int n = nb; n < ne; ++n) {
+        const int i0 = qlo + (n % per) * BN;
+        attn_row_dkv<T>(a, hk * a.group + n / per, tr, max(a.pl.key_lo[tr], i0),
+                        min(a.pl.key_hi[tr], i0 + BN), lane, xk, xv);
+      }
+      if (parts > 1) {
+        st2(pk + tr * ldp, lane, a.D, xk);
+        st2(pv + tr * ldp, lane, a.D, xv);
+      } else {
+        st2(gk + tr * a.lddk, lane, a.D, make_float2(xk.x * a.scale, xk.y * a.scale));
+        st2(gv + tr * a.lddv, lane, a.D, xv);
+      }
+    }
+    return;
+  }
   const long tt = in ? t : 0;
-  store_rowsT<L::NT>((T*)a.dk + tt * a.lddk + (long)hk * a.D, dk, a.scale, a.D, in, lane);
-  store_rowsT<L::NT>((T*)a.dv + tt * a.lddv + (long)hk * a.D, dv, 1.0f, a.D, in, lane);
+  if (parts > 1) {
+    store_rowsT<L::NT>(pk + tt * ldp, dk, 1.0f, a.D, in, lane);
+    store_rowsT<L::NT>(pv + tt * ldp, dv, 1.0f, a.D, in, lane);
+  } else {
+    store_rowsT<L::NT>(gk + tt * a.lddk, dk, a.scale, a.D, in, lane);
+    store_rowsT<L::NT>(gv + tt * a.lddv, dv, 1.0f, a.D, in, lane);
+  }
+}
+
+// out[t] = mul * sum over parts, in part order; eight elements a thread.
+// blockIdx.y selects one of two tensors.
+struct JoinArgs {
+  const float* part[2];
+  void* out[2];
+  long ld[2];
+  float mul[2];
+};
+template <typename T>
+__global__ __launch_bounds__(256) void k_attn_sum_parts(JoinArgs j, int parts, long stride, int rows, int width) {
+  const long e = ((long)blockIdx.x * 256 + threadIdx.x) * 8;
+  if (e >= (long)rows * width) return;
+  const long t = e / width, c = e - t * width;
+  const float* p = j.part[blockIdx.y] + e;
+  float v[8] = {};
+  for (int s = 0; s < parts; ++s, p += stride) {
+    const float4 x = *reinterpret_cast<const float4*>(p), y = *reinterpret_cast<const float4*>(p + 4);
+    v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+    v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+  }
+  T* o = (T*)j.out[blockIdx.y] + t * j.ld[blockIdx.y] + c;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) St<T>::st(o + i, v[i] * j.mul[blockIdx.y]);
+}
+
+int dq_parts(const AttnArgs& a) {
+  return parts_for((long)((a.Tq + BM - 1) / BM) * a.Hq, a.Tk / std::max(a.ndoc, 1) / 64);
+}
+int dkv_parts(const AttnArgs& a) {
+  return parts_for((long)((a.Tk + BM - 1) / BM) * a.Hkv, a.Tq / std::max(a.ndoc, 1) / 64 * a.group);
 }
 
 template <typename T, int DP, int MODE> hipError_t bwd(const AttnArgs& a, hipStream_t s) {
@@ -332,13 +396,30 @@ template <typename T, int DP, int MODE> hipError_t bwd(const AttnArgs& a, hipStr
   if (e == hipSuccess) e = lds_opt_in((const void*)k_attn_dkv<T, DP, MODE>, C::LDS_DKV);
   if (e != hipSuccess) return e;
   const int tq = (a.Tq + BM - 1) / BM, tk = (a.Tk + BM - 1) / BM;
+  const int pq = dq_parts(a), pk = dkv_parts(a);
+  const int wq = a.Hq * a.D, wk = a.Hkv * a.D;
+  const auto blocks = [](long n) { return (unsigned)((n / 8 + 255) / 256); };
   if (tq) {
-    k_attn_dq<T, DP, MODE><<<dim3((unsigned)tq * a.Hq), 64 * NW, C::LDS_DQ, s>>>(a, tq);
+    k_attn_dq<T, DP, MODE><<<dim3((unsigned)tq * a.Hq, pq), 64 * NW, C::LDS_DQ, s>>>(a, tq, pq);
     e = hipGetLastError();
+    if (e == hipSuccess && pq > 1) {
+      const JoinArgs j = {{a.part}, {a.dq}, {a.lddq}, {a.scale}};
+      k_attn_sum_parts<T><<<dim3(blocks((long)a.Tq * wq), 1), 256, 0, s>>>(j, pq, (long)a.Tq * wq, a.Tq, wq);
+      e = hipGetLastError();
+    }
     if (e != hipSuccess) return e;
   }
-  if (tk) k_attn_dkv<T, DP, MODE><<<dim3((unsigned)tk * a.Hkv), 64 * NW, C::LDS_DKV, s>>>(a, tk);
-  return hipGetLastError();
+  if (tk) {
+    k_attn_dkv<T, DP, MODE><<<dim3((unsigned)tk * a.Hkv, pk), 64 * NW, C::LDS_DKV, s>>>(a, pk);
+    e = hipGetLastError();
+    if (e == hipSuccess && pk > 1) {
+      const long n = (long)a.Tk * wk;
+      const JoinArgs j = {{a.part, a.part + n}, {a.dk, a.dv}, {a.lddk, a.lddv}, {a.scale, 1.0f}};
+      k_attn_sum_parts<T><<<dim3(blocks(n), 2), 256, 0, s>>>(j, pk, 2 * n, a.Tk, wk);
+      e = hipGetLastError();
+    }
+  }
+  return e;
 }
 
 template <typename T, int DP> hipError_t bwd_mode(const AttnArgs& a, hipStream_t s) {
@@ -347,6 +428,14 @@ template <typename T, int DP> hipError_t bwd_mode(const AttnArgs& a, hipStream_t
 }
 
 }  // namespace
+
+// the two passes use the same bytes one after the other
+size_t attn_bwd_part_bytes(const AttnArgs& a) {
+  const int pq = dq_parts(a), pk = dkv_parts(a);
+  const size_t q = pq > 1 ? (size_t)pq * a.Tq * a.Hq * a.D * 4 : 0;
+  const size_t k = pk > 1 ? (size_t)pk * 2 * a.Tk * a.Hkv * a.D * 4 : 0;
+  return std::max(q, k);
+}
 
 template <typename T> hipError_t launch_attn_bwd(const AttnArgs& a, hipStream_t s) {
   return a.D <= 64 ? bwd_mode<T, 64>(a, s) : bwd_mode<T, 128>(a, s);

@@ -8,6 +8,8 @@
 // is 16 or 32 register operations and one exchange with the lane that holds
 // the other keys, and the probabilities are the next product's operand
 // without leaving their lane.
+#include <algorithm>
+
 #include "attn_rows.h"
 #include "attn_tile.h"
 
@@ -30,15 +32,16 @@ template <typename T, int DP> struct FwdCfg {
 };
 
 template <typename T, int DP, int MODE>
-__global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void k_attn_fwd(AttnArgs a, int tiles) {
+__global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void k_attn_fwd(AttnArgs a, int tiles, int parts) {
   using L = Tile<T, DP>;
   using C = FwdCfg<T, DP>;
   constexpr int BN = C::BN, NS = BN / 32;
   extern __shared__ __align__(16) char smem[];
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  const int w = xcd_order(blockIdx.x, gridDim.x);
-  const int h = w / tiles, q0 = (tiles - 1 - w % tiles) * BM;  // long rows (causal) first
-  const int hk = h / a.group;
+  int h, tile;
+  work_of(blockIdx.x, a.Hq, h, tile);
+  const int q0 = (tiles - 1 - tile) * BM;  // long rows (causal) first
+  const int hk = h / a.group, part = blockIdx.y;
   const T* qp = (const T*)a.q + (long)h * a.D;
   const T* kp = (const T*)a.k + (long)hk * a.D;
   const T* vp = (const T*)a.v + (long)hk * a.D;
@@ -51,6 +54,10 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void 
   const Span sp = span_of(lo, hi);
   int klo, khi;
   span_rows(a.pl.row_lo, a.pl.row_hi, q0, BM, a.Tq, lane, klo, khi);
+  int jb, je;  // this part's keys
+  part_of((khi - klo + BN - 1) / BN, parts, part, jb, je);
+  jb = klo + jb * BN;
+  je = min(klo + je * BN, khi);
 
   uint4 qf[L::KS];
   rows_to_regs<T>(qf, qp, a.ldq, q0 + 32 * wave, a.Tq, a.D, lane);
@@ -65,18 +72,18 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void 
   for (int i = 0; i < L::NT; ++i) o[i] = (f32x16_t){};
   float m = -INFINITY, l = 0.0f;  // m: the reference of the exponentials, log2
 
-  if (klo < khi) {
-    lk.load(kp, a.ldk, klo, khi, lds0);
-    lv.load(vp, a.ldv, klo, khi, lds0 + 2 * C::TILE);
+  if (jb < je) {
+    lk.load(kp, a.ldk, jb, je, lds0);
+    lv.load(vp, a.ldv, jb, je, lds0 + 2 * C::TILE);
   }
   int buf = 0;
-  for (int j0 = klo; j0 < khi; j0 += BN, buf ^= 1) {
+  for (int j0 = jb; j0 < je; j0 += BN, buf ^= 1) {
     // this tile has landed, and every wave has left the other buffer
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    if (j0 + BN < khi) {
-      lk.load(kp, a.ldk, j0 + BN, khi, lds0 + (buf ^ 1) * C::TILE);
-      lv.load(vp, a.ldv, j0 + BN, khi, lds0 + (2 + (buf ^ 1)) * C::TILE);
+    if (j0 + BN < je) {
+      lk.load(kp, a.ldk, j0 + BN, je, lds0 + (buf ^ 1) * C::TILE);
+      lv.load(vp, a.ldv, j0 + BN, je, lds0 + (2 + (buf ^ 1)) * C::TILE);
     }
     if (sp.lo >= j0 + BN || sp.hi <= j0) continue;  // nothing here for this wave
     const char* kt = smem + buf * C::TILE;
@@ -144,39 +151,91 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void 
 
   l += other_half(l);
   const bool empty = lo >= hi;
-  // Hidden keys enter the products as 0 times their value.  Where that left
-  // anything that is not finite, the rows are formed again one at a time, from
-  // what each sees alone.
-  const float probe = empty ? 0.0f : finite_probe<L::NT>(o) + l * 0.0f;
-  if (__any(probe != 0.0f)) {
-    for (int r = 0; r < 32; ++r) {
-      const int tr = q0 + 32 * wave + r;
-      if (tr >= a.Tq) break;
-      float lse;
-      const float2 ov = attn_row<T>(qp + (long)tr * a.ldq, kp, a.ldk, vp, a.ldv, a.pl.row_lo[tr],
-                                    a.pl.row_hi[tr], a.pl.row_pos[tr], a.D, a.scale, a.cap,
-                                    a.slopes ? a.slopes[h] : 0.0f, lane, lse);
-      st2((T*)a.o + (long)tr * a.ldo + (long)h * a.D, lane, a.D, ov);
-      if (lane == 0) a.lse[(long)h * a.Tq + tr] = lse;
-    }
-    return;
-  }
-  const bool none = empty || l == 0.0f;
-  if (in && lane < 32) a.lse[(long)h * a.Tq + t] = none ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * LN2;
-  // an empty row of a tile that was not masked has sums of its own: cleared
-  if (empty) {
+  if (empty) {  // beside rows that see a whole tile it has sums of its own
+    m = -INFINITY;
+    l = 0.0f;
 #pragma unroll
     for (int i = 0; i < L::NT; ++i) o[i] = (f32x16_t){};
   }
-  store_rowsT<L::NT>((T*)a.o + (long)(in ? t : 0) * a.ldo + (long)h * a.D, o, none ? 0.0f : 1.0f / l, a.D, in, lane);
+  float* po = a.part + ((long)part * a.Hq + h) * a.Tq * a.D;
+  float* pm = a.part + (long)parts * a.Hq * a.Tq * a.D + ((long)part * a.Hq + h) * a.Tq * 2;
+  // Hidden keys enter the products as 0 times their value.  Where that left
+  // anything that is not finite, the rows are formed again one at a time, from
+  // what each sees alone.
+  if (__any(finite_probe<L::NT>(o) + l * 0.0f != 0.0f)) {
+    for (int r = 0; r < 32; ++r) {
+      const int tr = q0 + 32 * wave + r;
+      if (tr >= a.Tq) break;
+      float mr, lr;
+      const float2 ov = attn_row<T>(qp + (long)tr * a.ldq, kp, a.ldk, vp, a.ldv, max(a.pl.row_lo[tr], jb),
+                                    min(a.pl.row_hi[tr], je), a.pl.row_pos[tr], a.D, a.scale, a.cap,
+                                    a.slopes ? a.slopes[h] : 0.0f, lane, mr, lr);
+      if (parts == 1) {
+        const float inv = lr == 0.0f ? 0.0f : 1.0f / lr;
+        st2((T*)a.o + (long)tr * a.ldo + (long)h * a.D, lane, a.D, make_float2(ov.x * inv, ov.y * inv));
+        if (lane == 0) a.lse[(long)h * a.Tq + tr] = lr == 0.0f ? -INFINITY : mr + __logf(lr);
+      } else {
+        st2(po + (long)tr * a.D, lane, a.D, ov);
+        if (lane == 0) {
+          pm[2 * (long)tr] = mr * LOG2E;
+          pm[2 * (long)tr + 1] = lr;
+        }
+      }
+    }
+    return;
+  }
+  const long tt = in ? t : 0;
+  if (parts > 1) {
+    if (in && lane < 32) {
+      pm[2 * tt] = m;
+      pm[2 * tt + 1] = l;
+    }
+    store_rowsT<L::NT>(po + tt * a.D, o, 1.0f, a.D, in, lane);
+    return;
+  }
+  const bool none = l == 0.0f;
+  if (in && lane < 32) a.lse[(long)h * a.Tq + t] = none ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * LN2;
+  store_rowsT<L::NT>((T*)a.o + tt * a.ldo + (long)h * a.D, o, none ? 0.0f : 1.0f / l, a.D, in, lane);
+}
+
+// joins the parts of one query row: a wave a row, in part order
+template <typename T>
+__global__ __launch_bounds__(64 * NW) void k_attn_fwd_join(AttnArgs a, int parts) {
+  const int lane = threadIdx.x % 64, h = blockIdx.y;
+  const int t = blockIdx.x * NW + threadIdx.x / 64;
+  if (t >= a.Tq) return;
+  const long row = (long)h * a.Tq + t, stride = (long)a.Hq * a.Tq;
+  const float* pm = a.part + parts * stride * a.D;
+  float m = -INFINITY, l = 0.0f;
+  for (int s = 0; s < parts; ++s) m = fmaxf(m, pm[2 * (s * stride + row)]);
+  const float ref = m == -INFINITY ? 0.0f : m;
+  float2 o = make_float2(0.0f, 0.0f);
+  for (int s = 0; s < parts; ++s) {
+    const float f = exp2_hw(pm[2 * (s * stride + row)] - ref);
+    const float2 v = ld2(a.part + (s * stride + row) * a.D, lane, a.D);
+    l = fmaf(f, pm[2 * (s * stride + row) + 1], l);
+    o.x = fmaf(f, v.x, o.x);
+    o.y = fmaf(f, v.y, o.y);
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  st2((T*)a.o + (long)t * a.ldo + (long)h * a.D, lane, a.D, make_float2(o.x * inv, o.y * inv));
+  if (lane == 0) a.lse[row] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * LN2;
+}
+
+// a document's keys stand for the length of the loop
+int fwd_parts(const AttnArgs& a) {
+  return parts_for((long)((a.Tq + BM - 1) / BM) * a.Hq, a.Tk / std::max(a.ndoc, 1) / 64);
 }
 
 template <typename T, int DP, int MODE> hipError_t fwd(const AttnArgs& a, hipStream_t s) {
   constexpr int lds = FwdCfg<T, DP>::LDS;
   const hipError_t e = lds_opt_in((const void*)k_attn_fwd<T, DP, MODE>, lds);
   if (e != hipSuccess) return e;
-  const int tiles = (a.Tq + BM - 1) / BM;
-  k_attn_fwd<T, DP, MODE><<<dim3((unsigned)tiles * a.Hq), 64 * NW, lds, s>>>(a, tiles);
+  const int tiles = (a.Tq + BM - 1) / BM, parts = fwd_parts(a);
+  k_attn_fwd<T, DP, MODE><<<dim3((unsigned)tiles * a.Hq, parts), 64 * NW, lds, s>>>(a, tiles, parts);
+  const hipError_t e2 = hipGetLastError();
+  if (e2 != hipSuccess || parts == 1) return e2;
+  k_attn_fwd_join<T><<<dim3((a.Tq + NW - 1) / NW, a.Hq), 64 * NW, 0, s>>>(a, parts);
   return hipGetLastError();
 }
 
@@ -186,6 +245,11 @@ template <typename T, int DP> hipError_t fwd_mode(const AttnArgs& a, hipStream_t
 }
 
 }  // namespace
+
+size_t attn_fwd_part_bytes(const AttnArgs& a) {
+  const int parts = fwd_parts(a);
+  return parts == 1 ? 0 : (size_t)parts * a.Hq * a.Tq * (a.D + 2) * 4;
+}
 
 template <typename T> hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t s) {
   return a.D <= 64 ? fwd_mode<T, 64>(a, s) : fwd_mode<T, 128>(a, s);

@@ -44,14 +44,15 @@ __device__ __forceinline__ float pair_score(float qk, float scale, float cap, fl
   return s - slope * (float)abs(dist);
 }
 
-// o and lse of one query over keys [lo, hi) (running maximum and sum).  A
-// maximum of -inf is replaced by 0, so scores that are all -inf give o = 0.
+// One query over keys [lo, hi): running maximum m, sum l = sum exp(s - m) and
+// (returned) sum exp(s - m) v.  A maximum of -inf stands for 0, so scores that
+// are all -inf give sums of 0.
 template <typename TS>
 __device__ __forceinline__ float2 attn_row(const TS* q, const TS* k, long ldk, const TS* v, long ldv,
                                            int lo, int hi, int pos, int D, float scale, float cap,
-                                           float slope, int lane, float& lse) {
+                                           float slope, int lane, float& m, float& l) {
   const float2 qv = ld2(q, lane, D);
-  float m = -INFINITY, l = 0.0f;
+  m = -INFINITY, l = 0.0f;
   float2 o = make_float2(0.0f, 0.0f);
   for (int j = lo; j < hi; ++j) {
     const float2 kv = ld2(k + (long)j * ldk, lane, D), vv = ld2(v + (long)j * ldv, lane, D);
@@ -64,60 +65,50 @@ __device__ __forceinline__ float2 attn_row(const TS* q, const TS* k, long ldk, c
     o.x = o.x * f + p * vv.x;
     o.y = o.y * f + p * vv.y;
   }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  lse = l == 0.0f ? -INFINITY : m + __logf(l);
-  return make_float2(o.x * inv, o.y * inv);
+  return o;
 }
 
-// dq of one query; delta = do . o (returned)
+// dq / scale of one query over keys [lo, hi); delta = dout . o
 template <typename TS>
-__device__ __forceinline__ float2 attn_row_dq(const TS* q, const TS* dout, const TS* o, const TS* k,
-                                              long ldk, const TS* v, long ldv, int lo, int hi,
+__device__ __forceinline__ float2 attn_row_dq(const TS* q, const TS* dout, const TS* k, long ldk, const TS* v, long ldv, int lo, int hi,
                                               int pos, int D, float scale, float cap, float slope,
-                                              float lse, int lane, float& delta) {
-  const float2 qv = ld2(q, lane, D), dv = ld2(dout, lane, D), ov = ld2(o, lane, D);
-  delta = wave_sum(dv.x * ov.x + dv.y * ov.y);
+                                              float lse, float delta, int lane) {
+  const float2 qv = ld2(q, lane, D), dv = ld2(dout, lane, D);
   float2 dq = make_float2(0.0f, 0.0f);
   for (int j = lo; j < hi; ++j) {
     const float2 kv = ld2(k + (long)j * ldk, lane, D), vv = ld2(v + (long)j * ldv, lane, D);
     float dsdx;
     const float s = pair_score(wave_sum(qv.x * kv.x + qv.y * kv.y), scale, cap, slope, pos - j, dsdx);
     const float dp = wave_sum(dv.x * vv.x + dv.y * vv.y);
-    const float ds = lse == -INFINITY ? 0.0f : __expf(s - lse) * (dp - delta) * dsdx * scale;
+    const float ds = lse == -INFINITY ? 0.0f : __expf(s - lse) * (dp - delta) * dsdx;
     dq.x += ds * kv.x;
     dq.y += ds * kv.y;
   }
   return dq;
 }
 
-// dk and dv of one key row: every query head of its group, every query row
-// that sees it
+// adds to dk and dv of one key row what query head h, rows [lo, hi), gives
 template <typename TS>
-__device__ __forceinline__ void attn_row_dkv(const AttnArgs& a, int hk, int j, int lane, float2& dk,
-                                             float2& dv) {
-  const TS* kr = (const TS*)a.k + (long)j * a.ldk + (long)hk * a.D;
-  const TS* vr = (const TS*)a.v + (long)j * a.ldv + (long)hk * a.D;
-  const float2 kv = ld2(kr, lane, a.D), vv = ld2(vr, lane, a.D);
-  const int lo = a.pl.key_lo[j], hi = a.pl.key_hi[j];
-  dk = dv = make_float2(0.0f, 0.0f);
-  for (int g = 0; g < a.group; ++g) {
-    const int h = hk * a.group + g;
-    const float slope = a.slopes ? a.slopes[h] : 0.0f;
-    for (int i = lo; i < hi; ++i) {
-      const float2 qv = ld2((const TS*)a.q + (long)i * a.ldq + (long)h * a.D, lane, a.D);
-      const float2 ov = ld2((const TS*)a.dout + (long)i * a.lddo + (long)h * a.D, lane, a.D);
-      float dsdx;
-      const float s = pair_score(wave_sum(qv.x * kv.x + qv.y * kv.y), a.scale, a.cap, slope,
-                                 a.pl.row_pos[i] - j, dsdx);
-      const float dp = wave_sum(ov.x * vv.x + ov.y * vv.y);
-      const float lse = a.lse[(long)h * a.Tq + i];
-      const float p = lse == -INFINITY ? 0.0f : __expf(s - lse);
-      const float ds = p * (dp - a.delta[(long)h * a.Tq + i]) * dsdx * a.scale;
-      dv.x += p * ov.x;
-      dv.y += p * ov.y;
-      dk.x += ds * qv.x;
-      dk.y += ds * qv.y;
-    }
+__device__ __forceinline__ void attn_row_dkv(const AttnArgs& a, int h, int j, int lo, int hi, int lane,
+                                             float2& dk, float2& dv) {
+  const int hk = h / a.group;
+  const float2 kv = ld2((const TS*)a.k + (long)j * a.ldk + (long)hk * a.D, lane, a.D);
+  const float2 vv = ld2((const TS*)a.v + (long)j * a.ldv + (long)hk * a.D, lane, a.D);
+  const float slope = a.slopes ? a.slopes[h] : 0.0f;
+  for (int i = lo; i < hi; ++i) {
+    const float2 qv = ld2((const TS*)a.q + (long)i * a.ldq + (long)h * a.D, lane, a.D);
+    const float2 ov = ld2((const TS*)a.dout + (long)i * a.lddo + (long)h * a.D, lane, a.D);
+    float dsdx;
+    const float s = pair_score(wave_sum(qv.x * kv.x + qv.y * kv.y), a.scale, a.cap, slope,
+                               a.pl.row_pos[i] - j, dsdx);
+    const float dp = wave_sum(ov.x * vv.x + ov.y * vv.y);
+    const float lse = a.lse[(long)h * a.Tq + i];
+    const float p = lse == -INFINITY ? 0.0f : __expf(s - lse);
+    const float ds = p * (dp - a.delta[(long)h * a.Tq + i]) * dsdx;
+    dv.x += p * ov.x;
+    dv.y += p * ov.y;
+    dk.x += ds * qv.x;
+    dk.y += ds * qv.y;
   }
 }
 

@@ -296,11 +296,28 @@ __device__ __forceinline__ void span_rows(const int* los, const int* his, int r0
   }
 }
 
-// Consecutive workgroups are dealt round-robin over the 8 XCDs; renumbered so
-// that each XCD walks a contiguous range (the tiles of a head share its keys
-// and values in that XCD's L2).
-__device__ __forceinline__ int xcd_order(int id, int n) {
-  return n % 8 == 0 ? (id % 8) * (n / 8) + id / 8 : id;
+// Work order: tile by tile, all heads of one before the next, so that tiles
+// of like cost run at the same time and the long ones (the caller's first)
+// start first; head by head, each head's short tiles end beside another's
+// long ones and the last round waits (attn_docs: dk and dv 364 -> 274 us).
+// Consecutive workgroups are dealt round-robin over the 8 XCDs; a head stays
+// on one XCD, beside the heads that share its keys, where 8 divides the heads.
+__device__ __forceinline__ void work_of(int id, int heads, int& head, int& tile) {
+  if (heads % 8 == 0) {
+    const int per = heads / 8, y = id / 8;
+    head = (id % 8) * per + y % per;
+    tile = y / per;
+  } else {
+    head = id % heads;
+    tile = id / heads;
+  }
+}
+
+// Where the tiles are too few to fill the card, a tile's loop is cut into
+// parts whose float32 sums go to memory and are joined by a second kernel.
+__device__ __forceinline__ void part_of(int n, int parts, int part, int& begin, int& end) {
+  begin = (int)((long)n * part / parts);
+  end = (int)((long)n * (part + 1) / parts);
 }
 
 }  // namespace poetx

@@ -153,6 +153,10 @@ CASES = [  # q lengths, k lengths, rows before and after the documents, Hq, Hkv,
     dict(q=[5, 200, 3, 47], k=[64, 200, 0, 1], pad=(0, 70), Hq=5, Hkv=5, D=72, prefix=[0, 64, 1, 1]),
     dict(q=[257], k=[257], Hq=8, Hkv=1, D=64, bias=True, prefix=[100]),
     dict(q=[300], k=[300], Hq=2, Hkv=2, D=128, cap=30.0),
+    # few tiles and long loops: the loops are cut into parts and joined
+    dict(q=[64, 3], k=[1500, 1100], Hq=2, Hkv=1, D=64),
+    dict(q=[33], k=[2049], pad=(1, 2), Hq=4, Hkv=1, D=128, cap=6.0, bias=True),
+    dict(q=[700], k=[40], Hq=8, Hkv=1, D=128, causal=False),
 ]
 
 
@@ -257,6 +261,18 @@ def test_attention_non_finite_reaches_only_who_sees_it(dt, where, value):
         close("dq later rows", out["dq"][111:], ref["dq"][111:], dt)
     for n in ("dq", "dk", "dv", "o"):
         np.testing.assert_array_equal(np.isfinite(to_f64(out[n])), np.isfinite(ref[n]), err_msg=n)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("where,row", [("k", 1490), ("v", 700), ("q", 20), ("dout", 30)])
+def test_attention_non_finite_in_parts(dt, where, row):
+    """The same where loops are cut into parts."""
+    st = setup(dict(q=[40], k=[1500], Hq=4, Hkv=1, D=64), dt)
+    st[where][row, 0] = float("nan")
+    out = run(st)
+    ref, _ = reference(st)
+    for n in ("o", "dq", "dk", "dv"):
+        close(n, out[n], ref[n], dt)
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
