@@ -26,8 +26,19 @@ template <typename T, int DP> struct BwdCfg {
   static constexpr int VS = 64;                        // a wave's load fills 64 values
   static constexpr int ROWV = 3 * VS * 4;              // lse2, delta, position of a tile's queries
   static constexpr int LDS_DQ = 4 * TILE;
-  static constexpr int LDS_DKV = 4 * TILE + 2 * ROWV;
-  static constexpr int OCC = sizeof(T) == 2 || DP == 64 ? 2 : 1;  // waves a SIMD: by registers
+  // Second pass: two waves (NQ) take the same 32 keys and every other 32
+  // queries, and add their sums at the end, so that a workgroup's loop, whose
+  // length decides when the last workgroup ends, is half as long.  A wave
+  // holds two 32-row sums, keys and values; with 128 bf16 columns that is a
+  // few registers more than two waves a SIMD have: the values stay in LDS.
+  static constexpr int NQ = sizeof(T) == 2 || DP == 64 ? 2 : 1;
+  static constexpr bool VLDS = sizeof(T) == 2 && DP == 128;
+  static constexpr int BQ = 32 * NQ;
+  static constexpr int QTILE = BQ * Tile<T, DP>::RB;
+  static constexpr int VTILE = VLDS ? BM * Tile<T, DP>::RB : 0;
+  static constexpr int JOIN = NQ == 2 ? NW * 2 * 32 * DP * 4 : 0;
+  static constexpr int LDS_DKV = std::max(4 * QTILE + 2 * ROWV + VTILE, JOIN);
+  static constexpr int OCC = sizeof(T) == 2 || DP == 64 ? 2 : 1;  // waves a SIMD, by registers
 };
 
 __device__ __forceinline__ float dot8(const bf16*, uint4 a, uint4 b) {
@@ -192,16 +203,17 @@ __global__ __launch_bounds__(64 * NW, (BwdCfg<T, DP>::OCC)) void k_attn_dq(AttnA
 
 // dk and dv
 template <typename T, int DP, int MODE>
-__global__ __launch_bounds__(64 * NW, DP == 128 ? 1 : 2) void k_attn_dkv(AttnArgs a, int parts) {
+__global__ __launch_bounds__((64 * NW * BwdCfg<T, DP>::NQ), (BwdCfg<T, DP>::OCC)) void k_attn_dkv(AttnArgs a, int parts) {
   using L = Tile<T, DP>;
   using C = BwdCfg<T, DP>;
-  constexpr int BN = C::BN, NS = BN / 32;
+  constexpr int BN = C::BQ, NWA = NW * C::NQ;
   extern __shared__ __align__(16) char smem[];
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int wk = wave % NW, wq = wave / NW;  // 32 keys; 32 queries of a tile
   int hk, tile;
   work_of(blockIdx.x, a.Hkv, hk, tile);
   const int k0 = tile * BM;  // keys seen by many (causal) first
-  const int r0 = k0 + 32 * wave, part = blockIdx.y;
+  const int r0 = k0 + 32 * wk, part = blockIdx.y;
   const T* kp = (const T*)a.k + (long)hk * a.D;
   const T* vp = (const T*)a.v + (long)hk * a.D;
 
@@ -212,7 +224,7 @@ __global__ __launch_bounds__(64 * NW, DP == 128 ? 1 : 2) void k_attn_dkv(AttnArg
   int qlo, qhi;
   span_rows(a.pl.key_lo, a.pl.key_hi, k0, BM, a.Tk, lane, qlo, qhi);
 
-  Loader<T, DP, BN, NW> lq, lo_;
+  Loader<T, DP, BN, NWA> lq, lo_;
   lq.init(a.ldq, a.D, wave, lane);
   lo_.init(a.lddo, a.D, wave, lane);
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
@@ -220,102 +232,141 @@ __global__ __launch_bounds__(64 * NW, DP == 128 ? 1 : 2) void k_attn_dkv(AttnArg
   const int per = (qhi - qlo + BN - 1) / BN;
   int nb, ne;  // this part's tiles
   part_of(per * a.group, parts, part, nb, ne);
-  auto load = [&](int n, int buf) {
-    const int h = hk * a.group + n / per, i0 = qlo + (n % per) * BN;
-    lq.load((const T*)a.q + (long)h * a.D, a.ldq, i0, qhi, lds0 + buf * C::TILE);
-    lo_.load((const T*)a.dout + (long)h * a.D, a.lddo, i0, qhi, lds0 + (2 + buf) * C::TILE);
+  auto load = [&](int h, int i0, int buf) {
+    lq.load((const T*)a.q + (long)h * a.D, a.ldq, i0, qhi, lds0 + buf * C::QTILE);
+    lo_.load((const T*)a.dout + (long)h * a.D, a.lddo, i0, qhi, lds0 + (2 + buf) * C::QTILE);
     // one value a query: a dword a lane, wave by wave
     if (wave < (MODE == 2 ? 3 : 2)) {
       const float* src = wave == 0 ? a.lse2 + (long)h * a.Tq : wave == 1 ? a.delta + (long)h * a.Tq
                                                                          : (const float*)a.pl.row_pos;
       const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
           (void*)(src + i0), (short)0, min(qhi - i0, BN) * 4, 0x00020000);
-      const uint32_t m0v = __builtin_amdgcn_readfirstlane(lds0 + 4 * C::TILE + buf * C::ROWV + wave * C::VS * 4);
+      const uint32_t m0v = __builtin_amdgcn_readfirstlane(lds0 + 4 * C::QTILE + buf * C::ROWV + wave * C::VS * 4);
       asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(m0v),
                    "v"(lane < BN ? lane * 4 : 0x60000000), "s"(rs)
                    : "memory");
     }
   };
 
-  uint4 kf[L::KS], vf[L::KS];
+  uint4 kf[L::KS], vf[C::VLDS ? 1 : L::KS];
   rows_to_regs<T>(kf, kp, a.ldk, r0, a.Tk, a.D, lane);
-  rows_to_regs<T>(vf, vp, a.ldv, r0, a.Tk, a.D, lane);
+  const char* vt = smem + 4 * C::QTILE + 2 * C::ROWV;
+  if constexpr (C::VLDS) {
+    Loader<T, DP, BM, NWA> lv;
+    lv.init(a.ldv, a.D, wave, lane);
+    lv.load(vp, a.ldv, k0, a.Tk, lds0 + 4 * C::QTILE + 2 * C::ROWV);
+  } else {
+    rows_to_regs<T>(vf, vp, a.ldv, r0, a.Tk, a.D, lane);
+  }
+  auto vfrag = [&](int ks) {
+    if constexpr (C::VLDS) return L::row_frag(vt, 32 * wk, ks, lane);
+    else return vf[ks];
+  };
   f32x16_t dk[L::NT], dv[L::NT];
 #pragma unroll
   for (int i = 0; i < L::NT; ++i) dk[i] = dv[i] = (f32x16_t){};
 
+  if (wq) __builtin_amdgcn_s_setprio(1);
+  // no load may be in flight when a workgroup without work ends
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  int h = hk * a.group, i0 = qlo;  // of the current tile
   if (nb < ne) {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    load(nb, 0);
+    h += nb / per;
+    i0 += nb % per * BN;
+    load(h, i0, 0);
   }
   int buf = 0;
   for (int n = nb; n < ne; ++n, buf ^= 1) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    if (n + 1 < ne) load(n + 1, buf ^ 1);
-    const int i0 = qlo + (n % per) * BN;
-    const ScoreArgs sa = score_args(a, hk * a.group + n / per);
-    const char* qt = smem + buf * C::TILE;
-    const char* ot = smem + (2 + buf) * C::TILE;
-    const float* rv = reinterpret_cast<const float*>(smem + 4 * C::TILE + buf * C::ROWV);
+    const int hc = h, in0 = i0 + 32 * wq;
+    i0 += BN;
+    if (i0 >= qhi) {
+      i0 = qlo;
+      ++h;
+    }
+    if (n + 1 < ne) load(h, i0, buf ^ 1);
+    const ScoreArgs sa = score_args(a, hc);
+    const char* qt = smem + buf * C::QTILE;
+    const char* ot = smem + (2 + buf) * C::QTILE;
+    const float* rv = reinterpret_cast<const float*>(smem + 4 * C::QTILE + buf * C::ROWV);
+    if (sp.lo >= in0 + 32 || sp.hi <= in0) continue;  // nothing here for this wave
+    const float* row = rv + 32 * wq + 4 * (lane >> 5);  // quad g: row[8 g .. 8 g + 3]
+    f32x16_t s = {}, dp, p;
 #pragma unroll
-    for (int u = 0; u < NS; ++u) {
-      const int in0 = i0 + 32 * u;
-      if (sp.lo >= in0 + 32 || sp.hi <= in0) continue;  // nothing here for this wave
-      const float* row = rv + 32 * u + 4 * (lane >> 5);  // quad g: row[8 g .. 8 g + 3]
-      f32x16_t s = {}, dp, p;
+    for (int g = 0; g < 4; ++g) {
+      const float4 d = *reinterpret_cast<const float4*>(row + C::VS + 8 * g);
+      dp[4 * g] = -d.x, dp[4 * g + 1] = -d.y, dp[4 * g + 2] = -d.z, dp[4 * g + 3] = -d.w;
+    }
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const float4 d = *reinterpret_cast<const float4*>(row + C::VS + 8 * g);
-        dp[4 * g] = -d.x, dp[4 * g + 1] = -d.y, dp[4 * g + 2] = -d.z, dp[4 * g + 3] = -d.w;
-      }
+    for (int ks = 0; ks < L::KS; ++ks)
+      s = mma16((const T*)nullptr, L::row_frag(qt, 32 * wq, ks, lane), kf[ks], s);
 #pragma unroll
-      for (int ks = 0; ks < L::KS; ++ks)
-        s = mma16((const T*)nullptr, L::row_frag(qt, 32 * u, ks, lane), kf[ks], s);
+    for (int ks = 0; ks < L::KS; ++ks)
+      dp = mma16((const T*)nullptr, L::row_frag(ot, 32 * wq, ks, lane), vfrag(ks), dp);
+    const int il = in0 + 4 * (lane >> 5);  // query of register 0
 #pragma unroll
-      for (int ks = 0; ks < L::KS; ++ks)
-        dp = mma16((const T*)nullptr, L::row_frag(ot, 32 * u, ks, lane), vf[ks], dp);
-      const int il = in0 + 4 * (lane >> 5);  // query of register 0
+    for (int g = 0; g < 4; ++g) {
+      const float4 e4 = *reinterpret_cast<const float4*>(row + 8 * g);
+      const float e[4] = {e4.x, e4.y, e4.z, e4.w};
+      int4 pq = make_int4(0, 0, 0, 0);
+      if constexpr (MODE == 2) pq = *reinterpret_cast<const int4*>(row + 2 * C::VS + 8 * g);
+      const int ps[4] = {pq.x, pq.y, pq.z, pq.w};
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const float4 e4 = *reinterpret_cast<const float4*>(row + 8 * g);
-        const float e[4] = {e4.x, e4.y, e4.z, e4.w};
-        int4 pq = make_int4(0, 0, 0, 0);
-        if constexpr (MODE == 2) pq = *reinterpret_cast<const int4*>(row + 2 * C::VS + 8 * g);
-        const int ps[4] = {pq.x, pq.y, pq.z, pq.w};
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int i = 4 * g + x;
-          if constexpr (MODE == 0) {
-            p[i] = exp2_hw(fmaf(s[i], sa.c, -e[x]));
-            s[i] = p[i] * dp[i];
-          } else {
-            float tt;
-            p[i] = exp2_hw(score2<T, MODE>(s[i], sa, (float)(ps[x] - t), tt) - e[x]);
-            s[i] = p[i] * dp[i];
-            s[i] = fmaf(-s[i] * tt, tt, s[i]);
-          }
-        }
-      }
-      if (sp.all_lo > in0 || sp.all_hi < in0 + 32) {  // some pair is hidden
-        const uint32_t width = (uint32_t)(hi - lo);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const bool seen = (uint32_t)(il - lo + 8 * (i / 4) + i % 4) < width;
-          p[i] = seen ? p[i] : 0.0f;
-          s[i] = seen ? s[i] : 0.0f;
-        }
-      }
-#pragma unroll
-      for (int v = 0; v < L::CSTEP; ++v) {
-        const uint4 pf = L::score_frag(p, v), sf = L::score_frag(s, v);
-#pragma unroll
-        for (int ct = 0; ct < L::NT; ++ct) {
-          dv[ct] = mma16((const T*)nullptr, L::col_frag(ot, 32 * u, v, ct, lane), pf, dv[ct]);
-          dk[ct] = mma16((const T*)nullptr, L::col_frag(qt, 32 * u, v, ct, lane), sf, dk[ct]);
+      for (int x = 0; x < 4; ++x) {
+        const int i = 4 * g + x;
+        if constexpr (MODE == 0) {
+          p[i] = exp2_hw(fmaf(s[i], sa.c, -e[x]));
+          s[i] = p[i] * dp[i];
+        } else {
+          float tt;
+          p[i] = exp2_hw(score2<T, MODE>(s[i], sa, (float)(ps[x] - t), tt) - e[x]);
+          s[i] = p[i] * dp[i];
+          s[i] = fmaf(-s[i] * tt, tt, s[i]);
         }
       }
     }
+    if (sp.all_lo > in0 || sp.all_hi < in0 + 32) {  // some pair is hidden
+      const uint32_t width = (uint32_t)(hi - lo);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const bool seen = (uint32_t)(il - lo + 8 * (i / 4) + i % 4) < width;
+        p[i] = seen ? p[i] : 0.0f;
+        s[i] = seen ? s[i] : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < L::CSTEP; ++v) {
+      const uint4 pf = L::score_frag(p, v), sf = L::score_frag(s, v);
+#pragma unroll
+      for (int ct = 0; ct < L::NT; ++ct) {
+        dv[ct] = mma16((const T*)nullptr, L::col_frag(ot, 32 * wq, v, ct, lane), pf, dv[ct]);
+        dk[ct] = mma16((const T*)nullptr, L::col_frag(qt, 32 * wq, v, ct, lane), sf, dk[ct]);
+      }
+    }
+  }
+
+  if constexpr (C::NQ == 2) {
+    __syncthreads();
+    float* red = reinterpret_cast<float*>(smem) + wk * (2 * 32 * DP) + lane;
+    if (wq == 1) {
+#pragma unroll
+      for (int i = 0; i < L::NT; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          red[64 * (16 * i + r)] = dk[i][r];
+          red[64 * (16 * (L::NT + i) + r)] = dv[i][r];
+        }
+    }
+    __syncthreads();
+    if (wq == 1) return;
+#pragma unroll
+    for (int i = 0; i < L::NT; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        dk[i][r] += red[64 * (16 * i + r)];
+        dv[i][r] += red[64 * (16 * (L::NT + i) + r)];
+      }
   }
 
   const bool empty = lo >= hi;
@@ -410,7 +461,7 @@ template <typename T, int DP, int MODE> hipError_t bwd(const AttnArgs& a, hipStr
     if (e != hipSuccess) return e;
   }
   if (tk) {
-    k_attn_dkv<T, DP, MODE><<<dim3((unsigned)tk * a.Hkv, pk), 64 * NW, C::LDS_DKV, s>>>(a, pk);
+    k_attn_dkv<T, DP, MODE><<<dim3((unsigned)tk * a.Hkv, pk), 64 * NW * C::NQ, C::LDS_DKV, s>>>(a, pk);
     e = hipGetLastError();
     if (e == hipSuccess && pk > 1) {
       const long n = (long)a.Tk * wk;
