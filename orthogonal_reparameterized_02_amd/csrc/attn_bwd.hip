@@ -79,11 +79,13 @@ __global__ __launch_bounds__(64 * NW, (BwdCfg<T, DP>::OCC)) void k_attn_dq(AttnA
 
   const int t = r0 + (lane & 31);
   const bool in = t < a.Tq;
-  const int lo = in ? a.pl.row_lo[t] : 0, hi = in ? a.pl.row_hi[t] : 0;
-  const float pos = MODE == 2 && in ? (float)a.pl.row_pos[t] : 0.0f;
+  const int tc = min(t, a.Tq - 1);
+  const int rlo = a.pl.row_lo[tc], rhi = a.pl.row_hi[tc], rpos = MODE == 2 ? a.pl.row_pos[tc] : 0;
+  const int lo = in ? rlo : 0, hi = in ? rhi : 0;
+  const float pos = (float)rpos;
   const Span sp = span_of(lo, hi);
   int klo, khi;
-  span_rows(a.pl.row_lo, a.pl.row_hi, q0, BM, a.Tq, lane, klo, khi);
+  span_rows<BM>(a.pl.row_lo, a.pl.row_hi, q0, a.Tq, lane, klo, khi);
   int jb, je;  // this part's keys
   part_of((khi - klo + BN - 1) / BN, parts, part, jb, je);
   jb = klo + jb * BN;
@@ -104,7 +106,7 @@ __global__ __launch_bounds__(64 * NW, (BwdCfg<T, DP>::OCC)) void k_attn_dq(AttnA
     for (int ks = 0; ks < L::KS; ++ks) delta += dot8((const T*)nullptr, dof[ks], of[ks]);
   }
   delta += other_half(delta);
-  const float lse = in ? a.lse[(long)h * a.Tq + t] : 0.0f;
+  const float lse = a.lse[(long)h * a.Tq + tc];
   const float lse2 = lse == -INFINITY ? INFINITY : lse * LOG2E;
   if (in && lane < 32 && part == 0) {
     a.delta[(long)h * a.Tq + t] = delta;
@@ -112,13 +114,14 @@ __global__ __launch_bounds__(64 * NW, (BwdCfg<T, DP>::OCC)) void k_attn_dq(AttnA
   }
   rows_to_regs<T>(qf, qp, a.ldq, r0, a.Tq, a.D, lane);
 
+  const uint32_t rlane = L::row_lane(lane), clane = L::col_lane(lane);
   const ScoreArgs sa = score_args(a, h);
   f32x16_t dq[L::NT];
 #pragma unroll
   for (int i = 0; i < L::NT; ++i) dq[i] = (f32x16_t){};
 
+  wait_loads();
   if (jb < je) {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     lk.load(kp, a.ldk, jb, je, lds0);
     lv.load(vp, a.ldv, jb, je, lds0 + 2 * C::TILE);
   }
@@ -131,8 +134,7 @@ __global__ __launch_bounds__(64 * NW, (BwdCfg<T, DP>::OCC)) void k_attn_dq(AttnA
       lk.load(kp, a.ldk, j0 + BN, je, lds0 + (buf ^ 1) * C::TILE);
       lv.load(vp, a.ldv, j0 + BN, je, lds0 + (2 + (buf ^ 1)) * C::TILE);
     }
-    const char* kt = smem + buf * C::TILE;
-    const char* vt = smem + (2 + buf) * C::TILE;
+    const uint32_t kr = rlane + buf * C::TILE, vr = kr + 2 * C::TILE, kc = clane + buf * C::TILE;
 #pragma unroll
     for (int n = 0; n < NS; ++n) {
       const int jn = j0 + 32 * n;
@@ -140,12 +142,20 @@ __global__ __launch_bounds__(64 * NW, (BwdCfg<T, DP>::OCC)) void k_attn_dq(AttnA
       f32x16_t s = {}, dp;
 #pragma unroll
       for (int i = 0; i < 16; ++i) dp[i] = -delta;
-#pragma unroll
-      for (int ks = 0; ks < L::KS; ++ks)
-        s = mma16((const T*)nullptr, L::row_frag(kt, 32 * n, ks, lane), qf[ks], s);
-#pragma unroll
-      for (int ks = 0; ks < L::KS; ++ks)
-        dp = mma16((const T*)nullptr, L::row_frag(vt, 32 * n, ks, lane), dof[ks], dp);
+      {
+        Pipe<2 * L::KS, 8> pp;
+        const auto ld = [&](int i) {
+          return L::row_frag(smem, i < L::KS ? kr : vr, 32 * n, i % L::KS);
+        };
+        pp.start(ld);
+        pp.run(ld, [&](int i, uint4 f) {
+          if (i < L::KS) s = mma16((const T*)nullptr, f, qf[i], s);
+          else dp = mma16((const T*)nullptr, f, dof[i - L::KS], dp);
+        });
+      }
+      Pipe<L::CSTEP * L::NT, 4> cp;
+      const auto ldc = [&](int i) { return L::col_frag(smem, kc, 32 * n, i / L::NT, i % L::NT); };
+      cp.start(ldc);
       const int jl = jn + 4 * (lane >> 5);  // key of register 0
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
@@ -164,13 +174,11 @@ __global__ __launch_bounds__(64 * NW, (BwdCfg<T, DP>::OCC)) void k_attn_dq(AttnA
         for (int i = 0; i < 16; ++i)
           s[i] = (uint32_t)(jl - lo + 8 * (i / 4) + i % 4) < width ? s[i] : 0.0f;
       }
-#pragma unroll
-      for (int u = 0; u < L::CSTEP; ++u) {
-        const uint4 p = L::score_frag(s, u);
-#pragma unroll
-        for (int ct = 0; ct < L::NT; ++ct)
-          dq[ct] = mma16((const T*)nullptr, L::col_frag(kt, 32 * n, u, ct, lane), p, dq[ct]);
-      }
+      uint4 p;
+      cp.run(ldc, [&](int i, uint4 f) {
+        if (i % L::NT == 0) p = L::score_frag(s, i / L::NT);
+        dq[i % L::NT] = mma16((const T*)nullptr, f, p, dq[i % L::NT]);
+      });
     }
   }
 
@@ -219,10 +227,12 @@ __global__ __launch_bounds__((64 * NW * BwdCfg<T, DP>::NQ), (BwdCfg<T, DP>::OCC)
 
   const int t = r0 + (lane & 31);
   const bool in = t < a.Tk;
-  const int lo = in ? a.pl.key_lo[t] : 0, hi = in ? a.pl.key_hi[t] : 0;
+  const int tc = min(t, a.Tk - 1);
+  const int rlo = a.pl.key_lo[tc], rhi = a.pl.key_hi[tc];
+  const int lo = in ? rlo : 0, hi = in ? rhi : 0;
   const Span sp = span_of(lo, hi);
   int qlo, qhi;
-  span_rows(a.pl.key_lo, a.pl.key_hi, k0, BM, a.Tk, lane, qlo, qhi);
+  span_rows<BM>(a.pl.key_lo, a.pl.key_hi, k0, a.Tk, lane, qlo, qhi);
 
   Loader<T, DP, BN, NWA> lq, lo_;
   lq.init(a.ldq, a.D, wave, lane);
@@ -250,7 +260,9 @@ __global__ __launch_bounds__((64 * NW * BwdCfg<T, DP>::NQ), (BwdCfg<T, DP>::OCC)
 
   uint4 kf[L::KS], vf[C::VLDS ? 1 : L::KS];
   rows_to_regs<T>(kf, kp, a.ldk, r0, a.Tk, a.D, lane);
-  const char* vt = smem + 4 * C::QTILE + 2 * C::ROWV;
+  // lane offsets into this wave's 32 queries of a tile, and its values
+  const uint32_t rlane = L::row_lane(lane) + 32 * wq * L::RB, clane = L::col_lane(lane) + 32 * wq * L::RB;
+  const uint32_t vr = L::row_lane(lane) + 4 * C::QTILE + 2 * C::ROWV + 32 * wk * L::RB;
   if constexpr (C::VLDS) {
     Loader<T, DP, BM, NWA> lv;
     lv.init(a.ldv, a.D, wave, lane);
@@ -258,17 +270,12 @@ __global__ __launch_bounds__((64 * NW * BwdCfg<T, DP>::NQ), (BwdCfg<T, DP>::OCC)
   } else {
     rows_to_regs<T>(vf, vp, a.ldv, r0, a.Tk, a.D, lane);
   }
-  auto vfrag = [&](int ks) {
-    if constexpr (C::VLDS) return L::row_frag(vt, 32 * wk, ks, lane);
-    else return vf[ks];
-  };
   f32x16_t dk[L::NT], dv[L::NT];
 #pragma unroll
   for (int i = 0; i < L::NT; ++i) dk[i] = dv[i] = (f32x16_t){};
 
   if (wq) __builtin_amdgcn_s_setprio(1);
-  // no load may be in flight when a workgroup without work ends
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  wait_loads();  // also where there is no work: no load may outlive its workgroup
   int h = hk * a.group, i0 = qlo;  // of the current tile
   if (nb < ne) {
     h += nb / per;
@@ -287,8 +294,8 @@ __global__ __launch_bounds__((64 * NW * BwdCfg<T, DP>::NQ), (BwdCfg<T, DP>::OCC)
     }
     if (n + 1 < ne) load(h, i0, buf ^ 1);
     const ScoreArgs sa = score_args(a, hc);
-    const char* qt = smem + buf * C::QTILE;
-    const char* ot = smem + (2 + buf) * C::QTILE;
+    const uint32_t qr = rlane + buf * C::QTILE, qc = clane + buf * C::QTILE;
+    const uint32_t dr = qr + 2 * C::QTILE, dc = qc + 2 * C::QTILE;
     const float* rv = reinterpret_cast<const float*>(smem + 4 * C::QTILE + buf * C::ROWV);
     if (sp.lo >= in0 + 32 || sp.hi <= in0) continue;  // nothing here for this wave
     const float* row = rv + 32 * wq + 4 * (lane >> 5);  // quad g: row[8 g .. 8 g + 3]
@@ -298,12 +305,29 @@ __global__ __launch_bounds__((64 * NW * BwdCfg<T, DP>::NQ), (BwdCfg<T, DP>::OCC)
       const float4 d = *reinterpret_cast<const float4*>(row + C::VS + 8 * g);
       dp[4 * g] = -d.x, dp[4 * g + 1] = -d.y, dp[4 * g + 2] = -d.z, dp[4 * g + 3] = -d.w;
     }
-#pragma unroll
-    for (int ks = 0; ks < L::KS; ++ks)
-      s = mma16((const T*)nullptr, L::row_frag(qt, 32 * wq, ks, lane), kf[ks], s);
-#pragma unroll
-    for (int ks = 0; ks < L::KS; ++ks)
-      dp = mma16((const T*)nullptr, L::row_frag(ot, 32 * wq, ks, lane), vfrag(ks), dp);
+    {
+      Pipe<L::KS, 4> sp_;
+      const auto ld = [&](int i) { return L::row_frag(smem, qr, 0, i); };
+      sp_.start(ld);
+      sp_.run(ld, [&](int i, uint4 f) { s = mma16((const T*)nullptr, f, kf[i], s); });
+    }
+    if constexpr (C::VLDS) {
+      Pipe<2 * L::KS, 8> dp_;  // dout and value fragments in turn
+      const auto ld = [&](int i) {
+        return L::row_frag(smem, i % 2 ? vr : dr, 0, i / 2);
+      };
+      uint4 of;
+      dp_.start(ld);
+      dp_.run(ld, [&](int i, uint4 f) {
+        if (i % 2 == 0) of = f;
+        else dp = mma16((const T*)nullptr, of, f, dp);
+      });
+    } else {
+      Pipe<L::KS, 4> dp_;
+      const auto ld = [&](int i) { return L::row_frag(smem, dr, 0, i); };
+      dp_.start(ld);
+      dp_.run(ld, [&](int i, uint4 f) { dp = mma16((const T*)nullptr, f, vf[i], dp); });
+    }
     const int il = in0 + 4 * (lane >> 5);  // query of register 0
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
@@ -335,14 +359,19 @@ __global__ __launch_bounds__((64 * NW * BwdCfg<T, DP>::NQ), (BwdCfg<T, DP>::OCC)
         s[i] = seen ? s[i] : 0.0f;
       }
     }
-#pragma unroll
-    for (int v = 0; v < L::CSTEP; ++v) {
-      const uint4 pf = L::score_frag(p, v), sf = L::score_frag(s, v);
-#pragma unroll
-      for (int ct = 0; ct < L::NT; ++ct) {
-        dv[ct] = mma16((const T*)nullptr, L::col_frag(ot, 32 * wq, v, ct, lane), pf, dv[ct]);
-        dk[ct] = mma16((const T*)nullptr, L::col_frag(qt, 32 * wq, v, ct, lane), sf, dk[ct]);
-      }
+    {
+      constexpr int H = L::NT;  // dv and dk products of one fragment of p and ds
+      Pipe<2 * L::CSTEP * H, 4> cp;
+      const auto ld = [&](int i) {
+        return L::col_frag(smem, i % (2 * H) < H ? dc : qc, 0, i / (2 * H), i % H);
+      };
+      cp.start(ld);
+      uint4 f2;
+      cp.run(ld, [&](int i, uint4 f) {
+        if (i % H == 0) f2 = L::score_frag(i % (2 * H) < H ? p : s, i / (2 * H));
+        f32x16_t& acc = i % (2 * H) < H ? dv[i % H] : dk[i % H];
+        acc = mma16((const T*)nullptr, f, f2, acc);
+      });
     }
   }
 

@@ -63,14 +63,13 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void 
   ScoreArgs sa;
   sa.c = a.cap > 0.0f ? a.scale / a.cap : a.scale * LOG2E;
   sa.capl = a.cap * LOG2E;
-  sa.slope = a.slopes && in ? a.slopes[h0 + head] * LOG2E : 0.0f;
+  sa.slope = a.slopes ? a.slopes[h0 + min(head, heads - 1)] * LOG2E : 0.0f;
 
   Loader<T, DP, BN, 1> lk, lv;
   lk.init(a.ldk, a.D, 0, lane);
   lv.init(a.ldv, a.D, 0, lane);
-  char* kt = smem + wave * 2 * TILE;
-  char* vt = kt + TILE;
-  const uint32_t ldsk = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)kt);
+  const uint32_t kr = L::row_lane(lane) + wave * 2 * TILE, vc = L::col_lane(lane) + (wave * 2 + 1) * TILE;
+  const uint32_t ldsk = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem + wave * 2 * TILE;
   const uint32_t ldsv = ldsk + TILE;
 
   f32x16_t o[L::NT];
@@ -78,7 +77,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void 
   for (int i = 0; i < L::NT; ++i) o[i] = (f32x16_t){};
   float m = -INFINITY, l = 0.0f;
   int j0 = p0 + wave * BN;
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // counts below are of tile loads only
+  wait_loads();  // counts below are of tile loads only
   if (j0 < p1) {
     lk.load(kp, a.ldk, j0, p1, ldsk);
     lv.load(vp, a.ldv, j0, p1, ldsv);
@@ -88,7 +87,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void 
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(NL) : "memory");
     f32x16_t sc = {};
 #pragma unroll
-    for (int ks = 0; ks < L::KS; ++ks) sc = mma16((const T*)nullptr, L::row_frag(kt, 0, ks, lane), qf[ks], sc);
+    for (int ks = 0; ks < L::KS; ++ks) sc = mma16((const T*)nullptr, L::row_frag(smem, kr, 0, ks), qf[ks], sc);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     const int jn = min(j0 + GRAIN, p1);  // a load past the piece has no rows: zeros
     lk.load(kp, a.ldk, jn, p1, ldsk);
@@ -121,7 +120,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void 
       const uint4 p = L::score_frag(sc, u);
 #pragma unroll
       for (int ct = 0; ct < L::NT; ++ct)
-        o[ct] = mma16((const T*)nullptr, L::col_frag(vt, 0, u, ct, lane), p, o[ct]);
+        o[ct] = mma16((const T*)nullptr, L::col_frag(smem, vc, 0, u, ct), p, o[ct]);
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     lv.load(vp, a.ldv, jn, p1, ldsv);

@@ -49,11 +49,13 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void 
   // this lane's query, the wave's and the workgroup's keys
   const int t = q0 + 32 * wave + (lane & 31);
   const bool in = t < a.Tq;
-  const int lo = in ? a.pl.row_lo[t] : 0, hi = in ? a.pl.row_hi[t] : 0;
-  const float pos = MODE == 2 && in ? (float)a.pl.row_pos[t] : 0.0f;
+  const int tc = min(t, a.Tq - 1);
+  const int rlo = a.pl.row_lo[tc], rhi = a.pl.row_hi[tc], rpos = MODE == 2 ? a.pl.row_pos[tc] : 0;
+  const int lo = in ? rlo : 0, hi = in ? rhi : 0;
+  const float pos = (float)rpos;
   const Span sp = span_of(lo, hi);
   int klo, khi;
-  span_rows(a.pl.row_lo, a.pl.row_hi, q0, BM, a.Tq, lane, klo, khi);
+  span_rows<BM>(a.pl.row_lo, a.pl.row_hi, q0, a.Tq, lane, klo, khi);
   int jb, je;  // this part's keys
   part_of((khi - klo + BN - 1) / BN, parts, part, jb, je);
   jb = klo + jb * BN;
@@ -66,12 +68,14 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void 
   lv.init(a.ldv, a.D, wave, lane);
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
 
+  const uint32_t rlane = L::row_lane(lane), clane = L::col_lane(lane);
   const ScoreArgs sa = score_args(a, h);
   f32x16_t o[L::NT];
 #pragma unroll
   for (int i = 0; i < L::NT; ++i) o[i] = (f32x16_t){};
   float m = -INFINITY, l = 0.0f;  // m: the reference of the exponentials, log2
 
+  wait_loads();
   if (jb < je) {
     lk.load(kp, a.ldk, jb, je, lds0);
     lv.load(vp, a.ldv, jb, je, lds0 + 2 * C::TILE);
@@ -86,17 +90,23 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void 
       lv.load(vp, a.ldv, j0 + BN, je, lds0 + (2 + (buf ^ 1)) * C::TILE);
     }
     if (sp.lo >= j0 + BN || sp.hi <= j0) continue;  // nothing here for this wave
-    const char* kt = smem + buf * C::TILE;
-    const char* vt = smem + (2 + buf) * C::TILE;
+    const uint32_t kr = rlane + buf * C::TILE, vc = clane + (2 + buf) * C::TILE;
 
     f32x16_t s[NS];
 #pragma unroll
-    for (int n = 0; n < NS; ++n) {
-      s[n] = (f32x16_t){};
-#pragma unroll
-      for (int ks = 0; ks < L::KS; ++ks)
-        s[n] = mma16((const T*)nullptr, L::row_frag(kt, 32 * n, ks, lane), qf[ks], s[n]);
+    for (int n = 0; n < NS; ++n) s[n] = (f32x16_t){};
+    {
+      Pipe<NS * L::KS, 8> kp_;
+      const auto ld = [&](int i) { return L::row_frag(smem, kr, 32 * (i / L::KS), i % L::KS); };
+      kp_.start(ld);
+      kp_.run(ld, [&](int i, uint4 f) { s[i / L::KS] = mma16((const T*)nullptr, f, qf[i % L::KS], s[i / L::KS]); });
     }
+    // the first value fragments travel while the softmax is formed
+    Pipe<NS * L::CSTEP * L::NT, 8> vp_;
+    const auto ldv = [&](int i) {
+      return L::col_frag(smem, vc, 32 * (i / (L::CSTEP * L::NT)), i / L::NT % L::CSTEP, i % L::NT);
+    };
+    vp_.start(ldv);
     const int jl = j0 + 4 * (lane >> 5);  // key of register 0
     float top = -INFINITY;
     if constexpr (MODE != 0) {
@@ -133,20 +143,17 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void 
     }
     const float ref = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-    for (int n = 0; n < NS; ++n) {
+    for (int n = 0; n < NS; ++n)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         s[n][i] = exp2_hw(MODE == 0 ? fmaf(s[n][i], sa.c, -ref) : s[n][i] - ref);
         l += s[n][i];
       }
-#pragma unroll
-      for (int u = 0; u < L::CSTEP; ++u) {
-        const uint4 p = L::score_frag(s[n], u);
-#pragma unroll
-        for (int ct = 0; ct < L::NT; ++ct)
-          o[ct] = mma16((const T*)nullptr, L::col_frag(vt, 32 * n, u, ct, lane), p, o[ct]);
-      }
-    }
+    uint4 p;
+    vp_.run(ldv, [&](int i, uint4 f) {
+      if (i % L::NT == 0) p = L::score_frag(s[i / (L::CSTEP * L::NT)], i / L::NT % L::CSTEP);
+      o[i % L::NT] = mma16((const T*)nullptr, f, p, o[i % L::NT]);
+    });
   }
 
   l += other_half(l);

@@ -58,31 +58,45 @@ template <typename T, int DP> struct Tile {
     else if constexpr (RB == 256) return ((r & 3) << 2) | ((r >> 2) & 3);
     else return ((r & 2) << 1) | ((r >> 2) & 3);
   }
+  // Fragment addresses: a tile's byte offset in LDS (a multiple of 512) plus
+  // one of the two lane offsets below, then constants: the chunk numbers
+  // enter by XOR, the rows by addition.  A fragment costs one XOR, and no
+  // register is held for it.
+  //
   // row fragment ks of rows r0 .. r0 + 31 (r0 a multiple of 32)
-  static __device__ __forceinline__ uint4 row_frag(const char* tile, int r0, int ks, int lane) {
-    const int r = r0 + (lane & 31), c = 2 * ks + (lane >> 5);
-    return *reinterpret_cast<const uint4*>(tile + r * RB + ((c ^ key(r)) << 4));
+  static __device__ __forceinline__ uint32_t row_lane(int lane) {
+    const int r = lane & 31;
+    return r * RB + (((lane >> 5) ^ key(r)) << 4);
+  }
+  static __device__ __forceinline__ uint4 row_frag(const char* lds, uint32_t at, int r0, int ks) {
+    return *reinterpret_cast<const uint4*>(lds + ((at ^ (uint32_t)(ks << 5)) + r0 * RB));
   }
   // column fragment: columns 32 ct + 0..31 as rows of the operand, K = the
   // tile rows of score quads: bf16 quads 2t, 2t+1 (16 rows), float32 quad t
   // (8 rows) of the 32 rows from r0
-  static __device__ __forceinline__ uint4 col_frag(const char* tile, int r0, int t, int ct, int lane) {
+  static __device__ __forceinline__ uint32_t col_lane(int lane) {
     if constexpr (ES == 2) {
-      const int r = r0 + 16 * t + 4 * (lane >> 5) + ((lane & 15) >> 2);
-      const int col = 32 * ct + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
-      const int c = col >> 3, b = (col & 7) * 2;
-      const char* p0 = tile + r * RB + ((c ^ key(r)) << 4) + b;
-      const char* p1 = tile + (r + 8) * RB + ((c ^ key(r + 8)) << 4) + b;
-      const s16x4_t h0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(const_cast<char*>(p0)));
-      const s16x4_t h1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(const_cast<char*>(p1)));
+      const int r = 4 * (lane >> 5) + ((lane & 15) >> 2), c = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+      return r * RB + ((c ^ key(r)) << 4) + (lane & 1) * 8;
+    } else {
+      const int r = 4 * (lane >> 5), c = (lane & 31) >> 2;
+      return r * RB + ((c ^ key(r)) << 4) + (lane & 3) * 4;
+    }
+  }
+  static __device__ __forceinline__ uint4 col_frag(const char* lds, uint32_t at, int r0, int t, int ct) {
+    if constexpr (ES == 2) {
+      // 4 columns x 4 rows a lane; eight rows further the key differs in bit 1
+      const uint32_t p = at ^ (uint32_t)(ct << 6), q = at ^ (uint32_t)((ct << 6) | 32);
+      const int row = (r0 + 16 * t) * RB;
+      const s16x4_t h0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(const_cast<char*>(lds + (p + row))));
+      const s16x4_t h1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(const_cast<char*>(lds + (q + row + 8 * RB))));
       return __builtin_bit_cast(uint4, __builtin_shufflevector(h0, h1, 0, 1, 2, 3, 4, 5, 6, 7));
     } else {
-      const int col = 32 * ct + (lane & 31), c = col >> 2, b = (col & 3) * 4;
-      const int r = r0 + 8 * t + 4 * (lane >> 5);
       uint32_t u[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        u[e] = *reinterpret_cast<const uint32_t*>(tile + (r + e) * RB + ((c ^ key(r + e)) << 4) + b);
+        u[e] = *reinterpret_cast<const uint32_t*>(
+            lds + ((at ^ (uint32_t)((ct << 7) | (t & 1) << 6 | e << 4)) + (r0 + 8 * t + e) * RB));
       return make_uint4(u[0], u[1], u[2], u[3]);
     }
   }
@@ -142,17 +156,23 @@ template <typename T, int DP, int ROWS, int NW> struct Loader {
   }
 };
 
-// A wave's 32 rows as row fragments in registers, straight from memory: rows
-// from `end` on and elements past the head are zero.
+// A wave's 32 rows as row fragments in registers, straight from memory.
+// Rows from `end` (> 0) on repeat the last one (nothing of theirs is
+// stored), elements past the head are zero.  No branch: all loads are in
+// flight together.
 template <typename T, int KS>
 __device__ __forceinline__ void rows_to_regs(uint4 (&f)[KS], const T* base, long ld,
                                              int row0, int end, int D, int lane) {
-  const int r = row0 + (lane & 31);
-  const T* p = base + (long)r * ld;
+  const T* p = base + (long)min(row0 + (lane & 31), end - 1) * ld;
 #pragma unroll
   for (int ks = 0; ks < KS; ++ks) {
     const int e = (32 * ks + 16 * (lane >> 5)) / (int)sizeof(T);
-    f[ks] = r < end && e < D ? *reinterpret_cast<const uint4*>(p + e) : make_uint4(0, 0, 0, 0);
+    f[ks] = *reinterpret_cast<const uint4*>(p + (e < D ? e : 0));
+  }
+#pragma unroll
+  for (int ks = 0; ks < KS; ++ks) {
+    const int e = (32 * ks + 16 * (lane >> 5)) / (int)sizeof(T);
+    if (e >= D) f[ks] = make_uint4(0, 0, 0, 0);
   }
 }
 
@@ -210,6 +230,36 @@ __device__ __forceinline__ float other_half(float x) {
   const auto s = __builtin_amdgcn_permlane32_swap(u, u, false, false);
   return __uint_as_float((threadIdx.x & 32) ? s[0] : s[1]);
 }
+
+// Waits for every outstanding load in a form that the compiler counts: it
+// then knows that registers loaded before a loop have arrived.  Left to wait
+// at their first use, inside the loop, it would wait for the tile loads
+// issued just before (it cannot see them) in every turn.
+__device__ __forceinline__ void wait_loads() {
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+  asm volatile("" ::: "memory");
+}
+
+// N fragments read from LDS DEPTH ahead of the products that use them.  Left
+// to the compiler's order, a read sits right before its product and each
+// product waits for a whole LDS latency; here reads and products keep the
+// order written (other arithmetic may move).
+template <int N, int DEPTH> struct Pipe {
+  uint4 f[DEPTH];
+  template <class Ld> __device__ __forceinline__ void start(Ld ld) {
+#pragma unroll
+    for (int i = 0; i < DEPTH; ++i) f[i] = ld(i);
+    __builtin_amdgcn_sched_barrier(0x6);
+  }
+  template <class Ld, class Use> __device__ __forceinline__ void run(Ld ld, Use use) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      use(i, f[i % DEPTH]);
+      if (i + DEPTH < N) f[i % DEPTH] = ld(i + DEPTH);
+      __builtin_amdgcn_sched_barrier(0x6);
+    }
+  }
+};
 
 // ---- scores ----------------------------------------------------------------------
 // MODE 0: scale only; 1: capped; 2: distance bias, capped or not.
@@ -281,14 +331,21 @@ __device__ __forceinline__ Span span_of(int lo, int hi) {
   }
   return s;
 }
-// union of the intervals of rows [r0, r0 + n) of an array pair of `rows`
-__device__ __forceinline__ void span_rows(const int* los, const int* his, int r0, int n, int rows,
-                                          int lane, int& lo, int& hi) {
+// union of the intervals of rows r0 .. r0 + N - 1 (those below `rows` > 0)
+template <int N>
+__device__ __forceinline__ void span_rows(const int* los, const int* his, int r0, int rows, int lane,
+                                          int& lo, int& hi) {
+  int l[N / 64], h[N / 64];
+#pragma unroll
+  for (int b = 0; b < N / 64; ++b) {
+    const int r = min(r0 + 64 * b + lane, rows - 1);
+    l[b] = los[r];
+    h[b] = his[r];
+  }
   lo = hi = 0;
-  for (int b = 0; b < n; b += 64) {
-    const int r = r0 + b + lane;
-    const bool in = b + lane < n && r < rows;
-    const Span s = span_of(in ? los[r] : 0, in ? his[r] : 0);
+#pragma unroll
+  for (int b = 0; b < N / 64; ++b) {  // a row past the end repeats the last one
+    const Span s = span_of(l[b], h[b]);
     if (s.lo < s.hi) {
       if (lo >= hi) lo = s.lo;
       hi = s.hi;
@@ -316,8 +373,9 @@ __device__ __forceinline__ void work_of(int id, int heads, int& head, int& tile)
 // Where the tiles are too few to fill the card, a tile's loop is cut into
 // parts whose float32 sums go to memory and are joined by a second kernel.
 __device__ __forceinline__ void part_of(int n, int parts, int part, int& begin, int& end) {
-  begin = (int)((long)n * part / parts);
-  end = (int)((long)n * (part + 1) / parts);
+  const int each = parts == 1 ? n : (n + parts - 1) / parts;
+  begin = min(part * each, n);
+  end = min(begin + each, n);
 }
 
 }  // namespace poetx
