@@ -2,6 +2,8 @@
 // Declarations and argument documentation: include/poetx.h.
 #include <math.h>
 
+#include <algorithm>
+
 #include "../../include/poetx.h"
 #include "api_util.h"
 #include "attn.h"
@@ -70,20 +72,41 @@ int32_t check_attn(const char* fn, const poetx_attn_shape* sh, bool back) {
   return POETX_OK;
 }
 
-// five int32 arrays, each rounded up to 256 bytes
-size_t plan_bytes_of(const poetx_attn_shape* sh) {
-  return 3 * align_up((size_t)sh->Tq * 4) + 2 * align_up((size_t)sh->Tk * 4) + 256;
+// From this many tiles on a side, tiles are sorted by cost: fewer run side by
+// side in any order, and the sort is a launch of its own.
+constexpr int SORT_TILES = 16;
+
+bool sorts(const poetx_attn_shape* sh) { return attn_tiles(std::max(sh->Tq, sh->Tk)) >= SORT_TILES; }
+
+// Five int32 arrays and the tile tables, each rounded up to 256 bytes.
+struct PlanSizes { size_t q, k, tq, tk, total; };
+PlanSizes plan_sizes(const poetx_attn_shape* sh) {
+  PlanSizes z;
+  z.q = align_up((size_t)sh->Tq * 4);
+  z.k = align_up((size_t)sh->Tk * 4);
+  z.tq = align_up((size_t)attn_tiles(sh->Tq) * 16);
+  z.tk = align_up((size_t)attn_tiles(sh->Tk) * 16);
+  z.total = 3 * z.q + 2 * z.k + (sorts(sh) ? 2 : 1) * (z.tq + z.tk) + 256;
+  return z;
 }
+size_t plan_bytes_of(const poetx_attn_shape* sh) { return plan_sizes(sh).total; }
 
 AttnPlan plan_at(const poetx_attn_shape* sh, const void* plan) {
   char* p = (char*)const_cast<void*>(plan);
-  const size_t q = align_up((size_t)sh->Tq * 4), k = align_up((size_t)sh->Tk * 4);
+  const PlanSizes z = plan_sizes(sh);
   AttnPlan pl;
   pl.row_lo = (int*)p;
-  pl.row_hi = (int*)(p + q);
-  pl.row_pos = (int*)(p + 2 * q);
-  pl.key_lo = (int*)(p + 3 * q);
-  pl.key_hi = (int*)(p + 3 * q + k);
+  pl.row_hi = (int*)(p + z.q);
+  pl.row_pos = (int*)(p + 2 * z.q);
+  pl.key_lo = (int*)(p + 3 * z.q);
+  pl.key_hi = (int*)(p + 3 * z.q + z.k);
+  char* t = p + 3 * z.q + 2 * z.k;
+  pl.qraw = pl.qtab = (int4*)t;
+  pl.kraw = pl.ktab = (int4*)(t + z.tq);
+  if (sorts(sh)) {
+    pl.qtab = (int4*)(t + z.tq + z.tk);
+    pl.ktab = (int4*)(t + 2 * z.tq + z.tk);
+  }
   return pl;
 }
 

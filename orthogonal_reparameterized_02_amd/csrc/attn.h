@@ -28,10 +28,10 @@ hipError_t launch_dropout(long n, const TS* x, const TS* res, TS* out, uint32_t 
 
 // ---- attention (attn_*.hip) -------------------------------------------------
 // Parts that a loop of about `steps` tiles is cut into where `groups`
-// workgroups run it: none from one workgroup a CU on (256), else up to two
+// workgroups run it: none above one workgroup a CU (256), else up to two
 // workgroups a CU, four steps a part at least, 16 parts at most.
 inline int parts_for(long groups, int steps) {
-  if (groups >= 256 || groups < 1) return 1;
+  if (groups > 256 || groups < 1) return 1;
   const int want = (int)(512 / groups), most = steps / 4 < 16 ? steps / 4 : 16;
   return want < most ? want : most > 1 ? most : 1;
 }
@@ -43,7 +43,13 @@ inline int parts_for(long groups, int steps) {
 struct AttnPlan {
   int *row_lo, *row_hi, *row_pos;  // [Tq]
   int *key_lo, *key_hi;            // [Tk]
+  // tiles of ATTN_BM query (key) rows in the order they are worked on: {tile,
+  // first, end of the keys (queries) that its rows see, 0}
+  int4 *qtab, *ktab;
+  int4 *qraw, *kraw;               // the same before sorting
 };
+constexpr int ATTN_BM = 128;
+inline int attn_tiles(int rows) { return (rows + ATTN_BM - 1) / ATTN_BM; }
 
 struct AttnArgs {
   int Tq, Tk, Hq, Hkv, group, D;

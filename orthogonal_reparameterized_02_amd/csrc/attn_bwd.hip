@@ -18,7 +18,8 @@ namespace poetx {
 namespace {
 
 constexpr int NW = 4;         // waves
-constexpr int BM = 32 * NW;   // rows a workgroup owns
+constexpr int BM = ATTN_BM;   // rows a workgroup owns
+static_assert(BM == 32 * NW, "a wave owns 32 of them");
 
 template <typename T, int DP> struct BwdCfg {
   static constexpr int BN = sizeof(T) == 2 ? 64 : 32;  // rows of a streamed tile
@@ -61,7 +62,7 @@ __device__ __forceinline__ float dot8(const float*, uint4 a, uint4 b) {
 // dq, and for the second pass delta = dout . o and lse2 = lse log2e of every
 // query (lse2 = +inf where lse = -inf: such a query's p is 0)
 template <typename T, int DP, int MODE>
-__global__ __launch_bounds__(64 * NW, (BwdCfg<T, DP>::OCC)) void k_attn_dq(AttnArgs a, int tiles, int parts) {
+__global__ __launch_bounds__(64 * NW, (BwdCfg<T, DP>::OCC)) void k_attn_dq(AttnArgs a, int parts) {
   using L = Tile<T, DP>;
   using C = BwdCfg<T, DP>;
   constexpr int BN = C::BN, NS = BN / 32;
@@ -69,13 +70,27 @@ __global__ __launch_bounds__(64 * NW, (BwdCfg<T, DP>::OCC)) void k_attn_dq(AttnA
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   int h, tile;
   work_of(blockIdx.x, a.Hq, h, tile);
-  const int q0 = (tiles - 1 - tile) * BM;  // long rows (causal) first
+  int q0, klo, khi;
+  tile_entry(a.pl.qtab, tile, BM, q0, klo, khi);
   const int hk = h / a.group, r0 = q0 + 32 * wave, part = blockIdx.y;
   const T* qp = (const T*)a.q + (long)h * a.D;
   const T* kp = (const T*)a.k + (long)hk * a.D;
   const T* vp = (const T*)a.v + (long)hk * a.D;
   const T* dop = (const T*)a.dout + (long)h * a.D;
   const T* op = (const T*)a.o + (long)h * a.D;
+
+  int jb, je;  // this part's keys; the first tiles are on their way before all else
+  part_of((khi - klo + BN - 1) / BN, parts, part, jb, je);
+  jb = klo + jb * BN;
+  je = min(klo + je * BN, khi);
+  Loader<T, DP, BN, NW> lk, lv;
+  lk.init(a.ldk, a.D, wave, lane);
+  lv.init(a.ldv, a.D, wave, lane);
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
+  if (jb < je) {
+    lk.load(kp, a.ldk, jb, je, lds0);
+    lv.load(vp, a.ldv, jb, je, lds0 + 2 * C::TILE);
+  }
 
   const int t = r0 + (lane & 31);
   const bool in = t < a.Tq;
@@ -84,17 +99,6 @@ __global__ __launch_bounds__(64 * NW, (BwdCfg<T, DP>::OCC)) void k_attn_dq(AttnA
   const int lo = in ? rlo : 0, hi = in ? rhi : 0;
   const float pos = (float)rpos;
   const Span sp = span_of(lo, hi);
-  int klo, khi;
-  span_rows<BM>(a.pl.row_lo, a.pl.row_hi, q0, a.Tq, lane, klo, khi);
-  int jb, je;  // this part's keys
-  part_of((khi - klo + BN - 1) / BN, parts, part, jb, je);
-  jb = klo + jb * BN;
-  je = min(klo + je * BN, khi);
-
-  Loader<T, DP, BN, NW> lk, lv;
-  lk.init(a.ldk, a.D, wave, lane);
-  lv.init(a.ldv, a.D, wave, lane);
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
 
   uint4 qf[L::KS], dof[L::KS];
   rows_to_regs<T>(dof, dop, a.lddo, r0, a.Tq, a.D, lane);
@@ -121,10 +125,6 @@ __global__ __launch_bounds__(64 * NW, (BwdCfg<T, DP>::OCC)) void k_attn_dq(AttnA
   for (int i = 0; i < L::NT; ++i) dq[i] = (f32x16_t){};
 
   wait_loads();
-  if (jb < je) {
-    lk.load(kp, a.ldk, jb, je, lds0);
-    lv.load(vp, a.ldv, jb, je, lds0 + 2 * C::TILE);
-  }
   int buf = 0;
   for (int j0 = jb; j0 < je; j0 += BN, buf ^= 1) {
     // this tile has landed, and every wave has left the other buffer
@@ -220,19 +220,11 @@ __global__ __launch_bounds__((64 * NW * BwdCfg<T, DP>::NQ), (BwdCfg<T, DP>::OCC)
   const int wk = wave % NW, wq = wave / NW;  // 32 keys; 32 queries of a tile
   int hk, tile;
   work_of(blockIdx.x, a.Hkv, hk, tile);
-  const int k0 = tile * BM;  // keys seen by many (causal) first
+  int k0, qlo, qhi;
+  tile_entry(a.pl.ktab, tile, BM, k0, qlo, qhi);
   const int r0 = k0 + 32 * wk, part = blockIdx.y;
   const T* kp = (const T*)a.k + (long)hk * a.D;
   const T* vp = (const T*)a.v + (long)hk * a.D;
-
-  const int t = r0 + (lane & 31);
-  const bool in = t < a.Tk;
-  const int tc = min(t, a.Tk - 1);
-  const int rlo = a.pl.key_lo[tc], rhi = a.pl.key_hi[tc];
-  const int lo = in ? rlo : 0, hi = in ? rhi : 0;
-  const Span sp = span_of(lo, hi);
-  int qlo, qhi;
-  span_rows<BM>(a.pl.key_lo, a.pl.key_hi, k0, a.Tk, lane, qlo, qhi);
 
   Loader<T, DP, BN, NWA> lq, lo_;
   lq.init(a.ldq, a.D, wave, lane);
@@ -258,6 +250,20 @@ __global__ __launch_bounds__((64 * NW * BwdCfg<T, DP>::NQ), (BwdCfg<T, DP>::OCC)
     }
   };
 
+  int h = hk * a.group, i0 = qlo;  // of the current tile
+  if (nb < ne) {
+    h += nb / per;
+    i0 += nb % per * BN;
+    load(h, i0, 0);
+  }
+
+  const int t = r0 + (lane & 31);
+  const bool in = t < a.Tk;
+  const int tc = min(t, a.Tk - 1);
+  const int rlo = a.pl.key_lo[tc], rhi = a.pl.key_hi[tc];
+  const int lo = in ? rlo : 0, hi = in ? rhi : 0;
+  const Span sp = span_of(lo, hi);
+
   uint4 kf[L::KS], vf[C::VLDS ? 1 : L::KS];
   rows_to_regs<T>(kf, kp, a.ldk, r0, a.Tk, a.D, lane);
   // lane offsets into this wave's 32 queries of a tile, and its values
@@ -276,12 +282,6 @@ __global__ __launch_bounds__((64 * NW * BwdCfg<T, DP>::NQ), (BwdCfg<T, DP>::OCC)
 
   if (wq) __builtin_amdgcn_s_setprio(1);
   wait_loads();  // also where there is no work: no load may outlive its workgroup
-  int h = hk * a.group, i0 = qlo;  // of the current tile
-  if (nb < ne) {
-    h += nb / per;
-    i0 += nb % per * BN;
-    load(h, i0, 0);
-  }
   int buf = 0;
   for (int n = nb; n < ne; ++n, buf ^= 1) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -464,10 +464,10 @@ __global__ __launch_bounds__(256) void k_attn_sum_parts(JoinArgs j, int parts, l
 }
 
 int dq_parts(const AttnArgs& a) {
-  return parts_for((long)((a.Tq + BM - 1) / BM) * a.Hq, a.Tk / std::max(a.ndoc, 1) / 64);
+  return parts_for((long)(attn_tiles(a.Tq)) * a.Hq, a.Tk / std::max(a.ndoc, 1) / 64);
 }
 int dkv_parts(const AttnArgs& a) {
-  return parts_for((long)((a.Tk + BM - 1) / BM) * a.Hkv, a.Tq / std::max(a.ndoc, 1) / 64 * a.group);
+  return parts_for((long)(attn_tiles(a.Tk)) * a.Hkv, a.Tq / std::max(a.ndoc, 1) / 64 * a.group);
 }
 
 template <typename T, int DP, int MODE> hipError_t bwd(const AttnArgs& a, hipStream_t s) {
@@ -475,12 +475,12 @@ template <typename T, int DP, int MODE> hipError_t bwd(const AttnArgs& a, hipStr
   hipError_t e = lds_opt_in((const void*)k_attn_dq<T, DP, MODE>, C::LDS_DQ);
   if (e == hipSuccess) e = lds_opt_in((const void*)k_attn_dkv<T, DP, MODE>, C::LDS_DKV);
   if (e != hipSuccess) return e;
-  const int tq = (a.Tq + BM - 1) / BM, tk = (a.Tk + BM - 1) / BM;
+  const int tq = attn_tiles(a.Tq), tk = attn_tiles(a.Tk);
   const int pq = dq_parts(a), pk = dkv_parts(a);
   const int wq = a.Hq * a.D, wk = a.Hkv * a.D;
   const auto blocks = [](long n) { return (unsigned)((n / 8 + 255) / 256); };
   if (tq) {
-    k_attn_dq<T, DP, MODE><<<dim3((unsigned)tq * a.Hq, pq), 64 * NW, C::LDS_DQ, s>>>(a, tq, pq);
+    k_attn_dq<T, DP, MODE><<<dim3((unsigned)tq * a.Hq, pq), 64 * NW, C::LDS_DQ, s>>>(a, pq);
     e = hipGetLastError();
     if (e == hipSuccess && pq > 1) {
       const JoinArgs j = {{a.part}, {a.dq}, {a.lddq}, {a.scale}};

@@ -18,7 +18,8 @@ namespace poetx {
 namespace {
 
 constexpr int NW = 4;         // waves
-constexpr int BM = 32 * NW;   // query rows a workgroup
+constexpr int BM = ATTN_BM;   // query rows a workgroup
+static_assert(BM == 32 * NW, "a wave owns 32 rows");
 // The running maximum moves only when a score passes it by more than this
 // (log2): until then probabilities may reach 2^8, which float32 sums and bf16
 // operands hold with the same relative error, and the accumulators need not
@@ -32,7 +33,7 @@ template <typename T, int DP> struct FwdCfg {
 };
 
 template <typename T, int DP, int MODE>
-__global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void k_attn_fwd(AttnArgs a, int tiles, int parts) {
+__global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void k_attn_fwd(AttnArgs a, int parts) {
   using L = Tile<T, DP>;
   using C = FwdCfg<T, DP>;
   constexpr int BN = C::BN, NS = BN / 32;
@@ -40,13 +41,27 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void 
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   int h, tile;
   work_of(blockIdx.x, a.Hq, h, tile);
-  const int q0 = (tiles - 1 - tile) * BM;  // long rows (causal) first
+  int q0, klo, khi;
+  tile_entry(a.pl.qtab, tile, BM, q0, klo, khi);
   const int hk = h / a.group, part = blockIdx.y;
   const T* qp = (const T*)a.q + (long)h * a.D;
   const T* kp = (const T*)a.k + (long)hk * a.D;
   const T* vp = (const T*)a.v + (long)hk * a.D;
 
-  // this lane's query, the wave's and the workgroup's keys
+  int jb, je;  // this part's keys; the first tiles are on their way before all else
+  part_of((khi - klo + BN - 1) / BN, parts, part, jb, je);
+  jb = klo + jb * BN;
+  je = min(klo + je * BN, khi);
+  Loader<T, DP, BN, NW> lk, lv;
+  lk.init(a.ldk, a.D, wave, lane);
+  lv.init(a.ldv, a.D, wave, lane);
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
+  if (jb < je) {
+    lk.load(kp, a.ldk, jb, je, lds0);
+    lv.load(vp, a.ldv, jb, je, lds0 + 2 * C::TILE);
+  }
+
+  // this lane's query and the wave's keys
   const int t = q0 + 32 * wave + (lane & 31);
   const bool in = t < a.Tq;
   const int tc = min(t, a.Tq - 1);
@@ -54,19 +69,9 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void 
   const int lo = in ? rlo : 0, hi = in ? rhi : 0;
   const float pos = (float)rpos;
   const Span sp = span_of(lo, hi);
-  int klo, khi;
-  span_rows<BM>(a.pl.row_lo, a.pl.row_hi, q0, a.Tq, lane, klo, khi);
-  int jb, je;  // this part's keys
-  part_of((khi - klo + BN - 1) / BN, parts, part, jb, je);
-  jb = klo + jb * BN;
-  je = min(klo + je * BN, khi);
 
   uint4 qf[L::KS];
   rows_to_regs<T>(qf, qp, a.ldq, q0 + 32 * wave, a.Tq, a.D, lane);
-  Loader<T, DP, BN, NW> lk, lv;
-  lk.init(a.ldk, a.D, wave, lane);
-  lv.init(a.ldv, a.D, wave, lane);
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
 
   const uint32_t rlane = L::row_lane(lane), clane = L::col_lane(lane);
   const ScoreArgs sa = score_args(a, h);
@@ -76,10 +81,6 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void 
   float m = -INFINITY, l = 0.0f;  // m: the reference of the exponentials, log2
 
   wait_loads();
-  if (jb < je) {
-    lk.load(kp, a.ldk, jb, je, lds0);
-    lv.load(vp, a.ldv, jb, je, lds0 + 2 * C::TILE);
-  }
   int buf = 0;
   for (int j0 = jb; j0 < je; j0 += BN, buf ^= 1) {
     // this tile has landed, and every wave has left the other buffer
@@ -231,15 +232,15 @@ __global__ __launch_bounds__(64 * NW) void k_attn_fwd_join(AttnArgs a, int parts
 
 // a document's keys stand for the length of the loop
 int fwd_parts(const AttnArgs& a) {
-  return parts_for((long)((a.Tq + BM - 1) / BM) * a.Hq, a.Tk / std::max(a.ndoc, 1) / 64);
+  return parts_for((long)(attn_tiles(a.Tq)) * a.Hq, a.Tk / std::max(a.ndoc, 1) / 64);
 }
 
 template <typename T, int DP, int MODE> hipError_t fwd(const AttnArgs& a, hipStream_t s) {
   constexpr int lds = FwdCfg<T, DP>::LDS;
   const hipError_t e = lds_opt_in((const void*)k_attn_fwd<T, DP, MODE>, lds);
   if (e != hipSuccess) return e;
-  const int tiles = (a.Tq + BM - 1) / BM, parts = fwd_parts(a);
-  k_attn_fwd<T, DP, MODE><<<dim3((unsigned)tiles * a.Hq, parts), 64 * NW, lds, s>>>(a, tiles, parts);
+  const int tiles = attn_tiles(a.Tq), parts = fwd_parts(a);
+  k_attn_fwd<T, DP, MODE><<<dim3((unsigned)tiles * a.Hq, parts), 64 * NW, lds, s>>>(a, parts);
   const hipError_t e2 = hipGetLastError();
   if (e2 != hipSuccess || parts == 1) return e2;
   k_attn_fwd_join<T><<<dim3((a.Tq + NW - 1) / NW, a.Hq), 64 * NW, 0, s>>>(a, parts);

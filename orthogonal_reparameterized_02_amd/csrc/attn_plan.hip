@@ -3,7 +3,7 @@
 // key one interval of queries.
 #include <algorithm>
 
-#include "attn.h"
+#include "attn_tile.h"
 
 namespace poetx {
 
@@ -23,15 +23,16 @@ __device__ __forceinline__ int doc_of(const int* cu, int ndoc, int t, int T) {
   return lo >= 1 && lo <= ndoc ? lo - 1 : -1;
 }
 
-__global__ __launch_bounds__(NTH) void k_attn_plan(int Tq, int Tk, int ndoc, int causal,
+// Blocks of query rows, then blocks of key rows; two waves are one tile.
+__global__ __launch_bounds__(NTH) void k_attn_plan(int Tq, int Tk, int ndoc, int causal, int qblocks,
                                                    const int* __restrict__ cu_q,
                                                    const int* __restrict__ cu_k,
                                                    const int* __restrict__ prefix, AttnPlan pl) {
-  const long id = (long)blockIdx.x * NTH + threadIdx.x;
-  if (id >= (long)Tq + Tk) return;
-  const bool row = id < Tq;
-  const int t = (int)(row ? id : id - Tq);
-  const int d = doc_of(row ? cu_q : cu_k, ndoc, t, row ? Tq : Tk);
+  __shared__ int2 span[NTH / 64];
+  const bool row = (int)blockIdx.x < qblocks;
+  const int b = row ? blockIdx.x : blockIdx.x - qblocks, T = row ? Tq : Tk;
+  const int t = b * NTH + threadIdx.x;
+  const int d = t < T ? doc_of(row ? cu_q : cu_k, ndoc, t, T) : -1;
   int lo = 0, hi = 0, pos = 0;
   if (d >= 0) {
     const int q0 = min(max(cu_q[d], 0), Tq), q1 = min(max(cu_q[d + 1], q0), Tq);
@@ -41,30 +42,66 @@ __global__ __launch_bounds__(NTH) void k_attn_plan(int Tq, int Tk, int ndoc, int
       pos = k1 - (q1 - t);
       lo = k0;
       hi = causal ? max(min(pos + 1, k1), k0 + pre) : k1;
-      if (hi <= lo) lo = hi = 0;
     } else {
       lo = causal && t >= k0 + pre ? max(q0, q1 - (k1 - t)) : q0;
       hi = q1;
-      if (hi <= lo) lo = hi = 0;
+    }
+    if (hi <= lo) lo = hi = 0;
+  }
+  if (t < T) {
+    if (row) {
+      pl.row_lo[t] = lo;
+      pl.row_hi[t] = hi;
+      pl.row_pos[t] = pos;
+    } else {
+      pl.key_lo[t] = lo;
+      pl.key_hi[t] = hi;
     }
   }
-  if (row) {
-    pl.row_lo[t] = lo;
-    pl.row_hi[t] = hi;
-    pl.row_pos[t] = pos;
-  } else {
-    pl.key_lo[t] = lo;
-    pl.key_hi[t] = hi;
+  const Span s = span_of(lo, hi);
+  if (threadIdx.x % 64 == 0) span[threadIdx.x / 64] = make_int2(s.lo, s.hi);
+  __syncthreads();
+  constexpr int PER = NTH / ATTN_BM;  // tiles a block
+  const int tile = b * PER + threadIdx.x, tiles = (T + ATTN_BM - 1) / ATTN_BM;
+  if ((int)threadIdx.x < PER && tile < tiles) {
+    const int2 x = span[2 * threadIdx.x], y = span[2 * threadIdx.x + 1];
+    const int4 e = make_int4(tile, x.x < x.y ? x.x : y.x, y.x < y.y ? y.y : x.y, 0);
+    // causal rows see more the later they come, causal keys are seen by fewer
+    (row ? pl.qraw : pl.kraw)[row ? tiles - 1 - tile : tile] = e;
   }
+}
+
+// Tiles by falling cost: tile i goes where its rank among all puts it.
+__global__ __launch_bounds__(NTH) void k_attn_order(int tq, int tk, AttnPlan pl) {
+  __shared__ int cost[NTH];
+  const int n = blockIdx.y ? tk : tq;
+  const int4* raw = blockIdx.y ? pl.kraw : pl.qraw;
+  const int i = blockIdx.x * NTH + threadIdx.x;
+  if ((int)blockIdx.x * NTH >= n) return;
+  const int4 e = raw[min(i, n - 1)];
+  const int mine = e.z - e.y;
+  int rank = 0;
+  for (int b = 0; b < n; b += NTH) {
+    const int4 o = raw[min(b + (int)threadIdx.x, n - 1)];
+    __syncthreads();
+    cost[threadIdx.x] = o.z - o.y;
+    __syncthreads();
+    const int m = min(NTH, n - b);
+    for (int j = 0; j < m; ++j) rank += cost[j] > mine || (cost[j] == mine && b + j < i) ? 1 : 0;
+  }
+  if (i < n) (blockIdx.y ? pl.ktab : pl.qtab)[rank] = e;
 }
 
 }  // namespace
 
 hipError_t launch_attn_plan(int Tq, int Tk, int ndoc, int causal, const int* cu_q, const int* cu_k,
                             const int* prefix, const AttnPlan& pl, hipStream_t s) {
-  const long n = (long)Tq + Tk;
-  k_attn_plan<<<dim3((unsigned)((n + NTH - 1) / NTH)), NTH, 0, s>>>(Tq, Tk, ndoc, causal, cu_q,
-                                                                    cu_k, prefix, pl);
+  const int qb = (Tq + NTH - 1) / NTH, kb = (Tk + NTH - 1) / NTH;
+  k_attn_plan<<<dim3(qb + kb), NTH, 0, s>>>(Tq, Tk, ndoc, causal, qb, cu_q, cu_k, prefix, pl);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || pl.qtab == pl.qraw) return e;
+  const int tq = attn_tiles(Tq), tk = attn_tiles(Tk);
+  k_attn_order<<<dim3((std::max(tq, tk) + NTH - 1) / NTH, 2), NTH, 0, s>>>(tq, tk, pl);
   return hipGetLastError();
 }
 

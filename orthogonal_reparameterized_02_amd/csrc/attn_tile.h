@@ -331,32 +331,9 @@ __device__ __forceinline__ Span span_of(int lo, int hi) {
   }
   return s;
 }
-// union of the intervals of rows r0 .. r0 + N - 1 (those below `rows` > 0)
-template <int N>
-__device__ __forceinline__ void span_rows(const int* los, const int* his, int r0, int rows, int lane,
-                                          int& lo, int& hi) {
-  int l[N / 64], h[N / 64];
-#pragma unroll
-  for (int b = 0; b < N / 64; ++b) {
-    const int r = min(r0 + 64 * b + lane, rows - 1);
-    l[b] = los[r];
-    h[b] = his[r];
-  }
-  lo = hi = 0;
-#pragma unroll
-  for (int b = 0; b < N / 64; ++b) {  // a row past the end repeats the last one
-    const Span s = span_of(l[b], h[b]);
-    if (s.lo < s.hi) {
-      if (lo >= hi) lo = s.lo;
-      hi = s.hi;
-    }
-  }
-}
-
-// Work order: tile by tile, all heads of one before the next, so that tiles
-// of like cost run at the same time and the long ones (the caller's first)
-// start first; head by head, each head's short tiles end beside another's
-// long ones and the last round waits (attn_docs: dk and dv 364 -> 274 us).
+// Work order: tile by tile (long ones first, AttnPlan), all heads of one
+// before the next.  Head by head, a head's short tiles end beside another's
+// long ones and the last round waits for the latter.
 // Consecutive workgroups are dealt round-robin over the 8 XCDs; a head stays
 // on one XCD, beside the heads that share its keys, where 8 divides the heads.
 __device__ __forceinline__ void work_of(int id, int heads, int& head, int& tile) {
@@ -368,6 +345,14 @@ __device__ __forceinline__ void work_of(int id, int heads, int& head, int& tile)
     head = id % heads;
     tile = id / heads;
   }
+}
+
+// entry of a tile table (AttnPlan), in scalar registers
+__device__ __forceinline__ void tile_entry(const int4* tab, int tile, int bm, int& row0, int& lo, int& hi) {
+  const int4 e = tab[tile];
+  row0 = __builtin_amdgcn_readfirstlane(e.x) * bm;
+  lo = __builtin_amdgcn_readfirstlane(e.y);
+  hi = __builtin_amdgcn_readfirstlane(e.z);
 }
 
 // Where the tiles are too few to fill the card, a tile's loop is cut into
