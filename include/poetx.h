@@ -467,7 +467,8 @@ typedef struct {
 } poetx_attn_shape;
 
 /* Bytes of a plan (0 on bad arguments), and of the workspace of
- * poetx_attn_fwd (which = 0) or poetx_attn_bwd (1). */
+ * poetx_attn_fwd (which = 0) or poetx_attn_bwd (1; also enough for the
+ * forward pass of the same shape). */
 size_t poetx_attn_plan_bytes(const poetx_attn_shape* sh);
 size_t poetx_attn_workspace_bytes(const poetx_attn_shape* sh, int32_t which);
 

@@ -126,11 +126,16 @@ AttnArgs args_of(const poetx_attn_shape* sh, const void* q, const void* k, const
   return a;
 }
 
-// backward: delta and lse2, [Hq][Tq] float32 each; then partial sums
+// backward: delta and lse2, [Hq][Tq] float32 each; then partial sums (its
+// workspace is large enough for the forward pass too)
 size_t row_bytes(const poetx_attn_shape* sh) { return align_up((size_t)sh->Hq * sh->Tq * 4); }
 size_t attn_ws(const poetx_attn_shape* sh, int which) {
   const AttnArgs a = args_of(sh, nullptr, nullptr, nullptr, nullptr, nullptr);
-  return which == 0 ? align_up(attn_fwd_part_bytes(a)) : 2 * row_bytes(sh) + align_up(attn_bwd_part_bytes(a));
+  const bool h = sh->act == POETX_BF16;
+  const size_t fwd = align_up(h ? attn_fwd_part_bytes<bf16>(a) : attn_fwd_part_bytes<float>(a));
+  if (which == 0) return fwd;
+  const size_t bwd = 2 * row_bytes(sh) + align_up(h ? attn_bwd_part_bytes<bf16>(a) : attn_bwd_part_bytes<float>(a));
+  return std::max(fwd, bwd);
 }
 
 int32_t check_decode(const char* fn, const poetx_decode_shape* sh) {

@@ -27,13 +27,16 @@ hipError_t launch_dropout(long n, const TS* x, const TS* res, TS* out, uint32_t 
                           uint64_t offset, const uint64_t* offset_dev, hipStream_t s);
 
 // ---- attention (attn_*.hip) -------------------------------------------------
-// Parts that a loop of about `steps` tiles is cut into where `groups`
-// workgroups run it: none above one workgroup a CU (256), else up to two
-// workgroups a CU, four steps a part at least, 16 parts at most.
-inline int parts_for(long groups, int steps) {
-  if (groups > 256 || groups < 1) return 1;
-  const int want = (int)(512 / groups), most = steps / 4 < 16 ? steps / 4 : 16;
-  return want < most ? want : most > 1 ? most : 1;
+// Parts that a loop over about `rows` rows is cut into where `groups`
+// workgroups run it: enough for two workgroups a CU with bf16, eight with
+// float32 (whose products take eight times as long, so that unequal loops
+// wait longer for the longest and the traffic of partial sums counts less);
+// at least 256 bf16 or 128 float32 rows a part, 16 parts at most.
+template <typename T> int parts_for(long groups, long rows) {
+  const long want = groups < 1 ? 1 : (sizeof(T) == 2 ? 512 : 2048) / groups;
+  const long most = rows / (sizeof(T) == 2 ? 256 : 128);
+  const long n = want < most ? want : most;
+  return n < 1 ? 1 : n > 16 ? 16 : (int)n;
 }
 
 // The mask as intervals: query row t sees keys [row_lo, row_hi), stands at
@@ -74,8 +77,8 @@ hipError_t lds_opt_in(const void* kern, int bytes);
 hipError_t launch_attn_plan(int Tq, int Tk, int ndoc, int causal, const int* cu_q, const int* cu_k,
                             const int* prefix, const AttnPlan& pl, hipStream_t s);
 // bytes of a.part for the forward and the backward pass
-size_t attn_fwd_part_bytes(const AttnArgs& a);
-size_t attn_bwd_part_bytes(const AttnArgs& a);
+template <typename TS> size_t attn_fwd_part_bytes(const AttnArgs& a);
+template <typename TS> size_t attn_bwd_part_bytes(const AttnArgs& a);
 template <typename TS> hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t s);
 template <typename TS> hipError_t launch_attn_bwd(const AttnArgs& a, hipStream_t s);
 

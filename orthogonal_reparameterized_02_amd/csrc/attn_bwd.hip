@@ -217,7 +217,10 @@ __global__ __launch_bounds__((64 * NW * BwdCfg<T, DP>::NQ), (BwdCfg<T, DP>::OCC)
   constexpr int BN = C::BQ, NWA = NW * C::NQ;
   extern __shared__ __align__(16) char smem[];
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  const int wk = wave % NW, wq = wave / NW;  // 32 keys; 32 queries of a tile
+  // 32 keys; 32 queries of a tile.  Wave w runs on SIMD w % 4: near the
+  // diagonal, where the later keys have nothing to do, every SIMD then still
+  // has a wave of the earlier ones.
+  const int wk = wave / C::NQ, wq = wave % C::NQ;
   int hk, tile;
   work_of(blockIdx.x, a.Hkv, hk, tile);
   int k0, qlo, qhi;
@@ -463,11 +466,11 @@ __global__ __launch_bounds__(256) void k_attn_sum_parts(JoinArgs j, int parts, l
   for (int i = 0; i < 8; ++i) St<T>::st(o + i, v[i] * j.mul[blockIdx.y]);
 }
 
-int dq_parts(const AttnArgs& a) {
-  return parts_for((long)(attn_tiles(a.Tq)) * a.Hq, a.Tk / std::max(a.ndoc, 1) / 64);
+template <typename T> int dq_parts(const AttnArgs& a) {
+  return parts_for<T>((long)attn_tiles(a.Tq) * a.Hq, a.Tk / std::max(a.ndoc, 1));
 }
-int dkv_parts(const AttnArgs& a) {
-  return parts_for((long)(attn_tiles(a.Tk)) * a.Hkv, a.Tq / std::max(a.ndoc, 1) / 64 * a.group);
+template <typename T> int dkv_parts(const AttnArgs& a) {
+  return parts_for<T>((long)attn_tiles(a.Tk) * a.Hkv, (long)a.Tq / std::max(a.ndoc, 1) * a.group);
 }
 
 template <typename T, int DP, int MODE> hipError_t bwd(const AttnArgs& a, hipStream_t s) {
@@ -476,7 +479,7 @@ template <typename T, int DP, int MODE> hipError_t bwd(const AttnArgs& a, hipStr
   if (e == hipSuccess) e = lds_opt_in((const void*)k_attn_dkv<T, DP, MODE>, C::LDS_DKV);
   if (e != hipSuccess) return e;
   const int tq = attn_tiles(a.Tq), tk = attn_tiles(a.Tk);
-  const int pq = dq_parts(a), pk = dkv_parts(a);
+  const int pq = dq_parts<T>(a), pk = dkv_parts<T>(a);
   const int wq = a.Hq * a.D, wk = a.Hkv * a.D;
   const auto blocks = [](long n) { return (unsigned)((n / 8 + 255) / 256); };
   if (tq) {
@@ -510,8 +513,8 @@ template <typename T, int DP> hipError_t bwd_mode(const AttnArgs& a, hipStream_t
 }  // namespace
 
 // the two passes use the same bytes one after the other
-size_t attn_bwd_part_bytes(const AttnArgs& a) {
-  const int pq = dq_parts(a), pk = dkv_parts(a);
+template <typename T> size_t attn_bwd_part_bytes(const AttnArgs& a) {
+  const int pq = dq_parts<T>(a), pk = dkv_parts<T>(a);
   const size_t q = pq > 1 ? (size_t)pq * a.Tq * a.Hq * a.D * 4 : 0;
   const size_t k = pk > 1 ? (size_t)pk * 2 * a.Tk * a.Hkv * a.D * 4 : 0;
   return std::max(q, k);
@@ -521,6 +524,8 @@ template <typename T> hipError_t launch_attn_bwd(const AttnArgs& a, hipStream_t 
   return a.D <= 64 ? bwd_mode<T, 64>(a, s) : bwd_mode<T, 128>(a, s);
 }
 
+template size_t attn_bwd_part_bytes<bf16>(const AttnArgs&);
+template size_t attn_bwd_part_bytes<float>(const AttnArgs&);
 template hipError_t launch_attn_bwd<bf16>(const AttnArgs&, hipStream_t);
 template hipError_t launch_attn_bwd<float>(const AttnArgs&, hipStream_t);
 

@@ -231,15 +231,15 @@ __global__ __launch_bounds__(64 * NW) void k_attn_fwd_join(AttnArgs a, int parts
 }
 
 // a document's keys stand for the length of the loop
-int fwd_parts(const AttnArgs& a) {
-  return parts_for((long)(attn_tiles(a.Tq)) * a.Hq, a.Tk / std::max(a.ndoc, 1) / 64);
+template <typename T> int fwd_parts(const AttnArgs& a) {
+  return parts_for<T>((long)attn_tiles(a.Tq) * a.Hq, a.Tk / std::max(a.ndoc, 1));
 }
 
 template <typename T, int DP, int MODE> hipError_t fwd(const AttnArgs& a, hipStream_t s) {
   constexpr int lds = FwdCfg<T, DP>::LDS;
   const hipError_t e = lds_opt_in((const void*)k_attn_fwd<T, DP, MODE>, lds);
   if (e != hipSuccess) return e;
-  const int tiles = attn_tiles(a.Tq), parts = fwd_parts(a);
+  const int tiles = attn_tiles(a.Tq), parts = fwd_parts<T>(a);
   k_attn_fwd<T, DP, MODE><<<dim3((unsigned)tiles * a.Hq, parts), 64 * NW, lds, s>>>(a, parts);
   const hipError_t e2 = hipGetLastError();
   if (e2 != hipSuccess || parts == 1) return e2;
@@ -254,8 +254,8 @@ template <typename T, int DP> hipError_t fwd_mode(const AttnArgs& a, hipStream_t
 
 }  // namespace
 
-size_t attn_fwd_part_bytes(const AttnArgs& a) {
-  const int parts = fwd_parts(a);
+template <typename T> size_t attn_fwd_part_bytes(const AttnArgs& a) {
+  const int parts = fwd_parts<T>(a);
   return parts == 1 ? 0 : (size_t)parts * a.Hq * a.Tq * (a.D + 2) * 4;
 }
 
@@ -263,6 +263,8 @@ template <typename T> hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t 
   return a.D <= 64 ? fwd_mode<T, 64>(a, s) : fwd_mode<T, 128>(a, s);
 }
 
+template size_t attn_fwd_part_bytes<bf16>(const AttnArgs&);
+template size_t attn_fwd_part_bytes<float>(const AttnArgs&);
 template hipError_t launch_attn_fwd<bf16>(const AttnArgs&, hipStream_t);
 template hipError_t launch_attn_fwd<float>(const AttnArgs&, hipStream_t);
 

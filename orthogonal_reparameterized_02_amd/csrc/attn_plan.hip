@@ -10,6 +10,7 @@ namespace poetx {
 namespace {
 
 constexpr int NTH = 256;
+constexpr int STAGED = 1024;
 
 // document of row t: the last d with cu[d] <= t, if it ends after t
 // (offsets clamped to [0, T]); -1: none
@@ -25,10 +26,21 @@ __device__ __forceinline__ int doc_of(const int* cu, int ndoc, int t, int T) {
 
 // Blocks of query rows, then blocks of key rows; two waves are one tile.
 __global__ __launch_bounds__(NTH) void k_attn_plan(int Tq, int Tk, int ndoc, int causal, int qblocks,
-                                                   const int* __restrict__ cu_q,
-                                                   const int* __restrict__ cu_k,
+                                                   const int* cu_q, const int* cu_k,
                                                    const int* __restrict__ prefix, AttnPlan pl) {
   __shared__ int2 span[NTH / 64];
+  // few offsets are searched in LDS: a search in memory waits for each step
+  __shared__ int cu[2][STAGED];
+  const bool staged = ndoc < STAGED;
+  if (staged) {
+    for (int i = threadIdx.x; i <= ndoc; i += NTH) {
+      cu[0][i] = cu_q[i];
+      cu[1][i] = cu_k[i];
+    }
+    __syncthreads();
+    cu_q = cu[0];
+    cu_k = cu[1];
+  }
   const bool row = (int)blockIdx.x < qblocks;
   const int b = row ? blockIdx.x : blockIdx.x - qblocks, T = row ? Tq : Tk;
   const int t = b * NTH + threadIdx.x;
@@ -71,25 +83,23 @@ __global__ __launch_bounds__(NTH) void k_attn_plan(int Tq, int Tk, int ndoc, int
   }
 }
 
-// Tiles by falling cost: tile i goes where its rank among all puts it.
+// Tiles by falling cost: a tile goes where its rank among all puts it.  A
+// wave a tile, the others counted 64 at a time.
 __global__ __launch_bounds__(NTH) void k_attn_order(int tq, int tk, AttnPlan pl) {
-  __shared__ int cost[NTH];
-  const int n = blockIdx.y ? tk : tq;
+  const int lane = threadIdx.x % 64, n = blockIdx.y ? tk : tq;
   const int4* raw = blockIdx.y ? pl.kraw : pl.qraw;
-  const int i = blockIdx.x * NTH + threadIdx.x;
-  if ((int)blockIdx.x * NTH >= n) return;
-  const int4 e = raw[min(i, n - 1)];
+  const int i = blockIdx.x * (NTH / 64) + threadIdx.x / 64;
+  if (i >= n) return;
+  const int4 e = raw[i];
   const int mine = e.z - e.y;
   int rank = 0;
-  for (int b = 0; b < n; b += NTH) {
-    const int4 o = raw[min(b + (int)threadIdx.x, n - 1)];
-    __syncthreads();
-    cost[threadIdx.x] = o.z - o.y;
-    __syncthreads();
-    const int m = min(NTH, n - b);
-    for (int j = 0; j < m; ++j) rank += cost[j] > mine || (cost[j] == mine && b + j < i) ? 1 : 0;
+  for (int b = 0; b < n; b += 64) {
+    const int j = b + lane;
+    const int4 o = raw[min(j, n - 1)];
+    const int c = o.z - o.y;
+    rank += __popcll(__ballot(j < n && (c > mine || (c == mine && j < i))));
   }
-  if (i < n) (blockIdx.y ? pl.ktab : pl.qtab)[rank] = e;
+  if (lane == 0) (blockIdx.y ? pl.ktab : pl.qtab)[rank] = e;
 }
 
 }  // namespace
@@ -101,7 +111,7 @@ hipError_t launch_attn_plan(int Tq, int Tk, int ndoc, int causal, const int* cu_
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || pl.qtab == pl.qraw) return e;
   const int tq = attn_tiles(Tq), tk = attn_tiles(Tk);
-  k_attn_order<<<dim3((std::max(tq, tk) + NTH - 1) / NTH, 2), NTH, 0, s>>>(tq, tk, pl);
+  k_attn_order<<<dim3((std::max(tq, tk) + NTH / 64 - 1) / (NTH / 64), 2), NTH, 0, s>>>(tq, tk, pl);
   return hipGetLastError();
 }
 

@@ -284,13 +284,13 @@ def _rows(t: Optional[torch.Tensor], name: str, shape, dtype):
         raise ValueError(f"{name} must be a GPU tensor")
     if t.dtype != dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     T, H, D = shape
-    st = t.stride()
-    if t.numel() and ((D > 1 and st[2] != 1) or (H > 1 and st[1] != D)):
-        raise ValueError(f"{name}: heads must lie side by side in a row (strides {st})")
-    return C.c_void_p(t.data_ptr()), (st[0] if T > 1 else max(H * D, 8))
+    ld, sh, sd = t.stride()
+    if T and ((D > 1 and sd != 1) or (H > 1 and sh != D)):
+        raise ValueError(f"{name}: heads must lie side by side in a row (strides {t.stride()})")
+    return t.data_ptr(), (ld if T > 1 else max(H * D, 8))
 
 
 def _vec(t: Optional[torch.Tensor], name: str, dtype, numel: int, optional=False):
