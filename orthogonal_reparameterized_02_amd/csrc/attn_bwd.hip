@@ -65,6 +65,7 @@ template <typename T, int DP, int MODE>
 __global__ __launch_bounds__(64 * NW, (BwdCfg<T, DP>::OCC)) void k_attn_dq(AttnArgs a, int parts) {
   using L = Tile<T, DP>;
   using C = BwdCfg<T, DP>;
+  constexpr float FACTOR = short_cap<T, MODE> ? 4.0f : 1.0f;  // of 1 - tanh^2 = 4 (r - r^2)
   constexpr int BN = C::BN, NS = BN / 32;
   extern __shared__ __align__(16) char smem[];
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -111,7 +112,8 @@ __global__ __launch_bounds__(64 * NW, (BwdCfg<T, DP>::OCC)) void k_attn_dq(AttnA
   }
   delta += other_half(delta);
   const float lse = a.lse[(long)h * a.Tq + tc];
-  const float lse2 = lse == -INFINITY ? INFINITY : lse * LOG2E;
+  // with the short cap, less the cap itself (attn_tile.h)
+  const float lse2 = lse == -INFINITY ? INFINITY : lse * LOG2E - (short_cap<T, MODE> ? a.cap * LOG2E : 0.0f);
   if (in && lane < 32 && part == 0) {
     a.delta[(long)h * a.Tq + t] = delta;
     a.lse2[(long)h * a.Tq + t] = lse2;
@@ -162,6 +164,9 @@ __global__ __launch_bounds__(64 * NW, (BwdCfg<T, DP>::OCC)) void k_attn_dq(AttnA
         float tt;
         if constexpr (MODE == 0) {
           s[i] = exp2_hw(fmaf(s[i], sa.c, -lse2)) * dp[i];
+        } else if constexpr (short_cap<T, MODE>) {
+          const float r = cap_r(s[i], sa);
+          s[i] = exp2_hw(fmaf(-2.0f * sa.capl, r, -lse2)) * dp[i] * fmaf(-r, r, r);
         } else {
           const float x = score2<T, MODE>(s[i], sa, pos - (float)(jl + 8 * (i / 4) + i % 4), tt);
           s[i] = exp2_hw(x - lse2) * dp[i];
@@ -205,8 +210,8 @@ __global__ __launch_bounds__(64 * NW, (BwdCfg<T, DP>::OCC)) void k_attn_dq(AttnA
     return;
   }
   const long tt = in ? t : 0;
-  if (parts > 1) store_rowsT<L::NT>(pq + tt * ldp, dq, 1.0f, a.D, in, lane);
-  else store_rowsT<L::NT>((T*)a.dq + tt * a.lddq + (long)h * a.D, dq, a.scale, a.D, in, lane);
+  if (parts > 1) store_rowsT<L::NT>(pq + tt * ldp, dq, FACTOR, a.D, in, lane);
+  else store_rowsT<L::NT>((T*)a.dq + tt * a.lddq + (long)h * a.D, dq, a.scale * FACTOR, a.D, in, lane);
 }
 
 // dk and dv
@@ -214,6 +219,7 @@ template <typename T, int DP, int MODE>
 __global__ __launch_bounds__((64 * NW * BwdCfg<T, DP>::NQ), (BwdCfg<T, DP>::OCC)) void k_attn_dkv(AttnArgs a, int parts) {
   using L = Tile<T, DP>;
   using C = BwdCfg<T, DP>;
+  constexpr float FACTOR = short_cap<T, MODE> ? 4.0f : 1.0f;  // of 1 - tanh^2 = 4 (r - r^2)
   constexpr int BN = C::BQ, NWA = NW * C::NQ;
   extern __shared__ __align__(16) char smem[];
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -345,6 +351,10 @@ __global__ __launch_bounds__((64 * NW * BwdCfg<T, DP>::NQ), (BwdCfg<T, DP>::OCC)
         if constexpr (MODE == 0) {
           p[i] = exp2_hw(fmaf(s[i], sa.c, -e[x]));
           s[i] = p[i] * dp[i];
+        } else if constexpr (short_cap<T, MODE>) {
+          const float r = cap_r(s[i], sa);
+          p[i] = exp2_hw(fmaf(-2.0f * sa.capl, r, -e[x]));
+          s[i] = p[i] * dp[i] * fmaf(-r, r, r);
         } else {
           float tt;
           p[i] = exp2_hw(score2<T, MODE>(s[i], sa, (float)(ps[x] - t), tt) - e[x]);
@@ -433,10 +443,10 @@ __global__ __launch_bounds__((64 * NW * BwdCfg<T, DP>::NQ), (BwdCfg<T, DP>::OCC)
   }
   const long tt = in ? t : 0;
   if (parts > 1) {
-    store_rowsT<L::NT>(pk + tt * ldp, dk, 1.0f, a.D, in, lane);
+    store_rowsT<L::NT>(pk + tt * ldp, dk, FACTOR, a.D, in, lane);
     store_rowsT<L::NT>(pv + tt * ldp, dv, 1.0f, a.D, in, lane);
   } else {
-    store_rowsT<L::NT>(gk + tt * a.lddk, dk, a.scale, a.D, in, lane);
+    store_rowsT<L::NT>(gk + tt * a.lddk, dk, a.scale * FACTOR, a.D, in, lane);
     store_rowsT<L::NT>(gv + tt * a.lddv, dv, 1.0f, a.D, in, lane);
   }
 }

@@ -110,7 +110,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void 
     vp_.start(ldv);
     const int jl = j0 + 4 * (lane >> 5);  // key of register 0
     float top = -INFINITY;
-    if constexpr (MODE != 0) {
+    if constexpr (MODE != 0 && !short_cap<T, MODE>) {
       float unused;
 #pragma unroll
       for (int n = 0; n < NS; ++n)
@@ -118,8 +118,9 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void 
         for (int i = 0; i < 16; ++i)
           s[n][i] = score2<T, MODE>(s[n][i], sa, pos - (float)(jl + 32 * n + 8 * (i / 4) + i % 4), unused);
     }
-    if (sp.all_lo > j0 || sp.all_hi < j0 + BN) {  // some pair is hidden
-      const uint32_t width = (uint32_t)(hi - lo);
+    const bool masked = sp.all_lo > j0 || sp.all_hi < j0 + BN;  // some pair is hidden
+    const uint32_t width = (uint32_t)(hi - lo);
+    if (masked) {
 #pragma unroll
       for (int n = 0; n < NS; ++n)
 #pragma unroll
@@ -132,6 +133,8 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void 
       for (int i = 0; i < 16; ++i) top = fmaxf(top, s[n][i]);
     top = fmaxf(top, other_half(top));
     if constexpr (MODE == 0) top *= sa.c;
+    // the cap is monotone: the largest product has the largest score
+    if constexpr (short_cap<T, MODE>) top = top == -INFINITY ? top : fmaf(-2.0f * sa.capl, cap_r(top, sa), sa.capl);
     if (__any(top > m + SLACK)) {
       const float m2 = fmaxf(m, top);
       const float f = m2 == -INFINITY ? 1.0f : exp2_hw(m - m2);
@@ -147,9 +150,22 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void 
     for (int n = 0; n < NS; ++n)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        s[n][i] = exp2_hw(MODE == 0 ? fmaf(s[n][i], sa.c, -ref) : s[n][i] - ref);
-        l += s[n][i];
+        if constexpr (short_cap<T, MODE>) s[n][i] = exp2_hw(fmaf(-2.0f * sa.capl, cap_r(s[n][i], sa), sa.capl - ref));
+        else s[n][i] = exp2_hw(MODE == 0 ? fmaf(s[n][i], sa.c, -ref) : s[n][i] - ref);
       }
+    if constexpr (short_cap<T, MODE>) {
+      if (masked) {  // -inf is capped like any other product
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            s[n][i] = (uint32_t)(jl - lo + 32 * n + 8 * (i / 4) + i % 4) < width ? s[n][i] : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NS; ++n)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) l += s[n][i];
     uint4 p;
     vp_.run(ldv, [&](int i, uint4 f) {
       if (i % L::NT == 0) p = L::score_frag(s[i / (L::CSTEP * L::NT)], i / L::NT % L::CSTEP);

@@ -294,6 +294,15 @@ __device__ __forceinline__ ScoreArgs score_args(const AttnArgs& a, int h) {
   return s;
 }
 
+// The capped score with bf16 operands in its shortest form:
+//   r = 1 / (1 + e^(2 x / cap)),  cap tanh(x / cap) = cap - 2 cap r,
+//   1 - tanh^2 = 4 (r - r^2)
+// so that a probability is exp2(fma(-2 capl, r, capl - reference)).
+template <typename T, int MODE> constexpr bool short_cap = sizeof(T) == 2 && MODE == 1;
+__device__ __forceinline__ float cap_r(float qk, const ScoreArgs& s) {
+  return __builtin_amdgcn_rcpf(1.0f + exp2_hw(qk * (s.c * (2.0f * LOG2E))));
+}
+
 // s2 of q.k; t: tanh of the capped score (0 without a cap); dist: query
 // position - key
 template <typename T, int MODE>
