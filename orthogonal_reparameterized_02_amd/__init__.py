@@ -6,4 +6,4 @@ declared in include/poetx.h); `poetx` binds it under the same names and
 the library is opened on first use and a missing build raises.
 """
 
-__all__ = ["poetx", "layer", "inputs"]
+__all__ = ["poetx", "layer", "attention", "inputs"]
