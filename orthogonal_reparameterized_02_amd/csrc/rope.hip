@@ -16,55 +16,51 @@ constexpr int NTH = 256;
 // One thread per unit of one head of one token.  A unit is, in the half
 // layout, W elements of the first half with their partners (rot/2 further
 // on); in the interleaved one W consecutive elements; past rot, W elements
-// to copy.  W divides every part, so units never straddle.
+// to copy.  W divides every part, so units never straddle.  The unit's own
+// loads go out before the two dependent ones (position, then table row).
 template <typename TS, int W, bool PAIRS>
 __global__ __launch_bounds__(NTH) void k_rope(RopeArgs a, const TS* q, const TS* k, TS* qo, TS* ko,
-                                              int turn_units, int units, int per_token) {
-  const long id = (long)blockIdx.x * NTH + threadIdx.x;
-  const long t = id / per_token;
-  if (t >= a.T) return;
-  const int in = (int)(id - t * per_token);
-  const int h = in / units, u = in - h * units;
-  const bool isq = h < a.Hq;
-  const TS* src = isq ? q + t * a.ldq + (long)h * a.D : k + t * a.ldk + (long)(h - a.Hq) * a.D;
-  TS* dst = isq ? qo + t * a.ldqo + (long)h * a.D : ko + t * a.ldko + (long)(h - a.Hq) * a.D;
+                                              int turn_units, int units, int per_token,
+                                              float inv_units, float inv_token) {
   using V = Pack<TS, W>;
+  constexpr int C = PAIRS ? W / 2 : W;  // angles a unit
+  // the block's first unit by one scalar division, the thread's by products
+  // with reciprocals: (n + 1/2) / d truncates right for n below 2^21
+  const long id0 = (long)blockIdx.x * NTH;
+  const long t0 = id0 / per_token;
+  const int n = (int)(id0 - t0 * per_token) + threadIdx.x;
+  const int dt = (int)(((float)n + 0.5f) * inv_token);
+  const long t = t0 + dt;
+  if (t >= a.T) return;
+  const int in = n - dt * per_token;
+  const int h = (int)(((float)in + 0.5f) * inv_units), u = in - h * units;
+  const bool isq = h < a.Hq;
+  const int e = u < turn_units ? u * W : a.rot + (u - turn_units) * W;
+  const TS* src = (isq ? q + t * a.ldq + (long)h * a.D : k + t * a.ldk + (long)(h - a.Hq) * a.D) + e;
+  TS* dst = (isq ? qo + t * a.ldqo + (long)h * a.D : ko + t * a.ldko + (long)(h - a.Hq) * a.D) + e;
+  V x0 = *reinterpret_cast<const V*>(src);
   if (u >= turn_units) {
-    const int e = a.rot + (u - turn_units) * W;
-    *reinterpret_cast<V*>(dst + e) = *reinterpret_cast<const V*>(src + e);
+    *reinterpret_cast<V*>(dst) = x0;
     return;
   }
+  V x1;
+  if constexpr (!PAIRS) x1 = *reinterpret_cast<const V*>(src + a.rot / 2);
+
   const int p = a.pos[t];
   const bool in_table = (unsigned)p < (unsigned)a.P;
-  const float2* cs = reinterpret_cast<const float2*>(a.table) + (long)(in_table ? p : 0) * (a.rot / 2);
   const float bad = in_table ? 0.0f : __uint_as_float(0x7fc00000u);
-  if constexpr (PAIRS) {
-    const int e = u * W;
-    const V x = *reinterpret_cast<const V*>(src + e);
-    V y;
+  const float2* cs = reinterpret_cast<const float2*>(a.table) + (long)(in_table ? p : 0) * (a.rot / 2) + u * C;
+  V y0, y1;
 #pragma unroll
-    for (int i = 0; i < W; i += 2) {
-      const float2 c = cs[(e + i) / 2];
-      const float s = a.sgn * c.y, lo = St<TS>::ld(&x.e[i]), hi = St<TS>::ld(&x.e[i + 1]);
-      St<TS>::st(&y.e[i], lo * c.x - hi * s + bad);
-      St<TS>::st(&y.e[i + 1], lo * s + hi * c.x + bad);
-    }
-    *reinterpret_cast<V*>(dst + e) = y;
-  } else {
-    const int e = u * W, half = a.rot / 2;
-    const V x0 = *reinterpret_cast<const V*>(src + e);
-    const V x1 = *reinterpret_cast<const V*>(src + half + e);
-    V y0, y1;
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      const float2 c = cs[e + i];
-      const float s = a.sgn * c.y, lo = St<TS>::ld(&x0.e[i]), hi = St<TS>::ld(&x1.e[i]);
-      St<TS>::st(&y0.e[i], lo * c.x - hi * s + bad);
-      St<TS>::st(&y1.e[i], lo * s + hi * c.x + bad);
-    }
-    *reinterpret_cast<V*>(dst + e) = y0;
-    *reinterpret_cast<V*>(dst + half + e) = y1;
+  for (int i = 0; i < C; ++i) {
+    const float c = cs[i].x, s = a.sgn * cs[i].y;
+    const float lo = St<TS>::ld(PAIRS ? &x0.e[2 * i] : &x0.e[i]);
+    const float hi = St<TS>::ld(PAIRS ? &x0.e[2 * i + 1] : &x1.e[i]);
+    St<TS>::st(PAIRS ? &y0.e[2 * i] : &y0.e[i], lo * c - hi * s + bad);
+    St<TS>::st(PAIRS ? &y0.e[2 * i + 1] : &y1.e[i], lo * s + hi * c + bad);
   }
+  *reinterpret_cast<V*>(dst) = y0;
+  if constexpr (!PAIRS) *reinterpret_cast<V*>(dst + a.rot / 2) = y1;
 }
 
 template <typename TS, int W>
@@ -75,11 +71,13 @@ hipError_t rope_w(const RopeArgs& a, const TS* q, const TS* k, TS* qo, TS* ko, h
   const dim3 grid((unsigned)((total + NTH - 1) / NTH));
   if constexpr (W >= 2) {
     if (a.interleaved) {
-      k_rope<TS, W, true><<<grid, NTH, 0, s>>>(a, q, k, qo, ko, turn, units, per_token);
+      k_rope<TS, W, true><<<grid, NTH, 0, s>>>(a, q, k, qo, ko, turn, units, per_token,
+                                                     1.0f / units, 1.0f / per_token);
       return hipGetLastError();
     }
   }
-  k_rope<TS, W, false><<<grid, NTH, 0, s>>>(a, q, k, qo, ko, turn, units, per_token);
+  k_rope<TS, W, false><<<grid, NTH, 0, s>>>(a, q, k, qo, ko, turn, units, per_token,
+                                                     1.0f / units, 1.0f / per_token);
   return hipGetLastError();
 }
 
