@@ -65,7 +65,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void 
   sa.capl = a.cap * LOG2E;
   sa.slope = a.slopes ? a.slopes[h0 + min(head, heads - 1)] * LOG2E : 0.0f;
 
-  Loader<T, DP, BN, 1> lk, lv;
+  Loader<T, DP, BN, 1, true> lk, lv;
   lk.init(a.ldk, a.D, 0, lane);
   lv.init(a.ldv, a.D, 0, lane);
   const uint32_t kr = L::row_lane(lane) + wave * 2 * TILE, vc = L::col_lane(lane) + (wave * 2 + 1) * TILE;

@@ -118,7 +118,9 @@ template <typename T, int DP> struct Tile {
 // the chunk that belongs there.  The buffer range ends with the last row
 // that counts: rows past it, and chunks past the head (whose offset is put
 // out of range), arrive as zeros.  Completion is tracked by vmcnt.
-template <typename T, int DP, int ROWS, int NW> struct Loader {
+// NT: non-temporal, for rows that are read once (a cache of many gigabytes
+// pushes everything else out of the last-level cache, and waits for it).
+template <typename T, int DP, int ROWS, int NW, bool NT = false> struct Loader {
   using L = Tile<T, DP>;
   static constexpr int STEP = NW * L::RPL;        // rows one load of all waves fills
   static constexpr int N = ROWS / STEP;           // loads a wave
@@ -149,9 +151,13 @@ template <typename T, int DP, int ROWS, int NW> struct Loader {
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const uint32_t m0v = __builtin_amdgcn_readfirstlane(lds + (j * NW + wave) * 1024);
-      asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(m0v),
-                   "v"(vo[j % VAR] + (j - j % VAR) * STEP * ldb), "s"(rs)
-                   : "memory");
+      const int off = vo[j % VAR] + (j - j % VAR) * STEP * ldb;
+      if constexpr (NT)
+        asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds" ::"s"(m0v), "v"(off), "s"(rs)
+                     : "memory");
+      else
+        asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(m0v), "v"(off), "s"(rs)
+                     : "memory");
     }
   }
 };

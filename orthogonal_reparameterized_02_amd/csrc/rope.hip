@@ -45,7 +45,6 @@ __global__ __launch_bounds__(NTH) void k_rope(RopeArgs a, const TS* q, const TS*
   }
   V x1;
   if constexpr (!PAIRS) x1 = *reinterpret_cast<const V*>(src + a.rot / 2);
-
   const int p = a.pos[t];
   const bool in_table = (unsigned)p < (unsigned)a.P;
   const float bad = in_table ? 0.0f : __uint_as_float(0x7fc00000u);
