@@ -30,7 +30,23 @@ __device__ __forceinline__ uint4 philox10(uint32_t c0, uint32_t c1, uint32_t k0,
 
 template <typename TS> struct alignas(16) Pack8 { TS e[8]; };
 
-// eight elements a thread
+// 16-byte loads; NT: non-temporal
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+template <bool NT, typename TS> __device__ __forceinline__ Pack8<TS> load8(const TS* p) {
+  constexpr int N = sizeof(Pack8<TS>) / 16;
+  const u32x4_t* q = reinterpret_cast<const u32x4_t*>(p);
+  u32x4_t t[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) t[i] = NT ? __builtin_nontemporal_load(q + i) : q[i];
+  Pack8<TS> v;
+  __builtin_memcpy(&v, t, sizeof v);
+  return v;
+}
+
+// Eight elements a thread.  With a residual both inputs have their last
+// reader here and leave the last-level cache to the sum (non-temporal loads:
+// forward and backward of 8191 x 5120 bf16 75.3 -> 73 us); the backward
+// pass's dy is the residual's gradient too and stays.
 template <typename TS, bool RES>
 __global__ __launch_bounds__(NTH) void k_dropout(long n, const TS* x, const TS* res, TS* out,
                                                  uint32_t cut, float gain, uint64_t seed,
@@ -48,9 +64,9 @@ __global__ __launch_bounds__(NTH) void k_dropout(long n, const TS* x, const TS* 
   };
   if (i + 8 <= n) {
     using V = Pack8<TS>;
-    const V xv = *reinterpret_cast<const V*>(x + i);
+    const V xv = load8<RES>(x + i);
     V rv, yv;
-    if constexpr (RES) rv = *reinterpret_cast<const V*>(res + i);
+    if constexpr (RES) rv = load8<true>(res + i);
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       St<TS>::st(&yv.e[e], one(e, St<TS>::ld(&xv.e[e]), RES ? St<TS>::ld(&rv.e[e]) : 0.0f));
