@@ -65,7 +65,7 @@ template <typename T, int DP, int MODE>
 __global__ __launch_bounds__(64 * NW, (BwdCfg<T, DP>::OCC)) void k_attn_dq(AttnArgs a, int parts) {
   using L = Tile<T, DP>;
   using C = BwdCfg<T, DP>;
-  constexpr float FACTOR = short_cap<T, MODE> ? 4.0f : 1.0f;  // of 1 - tanh^2 = 4 (r - r^2)
+  constexpr float FACTOR = cap_factor<T, MODE>;
   constexpr int BN = C::BN, NS = BN / 32;
   extern __shared__ __align__(16) char smem[];
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -96,7 +96,7 @@ __global__ __launch_bounds__(64 * NW, (BwdCfg<T, DP>::OCC)) void k_attn_dq(AttnA
   const int t = r0 + (lane & 31);
   const bool in = t < a.Tq;
   const int tc = min(t, a.Tq - 1);
-  const int rlo = a.pl.row_lo[tc], rhi = a.pl.row_hi[tc], rpos = MODE == 2 ? a.pl.row_pos[tc] : 0;
+  const int rlo = a.pl.row_lo[tc], rhi = a.pl.row_hi[tc], rpos = MODE & 2 ? a.pl.row_pos[tc] : 0;
   const int lo = in ? rlo : 0, hi = in ? rhi : 0;
   const float pos = (float)rpos;
   const Span sp = span_of(lo, hi);
@@ -112,8 +112,7 @@ __global__ __launch_bounds__(64 * NW, (BwdCfg<T, DP>::OCC)) void k_attn_dq(AttnA
   }
   delta += other_half(delta);
   const float lse = a.lse[(long)h * a.Tq + tc];
-  // with the short cap, less the cap itself (attn_tile.h)
-  const float lse2 = lse == -INFINITY ? INFINITY : lse * LOG2E - (short_cap<T, MODE> ? a.cap * LOG2E : 0.0f);
+  const float lse2 = lse == -INFINITY ? INFINITY : lse * LOG2E;
   if (in && lane < 32 && part == 0) {
     a.delta[(long)h * a.Tq + t] = delta;
     a.lse2[(long)h * a.Tq + t] = lse2;
@@ -121,7 +120,7 @@ __global__ __launch_bounds__(64 * NW, (BwdCfg<T, DP>::OCC)) void k_attn_dq(AttnA
   rows_to_regs<T>(qf, qp, a.ldq, r0, a.Tq, a.D, lane);
 
   const uint32_t rlane = L::row_lane(lane), clane = L::col_lane(lane);
-  const ScoreArgs sa = score_args(a, h);
+  const ScoreArgs sa = score_args<T, MODE>(a, h);
   f32x16_t dq[L::NT];
 #pragma unroll
   for (int i = 0; i < L::NT; ++i) dq[i] = (f32x16_t){};
@@ -159,19 +158,13 @@ __global__ __launch_bounds__(64 * NW, (BwdCfg<T, DP>::OCC)) void k_attn_dq(AttnA
       const auto ldc = [&](int i) { return L::col_frag(smem, kc, 32 * n, i / L::NT, i % L::NT); };
       cp.start(ldc);
       const int jl = jn + 4 * (lane >> 5);  // key of register 0
+      const float d0 = pos - (float)jl;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        float tt;
-        if constexpr (MODE == 0) {
-          s[i] = exp2_hw(fmaf(s[i], sa.c, -lse2)) * dp[i];
-        } else if constexpr (short_cap<T, MODE>) {
-          const float r = cap_r(s[i], sa);
-          s[i] = exp2_hw(fmaf(-2.0f * sa.capl, r, -lse2)) * dp[i] * fmaf(-r, r, r);
-        } else {
-          const float x = score2<T, MODE>(s[i], sa, pos - (float)(jl + 8 * (i / 4) + i % 4), tt);
-          s[i] = exp2_hw(x - lse2) * dp[i];
-          s[i] = fmaf(-s[i] * tt, tt, s[i]);
-        }
+        float deriv;
+        if constexpr (MODE == 0) s[i] = exp2_hw(fmaf(s[i], sa.c, -lse2)) * dp[i];
+        else s[i] = exp2_hw(score2<T, MODE>(s[i], sa, d0 - (float)(8 * (i / 4) + i % 4), deriv) - lse2) * dp[i];
+        if constexpr (MODE & 1) s[i] *= deriv;
       }
       if (sp.all_lo > jn || sp.all_hi < jn + 32) {  // some pair is hidden
         const uint32_t width = (uint32_t)(hi - lo);
@@ -219,7 +212,7 @@ template <typename T, int DP, int MODE>
 __global__ __launch_bounds__((64 * NW * BwdCfg<T, DP>::NQ), (BwdCfg<T, DP>::OCC)) void k_attn_dkv(AttnArgs a, int parts) {
   using L = Tile<T, DP>;
   using C = BwdCfg<T, DP>;
-  constexpr float FACTOR = short_cap<T, MODE> ? 4.0f : 1.0f;  // of 1 - tanh^2 = 4 (r - r^2)
+  constexpr float FACTOR = cap_factor<T, MODE>;
   constexpr int BN = C::BQ, NWA = NW * C::NQ;
   extern __shared__ __align__(16) char smem[];
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -247,7 +240,7 @@ __global__ __launch_bounds__((64 * NW * BwdCfg<T, DP>::NQ), (BwdCfg<T, DP>::OCC)
     lq.load((const T*)a.q + (long)h * a.D, a.ldq, i0, qhi, lds0 + buf * C::QTILE);
     lo_.load((const T*)a.dout + (long)h * a.D, a.lddo, i0, qhi, lds0 + (2 + buf) * C::QTILE);
     // one value a query: a dword a lane, wave by wave
-    if (wave < (MODE == 2 ? 3 : 2)) {
+    if (wave < (MODE & 2 ? 3 : 2)) {
       const float* src = wave == 0 ? a.lse2 + (long)h * a.Tq : wave == 1 ? a.delta + (long)h * a.Tq
                                                                          : (const float*)a.pl.row_pos;
       const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
@@ -302,7 +295,7 @@ __global__ __launch_bounds__((64 * NW * BwdCfg<T, DP>::NQ), (BwdCfg<T, DP>::OCC)
       ++h;
     }
     if (n + 1 < ne) load(h, i0, buf ^ 1);
-    const ScoreArgs sa = score_args(a, hc);
+    const ScoreArgs sa = score_args<T, MODE>(a, hc);
     const uint32_t qr = rlane + buf * C::QTILE, qc = clane + buf * C::QTILE;
     const uint32_t dr = qr + 2 * C::QTILE, dc = qc + 2 * C::QTILE;
     const float* rv = reinterpret_cast<const float*>(smem + 4 * C::QTILE + buf * C::ROWV);
@@ -343,24 +336,16 @@ __global__ __launch_bounds__((64 * NW * BwdCfg<T, DP>::NQ), (BwdCfg<T, DP>::OCC)
       const float4 e4 = *reinterpret_cast<const float4*>(row + 8 * g);
       const float e[4] = {e4.x, e4.y, e4.z, e4.w};
       int4 pq = make_int4(0, 0, 0, 0);
-      if constexpr (MODE == 2) pq = *reinterpret_cast<const int4*>(row + 2 * C::VS + 8 * g);
+      if constexpr (MODE & 2) pq = *reinterpret_cast<const int4*>(row + 2 * C::VS + 8 * g);
       const int ps[4] = {pq.x, pq.y, pq.z, pq.w};
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         const int i = 4 * g + x;
-        if constexpr (MODE == 0) {
-          p[i] = exp2_hw(fmaf(s[i], sa.c, -e[x]));
-          s[i] = p[i] * dp[i];
-        } else if constexpr (short_cap<T, MODE>) {
-          const float r = cap_r(s[i], sa);
-          p[i] = exp2_hw(fmaf(-2.0f * sa.capl, r, -e[x]));
-          s[i] = p[i] * dp[i] * fmaf(-r, r, r);
-        } else {
-          float tt;
-          p[i] = exp2_hw(score2<T, MODE>(s[i], sa, (float)(ps[x] - t), tt) - e[x]);
-          s[i] = p[i] * dp[i];
-          s[i] = fmaf(-s[i] * tt, tt, s[i]);
-        }
+        float deriv;
+        if constexpr (MODE == 0) p[i] = exp2_hw(fmaf(s[i], sa.c, -e[x]));
+        else p[i] = exp2_hw(score2<T, MODE>(s[i], sa, (float)(ps[x] - t), deriv) - e[x]);
+        s[i] = p[i] * dp[i];
+        if constexpr (MODE & 1) s[i] *= deriv;
       }
     }
     if (sp.all_lo > in0 || sp.all_hi < in0 + 32) {  // some pair is hidden
@@ -516,7 +501,7 @@ template <typename T, int DP, int MODE> hipError_t bwd(const AttnArgs& a, hipStr
 }
 
 template <typename T, int DP> hipError_t bwd_mode(const AttnArgs& a, hipStream_t s) {
-  if (a.slopes) return bwd<T, DP, 2>(a, s);
+  if (a.slopes) return a.cap > 0.0f ? bwd<T, DP, 3>(a, s) : bwd<T, DP, 2>(a, s);
   return a.cap > 0.0f ? bwd<T, DP, 1>(a, s) : bwd<T, DP, 0>(a, s);
 }
 

@@ -60,10 +60,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void 
   rows_to_regs<T>(qf, (const T*)a.q + (long)b * a.ldq + (long)h0 * a.D, a.D, 0, heads, a.D, lane);
   const int head = lane & 31;
   const bool in = head < heads;
-  ScoreArgs sa;
-  sa.c = a.cap > 0.0f ? a.scale / a.cap : a.scale * LOG2E;
-  sa.capl = a.cap * LOG2E;
-  sa.slope = a.slopes ? a.slopes[h0 + min(head, heads - 1)] * LOG2E : 0.0f;
+  const ScoreArgs sa = score_args<T, MODE>(a.scale, a.cap, MODE & 2 ? a.slopes[h0 + min(head, heads - 1)] : 0.0f);
 
   Loader<T, DP, BN, 1, true> lk, lv;
   lk.init(a.ldk, a.D, 0, lane);
@@ -92,11 +89,12 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void 
     const int jn = min(j0 + GRAIN, p1);  // a load past the piece has no rows: zeros
     lk.load(kp, a.ldk, jn, p1, ldsk);
     const int jl = j0 + 4 * (lane >> 5);
+    const float d0 = (float)(hi - 1 - jl);
     float top = -INFINITY, unused;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const int j = jl + 8 * (i / 4) + i % 4;
-      sc[i] = score2<T, MODE>(sc[i], sa, (float)(hi - 1 - j), unused);
+      sc[i] = score2<T, MODE>(sc[i], sa, d0 - (float)(8 * (i / 4) + i % 4), unused);
       sc[i] = j < p1 ? sc[i] : -INFINITY;
       top = fmaxf(top, sc[i]);
     }
@@ -229,7 +227,7 @@ template <typename T, int DP, int MODE> hipError_t decode(const DecodeArgs& a, f
 }
 
 template <typename T, int DP> hipError_t decode_mode(const DecodeArgs& a, float* ws, hipStream_t s) {
-  if (a.slopes) return decode<T, DP, 2>(a, ws, s);
+  if (a.slopes) return a.cap > 0.0f ? decode<T, DP, 3>(a, ws, s) : decode<T, DP, 2>(a, ws, s);
   return a.cap > 0.0f ? decode<T, DP, 1>(a, ws, s) : decode<T, DP, 0>(a, ws, s);
 }
 

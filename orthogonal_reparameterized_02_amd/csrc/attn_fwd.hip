@@ -37,6 +37,9 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void 
   using L = Tile<T, DP>;
   using C = FwdCfg<T, DP>;
   constexpr int BN = C::BN, NS = BN / 32;
+  // capped bf16 scores: the maximum is taken of the products (the cap is
+  // monotone), a probability is exp2(fma(-2 cap, r, cap - reference))
+  constexpr bool LATE = MODE == 1 && sizeof(T) == 2;
   extern __shared__ __align__(16) char smem[];
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   int h, tile;
@@ -65,7 +68,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void 
   const int t = q0 + 32 * wave + (lane & 31);
   const bool in = t < a.Tq;
   const int tc = min(t, a.Tq - 1);
-  const int rlo = a.pl.row_lo[tc], rhi = a.pl.row_hi[tc], rpos = MODE == 2 ? a.pl.row_pos[tc] : 0;
+  const int rlo = a.pl.row_lo[tc], rhi = a.pl.row_hi[tc], rpos = MODE & 2 ? a.pl.row_pos[tc] : 0;
   const int lo = in ? rlo : 0, hi = in ? rhi : 0;
   const float pos = (float)rpos;
   const Span sp = span_of(lo, hi);
@@ -74,7 +77,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void 
   rows_to_regs<T>(qf, qp, a.ldq, q0 + 32 * wave, a.Tq, a.D, lane);
 
   const uint32_t rlane = L::row_lane(lane), clane = L::col_lane(lane);
-  const ScoreArgs sa = score_args(a, h);
+  const ScoreArgs sa = score_args<T, MODE>(a, h);
   f32x16_t o[L::NT];
 #pragma unroll
   for (int i = 0; i < L::NT; ++i) o[i] = (f32x16_t){};
@@ -110,13 +113,14 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void 
     vp_.start(ldv);
     const int jl = j0 + 4 * (lane >> 5);  // key of register 0
     float top = -INFINITY;
-    if constexpr (MODE != 0 && !short_cap<T, MODE>) {
+    if constexpr (MODE != 0 && !LATE) {
+      const float d0 = pos - (float)jl;
       float unused;
 #pragma unroll
       for (int n = 0; n < NS; ++n)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          s[n][i] = score2<T, MODE>(s[n][i], sa, pos - (float)(jl + 32 * n + 8 * (i / 4) + i % 4), unused);
+          s[n][i] = score2<T, MODE>(s[n][i], sa, d0 - (float)(32 * n + 8 * (i / 4) + i % 4), unused);
     }
     const bool masked = sp.all_lo > j0 || sp.all_hi < j0 + BN;  // some pair is hidden
     const uint32_t width = (uint32_t)(hi - lo);
@@ -133,8 +137,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void 
       for (int i = 0; i < 16; ++i) top = fmaxf(top, s[n][i]);
     top = fmaxf(top, other_half(top));
     if constexpr (MODE == 0) top *= sa.c;
-    // the cap is monotone: the largest product has the largest score
-    if constexpr (short_cap<T, MODE>) top = top == -INFINITY ? top : fmaf(-2.0f * sa.capl, cap_r(top, sa), sa.capl);
+    if constexpr (LATE) top = top == -INFINITY ? top : fmaf(-2.0f * sa.capl, cap_r(top, sa), sa.capl);
     if (__any(top > m + SLACK)) {
       const float m2 = fmaxf(m, top);
       const float f = m2 == -INFINITY ? 1.0f : exp2_hw(m - m2);
@@ -150,10 +153,10 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void 
     for (int n = 0; n < NS; ++n)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        if constexpr (short_cap<T, MODE>) s[n][i] = exp2_hw(fmaf(-2.0f * sa.capl, cap_r(s[n][i], sa), sa.capl - ref));
+        if constexpr (LATE) s[n][i] = exp2_hw(fmaf(-2.0f * sa.capl, cap_r(s[n][i], sa), sa.capl - ref));
         else s[n][i] = exp2_hw(MODE == 0 ? fmaf(s[n][i], sa.c, -ref) : s[n][i] - ref);
       }
-    if constexpr (short_cap<T, MODE>) {
+    if constexpr (LATE) {
       if (masked) {  // -inf is capped like any other product
 #pragma unroll
         for (int n = 0; n < NS; ++n)
@@ -264,7 +267,7 @@ template <typename T, int DP, int MODE> hipError_t fwd(const AttnArgs& a, hipStr
 }
 
 template <typename T, int DP> hipError_t fwd_mode(const AttnArgs& a, hipStream_t s) {
-  if (a.slopes) return fwd<T, DP, 2>(a, s);
+  if (a.slopes) return a.cap > 0.0f ? fwd<T, DP, 3>(a, s) : fwd<T, DP, 2>(a, s);
   return a.cap > 0.0f ? fwd<T, DP, 1>(a, s) : fwd<T, DP, 0>(a, s);
 }
 

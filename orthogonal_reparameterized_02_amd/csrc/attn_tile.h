@@ -268,15 +268,16 @@ template <int N, int DEPTH> struct Pipe {
 };
 
 // ---- scores ----------------------------------------------------------------------
-// MODE 0: scale only; 1: capped; 2: distance bias, capped or not.
-// In units of log2: s2 = log2(e) * score.
-template <typename T> __device__ __forceinline__ float tanh_fast(float x) {
-  // 1 - 2 / (e^2x + 1): absolute error of one unit in 2^-23, enough next to
-  // bf16 operands.  float32 near 0 takes an odd polynomial (least squares on
-  // [0, 0.65], relative error 8e-8): the difference would cancel there and the
-  // cap multiplies what is lost.
+// MODE bit 0: capped by a tanh; bit 1: distance bias.  Scores are in units of
+// log2: s2 = log2(e) * score.  With
+//   r = 1 / (1 + e^(2 x / cap)):  cap tanh(x / cap) = cap - 2 cap r,
+//   1 - tanh^2 = 4 (r - r^2),
+// bf16 takes the cap from one exponential and one reciprocal; its absolute
+// error, cap units in 2^-23, is small next to bf16 operands.  float32 takes
+// tanh itself: near 0, where the difference would cancel, an odd polynomial
+// (least squares on [0, 0.65], relative error 8e-8).
+__device__ __forceinline__ float tanh_f32(float x) {
   const float big = 1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + exp2_hw(x * (2.0f * LOG2E)));
-  if constexpr (sizeof(T) == 2) return big;
   const float u = x * x;
   float p = -0.005514524877071381f;
   p = fmaf(p, u, 0.020468397065997124f);
@@ -287,44 +288,49 @@ template <typename T> __device__ __forceinline__ float tanh_fast(float x) {
 }
 
 struct ScoreArgs {
-  float c;      // MODE 0, 2: scale log2e; capped: scale / cap
-  float capl;   // cap log2e, 0: no cap
+  float c;      // of q.k: scale log2e; capped: scale / cap, bf16: 2 log2e scale / cap
+  float capl;   // cap log2e
   float slope;  // slope log2e
 };
 
-__device__ __forceinline__ ScoreArgs score_args(const AttnArgs& a, int h) {
+template <typename T, int MODE>
+__device__ __forceinline__ ScoreArgs score_args(float scale, float cap, float slope) {
   ScoreArgs s;
-  s.c = a.cap > 0.0f ? a.scale / a.cap : a.scale * LOG2E;
-  s.capl = a.cap * LOG2E;
-  s.slope = a.slopes ? a.slopes[h] * LOG2E : 0.0f;
+  s.c = !(MODE & 1) ? scale * LOG2E : sizeof(T) == 2 ? scale / cap * (2.0f * LOG2E) : scale / cap;
+  s.capl = cap * LOG2E;
+  s.slope = slope * LOG2E;
   return s;
 }
-
-// The capped score with bf16 operands in its shortest form:
-//   r = 1 / (1 + e^(2 x / cap)),  cap tanh(x / cap) = cap - 2 cap r,
-//   1 - tanh^2 = 4 (r - r^2)
-// so that a probability is exp2(fma(-2 capl, r, capl - reference)).
-template <typename T, int MODE> constexpr bool short_cap = sizeof(T) == 2 && MODE == 1;
-__device__ __forceinline__ float cap_r(float qk, const ScoreArgs& s) {
-  return __builtin_amdgcn_rcpf(1.0f + exp2_hw(qk * (s.c * (2.0f * LOG2E))));
+template <typename T, int MODE> __device__ __forceinline__ ScoreArgs score_args(const AttnArgs& a, int h) {
+  return score_args<T, MODE>(a.scale, a.cap, MODE & 2 ? a.slopes[h] : 0.0f);
 }
 
-// s2 of q.k; t: tanh of the capped score (0 without a cap); dist: query
-// position - key
+__device__ __forceinline__ float cap_r(float qk, const ScoreArgs& s) {
+  return __builtin_amdgcn_rcpf(1.0f + exp2_hw(qk * s.c));
+}
+
+// What the gradient of a capped score holds beside the derivative that
+// score2 returns: 4 of 4 (r - r^2)
+template <typename T, int MODE> constexpr float cap_factor = (MODE & 1) && sizeof(T) == 2 ? 4.0f : 1.0f;
+
+// s2 of q.k; deriv: its derivative by scale * q.k, less cap_factor (1 without
+// a cap); dist: query position - key
 template <typename T, int MODE>
-__device__ __forceinline__ float score2(float qk, const ScoreArgs& s, float dist, float& t) {
-  t = 0.0f;
-  if constexpr (MODE == 0) return qk * s.c;
-  if constexpr (MODE == 1) {
-    t = tanh_fast<T>(qk * s.c);
-    return s.capl * t;
-  }
-  float x = qk * s.c;
-  if (s.capl > 0.0f) {
-    t = tanh_fast<T>(x);
+__device__ __forceinline__ float score2(float qk, const ScoreArgs& s, float dist, float& deriv) {
+  float x;
+  if constexpr (!(MODE & 1)) {
+    x = qk * s.c;
+  } else if constexpr (sizeof(T) == 2) {
+    const float r = cap_r(qk, s);
+    x = fmaf(-2.0f * s.capl, r, s.capl);
+    deriv = fmaf(-r, r, r);
+  } else {
+    const float t = tanh_f32(qk * s.c);
     x = s.capl * t;
+    deriv = fmaf(-t, t, 1.0f);
   }
-  return fmaf(-s.slope, fabsf(dist), x);
+  if constexpr (MODE & 2) x = fmaf(-s.slope, fabsf(dist), x);
+  return x;
 }
 
 // ---- a wave's or workgroup's interval of visible rows ------------------------------
