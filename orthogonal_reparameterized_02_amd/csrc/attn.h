@@ -28,14 +28,21 @@ hipError_t launch_dropout(long n, const TS* x, const TS* res, TS* out, uint32_t 
 
 // ---- attention (attn_*.hip) -------------------------------------------------
 // Parts that a loop over about `rows` rows is cut into where `groups`
-// workgroups run it: enough for two workgroups a CU with bf16, eight with
-// float32 (whose products take eight times as long, so that unequal loops
-// wait longer for the longest and the traffic of partial sums counts less);
-// at least 256 bf16 or 128 float32 rows a part, 16 parts at most.
+// workgroups run it; 16 at most.  bf16: up to one workgroup a CU, or two
+// where a part still has 1024 rows; cutting shorter loops costs more in
+// partial sums than it evens out (1024 causal tokens, 32 heads on 8: one
+// training pass 127 us with two a CU, 103 with one).  float32 products take
+// eight times as long, so the traffic counts less and a loop that ends last
+// is waited for longer: up to four a CU (two documents of 1024, 16 heads of
+// 64: 496 us with two, 414 with four, 430 with eight).
 template <typename T> int parts_for(long groups, long rows) {
-  const long want = groups < 1 ? 1 : (sizeof(T) == 2 ? 512 : 2048) / groups;
-  const long most = rows / (sizeof(T) == 2 ? 256 : 128);
-  const long n = want < most ? want : most;
+  if (groups < 1) return 1;
+  const auto cut = [&](long fill, long least) {
+    const long want = fill / groups, most = rows / least;
+    return want < most ? want : most;
+  };
+  const long a = cut(sizeof(T) == 2 ? 256 : 1024, 256), b = sizeof(T) == 2 ? cut(512, 1024) : 1;
+  const long n = a > b ? a : b;
   return n < 1 ? 1 : n > 16 ? 16 : (int)n;
 }
 

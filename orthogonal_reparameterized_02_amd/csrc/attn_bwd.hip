@@ -465,7 +465,9 @@ template <typename T> int dq_parts(const AttnArgs& a) {
   return parts_for<T>((long)attn_tiles(a.Tq) * a.Hq, a.Tk / std::max(a.ndoc, 1));
 }
 template <typename T> int dkv_parts(const AttnArgs& a) {
-  return parts_for<T>((long)attn_tiles(a.Tk) * a.Hkv, (long)a.Tq / std::max(a.ndoc, 1) * a.group);
+  // a bf16 workgroup has eight waves: it counts twice
+  return parts_for<T>((long)attn_tiles(a.Tk) * a.Hkv * (sizeof(T) == 2 ? 2 : 1),
+                      (long)a.Tq / std::max(a.ndoc, 1) * a.group);
 }
 
 template <typename T, int DP, int MODE> hipError_t bwd(const AttnArgs& a, hipStream_t s) {
