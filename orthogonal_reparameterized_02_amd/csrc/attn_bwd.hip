@@ -21,25 +21,30 @@ constexpr int NW = 4;         // waves
 constexpr int BM = ATTN_BM;   // rows a workgroup owns
 static_assert(BM == 32 * NW, "a wave owns 32 of them");
 
-template <typename T, int DP> struct BwdCfg {
+template <typename T, int DP> struct DqCfg {
   static constexpr int BN = sizeof(T) == 2 ? 64 : 32;  // rows of a streamed tile
   static constexpr int TILE = BN * Tile<T, DP>::RB;
+  static constexpr int LDS = 4 * TILE;
+  static constexpr int OCC = sizeof(T) == 2 || DP == 64 ? 2 : 1;  // waves a SIMD, by registers
+};
+
+// Second pass.  NQ = 2: two waves take the same 32 keys and every other 32
+// queries, and add their sums at the end: eight waves, one workgroup a CU,
+// whose loop, which decides when the last workgroup ends, is half as long.
+// NQ = 1: four waves, two workgroups a CU, one's start and end beside the
+// other's loop.  A wave holds two 32-row sums, keys and values; with 128 bf16
+// columns that is a few registers more than two waves a SIMD have: the values
+// stay in LDS.
+template <typename T, int DP, int NQ> struct DkvCfg {
+  static constexpr bool VLDS = sizeof(T) == 2 && DP == 128;
   static constexpr int VS = 64;                        // a wave's load fills 64 values
   static constexpr int ROWV = 3 * VS * 4;              // lse2, delta, position of a tile's queries
-  static constexpr int LDS_DQ = 4 * TILE;
-  // Second pass: two waves (NQ) take the same 32 keys and every other 32
-  // queries, and add their sums at the end, so that a workgroup's loop, whose
-  // length decides when the last workgroup ends, is half as long.  A wave
-  // holds two 32-row sums, keys and values; with 128 bf16 columns that is a
-  // few registers more than two waves a SIMD have: the values stay in LDS.
-  static constexpr int NQ = sizeof(T) == 2 || DP == 64 ? 2 : 1;
-  static constexpr bool VLDS = sizeof(T) == 2 && DP == 128;
-  static constexpr int BQ = 32 * NQ;
+  static constexpr int BQ = 32 * NQ;                   // queries of a streamed tile
   static constexpr int QTILE = BQ * Tile<T, DP>::RB;
   static constexpr int VTILE = VLDS ? BM * Tile<T, DP>::RB : 0;
   static constexpr int JOIN = NQ == 2 ? NW * 2 * 32 * DP * 4 : 0;
-  static constexpr int LDS_DKV = std::max(4 * QTILE + 2 * ROWV + VTILE, JOIN);
-  static constexpr int OCC = sizeof(T) == 2 || DP == 64 ? 2 : 1;  // waves a SIMD, by registers
+  static constexpr int LDS = std::max(4 * QTILE + 2 * ROWV + VTILE, JOIN);
+  static constexpr int OCC = DqCfg<T, DP>::OCC;
 };
 
 __device__ __forceinline__ float dot8(const bf16*, uint4 a, uint4 b) {
@@ -62,9 +67,9 @@ __device__ __forceinline__ float dot8(const float*, uint4 a, uint4 b) {
 // dq, and for the second pass delta = dout . o and lse2 = lse log2e of every
 // query (lse2 = +inf where lse = -inf: such a query's p is 0)
 template <typename T, int DP, int MODE>
-__global__ __launch_bounds__(64 * NW, (BwdCfg<T, DP>::OCC)) void k_attn_dq(AttnArgs a, int parts) {
+__global__ __launch_bounds__(64 * NW, (DqCfg<T, DP>::OCC)) void k_attn_dq(AttnArgs a, int parts) {
   using L = Tile<T, DP>;
-  using C = BwdCfg<T, DP>;
+  using C = DqCfg<T, DP>;
   constexpr float FACTOR = cap_factor<T, MODE>;
   constexpr int BN = C::BN, NS = BN / 32;
   extern __shared__ __align__(16) char smem[];
@@ -72,7 +77,7 @@ __global__ __launch_bounds__(64 * NW, (BwdCfg<T, DP>::OCC)) void k_attn_dq(AttnA
   int h, tile;
   work_of(blockIdx.x, a.Hq, h, tile);
   int q0, klo, khi;
-  tile_entry(a.pl.qtab, tile, BM, q0, klo, khi);
+  tile_entry(a.pl.qtab, tile, BM, a.Tq, a.Tk, q0, klo, khi);
   const int hk = h / a.group, r0 = q0 + 32 * wave, part = blockIdx.y;
   const T* qp = (const T*)a.q + (long)h * a.D;
   const T* kp = (const T*)a.k + (long)hk * a.D;
@@ -208,22 +213,22 @@ __global__ __launch_bounds__(64 * NW, (BwdCfg<T, DP>::OCC)) void k_attn_dq(AttnA
 }
 
 // dk and dv
-template <typename T, int DP, int MODE>
-__global__ __launch_bounds__((64 * NW * BwdCfg<T, DP>::NQ), (BwdCfg<T, DP>::OCC)) void k_attn_dkv(AttnArgs a, int parts) {
+template <typename T, int DP, int MODE, int NQ>
+__global__ __launch_bounds__(64 * NW * NQ, (DkvCfg<T, DP, NQ>::OCC)) void k_attn_dkv(AttnArgs a, int parts) {
   using L = Tile<T, DP>;
-  using C = BwdCfg<T, DP>;
+  using C = DkvCfg<T, DP, NQ>;
   constexpr float FACTOR = cap_factor<T, MODE>;
-  constexpr int BN = C::BQ, NWA = NW * C::NQ;
+  constexpr int BN = C::BQ, NWA = NW * NQ;
   extern __shared__ __align__(16) char smem[];
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   // 32 keys; 32 queries of a tile.  Wave w runs on SIMD w % 4: near the
   // diagonal, where the later keys have nothing to do, every SIMD then still
   // has a wave of the earlier ones.
-  const int wk = wave / C::NQ, wq = wave % C::NQ;
+  const int wk = wave / NQ, wq = wave % NQ;
   int hk, tile;
   work_of(blockIdx.x, a.Hkv, hk, tile);
   int k0, qlo, qhi;
-  tile_entry(a.pl.ktab, tile, BM, k0, qlo, qhi);
+  tile_entry(a.pl.ktab, tile, BM, a.Tk, a.Tq, k0, qlo, qhi);
   const int r0 = k0 + 32 * wk, part = blockIdx.y;
   const T* kp = (const T*)a.k + (long)hk * a.D;
   const T* vp = (const T*)a.v + (long)hk * a.D;
@@ -282,7 +287,6 @@ __global__ __launch_bounds__((64 * NW * BwdCfg<T, DP>::NQ), (BwdCfg<T, DP>::OCC)
 #pragma unroll
   for (int i = 0; i < L::NT; ++i) dk[i] = dv[i] = (f32x16_t){};
 
-  if (wq) __builtin_amdgcn_s_setprio(1);
   wait_loads();  // also where there is no work: no load may outlive its workgroup
   int buf = 0;
   for (int n = nb; n < ne; ++n, buf ^= 1) {
@@ -373,7 +377,7 @@ __global__ __launch_bounds__((64 * NW * BwdCfg<T, DP>::NQ), (BwdCfg<T, DP>::OCC)
     }
   }
 
-  if constexpr (C::NQ == 2) {
+  if constexpr (NQ == 2) {
     __syncthreads();
     float* red = reinterpret_cast<float*>(smem) + wk * (2 * 32 * DP) + lane;
     if (wq == 1) {
@@ -414,7 +418,7 @@ __global__ __launch_bounds__((64 * NW * BwdCfg<T, DP>::NQ), (BwdCfg<T, DP>::OCC)
       for (int n = nb; n < ne; ++n) {
         const int i0 = qlo + (n % per) * BN;
         attn_row_dkv<T>(a, hk * a.group + n / per, tr, max(a.pl.key_lo[tr], i0),
-                        min(a.pl.key_hi[tr], i0 + BN), lane, xk, xv);
+                        min(a.pl.key_hi[tr], min(i0 + BN, qhi)), lane, xk, xv);
       }
       if (parts > 1) {
         st2(pk + tr * ldp, lane, a.D, xk);
@@ -470,17 +474,29 @@ template <typename T> int dkv_parts(const AttnArgs& a) {
                       (long)a.Tq / std::max(a.ndoc, 1) * a.group);
 }
 
-template <typename T, int DP, int MODE> hipError_t bwd(const AttnArgs& a, hipStream_t s) {
-  using C = BwdCfg<T, DP>;
-  hipError_t e = lds_opt_in((const void*)k_attn_dq<T, DP, MODE>, C::LDS_DQ);
-  if (e == hipSuccess) e = lds_opt_in((const void*)k_attn_dkv<T, DP, MODE>, C::LDS_DKV);
+// From 1024 workgroups on, two rounds of two a CU, the loops even out by
+// themselves and NQ = 1 is faster (forward and backward of 8192 tokens in 8
+// documents, 32 heads of 128 without groups: 513 against 552 us); below, NQ =
+// 2 (the same tokens in one document, 32 heads on 8: 2382 against 2620 us).
+bool one_query_wave(const AttnArgs& a) { return (long)attn_tiles(a.Tk) * a.Hkv >= 1024; }
+
+template <typename T, int DP, int MODE, int NQ> hipError_t dkv(const AttnArgs& a, int parts, hipStream_t s) {
+  constexpr int lds = DkvCfg<T, DP, NQ>::LDS;
+  const hipError_t e = lds_opt_in((const void*)k_attn_dkv<T, DP, MODE, NQ>, lds);
   if (e != hipSuccess) return e;
-  const int tq = attn_tiles(a.Tq), tk = attn_tiles(a.Tk);
+  k_attn_dkv<T, DP, MODE, NQ><<<dim3((unsigned)attn_tiles(a.Tk) * a.Hkv, parts), 64 * NW * NQ, lds, s>>>(a, parts);
+  return hipGetLastError();
+}
+
+template <typename T, int DP, int MODE> hipError_t bwd(const AttnArgs& a, hipStream_t s) {
+  constexpr int lds = DqCfg<T, DP>::LDS;
+  hipError_t e = lds_opt_in((const void*)k_attn_dq<T, DP, MODE>, lds);
+  if (e != hipSuccess) return e;
   const int pq = dq_parts<T>(a), pk = dkv_parts<T>(a);
   const int wq = a.Hq * a.D, wk = a.Hkv * a.D;
   const auto blocks = [](long n) { return (unsigned)((n / 8 + 255) / 256); };
-  if (tq) {
-    k_attn_dq<T, DP, MODE><<<dim3((unsigned)tq * a.Hq, pq), 64 * NW, C::LDS_DQ, s>>>(a, pq);
+  if (a.Tq) {
+    k_attn_dq<T, DP, MODE><<<dim3((unsigned)attn_tiles(a.Tq) * a.Hq, pq), 64 * NW, lds, s>>>(a, pq);
     e = hipGetLastError();
     if (e == hipSuccess && pq > 1) {
       const JoinArgs j = {{a.part}, {a.dq}, {a.lddq}, {a.scale}};
@@ -489,9 +505,10 @@ template <typename T, int DP, int MODE> hipError_t bwd(const AttnArgs& a, hipStr
     }
     if (e != hipSuccess) return e;
   }
-  if (tk) {
-    k_attn_dkv<T, DP, MODE><<<dim3((unsigned)tk * a.Hkv, pk), 64 * NW * C::NQ, C::LDS_DKV, s>>>(a, pk);
-    e = hipGetLastError();
+  if (a.Tk) {
+    // float32 rows of 128 need all the registers of a SIMD: four waves
+    if constexpr (sizeof(T) == 4 && DP == 128) e = dkv<T, DP, MODE, 1>(a, pk, s);
+    else e = one_query_wave(a) ? dkv<T, DP, MODE, 1>(a, pk, s) : dkv<T, DP, MODE, 2>(a, pk, s);
     if (e == hipSuccess && pk > 1) {
       const long n = (long)a.Tk * wk;
       const JoinArgs j = {{a.part, a.part + n}, {a.dk, a.dv}, {a.lddk, a.lddv}, {a.scale, 1.0f}};

@@ -45,7 +45,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void 
   int h, tile;
   work_of(blockIdx.x, a.Hq, h, tile);
   int q0, klo, khi;
-  tile_entry(a.pl.qtab, tile, BM, q0, klo, khi);
+  tile_entry(a.pl.qtab, tile, BM, a.Tq, a.Tk, q0, klo, khi);
   const int hk = h / a.group, part = blockIdx.y;
   const T* qp = (const T*)a.q + (long)h * a.D;
   const T* kp = (const T*)a.k + (long)hk * a.D;

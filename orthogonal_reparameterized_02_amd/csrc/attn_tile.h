@@ -368,12 +368,15 @@ __device__ __forceinline__ void work_of(int id, int heads, int& head, int& tile)
   }
 }
 
-// entry of a tile table (AttnPlan), in scalar registers
-__device__ __forceinline__ void tile_entry(const int4* tab, int tile, int bm, int& row0, int& lo, int& hi) {
+// Entry of a tile table (AttnPlan) in scalar registers: first row, and the
+// range of the other side's rows.  Clamped, so that a plan that was never
+// made gives wrong results and no access out of range.
+__device__ __forceinline__ void tile_entry(const int4* tab, int tile, int bm, int rows, int others,
+                                           int& row0, int& lo, int& hi) {
   const int4 e = tab[tile];
-  row0 = __builtin_amdgcn_readfirstlane(e.x) * bm;
-  lo = __builtin_amdgcn_readfirstlane(e.y);
-  hi = __builtin_amdgcn_readfirstlane(e.z);
+  row0 = min((unsigned)__builtin_amdgcn_readfirstlane(e.x), (unsigned)((rows - 1) / bm)) * bm;
+  lo = min(max(__builtin_amdgcn_readfirstlane(e.y), 0), others);
+  hi = min(max(__builtin_amdgcn_readfirstlane(e.z), 0), others);
 }
 
 // Where the tiles are too few to fill the card, a tile's loop is cut into
