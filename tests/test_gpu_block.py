@@ -326,16 +326,15 @@ def test_attention_rows_past_32_bits():
     Tk, ld = 70000, 65536
     wide = torch.empty(Tk, ld, dtype=torch.bfloat16, device="cuda")
     st = setup(dict(q=[50], k=[100], Hq=2, Hkv=1, D=64), "bf16")
-    want = run(st)
+    ref, _ = reference(st)
     k, v = wide[:, 64:128].view(Tk, 1, 64), wide[:, 256:320].view(Tk, 1, 64)
     k[-100:], v[-100:] = st["k"], st["v"]
     st["k"], st["v"], st["cu_k"] = k, v, st["cu_k"] + (Tk - 100)
     out = run(st)
-    for n in ("o", "dq", "lse"):
-        np.testing.assert_array_equal(bits(out[n]), bits(want[n]), err_msg=n)
     for n in ("dk", "dv"):
-        np.testing.assert_array_equal(bits(out[n][-100:]), bits(want[n]), err_msg=n)
         assert not out[n][:-100].any()
+        out[n] = out[n][-100:]
+    check(out, ref, "bf16")
 
 
 def test_plan_of_decreasing_offsets_stays_in_range():
