@@ -74,11 +74,11 @@ __global__ __launch_bounds__(64 * NW, (DqCfg<T, DP>::OCC)) void k_attn_dq(AttnAr
   constexpr int BN = C::BN, NS = BN / 32;
   extern __shared__ __align__(16) char smem[];
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  int h, tile;
-  work_of(blockIdx.x, a.Hq, h, tile);
+  int h, part, tile;
+  work_of(blockIdx.x, a.Hq, parts, h, part, tile);
   int q0, klo, khi;
   tile_entry(a.pl.qtab, tile, BM, a.Tq, a.Tk, q0, klo, khi);
-  const int hk = h / a.group, r0 = q0 + 32 * wave, part = blockIdx.y;
+  const int hk = h / a.group, r0 = q0 + 32 * wave;
   const T* qp = (const T*)a.q + (long)h * a.D;
   const T* kp = (const T*)a.k + (long)hk * a.D;
   const T* vp = (const T*)a.v + (long)hk * a.D;
@@ -225,11 +225,11 @@ __global__ __launch_bounds__(64 * NW * NQ, (DkvCfg<T, DP, NQ>::OCC)) void k_attn
   // diagonal, where the later keys have nothing to do, every SIMD then still
   // has a wave of the earlier ones.
   const int wk = wave / NQ, wq = wave % NQ;
-  int hk, tile;
-  work_of(blockIdx.x, a.Hkv, hk, tile);
+  int hk, part, tile;
+  work_of(blockIdx.x, a.Hkv, parts, hk, part, tile);
   int k0, qlo, qhi;
   tile_entry(a.pl.ktab, tile, BM, a.Tk, a.Tq, k0, qlo, qhi);
-  const int r0 = k0 + 32 * wk, part = blockIdx.y;
+  const int r0 = k0 + 32 * wk;
   const T* kp = (const T*)a.k + (long)hk * a.D;
   const T* vp = (const T*)a.v + (long)hk * a.D;
 
@@ -484,7 +484,7 @@ template <typename T, int DP, int MODE, int NQ> hipError_t dkv(const AttnArgs& a
   constexpr int lds = DkvCfg<T, DP, NQ>::LDS;
   const hipError_t e = lds_opt_in((const void*)k_attn_dkv<T, DP, MODE, NQ>, lds);
   if (e != hipSuccess) return e;
-  k_attn_dkv<T, DP, MODE, NQ><<<dim3((unsigned)attn_tiles(a.Tk) * a.Hkv, parts), 64 * NW * NQ, lds, s>>>(a, parts);
+  k_attn_dkv<T, DP, MODE, NQ><<<dim3((unsigned)attn_tiles(a.Tk) * a.Hkv * parts), 64 * NW * NQ, lds, s>>>(a, parts);
   return hipGetLastError();
 }
 
@@ -496,7 +496,7 @@ template <typename T, int DP, int MODE> hipError_t bwd(const AttnArgs& a, hipStr
   const int wq = a.Hq * a.D, wk = a.Hkv * a.D;
   const auto blocks = [](long n) { return (unsigned)((n / 8 + 255) / 256); };
   if (a.Tq) {
-    k_attn_dq<T, DP, MODE><<<dim3((unsigned)attn_tiles(a.Tq) * a.Hq, pq), 64 * NW, lds, s>>>(a, pq);
+    k_attn_dq<T, DP, MODE><<<dim3((unsigned)attn_tiles(a.Tq) * a.Hq * pq), 64 * NW, lds, s>>>(a, pq);
     e = hipGetLastError();
     if (e == hipSuccess && pq > 1) {
       const JoinArgs j = {{a.part}, {a.dq}, {a.lddq}, {a.scale}};

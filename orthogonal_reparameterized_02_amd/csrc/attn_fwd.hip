@@ -42,11 +42,11 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void 
   constexpr bool LATE = MODE == 1 && sizeof(T) == 2;
   extern __shared__ __align__(16) char smem[];
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  int h, tile;
-  work_of(blockIdx.x, a.Hq, h, tile);
+  int h, part, tile;
+  work_of(blockIdx.x, a.Hq, parts, h, part, tile);
   int q0, klo, khi;
   tile_entry(a.pl.qtab, tile, BM, a.Tq, a.Tk, q0, klo, khi);
-  const int hk = h / a.group, part = blockIdx.y;
+  const int hk = h / a.group;
   const T* qp = (const T*)a.q + (long)h * a.D;
   const T* kp = (const T*)a.k + (long)hk * a.D;
   const T* vp = (const T*)a.v + (long)hk * a.D;
@@ -225,28 +225,33 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void 
   store_rowsT<L::NT>((T*)a.o + tt * a.ldo + (long)h * a.D, o, none ? 0.0f : 1.0f / l, a.D, in, lane);
 }
 
-// joins the parts of one query row: a wave a row, in part order
+// joins the parts of the query rows, in part order: eight elements a thread
 template <typename T>
-__global__ __launch_bounds__(64 * NW) void k_attn_fwd_join(AttnArgs a, int parts) {
-  const int lane = threadIdx.x % 64, h = blockIdx.y;
-  const int t = blockIdx.x * NW + threadIdx.x / 64;
-  if (t >= a.Tq) return;
+__global__ __launch_bounds__(256) void k_attn_fwd_join(AttnArgs a, int parts) {
+  const int per = a.D / 8, r = threadIdx.x / per, e = (threadIdx.x - r * per) * 8;
+  const int h = blockIdx.y, t = blockIdx.x * (256 / per) + r;
+  if (r >= 256 / per || t >= a.Tq) return;
   const long row = (long)h * a.Tq + t, stride = (long)a.Hq * a.Tq;
-  const float* pm = a.part + parts * stride * a.D;
+  const float2* pm = reinterpret_cast<const float2*>(a.part + parts * stride * a.D) + row;
   float m = -INFINITY, l = 0.0f;
-  for (int s = 0; s < parts; ++s) m = fmaxf(m, pm[2 * (s * stride + row)]);
+  for (int s = 0; s < parts; ++s) m = fmaxf(m, pm[s * stride].x);
   const float ref = m == -INFINITY ? 0.0f : m;
-  float2 o = make_float2(0.0f, 0.0f);
+  float o[8] = {};
   for (int s = 0; s < parts; ++s) {
-    const float f = exp2_hw(pm[2 * (s * stride + row)] - ref);
-    const float2 v = ld2(a.part + (s * stride + row) * a.D, lane, a.D);
-    l = fmaf(f, pm[2 * (s * stride + row) + 1], l);
-    o.x = fmaf(f, v.x, o.x);
-    o.y = fmaf(f, v.y, o.y);
+    const float2 ml = pm[s * stride];
+    const float f = exp2_hw(ml.x - ref);
+    const float4* p = reinterpret_cast<const float4*>(a.part + (s * stride + row) * a.D + e);
+    const float4 x = p[0], y = p[1];
+    l = fmaf(f, ml.y, l);
+    const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = fmaf(f, v[i], o[i]);
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  st2((T*)a.o + (long)t * a.ldo + (long)h * a.D, lane, a.D, make_float2(o.x * inv, o.y * inv));
-  if (lane == 0) a.lse[row] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * LN2;
+  T* out = (T*)a.o + (long)t * a.ldo + (long)h * a.D + e;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) St<T>::st(out + i, o[i] * inv);
+  if (e == 0) a.lse[row] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * LN2;
 }
 
 // a document's keys stand for the length of the loop
@@ -259,10 +264,11 @@ template <typename T, int DP, int MODE> hipError_t fwd(const AttnArgs& a, hipStr
   const hipError_t e = lds_opt_in((const void*)k_attn_fwd<T, DP, MODE>, lds);
   if (e != hipSuccess) return e;
   const int tiles = attn_tiles(a.Tq), parts = fwd_parts<T>(a);
-  k_attn_fwd<T, DP, MODE><<<dim3((unsigned)tiles * a.Hq, parts), 64 * NW, lds, s>>>(a, parts);
+  k_attn_fwd<T, DP, MODE><<<dim3((unsigned)tiles * a.Hq * parts), 64 * NW, lds, s>>>(a, parts);
   const hipError_t e2 = hipGetLastError();
   if (e2 != hipSuccess || parts == 1) return e2;
-  k_attn_fwd_join<T><<<dim3((a.Tq + NW - 1) / NW, a.Hq), 64 * NW, 0, s>>>(a, parts);
+  const int rows = 256 / (a.D / 8);
+  k_attn_fwd_join<T><<<dim3((a.Tq + rows - 1) / rows, a.Hq), 256, 0, s>>>(a, parts);
   return hipGetLastError();
 }
 

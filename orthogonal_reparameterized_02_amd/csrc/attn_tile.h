@@ -357,15 +357,20 @@ __device__ __forceinline__ Span span_of(int lo, int hi) {
 // long ones and the last round waits for the latter.
 // Consecutive workgroups are dealt round-robin over the 8 XCDs; a head stays
 // on one XCD, beside the heads that share its keys, where 8 divides the heads.
-__device__ __forceinline__ void work_of(int id, int heads, int& head, int& tile) {
-  if (heads % 8 == 0) {
-    const int per = heads / 8, y = id / 8;
-    head = (id % 8) * per + y % per;
+// The parts of a tile's loop (part_of) count as heads of their own here.
+__device__ __forceinline__ void work_of(int id, int heads, int parts, int& head, int& part, int& tile) {
+  const int n = heads * parts;
+  int v;
+  if (n % 8 == 0) {
+    const int per = n / 8, y = id / 8;
+    v = (id % 8) * per + y % per;
     tile = y / per;
   } else {
-    head = id % heads;
-    tile = id / heads;
+    v = id % n;
+    tile = id / n;
   }
+  head = v / parts;
+  part = v - head * parts;
 }
 
 // Entry of a tile table (AttnPlan) in scalar registers: first row, and the
