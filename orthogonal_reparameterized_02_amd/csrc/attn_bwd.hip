@@ -478,7 +478,9 @@ template <typename T> int dkv_parts(const AttnArgs& a) {
 // themselves and NQ = 1 is faster (forward and backward of 8192 tokens in 8
 // documents, 32 heads of 128 without groups: 513 against 552 us); below, NQ =
 // 2 (the same tokens in one document, 32 heads on 8: 2382 against 2620 us).
-bool one_query_wave(const AttnArgs& a) { return (long)attn_tiles(a.Tk) * a.Hkv >= 1024; }
+// Parts count as workgroups: float32, two documents of 1024, 16 heads of 64
+// in 16 parts: 302 against 330 us.
+bool one_query_wave(const AttnArgs& a, int parts) { return (long)attn_tiles(a.Tk) * a.Hkv * parts >= 1024; }
 
 template <typename T, int DP, int MODE, int NQ> hipError_t dkv(const AttnArgs& a, int parts, hipStream_t s) {
   constexpr int lds = DkvCfg<T, DP, NQ>::LDS;
@@ -508,7 +510,7 @@ template <typename T, int DP, int MODE> hipError_t bwd(const AttnArgs& a, hipStr
   if (a.Tk) {
     // float32 rows of 128 need all the registers of a SIMD: four waves
     if constexpr (sizeof(T) == 4 && DP == 128) e = dkv<T, DP, MODE, 1>(a, pk, s);
-    else e = one_query_wave(a) ? dkv<T, DP, MODE, 1>(a, pk, s) : dkv<T, DP, MODE, 2>(a, pk, s);
+    else e = one_query_wave(a, pk) ? dkv<T, DP, MODE, 1>(a, pk, s) : dkv<T, DP, MODE, 2>(a, pk, s);
     if (e == hipSuccess && pk > 1) {
       const long n = (long)a.Tk * wk;
       const JoinArgs j = {{a.part, a.part + n}, {a.dk, a.dv}, {a.lddk, a.lddv}, {a.scale, 1.0f}};
