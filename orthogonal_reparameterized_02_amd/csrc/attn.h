@@ -27,21 +27,31 @@ hipError_t launch_dropout(long n, const TS* x, const TS* res, TS* out, uint32_t 
                           uint64_t offset, const uint64_t* offset_dev, hipStream_t s);
 
 // ---- attention (attn_*.hip) -------------------------------------------------
+constexpr int ATTN_BM = 128;  // query (key) rows of a tile
+
+// About the rows that a tile's loop goes through: a document and what a tile
+// spans beside it.
+inline long loop_rows(int T, int ndoc) {
+  const long r = T / (ndoc > 1 ? ndoc : 1) + ATTN_BM;
+  return r < T ? r : T;
+}
+
 // Parts that a loop over about `rows` rows is cut into where `groups`
 // workgroups run it; 16 at most.  bf16: up to one workgroup a CU, or two
-// where a part still has 1024 rows; cutting shorter loops costs more in
+// where a part still has 768 rows; cutting shorter loops costs more in
 // partial sums than it evens out (1024 causal tokens, 32 heads on 8: one
 // training pass 127 us with two a CU, 103 with one).  float32 products take
 // eight times as long, so the traffic counts less and a loop that ends last
 // is waited for longer: up to four a CU (two documents of 1024, 16 heads of
-// 64: 496 us with two, 414 with four, 430 with eight).
+// 64: 330 us with four, 354 with eight), in parts of 64 rows at least (765
+// tokens in 9 documents, 5 heads on 1: 173 us with 256 rows, 70 with 64).
 template <typename T> int parts_for(long groups, long rows) {
   if (groups < 1) return 1;
   const auto cut = [&](long fill, long least) {
     const long want = fill / groups, most = rows / least;
     return want < most ? want : most;
   };
-  const long a = cut(sizeof(T) == 2 ? 256 : 1024, 256), b = sizeof(T) == 2 ? cut(512, 1024) : 1;
+  const long a = sizeof(T) == 2 ? cut(256, 256) : cut(1024, 64), b = sizeof(T) == 2 ? cut(512, 768) : 1;
   const long n = a > b ? a : b;
   return n < 1 ? 1 : n > 16 ? 16 : (int)n;
 }
@@ -58,7 +68,6 @@ struct AttnPlan {
   int4 *qtab, *ktab;
   int4 *qraw, *kraw;               // the same before sorting
 };
-constexpr int ATTN_BM = 128;
 inline int attn_tiles(int rows) { return (rows + ATTN_BM - 1) / ATTN_BM; }
 
 struct AttnArgs {

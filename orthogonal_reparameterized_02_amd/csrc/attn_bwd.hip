@@ -466,12 +466,12 @@ __global__ __launch_bounds__(256) void k_attn_sum_parts(JoinArgs j, int parts, l
 }
 
 template <typename T> int dq_parts(const AttnArgs& a) {
-  return parts_for<T>((long)attn_tiles(a.Tq) * a.Hq, a.Tk / std::max(a.ndoc, 1));
+  return parts_for<T>((long)attn_tiles(a.Tq) * a.Hq, loop_rows(a.Tk, a.ndoc));
 }
 template <typename T> int dkv_parts(const AttnArgs& a) {
   // a bf16 workgroup has eight waves: it counts twice
   return parts_for<T>((long)attn_tiles(a.Tk) * a.Hkv * (sizeof(T) == 2 ? 2 : 1),
-                      (long)a.Tq / std::max(a.ndoc, 1) * a.group);
+                      loop_rows(a.Tq, a.ndoc) * a.group);
 }
 
 // From 1024 workgroups on, two rounds of two a CU, the loops even out by

@@ -256,7 +256,7 @@ __global__ __launch_bounds__(256) void k_attn_fwd_join(AttnArgs a, int parts) {
 
 // a document's keys stand for the length of the loop
 template <typename T> int fwd_parts(const AttnArgs& a) {
-  return parts_for<T>((long)attn_tiles(a.Tq) * a.Hq, a.Tk / std::max(a.ndoc, 1));
+  return parts_for<T>((long)attn_tiles(a.Tq) * a.Hq, loop_rows(a.Tk, a.ndoc));
 }
 
 template <typename T, int DP, int MODE> hipError_t fwd(const AttnArgs& a, hipStream_t s) {
