@@ -22,12 +22,15 @@ constexpr int BN = 32;         // keys a tile
 constexpr int GRAIN = NW * BN; // a piece is a multiple of this
 constexpr int MAX_PIECES = 64;
 
-// pieces a sequence is cut into at most
+// Pieces that a sequence is cut into at most: 2048 workgroups, so that unequal
+// lengths even out over the 512 resident ones, in pieces of 512 rows at least
+// (a piece's start and join cost as much as a hundred rows: 8 sequences of up
+// to 4096 rows 33.3 us in pieces of 128, 27.3 in 512); but one workgroup a CU
+// from 128 rows on, where latency counts.
 int pieces_of(const DecodeArgs& a) {
   const int per = a.B * a.Hkv * ((a.group + 31) / 32);
-  // enough workgroups that unequal lengths even out over 512 resident ones
-  const int want = (4096 + per - 1) / per;
-  return std::max(1, std::min({want, MAX_PIECES, (a.rows + GRAIN - 1) / GRAIN}));
+  const auto cut = [&](int fill, int least) { return std::min((fill + per - 1) / per, (a.rows + least - 1) / least); };
+  return std::max(1, std::min(std::max(cut(2048, 512), cut(256, GRAIN)), MAX_PIECES));
 }
 
 // the sequence's range and the piece length in effect
