@@ -7,7 +7,16 @@
 //   p = exp2(s2 - lse2),  ds = p (dp - delta) (1 - t^2),
 //   dq = scale ds k,  dk = scale ds^T q,  dv = p^T dout
 // -delta is the initial value of the dp accumulators; scale multiplies the
-// finished sums.
+// finished sums.  In bf16, p and ds are rounded to bf16 as matrix operands
+// (float32 operands would take eight times as long), and delta comes from the
+// stored, rounded o: of a relative error of 2.6e-3 in dq and dk, the rounding
+// of the result itself makes 1.7e-3, that of ds as much again, delta 1.1e-3.
+//
+// Measured (bf16, D 128, 32 heads on 8): 8192 causal tokens in one document
+// 1.75 ms for both passes, dq at 1.19 and dk, dv at 1.06 PFLOP/s of the products
+// they form, at the power limit; in 9 documents 315 us, a fifth of the wave
+// slots empty as in the forward pass.  float32, D 64, two documents of 1024,
+// 16 heads on 4, capped: 225 us, a third of the float32 matrix rate.
 #include <algorithm>
 
 #include "attn_rows.h"

@@ -8,6 +8,14 @@
 // is 16 or 32 register operations and one exchange with the lane that holds
 // the other keys, and the probabilities are the next product's operand
 // without leaving their lane.
+//
+// Measured (bf16, D 128): 8192 causal tokens in one document, 32 heads on 8,
+// 515 us = 1.07 PFLOP/s, where the library's 8192^3 product reaches 1.30: the
+// matrix pipes are busy 0.56 of the cycles at a clock that the power limit
+// holds at 1.5 GHz.  In 9 documents 95 us = 0.75 PFLOP/s: a fifth of the wave
+// slots stands empty at the starts and ends of the short loops.  Capped, 2048
+// queries on 16384 keys, 620 us = 0.83 PFLOP/s: bound by vector instructions,
+// three transcendentals a score (16 issue cycles each) beside four others.
 #include <algorithm>
 
 #include "attn_rows.h"
