@@ -157,6 +157,8 @@ CASES = [  # q lengths, k lengths, rows before and after the documents, Hq, Hkv,
     dict(q=[64, 3], k=[1500, 1100], Hq=2, Hkv=1, D=64),
     dict(q=[33], k=[2049], pad=(1, 2), Hq=4, Hkv=1, D=128, cap=6.0, bias=True),
     dict(q=[700], k=[40], Hq=8, Hkv=1, D=128, causal=False),
+    # enough tiles to be sorted by cost
+    dict(q=[900, 5, 1300], k=[900, 5, 1300], Hq=1, Hkv=1, D=64),
 ]
 
 
@@ -221,6 +223,28 @@ def test_attention(i, dt):
     again = run(st)
     for n in out:
         np.testing.assert_array_equal(bits(out[n]), bits(again[n]))
+
+
+@pytest.mark.parametrize("dt,D,cap,bias", [("bf16", 128, 0.0, False), ("bf16", 72, 8.0, True), ("f32", 64, 0.0, False)])
+def test_attention_many_heads(dt, D, cap, bias):
+    """Over 1024 workgroups of dk and dv: a few of the heads against the oracle."""
+    st = setup(dict(q=[100, 33], k=[100, 33], Hq=520, Hkv=520, D=D, cap=cap), dt)
+    st["slopes"] = np.linspace(0.5, 0.01, 520).astype(np.float32) if bias else None
+    out = run(st)
+    heads = [0, 7, 263, 519]
+    part = {**st, **{n: st[n][:, heads].contiguous() for n in ("q", "k", "v", "dout")},
+            "slopes": st["slopes"][heads] if bias else None}
+    ref, _ = reference(part)
+    check({n: (t[heads] if n == "lse" else t[:, heads]) for n, t in out.items()}, ref, dt)
+
+
+def test_attention_many_documents():
+    """More documents than are searched in LDS, most of them a token or none."""
+    lens = [int(x) for x in np.random.default_rng(0).integers(0, 3, 1500)]
+    st = setup(dict(q=lens, k=lens, pad=(2, 5), Hq=2, Hkv=1, D=64), "bf16")
+    out = run(st)
+    ref, _ = reference(st)
+    check(out, ref, "bf16")
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
