@@ -29,11 +29,11 @@ hipError_t launch_dropout(long n, const TS* x, const TS* res, TS* out, uint32_t 
 // ---- attention (attn_*.hip) -------------------------------------------------
 constexpr int ATTN_BM = 128;  // query (key) rows of a tile
 
-// About the rows that a tile's loop goes through: a document and what a tile
-// spans beside it.
-inline long loop_rows(int T, int ndoc) {
-  const long r = T / (ndoc > 1 ? ndoc : 1) + ATTN_BM;
-  return r < T ? r : T;
+// About the rows of the other side that a tile's loop goes through: a
+// document's, and those of the documents that a tile spans.
+inline long loop_rows(int others, int own, int ndoc) {
+  const long r = others / (ndoc > 1 ? ndoc : 1) + (long)ATTN_BM * others / (own > 1 ? own : 1);
+  return r < others ? r : others;
 }
 
 // Parts that a loop over about `rows` rows is cut into where `groups`
@@ -43,15 +43,16 @@ inline long loop_rows(int T, int ndoc) {
 // training pass 127 us with two a CU, 103 with one).  float32 products take
 // eight times as long, so the traffic counts less and a loop that ends last
 // is waited for longer: up to four a CU (two documents of 1024, 16 heads of
-// 64: 330 us with four, 354 with eight), in parts of 64 rows at least (765
-// tokens in 9 documents, 5 heads on 1: 173 us with 256 rows, 70 with 64).
-template <typename T> int parts_for(long groups, long rows) {
+// 64: 330 us with four, 354 with eight), in parts of `least` rows, a
+// tile of their kernels (765 tokens in 9 documents, 5 heads on 1: 173 us in
+// parts of 256 rows, 70 of 64).
+template <typename T> int parts_for(long groups, long rows, int least) {
   if (groups < 1) return 1;
-  const auto cut = [&](long fill, long least) {
-    const long want = fill / groups, most = rows / least;
+  const auto cut = [&](long fill, long rows_a_part) {
+    const long want = fill / groups, most = rows / rows_a_part;
     return want < most ? want : most;
   };
-  const long a = sizeof(T) == 2 ? cut(256, 256) : cut(1024, 64), b = sizeof(T) == 2 ? cut(512, 768) : 1;
+  const long a = sizeof(T) == 2 ? cut(256, 256) : cut(1024, least), b = sizeof(T) == 2 ? cut(512, 768) : 1;
   const long n = a > b ? a : b;
   return n < 1 ? 1 : n > 16 ? 16 : (int)n;
 }

@@ -475,12 +475,12 @@ __global__ __launch_bounds__(256) void k_attn_sum_parts(JoinArgs j, int parts, l
 }
 
 template <typename T> int dq_parts(const AttnArgs& a) {
-  return parts_for<T>((long)attn_tiles(a.Tq) * a.Hq, loop_rows(a.Tk, a.ndoc));
+  return parts_for<T>((long)attn_tiles(a.Tq) * a.Hq, loop_rows(a.Tk, a.Tq, a.ndoc), 64);
 }
 template <typename T> int dkv_parts(const AttnArgs& a) {
   // a bf16 workgroup has eight waves: it counts twice
   return parts_for<T>((long)attn_tiles(a.Tk) * a.Hkv * (sizeof(T) == 2 ? 2 : 1),
-                      loop_rows(a.Tq, a.ndoc) * a.group);
+                      loop_rows(a.Tq, a.Tk, a.ndoc) * a.group, a.D > 64 ? 32 : 64);
 }
 
 // From 1024 workgroups on, two rounds of two a CU, the loops even out by

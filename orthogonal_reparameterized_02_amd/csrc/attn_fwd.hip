@@ -41,7 +41,7 @@ template <typename T, int DP> struct FwdCfg {
 };
 
 template <typename T, int DP, int MODE>
-__global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void k_attn_fwd(AttnArgs a, int parts) {
+__global__ __launch_bounds__(64 * NW, 2) void k_attn_fwd(AttnArgs a, int parts) {
   using L = Tile<T, DP>;
   using C = FwdCfg<T, DP>;
   constexpr int BN = C::BN, NS = BN / 32;
@@ -262,9 +262,8 @@ __global__ __launch_bounds__(256) void k_attn_fwd_join(AttnArgs a, int parts) {
   if (e == 0) a.lse[row] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * LN2;
 }
 
-// a document's keys stand for the length of the loop
 template <typename T> int fwd_parts(const AttnArgs& a) {
-  return parts_for<T>((long)attn_tiles(a.Tq) * a.Hq, loop_rows(a.Tk, a.ndoc));
+  return parts_for<T>((long)attn_tiles(a.Tq) * a.Hq, loop_rows(a.Tk, a.Tq, a.ndoc), 64);
 }
 
 template <typename T, int DP, int MODE> hipError_t fwd(const AttnArgs& a, hipStream_t s) {
