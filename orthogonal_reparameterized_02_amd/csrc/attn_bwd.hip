@@ -158,7 +158,7 @@ __global__ __launch_bounds__(64 * NW, (DqCfg<T, DP>::OCC)) void k_attn_dq(AttnAr
 #pragma unroll
       for (int i = 0; i < 16; ++i) dp[i] = -delta;
       {
-        Pipe<2 * L::KS, 8> pp;
+        Pipe<2 * L::KS, 4> pp;
         const auto ld = [&](int i) {
           return L::row_frag(smem, i < L::KS ? kr : vr, 32 * n, i % L::KS);
         };

@@ -108,13 +108,13 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_fwd(AttnArgs a, int parts) 
 #pragma unroll
     for (int n = 0; n < NS; ++n) s[n] = (f32x16_t){};
     {
-      Pipe<NS * L::KS, 8> kp_;
+      Pipe<NS * L::KS, 4> kp_;
       const auto ld = [&](int i) { return L::row_frag(smem, kr, 32 * (i / L::KS), i % L::KS); };
       kp_.start(ld);
       kp_.run(ld, [&](int i, uint4 f) { s[i / L::KS] = mma16((const T*)nullptr, f, qf[i % L::KS], s[i / L::KS]); });
     }
     // the first value fragments travel while the softmax is formed
-    Pipe<NS * L::CSTEP * L::NT, 8> vp_;
+    Pipe<NS * L::CSTEP * L::NT, 4> vp_;
     const auto ldv = [&](int i) {
       return L::col_frag(smem, vc, 32 * (i / (L::CSTEP * L::NT)), i / L::NT % L::CSTEP, i % L::NT);
     };
