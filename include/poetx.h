@@ -386,8 +386,9 @@ size_t poetx_saved_bytes(const poetx_shape* sh);
  * of type `act`; rows may have a pitch: a tensor of T rows of H heads of D
  * values has head h of row t at t * ld + h * D, so q, k and v may be column
  * ranges of one projection's output.  Pitches count elements, are at least
- * H * D, at most 2^20 and multiples of 8 (16 bytes for bf16, 32 for float32); the rows of
- * an output must not overlap each other or an input, except where stated.
+ * H * D, at most 2^20 and multiples of 8 (16 bytes for bf16, 32 for
+ * float32); the rows of an output must not overlap each other or an input,
+ * except where stated.
  */
 
 /*
@@ -449,7 +450,8 @@ int32_t poetx_dropout_bwd(int64_t n, int32_t act, const void* dy, void* dx, doub
  *   p = exp(s - lse),  lse = log sum_j exp(s),  o = sum_j p v_j
  * over the keys seen.  A query that sees none has o = 0, lse = -inf and
  * takes no part in any gradient.  Keys and values that a query does not see
- * have no influence on it, whatever they hold (NaN included).
+ * have no influence on it, whatever they hold (NaN included); rows whose
+ * result is not finite are formed once more, one at a time, which is slow.
  * Backward: delta = do.o;  dl = p (do.v - delta);  ds = dl (1 - tanh^2) scale;
  *   dq = sum ds k;  dk, dv sum over the query heads that share a key head.
  * slopes are constants (no gradient).  The bf16 path rounds p and ds to bf16
