@@ -112,7 +112,6 @@ __global__ __launch_bounds__(64 * NW, (DqCfg<T, DP>::OCC)) void k_attn_dq(AttnAr
   const int tc = min(t, a.Tq - 1);
   const int rlo = a.pl.row_lo[tc], rhi = a.pl.row_hi[tc], rpos = MODE & 2 ? a.pl.row_pos[tc] : 0;
   const int lo = in ? rlo : 0, hi = in ? rhi : 0;
-  const float pos = (float)rpos;
   const Span sp = span_of(lo, hi);
 
   uint4 qf[L::KS], dof[L::KS];
@@ -172,7 +171,7 @@ __global__ __launch_bounds__(64 * NW, (DqCfg<T, DP>::OCC)) void k_attn_dq(AttnAr
       const auto ldc = [&](int i) { return L::col_frag(smem, kc, 32 * n, i / L::NT, i % L::NT); };
       cp.start(ldc);
       const int jl = jn + 4 * (lane >> 5);  // key of register 0
-      const float d0 = pos - (float)jl;
+      const float d0 = (float)(rpos - jl);  // exact: rows past 2^24 are no float32 numbers
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         float deriv;

@@ -78,7 +78,6 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_fwd(AttnArgs a, int parts) 
   const int tc = min(t, a.Tq - 1);
   const int rlo = a.pl.row_lo[tc], rhi = a.pl.row_hi[tc], rpos = MODE & 2 ? a.pl.row_pos[tc] : 0;
   const int lo = in ? rlo : 0, hi = in ? rhi : 0;
-  const float pos = (float)rpos;
   const Span sp = span_of(lo, hi);
 
   uint4 qf[L::KS];
@@ -122,7 +121,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_fwd(AttnArgs a, int parts) 
     const int jl = j0 + 4 * (lane >> 5);  // key of register 0
     float top = -INFINITY;
     if constexpr (MODE != 0 && !LATE) {
-      const float d0 = pos - (float)jl;
+      const float d0 = (float)(rpos - jl);  // exact: rows past 2^24 are no float32 numbers
       float unused;
 #pragma unroll
       for (int n = 0; n < NS; ++n)
