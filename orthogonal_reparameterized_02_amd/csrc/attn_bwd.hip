@@ -530,8 +530,7 @@ template <typename T, int DP, int MODE> hipError_t bwd(const AttnArgs& a, hipStr
 }
 
 template <typename T, int DP> hipError_t bwd_mode(const AttnArgs& a, hipStream_t s) {
-  if (a.slopes) return a.cap > 0.0f ? bwd<T, DP, 3>(a, s) : bwd<T, DP, 2>(a, s);
-  return a.cap > 0.0f ? bwd<T, DP, 1>(a, s) : bwd<T, DP, 0>(a, s);
+  return by_mode<T>(a.slopes, a.cap, [&](auto mode) { return bwd<T, DP, decltype(mode)::value>(a, s); });
 }
 
 }  // namespace

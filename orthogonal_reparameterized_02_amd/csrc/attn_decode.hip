@@ -235,8 +235,7 @@ template <typename T, int DP, int MODE> hipError_t decode(const DecodeArgs& a, f
 }
 
 template <typename T, int DP> hipError_t decode_mode(const DecodeArgs& a, float* ws, hipStream_t s) {
-  if (a.slopes) return a.cap > 0.0f ? decode<T, DP, 3>(a, ws, s) : decode<T, DP, 2>(a, ws, s);
-  return a.cap > 0.0f ? decode<T, DP, 1>(a, ws, s) : decode<T, DP, 0>(a, ws, s);
+  return by_mode<T>(a.slopes, a.cap, [&](auto mode) { return decode<T, DP, decltype(mode)::value>(a, ws, s); });
 }
 
 }  // namespace

@@ -45,9 +45,9 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_fwd(AttnArgs a, int parts) 
   using L = Tile<T, DP>;
   using C = FwdCfg<T, DP>;
   constexpr int BN = C::BN, NS = BN / 32;
-  // capped bf16 scores: the maximum is taken of the products (the cap is
-  // monotone), a probability is exp2(fma(-2 cap, r, cap - reference))
-  constexpr bool LATE = MODE == 1 && sizeof(T) == 2;
+  // scores capped by r, no bias: the maximum is taken of the products (the cap
+  // is monotone), a probability is exp2(fma(-2 cap, r, cap - reference))
+  constexpr bool LATE = cap_by_r<T, MODE> && !(MODE & 2);
   extern __shared__ __align__(16) char smem[];
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   int h, part, tile;
@@ -279,8 +279,7 @@ template <typename T, int DP, int MODE> hipError_t fwd(const AttnArgs& a, hipStr
 }
 
 template <typename T, int DP> hipError_t fwd_mode(const AttnArgs& a, hipStream_t s) {
-  if (a.slopes) return a.cap > 0.0f ? fwd<T, DP, 3>(a, s) : fwd<T, DP, 2>(a, s);
-  return a.cap > 0.0f ? fwd<T, DP, 1>(a, s) : fwd<T, DP, 0>(a, s);
+  return by_mode<T>(a.slopes, a.cap, [&](auto mode) { return fwd<T, DP, decltype(mode)::value>(a, s); });
 }
 
 }  // namespace

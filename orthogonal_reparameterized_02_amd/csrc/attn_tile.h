@@ -15,6 +15,8 @@
 // (rows of V, K, Q or dO read down their columns) takes the same K order.
 #pragma once
 
+#include <type_traits>
+
 #include "attn.h"
 
 namespace poetx {
@@ -268,14 +270,28 @@ template <int N, int DEPTH> struct Pipe {
 };
 
 // ---- scores ----------------------------------------------------------------------
-// MODE bit 0: capped by a tanh; bit 1: distance bias.  Scores are in units of
-// log2: s2 = log2(e) * score.  With
+// MODE bit 0: capped by a tanh; bit 1: distance bias; bit 2 (with bit 0): the
+// tanh of bf16 scores formed as for float32.  Scores are in units of log2:
+// s2 = log2(e) * score.  With
 //   r = 1 / (1 + e^(2 x / cap)):  cap tanh(x / cap) = cap - 2 cap r,
 //   1 - tanh^2 = 4 (r - r^2),
-// bf16 takes the cap from one exponential and one reciprocal; its absolute
-// error, cap units in 2^-23, is small next to bf16 operands.  float32 takes
-// tanh itself: near 0, where the difference would cancel, an odd polynomial
-// (least squares on [0, 0.65], relative error 8e-8).
+// bf16 takes caps up to CAP_R_MAX from one exponential and one reciprocal.
+// The difference cancels where x is small: its absolute error is about cap
+// 2^-23 (lse off by 1e-4 at a cap of 1024; at 1e6 o is off by 3%, at 1e8
+// nothing is left of the scores), up to a cap of 128 below 2^-16, that of a
+// float32 lse of a hundred.  Wider caps, and float32, take tanh itself: near
+// 0 an odd polynomial (least squares on [0, 0.65], relative error 8e-8).
+constexpr float CAP_R_MAX = 128.0f;
+template <typename T, int MODE> constexpr bool cap_by_r = (MODE & 1) && !(MODE & 4) && sizeof(T) == 2;
+
+// launches f with the MODE of these scores as a constant
+template <typename T, class F> auto by_mode(const float* slopes, float cap, F f) {
+  if constexpr (sizeof(T) == 2)
+    if (cap > CAP_R_MAX) return slopes ? f(std::integral_constant<int, 7>{}) : f(std::integral_constant<int, 5>{});
+  if (slopes) return cap > 0.0f ? f(std::integral_constant<int, 3>{}) : f(std::integral_constant<int, 2>{});
+  return cap > 0.0f ? f(std::integral_constant<int, 1>{}) : f(std::integral_constant<int, 0>{});
+}
+
 __device__ __forceinline__ float tanh_f32(float x) {
   const float big = 1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + exp2_hw(x * (2.0f * LOG2E)));
   const float u = x * x;
@@ -288,7 +304,7 @@ __device__ __forceinline__ float tanh_f32(float x) {
 }
 
 struct ScoreArgs {
-  float c;      // of q.k: scale log2e; capped: scale / cap, bf16: 2 log2e scale / cap
+  float c;      // of q.k: scale log2e; capped: scale / cap, by r: 2 log2e scale / cap
   float capl;   // cap log2e
   float slope;  // slope log2e
 };
@@ -296,7 +312,7 @@ struct ScoreArgs {
 template <typename T, int MODE>
 __device__ __forceinline__ ScoreArgs score_args(float scale, float cap, float slope) {
   ScoreArgs s;
-  s.c = !(MODE & 1) ? scale * LOG2E : sizeof(T) == 2 ? scale / cap * (2.0f * LOG2E) : scale / cap;
+  s.c = !(MODE & 1) ? scale * LOG2E : cap_by_r<T, MODE> ? scale / cap * (2.0f * LOG2E) : scale / cap;
   s.capl = cap * LOG2E;
   s.slope = slope * LOG2E;
   return s;
@@ -311,7 +327,7 @@ __device__ __forceinline__ float cap_r(float qk, const ScoreArgs& s) {
 
 // What the gradient of a capped score holds beside the derivative that
 // score2 returns: 4 of 4 (r - r^2)
-template <typename T, int MODE> constexpr float cap_factor = (MODE & 1) && sizeof(T) == 2 ? 4.0f : 1.0f;
+template <typename T, int MODE> constexpr float cap_factor = cap_by_r<T, MODE> ? 4.0f : 1.0f;
 
 // s2 of q.k; deriv: its derivative by scale * q.k, less cap_factor (1 without
 // a cap); dist: query position - key
@@ -320,7 +336,7 @@ __device__ __forceinline__ float score2(float qk, const ScoreArgs& s, float dist
   float x;
   if constexpr (!(MODE & 1)) {
     x = qk * s.c;
-  } else if constexpr (sizeof(T) == 2) {
+  } else if constexpr (cap_by_r<T, MODE>) {
     const float r = cap_r(qk, s);
     x = fmaf(-2.0f * s.capl, r, s.capl);
     deriv = fmaf(-r, r, r);

@@ -1,10 +1,13 @@
 """GPU parity of the attention-block operators at the ends of their ranges,
 against the float64 oracle; tolerances as in test_gpu_block.py."""
+import numpy as np
 import pytest
 import torch
 
+from gpu_util import to_dev, to_f64
 from orthogonal_reparameterized_02_amd import poetx as P
-from test_gpu_block import DT, check, reference, run, setup
+from oracle import block_oracle as B
+from test_gpu_block import DT, check, close, normal, reference, run, setup
 
 pytestmark = pytest.mark.gpu
 
@@ -14,6 +17,16 @@ def _gpu():
     if not torch.cuda.is_available():
         pytest.skip("no GPU")
     P.lib()
+
+
+def decode(q, k, v, lens, cap=0.0, slopes=None):
+    sh = P.decode_shape(q, k, v, cap=cap)
+    ws = torch.empty(P.poetx_attn_decode_workspace_bytes(sh), dtype=torch.uint8, device="cuda")
+    o = torch.full_like(q, 7.0)
+    P.poetx_attn_decode(sh, q, k, v, to_dev(np.asarray(lens, np.int32)), o, ws,
+                        slopes=None if slopes is None else to_dev(slopes))
+    torch.cuda.synchronize()
+    return o
 
 
 # ---- distances -----------------------------------------------------------------------
@@ -50,3 +63,25 @@ def test_bias_of_query_rows_past_2_24(dt):
     assert torch.isneginf(out["lse"][:, :first]).all()
     out["lse"] = out["lse"][:, first:]
     check(out, ref, dt)
+
+
+# ---- caps ------------------------------------------------------------------------------
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("cap", [128.0, 129.0, 300.0, 1024.0, 1025.0, 1e4, 1e6, 1e8, 1e38])
+@pytest.mark.parametrize("c", [dict(q=[70, 60], k=[70, 60], Hq=4, Hkv=1, D=64), dict(q=[129], k=[200], Hq=2, Hkv=1, D=128, bias=True),
+                               dict(q=[33], k=[2049], pad=(1, 2), Hq=4, Hkv=1, D=104)])
+def test_attention_wide_caps(dt, cap, c):
+    """A cap far above the scores changes next to nothing."""
+    st = setup({**c, "cap": cap}, dt)
+    check(run(st), reference(st)[0], dt)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("cap", [128.0, 129.0, 300.0, 1e4, 1e6, 1e8])
+@pytest.mark.parametrize("bias", [False, True])
+def test_decode_wide_caps(dt, cap, bias):
+    rng = np.random.default_rng(int(np.log10(cap)))
+    q, k, v = normal(rng, (2, 8, 128), dt, 1.5), normal(rng, (2, 700, 2, 128), dt), normal(rng, (2, 700, 2, 128), dt)
+    slopes = (2.0 ** -np.arange(1, 9)).astype(np.float32) if bias else None
+    o = decode(q, k, v, [700, 33], cap, slopes)
+    close("o", o, B.decode(to_f64(q), to_f64(k), to_f64(v), None, [700, 33], None, cap, slopes), dt)
