@@ -144,7 +144,9 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_fwd(AttnArgs a, int parts) 
       for (int i = 0; i < 16; ++i) top = fmaxf(top, s[n][i]);
     top = fmaxf(top, other_half(top));
     if constexpr (MODE == 0) top *= sa.c;
-    if constexpr (LATE) top = top == -INFINITY ? top : fmaf(-2.0f * sa.capl, cap_r(top, sa), sa.capl);
+    // a product of -inf is -cap like any other; where every key is hidden, -cap
+    // is no more than the scores to come
+    if constexpr (LATE) top = fmaf(-2.0f * sa.capl, cap_r(top, sa), sa.capl);
     if (__any(top > m + SLACK)) {
       const float m2 = fmaxf(m, top);
       const float f = m2 == -INFINITY ? 1.0f : exp2_hw(m - m2);

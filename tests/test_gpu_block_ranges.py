@@ -85,3 +85,23 @@ def test_decode_wide_caps(dt, cap, bias):
     slopes = (2.0 ** -np.arange(1, 9)).astype(np.float32) if bias else None
     o = decode(q, k, v, [700, 33], cap, slopes)
     close("o", o, B.decode(to_f64(q), to_f64(k), to_f64(v), None, [700, 33], None, cap, slopes), dt)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("c", [dict(q=[130], k=[130], D=64), dict(q=[20], k=[600], D=128), dict(q=[40], k=[1500], D=128)])
+def test_capped_products_of_minus_infinity(dt, bias, c):
+    """cap * tanh(-inf) = -cap is a score like any other: for the first 64
+    keys of the document next to scores of almost -cap, and alone."""
+    for alone in (False, True):
+        st = setup(dict(Hq=2, Hkv=1, cap=30.0, bias=bias, causal=False, **c), dt)
+        st["q"][..., 0] = 1.0
+        st["k"][:, 0] *= 0.125
+        st["k"][:, 0, 0] = float("-inf") if alone else -2.0 ** 14
+        st["k"][:64, 0, 0] = float("-inf")
+        if bias:  # flat enough for the far keys to count
+            st["slopes"] = np.asarray([2.0 ** -9, 2.0 ** -10], np.float32)
+        out = run(st)
+        ref, _ = reference(st)
+        close("o", out["o"], ref["o"], dt)
+        assert np.abs(to_f64(out["lse"]) - ref["lse"]).max() <= 5e-5
