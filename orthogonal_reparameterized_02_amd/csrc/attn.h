@@ -9,6 +9,10 @@
 
 namespace poetx {
 
+// A dispatch counts its threads in 32 bits, and what is past them is not run,
+// without an error: larger work goes out in launches of at most this many.
+constexpr long LAUNCH_THREADS = 1L << 31;
+
 // ---- rotary positions (rope.hip) -------------------------------------------
 struct RopeArgs {
   int T, Hq, Hk, D, rot, P, interleaved;

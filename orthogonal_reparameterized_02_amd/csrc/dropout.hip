@@ -87,12 +87,18 @@ hipError_t launch_dropout(long n, const TS* x, const TS* res, TS* out, uint32_t 
                           uint64_t offset, const uint64_t* offset_dev, hipStream_t s) {
   // cut = 65536 drops every element: the gain is never used
   const float gain = cut < 65536u ? 65536.0f / (float)(65536u - cut) : 0.0f;
-  const dim3 grid((unsigned)((n + 8L * NTH - 1) / (8L * NTH)));
-  if (res)
-    k_dropout<TS, true><<<grid, NTH, 0, s>>>(n, x, res, out, cut, gain, seed, offset, offset_dev);
-  else
-    k_dropout<TS, false><<<grid, NTH, 0, s>>>(n, x, res, out, cut, gain, seed, offset, offset_dev);
-  return hipGetLastError();
+  constexpr long MOST = 8 * LAUNCH_THREADS;  // elements a launch
+  for (; n > 0; n -= MOST, x += MOST, res = res ? res + MOST : nullptr, out += MOST, offset += MOST) {
+    const long m = std::min(n, MOST);
+    const dim3 grid((unsigned)((m + 8L * NTH - 1) / (8L * NTH)));
+    if (res)
+      k_dropout<TS, true><<<grid, NTH, 0, s>>>(m, x, res, out, cut, gain, seed, offset, offset_dev);
+    else
+      k_dropout<TS, false><<<grid, NTH, 0, s>>>(m, x, res, out, cut, gain, seed, offset, offset_dev);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template hipError_t launch_dropout<bf16>(long, const bf16*, const bf16*, bf16*, uint32_t, uint64_t, uint64_t, const uint64_t*, hipStream_t);

@@ -6,6 +6,9 @@
 // 4099 tokens of 40 heads of 104, 40 elements turned, float32, 27.3 us = 5.0
 // TB/s (a copy of 1 GiB: 5.0).  Two or four units a thread were slower (65 and
 // 72 us for the first).
+#include <algorithm>
+#include <type_traits>
+
 #include "attn.h"
 
 namespace poetx {
@@ -70,18 +73,25 @@ template <typename TS, int W>
 hipError_t rope_w(const RopeArgs& a, const TS* q, const TS* k, TS* qo, TS* ko, hipStream_t s) {
   const int turn = (a.interleaved ? a.rot : a.rot / 2) / W, units = turn + (a.D - a.rot) / W;
   const int per_token = units * (a.Hq + a.Hk);
-  const long total = (long)a.T * per_token;
-  const dim3 grid((unsigned)((total + NTH - 1) / NTH));
-  if constexpr (W >= 2) {
-    if (a.interleaved) {
-      k_rope<TS, W, true><<<grid, NTH, 0, s>>>(a, q, k, qo, ko, turn, units, per_token,
-                                                     1.0f / units, 1.0f / per_token);
-      return hipGetLastError();
-    }
+  const int most = (int)std::min((long)a.T, LAUNCH_THREADS / per_token);  // tokens a launch
+  RopeArgs b = a;
+  for (long t = 0; t < a.T; t += most) {
+    b.T = (int)std::min((long)most, a.T - t);
+    b.pos = a.pos + t;
+    const TS *bq = q + t * a.ldq, *bk = k ? k + t * a.ldk : nullptr;
+    TS *bqo = qo + t * a.ldqo, *bko = ko ? ko + t * a.ldko : nullptr;
+    const dim3 grid((unsigned)(((long)b.T * per_token + NTH - 1) / NTH));
+    const auto launch = [&](auto pairs) {
+      k_rope<TS, W, decltype(pairs)::value><<<grid, NTH, 0, s>>>(b, bq, bk, bqo, bko, turn, units, per_token,
+                                                                 1.0f / units, 1.0f / per_token);
+    };
+    // an even rot leaves pairs at least two wide
+    if constexpr (W >= 2) a.interleaved ? launch(std::true_type{}) : launch(std::false_type{});
+    else launch(std::false_type{});
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
   }
-  k_rope<TS, W, false><<<grid, NTH, 0, s>>>(a, q, k, qo, ko, turn, units, per_token,
-                                                     1.0f / units, 1.0f / per_token);
-  return hipGetLastError();
+  return hipSuccess;
 }
 
 }  // namespace

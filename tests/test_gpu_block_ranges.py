@@ -105,3 +105,26 @@ def test_capped_products_of_minus_infinity(dt, bias, c):
         ref, _ = reference(st)
         close("o", out["o"], ref["o"], dt)
         assert np.abs(to_f64(out["lse"]) - ref["lse"]).max() <= 5e-5
+
+
+# ---- launches of more than 2^32 threads ----------------------------------------------------
+def test_dropout_past_2_35_elements():
+    n = 2 ** 35 + 2 ** 34 + 88
+    x = torch.ones(n, dtype=torch.bfloat16, device="cuda")
+    P.poetx_dropout_bwd(x, x, 0.5, 11, 8)
+    for at in (0, 2 ** 34 - 24, 2 ** 35 - 24, n - 48):
+        np.testing.assert_array_equal(to_f64(x[at:at + 48]) != 0, B.keep(48, 0.5, 11, 8 + at))
+
+
+def test_rope_past_2_32_units():
+    """Pairs of single elements: seven units a head, more of them than one
+    launch can have threads."""
+    T, D = 2 ** 32 // 7 + 1000, 8
+    q = torch.ones(T, 1, D, dtype=torch.bfloat16, device="cuda")
+    ang = np.random.default_rng(0).uniform(-3, 3, (64, 1))
+    table = np.stack([np.cos(ang), np.sin(ang)], -1).astype(np.float32)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda") % 64
+    P.poetx_rope(q, None, pos, to_dev(table), q, None)
+    for at in (0, 2 ** 31 // 7 - 50, T - 100):
+        got, p = to_f64(q[at:at + 100]), pos[at:at + 100].cpu().numpy()
+        np.testing.assert_allclose(got, B.rope(np.ones((100, 1, D)), p, table), rtol=2.0 ** -8, atol=1e-6)
