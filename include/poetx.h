@@ -458,7 +458,8 @@ int32_t poetx_dropout_bwd(int64_t n, int32_t act, const void* dy, void* dx, doub
  * as matrix operands; sums, lse and delta are float32.  Results are
  * deterministic (no atomics).
  *   scale <= 0 selects 1 / sqrt(D); cap = 0: no cap; slopes [Hq] or NULL.
- *   D a multiple of 8 up to 128; Hq a multiple of Hkv.
+ *   D a multiple of 8 up to 128; Hq a multiple of Hkv.  Tq and Tk are at most
+ *   2^31 - 2^16, and tiles of 128 rows times heads fewer than 2^24 on a side.
  *   ldq, ldk, ldv, ldo: pitches of q, k, v, o; lddo, lddq, lddk, lddv of dout
  *   and the gradients.
  */
@@ -510,7 +511,8 @@ int32_t poetx_attn_bwd(const poetx_attn_shape* sh, const void* dout, const void*
  * position len[b] - 1.  An empty range gives o = 0.
  *   q, o [B][Hq][D] (pitches ldq, ldo); row j of sequence b of the caches
  *   at b * bsk + j * ldk, b * bsv + j * ldv (offsets are 64-bit), heads of
- *   D values side by side; rows: cache capacity per sequence.
+ *   D values side by side; rows: cache capacity per sequence, at most
+ *   2^31 - 2^16.
  *   ws poetx_attn_decode_workspace_bytes(sh) bytes.
  * Errors: ERR_ARG, ERR_WORKSPACE, ERR_DEVICE.
  */

@@ -1,6 +1,7 @@
 // C ABI of the attention-block operators: validation, layouts and dispatch.
 // Declarations and argument documentation: include/poetx.h.
 #include <math.h>
+#include <stdint.h>
 
 #include <algorithm>
 
@@ -16,6 +17,9 @@ constexpr int D_MAX = 128;       // attention head width
 constexpr int ROPE_D_MAX = 512;
 constexpr int H_MAX = 1024;      // heads
 constexpr int B_MAX = 65535;     // sequences of a decode call
+// packed rows, cache rows: a tile, or a piece of a cut loop, past the last one
+// is still an int
+constexpr int ROWS_MAX = INT32_MAX - 65535;
 
 int32_t check_act(const char* fn, int32_t act) {
   if (act != POETX_F32 && act != POETX_BF16) return fail(POETX_ERR_ARG, "%s: act dtype %d", fn, act);
@@ -55,7 +59,13 @@ int32_t check_attn(const char* fn, const poetx_attn_shape* sh, bool back) {
   if (!sh) return fail(POETX_ERR_ARG, "%s: null shape", fn);
   if (sh->Tq < 0 || sh->Tk < 0 || sh->ndoc < 0 || sh->ndoc > (1 << 30))
     return fail(POETX_ERR_ARG, "%s: Tq=%d Tk=%d ndoc=%d must be >= 0", fn, sh->Tq, sh->Tk, sh->ndoc);
+  if (sh->Tq > ROWS_MAX || sh->Tk > ROWS_MAX)
+    return fail(POETX_ERR_ARG, "%s: Tq=%d Tk=%d above %d", fn, sh->Tq, sh->Tk, ROWS_MAX);
   TRY(check_heads(fn, sh->Hq, sh->Hkv, sh->D));
+  // a tile of one head is 256 threads, a dispatch 2^32 - 1 of them at most
+  if (std::max((int64_t)attn_tiles(sh->Tq) * sh->Hq, (int64_t)attn_tiles(sh->Tk) * sh->Hkv) >= 1 << 24)
+    return fail(POETX_ERR_ARG, "%s: Tq=%d rows of Hq=%d heads, Tk=%d of Hkv=%d: 2^31 or more", fn, sh->Tq,
+                sh->Hq, sh->Tk, sh->Hkv);
   TRY(check_act(fn, sh->act));
   TRY(check_scores(fn, sh->scale, sh->cap));
   const int64_t wq = (int64_t)sh->Hq * sh->D, wk = (int64_t)sh->Hkv * sh->D;
@@ -142,6 +152,7 @@ int32_t check_decode(const char* fn, const poetx_decode_shape* sh) {
   if (!sh) return fail(POETX_ERR_ARG, "%s: null shape", fn);
   if (sh->B < 0 || sh->B > B_MAX || sh->rows < 0)
     return fail(POETX_ERR_ARG, "%s: B=%d (0..%d) rows=%d (>= 0)", fn, sh->B, B_MAX, sh->rows);
+  if (sh->rows > ROWS_MAX) return fail(POETX_ERR_ARG, "%s: rows=%d above %d", fn, sh->rows, ROWS_MAX);
   TRY(check_heads(fn, sh->Hq, sh->Hkv, sh->D));
   TRY(check_act(fn, sh->act));
   TRY(check_scores(fn, sh->scale, sh->cap));

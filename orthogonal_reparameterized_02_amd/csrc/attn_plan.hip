@@ -18,7 +18,7 @@ constexpr int STAGED = 1024;
 __device__ __forceinline__ int doc_of(const int* cu, int ndoc, int t, int T) {
   int lo = 0, hi = ndoc + 1;  // cu[lo - 1] <= t < cu[hi] in sorted offsets
   while (lo < hi) {
-    const int mid = (lo + hi) / 2;
+    const int mid = lo + (hi - lo) / 2;
     if (min(max(cu[mid], 0), T) <= t) lo = mid + 1;
     else hi = mid;
   }
