@@ -49,6 +49,9 @@ int32_t check_scores(const char* fn, float scale, float cap) {
   return POETX_OK;
 }
 
+// a cap in units of log2 stays finite: above 1e38 float32 scores feel none
+float cap_of(float cap) { return fminf(cap, 1e38f); }
+
 #define TRY(x)                          \
   do {                                  \
     const int32_t st_ = (x);            \
@@ -126,7 +129,7 @@ AttnArgs args_of(const poetx_attn_shape* sh, const void* q, const void* k, const
   a.Tq = sh->Tq, a.Tk = sh->Tk, a.Hq = sh->Hq, a.Hkv = sh->Hkv, a.D = sh->D;
   a.group = sh->Hq / sh->Hkv;
   a.scale = sh->scale > 0.0f ? sh->scale : 1.0f / sqrtf((float)sh->D);
-  a.cap = sh->cap;
+  a.cap = cap_of(sh->cap);
   a.slopes = slopes;
   a.ldq = sh->ldq, a.ldk = sh->ldk, a.ldv = sh->ldv, a.ldo = sh->ldo;
   a.lddo = sh->lddo, a.lddq = sh->lddq, a.lddk = sh->lddk, a.lddv = sh->lddv;
@@ -171,7 +174,7 @@ DecodeArgs decode_args(const poetx_decode_shape* sh) {
   DecodeArgs a = {};
   a.B = sh->B, a.Hq = sh->Hq, a.Hkv = sh->Hkv, a.group = sh->Hq / sh->Hkv, a.D = sh->D, a.rows = sh->rows;
   a.scale = sh->scale > 0.0f ? sh->scale : 1.0f / sqrtf((float)sh->D);
-  a.cap = sh->cap;
+  a.cap = cap_of(sh->cap);
   a.ldq = sh->ldq, a.ldo = sh->ldo, a.ldk = sh->ldk, a.ldv = sh->ldv, a.bsk = sh->bsk, a.bsv = sh->bsv;
   return a;
 }

@@ -15,6 +15,8 @@
 // (rows of V, K, Q or dO read down their columns) takes the same K order.
 #pragma once
 
+#include <float.h>
+
 #include <type_traits>
 
 #include "attn.h"
@@ -312,7 +314,8 @@ struct ScoreArgs {
 template <typename T, int MODE>
 __device__ __forceinline__ ScoreArgs score_args(float scale, float cap, float slope) {
   ScoreArgs s;
-  s.c = !(MODE & 1) ? scale * LOG2E : cap_by_r<T, MODE> ? scale / cap * (2.0f * LOG2E) : scale / cap;
+  // finite: a product of 0 stays 0 beside a large scale or a tiny cap
+  s.c = fminf(!(MODE & 1) ? scale * LOG2E : cap_by_r<T, MODE> ? scale / cap * (2.0f * LOG2E) : scale / cap, FLT_MAX);
   s.capl = cap * LOG2E;
   s.slope = slope * LOG2E;
   return s;

@@ -107,6 +107,24 @@ def test_capped_products_of_minus_infinity(dt, bias, c):
         assert np.abs(to_f64(out["lse"]) - ref["lse"]).max() <= 5e-5
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("scale,cap", [(0.1, 3e38), (0.1, float(np.finfo(np.float32).max)), (1e10, 1e-30)])
+def test_scale_and_cap_at_the_ends_of_float32(dt, scale, cap):
+    """The largest cap is none; a tiny one leaves the sign of a score.  Some
+    products are 0, which no factor changes."""
+    rng = np.random.default_rng(3)
+    q, k, v = normal(rng, (2, 4, 64), dt), normal(rng, (2, 300, 2, 64), dt), normal(rng, (2, 300, 2, 64), dt)
+    k[:, ::3] = 0
+    sh = P.decode_shape(q, k, v, scale, cap)
+    ws = torch.empty(P.poetx_attn_decode_workspace_bytes(sh), dtype=torch.uint8, device="cuda")
+    o = torch.full_like(q, 7.0)
+    P.poetx_attn_decode(sh, q, k, v, to_dev(np.asarray([300, 33], np.int32)), o, ws)
+    close("decode", o, B.decode(to_f64(q), to_f64(k), to_f64(v), None, [300, 33], scale, cap), dt)
+    st = setup(dict(q=[70], k=[90], Hq=4, Hkv=2, D=64, cap=cap), dt)
+    st["k"][::3] = 0
+    check(run(st, scale=scale), reference(st, scale=scale)[0], dt)
+
+
 # ---- launches of more than 2^32 threads ----------------------------------------------------
 def test_dropout_past_2_35_elements():
     n = 2 ** 35 + 2 ** 34 + 88
