@@ -189,14 +189,15 @@ def alibi_slopes(heads: int, device="cuda") -> torch.Tensor:
 
 # ---- single tokens over a cache -----------------------------------------------------------
 class KVCache:
-    """Keys and values of B sequences, up to `rows` tokens each."""
+    """Keys and values of B sequences, up to `rows` tokens each.  An idle slot
+    counts tokens like the others; fill it with none of them to empty it."""
 
     def __init__(self, B: int, rows: int, Hkv: int, D: int, dtype=torch.bfloat16, device="cuda"):
         self.k = torch.empty(B, rows, Hkv, D, dtype=dtype, device=device)
         self.v = torch.empty_like(self.k)
         self.length = torch.zeros(B, dtype=torch.int32, device=device)
         self.B, self.rows = B, rows
-        self._most = 0  # host-side bound of the lengths: no device read per token
+        self._lengths = [0] * B  # the same on the host: no device read per token
         self._at = torch.arange(B, device=device)
 
     def fill(self, b: int, k: torch.Tensor, v: torch.Tensor) -> None:
@@ -206,16 +207,16 @@ class KVCache:
             raise ValueError(f"{n} tokens do not fit a cache of {self.rows} rows")
         self.k[b, :n], self.v[b, :n] = k, v
         self.length[b] = n
-        self._most = max(self._most, n)
+        self._lengths[b] = n
 
     def append(self, k: torch.Tensor, v: torch.Tensor) -> None:
         """One token more for every sequence: k, v [B][Hkv][D]."""
-        if self._most >= self.rows:
+        if max(self._lengths, default=0) >= self.rows:
             raise ValueError(f"the cache is full ({self.rows} rows)")
         at = self.length.long()
         self.k[self._at, at], self.v[self._at, at] = k, v
         self.length += 1
-        self._most += 1
+        self._lengths = [n + 1 for n in self._lengths]
 
 
 def attention_decode(q: torch.Tensor, cache: KVCache, scale: float = 0.0, cap: float = 0.0,
