@@ -190,15 +190,27 @@ def alibi_slopes(heads: int, device="cuda") -> torch.Tensor:
 # ---- single tokens over a cache -----------------------------------------------------------
 class KVCache:
     """Keys and values of B sequences, up to `rows` tokens each.  An idle slot
-    counts tokens like the others; fill it with none of them to empty it."""
+    counts tokens like the others; fill it with none of them to empty it.
+
+    append refuses a full cache from a count on the host.  A replayed graph
+    appends without the host: there a sequence without room keeps its rows and
+    its length, and from the first captured call on the count is read from the
+    GPU."""
 
     def __init__(self, B: int, rows: int, Hkv: int, D: int, dtype=torch.bfloat16, device="cuda"):
         self.k = torch.empty(B, rows, Hkv, D, dtype=dtype, device=device)
         self.v = torch.empty_like(self.k)
         self.length = torch.zeros(B, dtype=torch.int32, device=device)
         self.B, self.rows = B, rows
-        self._lengths = [0] * B  # the same on the host: no device read per token
+        # the same on the host, so that no token waits for the GPU; None: replays may have changed it
+        self._lengths: Optional[list] = [0] * B
         self._at = torch.arange(B, device=device)
+
+    def longest(self) -> Optional[int]:
+        """Tokens of the longest sequence; None while a graph is captured."""
+        if torch.cuda.is_current_stream_capturing():
+            return None
+        return max(self.length.tolist() if self._lengths is None else self._lengths, default=0)
 
     def fill(self, b: int, k: torch.Tensor, v: torch.Tensor) -> None:
         """Sequence b becomes k, v [n][Hkv][D] (a prompt's)."""
@@ -207,16 +219,33 @@ class KVCache:
             raise ValueError(f"{n} tokens do not fit a cache of {self.rows} rows")
         self.k[b, :n], self.v[b, :n] = k, v
         self.length[b] = n
-        self._lengths[b] = n
+        if torch.cuda.is_current_stream_capturing():
+            self._lengths = None
+        elif self._lengths is not None:
+            self._lengths[b] = n
 
     def append(self, k: torch.Tensor, v: torch.Tensor) -> None:
         """One token more for every sequence: k, v [B][Hkv][D]."""
-        if max(self._lengths, default=0) >= self.rows:
+        n = self.longest()
+        if self.rows == 0 or (n is not None and n >= self.rows):
             raise ValueError(f"the cache is full ({self.rows} rows)")
+        if n is None:
+            self._append_where_room(k, v)
+            return
         at = self.length.long()
         self.k[self._at, at], self.v[self._at, at] = k, v
         self.length += 1
-        self._lengths = [n + 1 for n in self._lengths]
+        if self._lengths is not None:
+            self._lengths = [m + 1 for m in self._lengths]
+
+    def _append_where_room(self, k: torch.Tensor, v: torch.Tensor) -> None:
+        """append for a graph: what a replay finds full is written back as it
+        was, so no replay writes outside the cache."""
+        self._lengths = None
+        at, full = self.length.clamp(0, self.rows - 1).long(), (self.length >= self.rows)[:, None, None]
+        for rows, new in ((self.k, k), (self.v, v)):
+            rows[self._at, at] = torch.where(full, rows[self._at, at], new)
+        self.length.add_(1).clamp_(max=self.rows)
 
 
 def attention_decode(q: torch.Tensor, cache: KVCache, scale: float = 0.0, cap: float = 0.0,
@@ -284,8 +313,12 @@ class POETXAttention(torch.nn.Module):
 
     @torch.no_grad()
     def decode(self, x: torch.Tensor, cache: KVCache) -> torch.Tensor:
-        """The next token of every sequence, x [B][n]."""
+        """The next token of every sequence, x [B][n].  In a captured graph a
+        sequence without room for it answers NaN."""
+        full = cache.length >= cache.rows if cache.longest() is None else None
         q, k, v = self._heads(x, cache.length)
         cache.append(k, v)
         o = attention_decode(q, cache, cap=self.cap, slopes=self.slopes)
+        if full is not None:
+            o.masked_fill_(full[:, None, None], math.nan)
         return x + self.o(o.view(x.shape[0], -1))

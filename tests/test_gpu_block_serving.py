@@ -1,9 +1,11 @@
 """The attention block's module and cache in use: slots filled again, captured
 decoding steps, positions past the table, recomputation, second derivatives.
 Tolerances as in test_gpu_block.py."""
+import numpy as np
 import pytest
 import torch
 
+from gpu_util import bits
 from orthogonal_reparameterized_02_amd import attention as A
 from test_gpu_attention_block import randn
 
@@ -14,6 +16,15 @@ pytestmark = pytest.mark.gpu
 def _gpu():
     if not torch.cuda.is_available():
         pytest.skip("no GPU")
+
+
+def block_of(**kw):
+    """A small block whose projections are not the identity."""
+    block = A.POETXAttention(256, 4, 2, 32, 3, **kw)
+    with torch.no_grad():
+        for i, p in enumerate(block.parameters()):
+            p.copy_(0.02 * randn(*p.shape, dtype=torch.float32, seed=i))
+    return block
 
 
 # ---- the cache ---------------------------------------------------------------------------
@@ -36,3 +47,48 @@ def test_a_cache_slot_is_filled_again():
     cache.fill(0, kv(0), kv(0))
     cache.append(kv(2), kv(2))
     assert cache.length.tolist() == [1, 6]
+
+
+def test_captured_appends_stay_inside_the_cache():
+    """A step captured once and replayed past the cache's end: the steps that
+    fit are the eager ones, a sequence without room is left as it is and the
+    block answers NaN for it; the host reads the lengths again afterwards."""
+    block = block_of(positions=64).eval()
+    x = randn(2, 256)
+    fresh = lambda: A.KVCache(2, 8, 2, block.D)
+    prompts = randn(5, 256, seed=1), randn(2, 256, seed=2)
+
+    def start(cache):
+        for b, p in enumerate(prompts):
+            block.prefill(p, cache, b)
+
+    eager, cache = fresh(), fresh()
+    start(eager)
+    block.decode(x, fresh())  # whatever is loaded or sized on first use
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y = block.decode(x, cache)
+    start(cache)
+    for i in range(3):
+        want = block.decode(x, eager)
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in ((y, want), (cache.length, eager.length), (cache.k[0, :6 + i], eager.k[0, :6 + i]),
+                     (cache.v[1, :3 + i], eager.v[1, :3 + i])):
+            np.testing.assert_array_equal(bits(a), bits(b))
+    assert cache.length.tolist() == [8, 5]
+    kept = cache.k.clone(), cache.v.clone()
+    for i in range(5):
+        g.replay()
+        torch.cuda.synchronize()
+        assert cache.length.tolist() == [8, min(6 + i, 8)]
+        assert torch.isnan(y[0]).all() and torch.isnan(y[1]).all() == (i >= 3)
+        assert torch.isfinite(y[1]).all() == (i < 3)
+    assert torch.equal(cache.k[0], kept[0][0]) and torch.equal(cache.v[0], kept[1][0])
+    assert torch.equal(cache.k[1, :5], kept[0][1, :5])
+    with pytest.raises(ValueError, match="full"):
+        block.decode(x, cache)
+    cache.fill(0, kept[0][0, :1], kept[1][0, :1])
+    cache.fill(1, kept[0][1, :4], kept[1][1, :4])
+    assert torch.isfinite(block.decode(x, cache)).all() and cache.length.tolist() == [2, 5]
