@@ -265,8 +265,9 @@ class POETXAttention(torch.nn.Module):
     projections of block size b and Neumann order k.
 
     forward(x, plan, pos): x [T][n] packed tokens, plan their AttentionPlan,
-    pos [T] int32 positions (of each token in its document).  prefill and
-    decode serve: no dropout, no gradients."""
+    pos [T] int32 positions (of each token in its document; one outside the
+    table gives NaN).  prefill and decode serve: no dropout, no gradients, and
+    no token past the table."""
 
     def __init__(self, n: int, heads: int, kv_heads: int, b: int, k: int, head_dim: Optional[int] = None,
                  positions: int = 8192, rot: Optional[int] = None, base: float = 10000.0, scaling=None,
@@ -291,6 +292,10 @@ class POETXAttention(torch.nn.Module):
         q, k = apply_rope(q, k, pos, self.table, self.interleaved)
         return q, k, self.v(x).view(T, self.Hkv, self.D)
 
+    def _check_positions(self, n: int) -> None:
+        if n > self.table.shape[0]:
+            raise ValueError(f"{n} tokens, the rotary table has {self.table.shape[0]} positions")
+
     def forward(self, x: torch.Tensor, plan: AttentionPlan, pos: torch.Tensor) -> torch.Tensor:
         q, k, v = self._heads(x, pos)
         y = self.o(attention(q, k, v, plan, cap=self.cap, slopes=self.slopes).view(x.shape[0], -1))
@@ -305,6 +310,7 @@ class POETXAttention(torch.nn.Module):
         """A prompt x [n tokens][n] of sequence b from position 0; fills its
         cache rows."""
         T = x.shape[0]
+        self._check_positions(T)
         pos = torch.arange(T, dtype=torch.int32, device=x.device)
         q, k, v = self._heads(x, pos)
         cache.fill(b, k, v)
@@ -314,8 +320,12 @@ class POETXAttention(torch.nn.Module):
     @torch.no_grad()
     def decode(self, x: torch.Tensor, cache: KVCache) -> torch.Tensor:
         """The next token of every sequence, x [B][n].  In a captured graph a
-        sequence without room for it answers NaN."""
-        full = cache.length >= cache.rows if cache.longest() is None else None
+        sequence without room for it, or without a position in the rotary
+        table, answers NaN."""
+        n = cache.longest()
+        full = cache.length >= cache.rows if n is None else None
+        if n is not None:
+            self._check_positions(n + 1)
         q, k, v = self._heads(x, cache.length)
         cache.append(k, v)
         o = attention_decode(q, cache, cap=self.cap, slopes=self.slopes)

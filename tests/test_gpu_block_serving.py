@@ -92,3 +92,17 @@ def test_captured_appends_stay_inside_the_cache():
     cache.fill(0, kept[0][0, :1], kept[1][0, :1])
     cache.fill(1, kept[0][1, :4], kept[1][1, :4])
     assert torch.isfinite(block.decode(x, cache)).all() and cache.length.tolist() == [2, 5]
+
+
+# ---- positions past the table ----------------------------------------------------------------
+def test_serving_past_the_table_is_refused():
+    block = block_of(positions=8).eval()
+    cache = A.KVCache(1, 16, 2, block.D)
+    with pytest.raises(ValueError, match="8 positions"):
+        block.prefill(randn(9, 256), cache)
+    assert cache.length.tolist() == [0]
+    block.prefill(randn(7, 256), cache)
+    assert torch.isfinite(block.decode(randn(1, 256), cache)).all()
+    with pytest.raises(ValueError, match="8 positions"):
+        block.decode(randn(1, 256), cache)
+    assert cache.length.tolist() == [8]
