@@ -264,10 +264,11 @@ class POETXAttention(torch.nn.Module):
     """x + dropout(Wo attention(rope(Wq x), rope(Wk x), Wv x)) with POET-X
     projections of block size b and Neumann order k.
 
-    forward(x, plan, pos): x [T][n] packed tokens, plan their AttentionPlan,
+    forward(x, plan, pos, at): x [T][n] packed tokens, plan their AttentionPlan,
     pos [T] int32 positions (of each token in its document; one outside the
-    table gives NaN).  prefill and decode serve: no dropout, no gradients, and
-    no token past the table."""
+    table gives NaN), at the place of the dropout mask (draw; by default the
+    next one, which a recomputed pass could not find again).  prefill and
+    decode serve: no dropout, no gradients, and no token past the table."""
 
     def __init__(self, n: int, heads: int, kv_heads: int, b: int, k: int, head_dim: Optional[int] = None,
                  positions: int = 8192, rot: Optional[int] = None, base: float = 10000.0, scaling=None,
@@ -296,13 +297,27 @@ class POETXAttention(torch.nn.Module):
         if n > self.table.shape[0]:
             raise ValueError(f"{n} tokens, the rotary table has {self.table.shape[0]} positions")
 
-    def forward(self, x: torch.Tensor, plan: AttentionPlan, pos: torch.Tensor) -> torch.Tensor:
+    def draw(self, tokens: int) -> torch.Tensor:
+        """The place of the next `tokens` tokens' mask in the seed's sequence
+        ([1] int64 on the GPU), which moves on past it.  For a forward pass
+        that will be recomputed:
+            checkpoint(block, x, plan, pos, block.draw(x.shape[0]))"""
+        at = self.drawn.clone()
+        self.drawn += (tokens * self.n + 7) // 8 * 8
+        return at
+
+    def forward(self, x: torch.Tensor, plan: AttentionPlan, pos: torch.Tensor,
+                at: Optional[torch.Tensor] = None) -> torch.Tensor:
         q, k, v = self._heads(x, pos)
         y = self.o(attention(q, k, v, plan, cap=self.cap, slopes=self.slopes).view(x.shape[0], -1))
         if not (self.training and self.p > 0):
             return x + y
-        at = self.drawn.clone()
-        self.drawn += (y.numel() + 7) // 8 * 8
+        if at is None:
+            # inside a backward pass: the sequence has moved on since the loss was formed
+            if torch._C._current_graph_task_id() != -1:
+                raise RuntimeError("a forward pass recomputed for the backward pass needs the place of its dropout "
+                                   "mask: pass at=block.draw(tokens) (see POETXAttention.draw)")
+            at = self.draw(x.shape[0])
         return dropout_add(y, x, self.p, self.seed, 0, at)
 
     @torch.no_grad()

@@ -4,10 +4,11 @@ Tolerances as in test_gpu_block.py."""
 import numpy as np
 import pytest
 import torch
+from torch.utils.checkpoint import checkpoint
 
-from gpu_util import bits
+from gpu_util import bits, to_f64
 from orthogonal_reparameterized_02_amd import attention as A
-from test_gpu_attention_block import randn
+from test_gpu_attention_block import BF16, randn, rel
 
 pytestmark = pytest.mark.gpu
 
@@ -16,6 +17,10 @@ pytestmark = pytest.mark.gpu
 def _gpu():
     if not torch.cuda.is_available():
         pytest.skip("no GPU")
+
+
+def i32(*x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
 
 
 def block_of(**kw):
@@ -106,3 +111,49 @@ def test_serving_past_the_table_is_refused():
     with pytest.raises(ValueError, match="8 positions"):
         block.decode(randn(1, 256), cache)
     assert cache.length.tolist() == [8]
+
+
+# ---- recomputation ------------------------------------------------------------------------------
+@pytest.mark.parametrize("reentrant", [False, True])
+def test_gradients_under_recomputation(reentrant):
+    """Two blocks recomputed in the backward pass draw the masks that the loss
+    saw: the gradients are those without recomputation."""
+    blocks = [block_of(dropout=0.4, positions=64, seed=s) for s in (0, 1)]
+    T = 48
+    plan, pos, g = A.AttentionPlan(i32(0, 20, T), T), i32(*range(20), *range(28)), randn(T, 256, seed=9)
+    grads = []
+    for again in (False, True):
+        for b in blocks:
+            b.drawn.zero_()
+            b.zero_grad()
+        x = randn(T, 256).requires_grad_()
+        for _ in range(2):  # a second step: the sequence has moved on before the backward pass
+            at = [b.draw(T) for b in blocks]
+            both = lambda x, at: blocks[1](blocks[0](x, plan, pos, at[0]), plan, pos, at[1])
+            y = checkpoint(both, x, at, use_reentrant=reentrant) if again else both(x, at)
+            y.backward(g)
+        grads.append([x.grad] + [p.grad for b in blocks for p in b.parameters()])
+    for a, b in zip(*grads):
+        assert rel(a, to_f64(b)) <= BF16
+
+
+@pytest.mark.parametrize("reentrant", [False, True])
+def test_recomputation_without_its_mask_is_refused(reentrant):
+    block = block_of(dropout=0.4, positions=64)
+    plan, pos = A.AttentionPlan(i32(0, 48), 48), i32(*range(48))
+    y = checkpoint(block, randn(48, 256).requires_grad_(), plan, pos, use_reentrant=reentrant)
+    with pytest.raises(RuntimeError, match="recomput"):
+        y.float().sum().backward()
+    block.eval()  # no mask, nothing to draw
+    x = randn(48, 256).requires_grad_()
+    checkpoint(block, x, plan, pos, use_reentrant=reentrant).float().sum().backward()
+    assert torch.isfinite(x.grad).all()
+
+
+def test_drawn_masks_are_those_of_plain_calls():
+    block = block_of(dropout=0.4, positions=64)
+    x, plan, pos = randn(48, 256), A.AttentionPlan(i32(0, 48), 48), i32(*range(48))
+    plain = [block(x, plan, pos) for _ in range(2)]
+    block.drawn.zero_()
+    at = [block.draw(48) for _ in range(2)]
+    assert torch.equal(block(x, plan, pos, at[1]), plain[1]) and torch.equal(block(x, plan, pos, at[0]), plain[0])
