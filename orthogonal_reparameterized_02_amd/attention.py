@@ -5,7 +5,8 @@
 (include/poetx.h) with autograd and their workspaces; `POETXAttention` puts
 them between four `POETXLinear` projections: packed documents for training,
 single tokens over a cache for serving.  PyTorch supplies device memory,
-streams and autograd only.
+streams and autograd only.  The gradients have no gradients of their own:
+differentiating them raises.
 """
 from __future__ import annotations
 
@@ -13,6 +14,7 @@ import math
 from typing import Optional, Sequence
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import poetx as P
 from .layer import POETXLinear
@@ -75,6 +77,7 @@ class _Rope(torch.autograd.Function):
         return (qo,) if k is None else (qo, ko)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, *grads):
         pos, table = ctx.saved_tensors
         g = [x.contiguous() for x in grads]
@@ -104,6 +107,7 @@ class _DropoutAdd(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         p, seed, offset = ctx.args
         dx = None
@@ -162,6 +166,7 @@ class _Attention(torch.autograd.Function):
         return o
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         q, k, v, o, lse, slopes = ctx.saved_tensors
         dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))

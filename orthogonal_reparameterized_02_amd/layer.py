@@ -10,6 +10,7 @@ PyTorch supplies device memory and streams only.
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import poetx as P
 
@@ -212,6 +213,7 @@ class _POETXFn(torch.autograd.Function):
         return y.reshape(*lead, m)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         mod, sh = ctx.mod, ctx.sh
         theta, GT, saved, ws_cnp = ctx.state

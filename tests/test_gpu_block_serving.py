@@ -157,3 +157,22 @@ def test_drawn_masks_are_those_of_plain_calls():
     block.drawn.zero_()
     at = [block.draw(48) for _ in range(2)]
     assert torch.equal(block(x, plan, pos, at[1]), plain[1]) and torch.equal(block(x, plan, pos, at[0]), plain[0])
+
+
+# ---- second derivatives ---------------------------------------------------------------------------
+@pytest.mark.parametrize("op", ["rope", "dropout", "attention", "projection"])
+def test_second_derivatives_are_refused(op):
+    """Where they would come out without the operator's own terms."""
+    T = 8
+    x = randn(T, 2, 64, dtype=torch.float32).requires_grad_()
+    if op == "rope":
+        y = A.apply_rope(x, None, i32(*range(T)), A.rope_table(T, 64))
+    elif op == "dropout":
+        y = A.dropout_add(x, x, 0.3, 1)
+    elif op == "attention":
+        y = A.attention(x, x, x, A.AttentionPlan(i32(0, T), T))
+    else:
+        y = A.POETXLinear(128, 128, 32, 2, dtype=torch.float32)(x.view(T, 128))
+    g, = torch.autograd.grad(y.square().sum() + x.square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        g.sum().backward()
