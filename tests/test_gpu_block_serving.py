@@ -1,6 +1,6 @@
 """The attention block's module and cache in use: slots filled again, captured
-decoding steps, positions past the table, recomputation, second derivatives.
-Tolerances as in test_gpu_block.py."""
+decoding steps, positions past the table, recomputation, second derivatives,
+forms of the calls.  Tolerances as in test_gpu_block.py."""
 import numpy as np
 import pytest
 import torch
@@ -8,6 +8,7 @@ from torch.utils.checkpoint import checkpoint
 
 from gpu_util import bits, to_f64
 from orthogonal_reparameterized_02_amd import attention as A
+from oracle import block_oracle as B
 from test_gpu_attention_block import BF16, randn, rel
 
 pytestmark = pytest.mark.gpu
@@ -176,3 +177,53 @@ def test_second_derivatives_are_refused(op):
     g, = torch.autograd.grad(y.square().sum() + x.square().sum(), x, create_graph=True)
     with pytest.raises(RuntimeError, match="once_differentiable"):
         g.sum().backward()
+
+
+# ---- forms of the Python calls ------------------------------------------------------------------------
+def test_attention_with_longer_keys():
+    """The last rows of a prompt against all of its keys: AttentionPlan with
+    key offsets of its own, through autograd."""
+    Tq, Tk, Hq, Hkv, D = 30, 100, 4, 2, 64
+    q, k, v = randn(Tq, Hq, D).requires_grad_(), randn(Tk, Hkv, D, seed=1).requires_grad_(), randn(Tk, Hkv, D, seed=2).requires_grad_()
+    g = randn(Tq, Hq, D, seed=3)
+    o = A.attention(q, k, v, A.AttentionPlan(i32(0, 10, 30), Tq, i32(0, 60, 100), Tk), scale=0.2)
+    o.backward(g)
+    seen, pos = B.mask(Tq, Tk, [0, 10, 30], [0, 60, 100])
+    ref = B.attention(to_f64(q), to_f64(k), to_f64(v), seen, pos, 0.2, dout=to_f64(g))
+    for n, t in (("o", o), ("dq", q.grad), ("dk", k.grad), ("dv", v.grad)):
+        assert rel(t, ref[n]) <= BF16
+
+
+def test_attention_decode_over_a_window():
+    cache = A.KVCache(2, 90, 2, 64)
+    for b, n in enumerate((90, 31)):
+        cache.fill(b, randn(n, 2, 64, seed=b), randn(n, 2, 64, seed=b + 5))
+    q, slopes = randn(2, 4, 64), A.alibi_slopes(4)
+    o = A.attention_decode(q, cache, scale=0.2, cap=9.0, slopes=slopes, start=i32(40, 31))
+    k, v = (to_f64(t) for t in (cache.k, cache.v))
+    k[1, 31:] = v[1, 31:] = 0.0
+    ref = B.decode(to_f64(q), k, v, [40, 31], [90, 31], 0.2, 9.0, slopes.cpu().numpy())
+    assert rel(o, ref) <= BF16 and not o[1].any()
+
+
+def test_float32_block():
+    """Packed, served and trained in float32: served tokens are the packed
+    ones to float32's tolerance, a directional derivative is that of a central
+    difference.  Its error: rounding 2^-22 |loss| / step, truncation step^2."""
+    block = block_of(dtype=torch.float32, positions=64, cap=20.0)
+    T = 40
+    x, g = randn(T, 256, dtype=torch.float32), randn(T, 256, dtype=torch.float32, seed=1)
+    plan, pos = A.AttentionPlan(i32(0, T), T), i32(*range(T))
+    with torch.no_grad():
+        packed = block(x, plan, pos)
+        cache = A.KVCache(1, 64, 2, block.D, dtype=torch.float32)
+        got = torch.cat([block.prefill(x[:25], cache)] + [block.decode(x[t:t + 1], cache) for t in range(25, T)])
+    assert rel(got, to_f64(packed)) <= 1e-5
+    leaf = x.clone().requires_grad_()
+    (block(leaf, plan, pos) * g).sum().backward()
+    d, h = randn(T, 256, dtype=torch.float32, seed=2), 2.0 ** -6
+    with torch.no_grad():
+        up, down = ((block(x + s * h * d, plan, pos).double() * g.double()).sum().item() for s in (1, -1))
+    want = (leaf.grad.double() * d.double()).sum().item()
+    scale = (leaf.grad.double().norm() * d.double().norm()).item()
+    assert abs((up - down) / (2 * h) - want) <= 1e-3 * scale
