@@ -9,6 +9,10 @@
 // without any barrier (the next key tile is requested as soon as the scores
 // are formed, the next value tile as soon as the sums are).  Waves join in
 // LDS, pieces in a second small kernel, in a fixed order.
+// bf16 operands hold a probability in two parts (score_parts): twice the value
+// products, which the read hides but for 1% (16 long sequences 234.7 us, from
+// one part 232.8), and o is off by its own rounding alone (2-norm 1.66e-3, from
+// one part 1.80e-3).
 //
 // Measured (bf16, 32 heads on 8, D 128): 16 sequences of 8000 to 32768 rows
 // 233 us = 6.1 TB/s (a copy of 1 GiB moves 5.0, reading alone 6.5); one
@@ -123,10 +127,15 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void 
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(NL) : "memory");
 #pragma unroll
     for (int u = 0; u < L::CSTEP; ++u) {
-      const uint4 p = L::score_frag(sc, u);
+      uint4 p, rest;
+      if constexpr (sizeof(T) == 2) L::score_parts(sc, u, p, rest);
+      else p = L::score_frag(sc, u);
 #pragma unroll
-      for (int ct = 0; ct < L::NT; ++ct)
-        o[ct] = mma16((const T*)nullptr, L::col_frag(smem, vc, 0, u, ct), p, o[ct]);
+      for (int ct = 0; ct < L::NT; ++ct) {
+        const uint4 f = L::col_frag(smem, vc, 0, u, ct);
+        o[ct] = mma16((const T*)nullptr, f, p, o[ct]);
+        if constexpr (sizeof(T) == 2) o[ct] = mma16((const T*)nullptr, f, rest, o[ct]);
+      }
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     lv.load(vp, a.ldv, jn, p1, ldsv);

@@ -115,6 +115,23 @@ template <typename T, int DP> struct Tile {
       return make_uint4(__float_as_uint(p[4 * t]), __float_as_uint(p[4 * t + 1]),
                         __float_as_uint(p[4 * t + 2]), __float_as_uint(p[4 * t + 3]));
   }
+  // The same in two parts that together hold 16 bits: f the next bf16 below
+  // each score (>= 0), rest what that leaves, rounded.  Both are above 0 where
+  // the score is: an infinite row of the other operand stays one, which 0 or
+  // a negative rest would turn into NaN.
+  static __device__ __forceinline__ void score_parts(const f32x16_t& p, int t, uint4& f, uint4& rest) {
+    uint32_t h[4], r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x = p[8 * t + 2 * i], y = p[8 * t + 2 * i + 1];
+      const uint32_t a = __builtin_elementwise_sub_sat(__float_as_uint(x), 1u) & 0xffff0000u;
+      const uint32_t b = __builtin_elementwise_sub_sat(__float_as_uint(y), 1u) & 0xffff0000u;
+      h[i] = a >> 16 | b;
+      r[i] = pack2bf(x - __uint_as_float(a), y - __uint_as_float(b));
+    }
+    f = make_uint4(h[0], h[1], h[2], h[3]);
+    rest = make_uint4(r[0], r[1], r[2], r[3]);
+  }
 };
 
 // Loads of a tile straight into LDS (buffer_load_dwordx4 ... lds: a wave

@@ -125,6 +125,43 @@ def test_scale_and_cap_at_the_ends_of_float32(dt, scale, cap):
     check(run(st, scale=scale), reference(st, scale=scale)[0], dt)
 
 
+# ---- probabilities ------------------------------------------------------------------------
+@pytest.mark.parametrize("Hq,Hkv,D,rows,lens,cap", [(8, 2, 128, 600, [600, 333], 0.0), (4, 4, 64, 5000, [5000, 17], 0.0), (32, 4, 104, 300, [300, 299], 30.0)])
+def test_decode_rounds_once(Hq, Hkv, D, rows, lens, cap):
+    """Probabilities keep 2^-16, 2^-17 in the root mean square, beside bf16
+    values, sums are float32; values lie 2^-8 apart or more, so one element in
+    2^9 rounds the other way than the oracle's, by 2^-7 at most: 2-norm
+    2^-4.5 * 2^-7."""
+    rng = np.random.default_rng(D)
+    q, k, v = normal(rng, (2, Hq, D), "bf16", 1.5), normal(rng, (2, rows, Hkv, D), "bf16"), normal(rng, (2, rows, Hkv, D), "bf16")
+    got = to_f64(decode(q, k, v, lens, cap))
+    ref = torch.from_numpy(B.decode(to_f64(q), to_f64(k), to_f64(v), None, lens, None, cap))
+    want = to_f64(ref.to(torch.bfloat16))
+    assert np.linalg.norm(got - want) <= 2.0 ** -11 * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("where", ["k", "v"])
+@pytest.mark.parametrize("rows,cap", [(40, 0.0), (700, 0.0), (700, 8.0)])
+def test_decode_of_rows_that_are_not_finite(dt, where, rows, cap):
+    """Seen keys and values of infinity and NaN: the oracle's pattern."""
+    rng = np.random.default_rng(rows)
+    q, k, v = normal(rng, (4, 4, 64), dt, 1.5), normal(rng, (4, rows, 2, 64), dt), normal(rng, (4, rows, 2, 64), dt)
+    t = k if where == "k" else v
+    t[0, 30, 0], t[1, 7, 1, 5], t[2, 0, 0, 3] = float("nan"), float("inf"), float("-inf")
+    if where == "v":  # one key takes all of a query: its probability is 1 to the last bit
+        q[3] = 0
+        q[3, :, 0] = 64.0
+        k[3, :, :, 0] = 0
+        k[3, 11, :, 0] = 64.0
+        v[3, 11, 0, 9] = float("inf")
+    o = decode(q, k, v, [rows] * 4, cap)
+    with np.errstate(invalid="ignore"):
+        ref = B.decode(to_f64(q), to_f64(k), to_f64(v), None, [rows] * 4, None, cap)
+    assert not np.isfinite(ref).all()
+    close("o", o, ref, dt)
+
+
 # ---- launches of more than 2^32 threads ----------------------------------------------------
 def test_dropout_past_2_35_elements():
     n = 2 ** 35 + 2 ** 34 + 88
