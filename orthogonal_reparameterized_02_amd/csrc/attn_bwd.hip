@@ -259,7 +259,7 @@ __global__ __launch_bounds__(64 * NW * NQ, (DkvCfg<T, DP, NQ>::OCC)) void k_attn
       const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
           (void*)(src + i0), (short)0, min(qhi - i0, BN) * 4, 0x00020000);
       const uint32_t m0v = __builtin_amdgcn_readfirstlane(lds0 + 4 * C::QTILE + buf * C::ROWV + wave * C::VS * 4);
-      asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(m0v),
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(m0v),
                    "v"(lane < BN ? lane * 4 : 0x60000000), "s"(rs)
                    : "memory");
     }

@@ -138,7 +138,9 @@ template <typename T, int DP> struct Tile {
 // fills 1 KB).  Lane l lands at byte 16 l of the wave's part, so it fetches
 // the chunk that belongs there.  The buffer range ends with the last row
 // that counts: rows past it, and chunks past the head (whose offset is put
-// out of range), arrive as zeros.  Completion is tracked by vmcnt.
+// out of range), arrive as zeros.  Completion is tracked by vmcnt.  A load needs
+// a wait state after the write of m0, which the compiler does not add inside
+// asm.
 // NT: non-temporal, for rows that are read once (a cache of many gigabytes
 // pushes everything else out of the last-level cache, and waits for it).
 template <typename T, int DP, int ROWS, int NW, bool NT = false> struct Loader {
@@ -174,10 +176,10 @@ template <typename T, int DP, int ROWS, int NW, bool NT = false> struct Loader {
       const uint32_t m0v = __builtin_amdgcn_readfirstlane(lds + (j * NW + wave) * 1024);
       const int off = vo[j % VAR] + (j - j % VAR) * STEP * ldb;
       if constexpr (NT)
-        asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds" ::"s"(m0v), "v"(off), "s"(rs)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds" ::"s"(m0v), "v"(off), "s"(rs)
                      : "memory");
       else
-        asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(m0v), "v"(off), "s"(rs)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(m0v), "v"(off), "s"(rs)
                      : "memory");
     }
   }

@@ -105,7 +105,7 @@ __global__ __launch_bounds__(GB_NTH, 1) void k_gather_blocks(
         const int row = p0 / cpr, c0 = p0 % cpr;
         const uint32_t m0v = __builtin_amdgcn_readfirstlane(lds0 + row * pitch + c0 * 16);
         const int vo = row * W * 2 + (c0 + lane) * 16;
-        asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(m0v),
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(m0v),
                      "v"(vo), "s"(rs)
                      : "memory");
       }

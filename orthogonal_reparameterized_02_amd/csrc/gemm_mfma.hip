@@ -488,12 +488,13 @@ __global__ __launch_bounds__(256, 1) __attribute__((amdgpu_waves_per_eu(1, 1))) 
   // load q of slab `from` into the slot at byte offset slotb.  M0 (the LDS
   // destination) is set inside the same asm statement; nothing else in these
   // kernels reads M0 (no indirect register indexing, no LDS-DMA builtins),
-  // so the asm does not declare it.
+  // so the asm does not declare it.  The load needs a wait state after the
+  // write, which the compiler does not add inside asm.
 #define POETX_DMA1(slotb, from, q, vo, g, rs)                                                  \
   {                                                                                            \
     const uint32_t m0v_ =                                                                      \
         __builtin_amdgcn_readfirstlane(lds0 + (slotb) + ((q) * 4 + wave) * 1024);              \
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(m0v_),    \
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(m0v_), \
                  "v"(vo[(q) & 1] + (q) * (g) + (from) * 128), "s"(rs)                          \
                  : "memory");                                                                 \
   }
@@ -502,7 +503,7 @@ __global__ __launch_bounds__(256, 1) __attribute__((amdgpu_waves_per_eu(1, 1))) 
   {                                                                                            \
     const uint32_t m0v_ =                                                                      \
         __builtin_amdgcn_readfirstlane(lds0 + (slotb) + ((q) * 4 + wave) * 1024);              \
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(m0v_),    \
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(m0v_), \
                  "v"(voQ[q] + (from) * 64), "s"(rsB)                                           \
                  : "memory");                                                                 \
   }
@@ -511,7 +512,7 @@ __global__ __launch_bounds__(256, 1) __attribute__((amdgpu_waves_per_eu(1, 1))) 
   {                                                                                            \
     const uint32_t m0v_ =                                                                      \
         __builtin_amdgcn_readfirstlane(lds0 + (slotb) + ((q) * 4 + wave) * 1024);              \
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(m0v_),    \
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(m0v_), \
                  "v"(voN[q] + (from) * slabN), "s"(rsB)                                        \
                  : "memory");                                                                 \
   }
@@ -818,10 +819,10 @@ __global__ __launch_bounds__(256, 1) __attribute__((amdgpu_waves_per_eu(1, 1))) 
     const uint32_t m0v_ = __builtin_amdgcn_readfirstlane(                                     \
         lds0 + ((slot) % NSTG) * STG + ((q) * 4 + wave) * 1024);                              \
     if ((q) * 4 < A_BYTES / 1024)                                                             \
-      asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(m0v_),  \
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(m0v_), \
                    "v"(vo[q] + (from) * slabA), "s"(rsA) : "memory");                         \
     else                                                                                      \
-      asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(m0v_),  \
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(m0v_), \
                    "v"(vo[q] + (from) * slabB), "s"(rsB) : "memory");                         \
   }
   const int tk_l = 8 * (lane / 32) + (lane % 16) / 4;
