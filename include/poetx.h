@@ -455,8 +455,9 @@ int32_t poetx_dropout_bwd(int64_t n, int32_t act, const void* dy, void* dx, doub
  * Backward: delta = do.o;  dl = p (do.v - delta);  ds = dl (1 - tanh^2) scale;
  *   dq = sum ds k;  dk, dv sum over the query heads that share a key head.
  * slopes are constants (no gradient).  The bf16 path rounds p and ds to bf16
- * as matrix operands; sums, lse and delta are float32.  Results are
- * deterministic (no atomics).
+ * as matrix operands; sums, lse and delta are float32.  The same call gives
+ * the same bits (no atomics); Tq, Tk, ndoc and the heads decide the order of
+ * the sums, so a document's last bits may differ in another batch.
  *   scale <= 0 selects 1 / sqrt(D); cap = 0: no cap; slopes [Hq] or NULL.
  *   D a multiple of 8 up to 128; Hq a multiple of Hkv.  Tq and Tk are at most
  *   2^31 - 2^16, and tiles of 128 rows times heads fewer than 2^24 on a side.
@@ -506,7 +507,7 @@ int32_t poetx_attn_bwd(const poetx_attn_shape* sh, const void* dout, const void*
 
 /*
  * poetx_attn_decode -- the single-token form: one query row per sequence over
- * a cache, same scores as above.  Sequence b sees cache rows [start[b],
+ * a cache, same scores as above (bf16: p in two bf16 parts).  Sequence b sees cache rows [start[b],
  * len[b]) (start NULL: 0; both clamped to [0, rows]); its query stands at
  * position len[b] - 1.  An empty range gives o = 0.
  *   q, o [B][Hq][D] (pitches ldq, ldo); row j of sequence b of the caches

@@ -49,7 +49,9 @@ inline long loop_rows(int others, int own, int ndoc) {
 // is waited for longer: up to four a CU (two documents of 1024, 16 heads of
 // 64: 330 us with four, 354 with eight), in parts of `least` rows, a
 // tile of their kernels (765 tokens in 9 documents, 5 heads on 1: 173 us in
-// parts of 256 rows, 70 of 64).
+// parts of 256 rows, 70 of 64).  All tiles of a launch get the same number,
+// from the mean loop: one long document beside many tiny ones is taken for
+// short loops.
 template <typename T> int parts_for(long groups, long rows, int least) {
   if (groups < 1) return 1;
   const auto cut = [&](long fill, long rows_a_part) {

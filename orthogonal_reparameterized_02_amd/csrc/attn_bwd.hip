@@ -11,10 +11,13 @@
 // (float32 operands would take eight times as long), and delta comes from the
 // stored, rounded o: of a relative error of 2.6e-3 in dq and dk, the rounding
 // of the result itself makes 1.7e-3, that of ds as much again, delta 1.1e-3.
+// ds in two bf16 parts would leave 1.9e-3 (with a bias 2.3e-3), for two products
+// more beside seven: a training pass of 9 documents 414 -> 462 us, of one 2235
+// -> 2591 us.
 //
 // Measured (bf16, D 128, 32 heads on 8): 8192 causal tokens in one document
 // 1.75 ms for both passes, dq at 1.19 and dk, dv at 1.06 PFLOP/s of the products
-// they form, at the power limit; in 9 documents 315 us, a fifth of the wave
+// they form, at the power limit; in 9 documents 320 us, a fifth of the wave
 // slots empty as in the forward pass.  float32, D 64, two documents of 1024,
 // 16 heads on 4, capped: 225 us, a third of the float32 matrix rate.
 #include <algorithm>
@@ -43,7 +46,8 @@ template <typename T, int DP> struct DqCfg {
 // NQ = 1: four waves, two workgroups a CU, one's start and end beside the
 // other's loop.  A wave holds two 32-row sums, keys and values; with 128 bf16
 // columns that is a few registers more than two waves a SIMD have: the values
-// stay in LDS.
+// stay in LDS, and three forms still spill one to three registers (NQ = 1
+// plain; cap and bias together).
 template <typename T, int DP, int NQ> struct DkvCfg {
   static constexpr bool VLDS = sizeof(T) == 2 && DP == 128;
   static constexpr int VS = 64;                        // a wave's load fills 64 values

@@ -9,13 +9,19 @@
 // the other keys, and the probabilities are the next product's operand
 // without leaving their lane.
 //
+// bf16 rounds the probabilities to bf16 as that operand: o is off by 2.1e-3
+// (2-norm) where its own rounding makes 1.6e-3.  In two parts, as decoding has
+// them, they would cost a third product beside two: 95 -> 118 us for the 9
+// documents below, 517 -> 709 us for the one, 610 -> 774 us capped.
+//
 // Measured (bf16, D 128): 8192 causal tokens in one document, 32 heads on 8,
-// 515 us = 1.07 PFLOP/s, where the library's 8192^3 product reaches 1.30: the
-// matrix pipes are busy 0.56 of the cycles at a clock that the power limit
-// holds at 1.5 GHz.  In 9 documents 95 us = 0.75 PFLOP/s: a fifth of the wave
-// slots stands empty at the starts and ends of the short loops.  Capped, 2048
-// queries on 16384 keys, 620 us = 0.83 PFLOP/s: bound by vector instructions,
-// three transcendentals a score (16 issue cycles each) beside four others.
+// 515 us = 1.07 PFLOP/s, where the library's 8192^3 product reaches 1.30; with
+// counters 533 us, matrix pipes busy 0.55 of the cycles at a clock that the
+// power limit holds at 1.8 GHz, 1.5 in later launches.  In 9 documents 94 us =
+// 0.75 PFLOP/s: a fifth of the wave slots stands empty at the starts and ends
+// of the short loops.  Capped, 2048 queries on 16384 keys, 611 us = 0.84
+// PFLOP/s: bound by vector instructions, three transcendentals a score (16
+// issue cycles each) beside four others.
 #include <algorithm>
 
 #include "attn_rows.h"

@@ -301,7 +301,9 @@ template <int N, int DEPTH> struct Pipe {
 // 2^-23 (lse off by 1e-4 at a cap of 1024; at 1e6 o is off by 3%, at 1e8
 // nothing is left of the scores), up to a cap of 128 below 2^-16, that of a
 // float32 lse of a hundred.  Wider caps, and float32, take tanh itself: near
-// 0 an odd polynomial (least squares on [0, 0.65], relative error 8e-8).
+// 0 an odd polynomial (least squares on [0, 0.65], relative error 8e-8).  By r
+// against tanh (caps of 128 and 200): 2048 queries on 16384 keys 614 and 739
+// us, training on 9 documents 479 and 551, 16 long decoded sequences 234, 237.
 constexpr float CAP_R_MAX = 128.0f;
 template <typename T, int MODE> constexpr bool cap_by_r = (MODE & 1) && !(MODE & 4) && sizeof(T) == 2;
 
