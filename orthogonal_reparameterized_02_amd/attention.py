@@ -211,9 +211,12 @@ class KVCache:
         self._lengths: Optional[list] = [0] * B
         self._at = torch.arange(B, device=device)
 
+    def _captured(self) -> bool:
+        return self.k.is_cuda and torch.cuda.is_current_stream_capturing()
+
     def longest(self) -> Optional[int]:
         """Tokens of the longest sequence; None while a graph is captured."""
-        if torch.cuda.is_current_stream_capturing():
+        if self._captured():
             return None
         return max(self.length.tolist() if self._lengths is None else self._lengths, default=0)
 
@@ -224,7 +227,7 @@ class KVCache:
             raise ValueError(f"{n} tokens do not fit a cache of {self.rows} rows")
         self.k[b, :n], self.v[b, :n] = k, v
         self.length[b] = n
-        if torch.cuda.is_current_stream_capturing():
+        if self._captured():
             self._lengths = None
         elif self._lengths is not None:
             self._lengths[b] = n
