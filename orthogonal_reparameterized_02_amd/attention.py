@@ -207,8 +207,10 @@ class KVCache:
         self.v = torch.empty_like(self.k)
         self.length = torch.zeros(B, dtype=torch.int32, device=device)
         self.B, self.rows = B, rows
-        # the same on the host, so that no token waits for the GPU; None: replays may have changed it
-        self._lengths: Optional[list] = [0] * B
+        # the same on the host, so that no token waits for the GPU: each length less the tokens appended
+        # to all, and the largest of them.  None: replays may have changed it
+        self._filled: Optional[list] = [0] * B
+        self._most, self._appended = 0, 0
         self._at = torch.arange(B, device=device)
 
     def _captured(self) -> bool:
@@ -218,7 +220,9 @@ class KVCache:
         """Tokens of the longest sequence; None while a graph is captured."""
         if self._captured():
             return None
-        return max(self.length.tolist() if self._lengths is None else self._lengths, default=0)
+        if self._filled is None or self.B == 0:
+            return max(self.length.tolist(), default=0)
+        return self._most + self._appended
 
     def fill(self, b: int, k: torch.Tensor, v: torch.Tensor) -> None:
         """Sequence b becomes k, v [n][Hkv][D] (a prompt's)."""
@@ -228,9 +232,10 @@ class KVCache:
         self.k[b, :n], self.v[b, :n] = k, v
         self.length[b] = n
         if self._captured():
-            self._lengths = None
-        elif self._lengths is not None:
-            self._lengths[b] = n
+            self._filled = None
+        elif self._filled is not None:
+            self._filled[b] = n - self._appended
+            self._most = max(self._filled)
 
     def append(self, k: torch.Tensor, v: torch.Tensor) -> None:
         """One token more for every sequence: k, v [B][Hkv][D]."""
@@ -243,13 +248,12 @@ class KVCache:
         at = self.length.long()
         self.k[self._at, at], self.v[self._at, at] = k, v
         self.length += 1
-        if self._lengths is not None:
-            self._lengths = [m + 1 for m in self._lengths]
+        self._appended += 1
 
     def _append_where_room(self, k: torch.Tensor, v: torch.Tensor) -> None:
         """append for a graph: what a replay finds full is written back as it
         was, so no replay writes outside the cache."""
-        self._lengths = None
+        self._filled = None
         at, full = self.length.clamp(0, self.rows - 1).long(), (self.length >= self.rows)[:, None, None]
         for rows, new in ((self.k, k), (self.v, v)):
             rows[self._at, at] = torch.where(full, rows[self._at, at], new)
