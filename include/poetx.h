@@ -414,6 +414,41 @@ int32_t poetx_rope(const poetx_rope_shape* sh, const void* q, const void* k, con
                    const float* table, void* qo, void* ko, poetx_stream_t stream);
 
 /*
+ * poetx_qk_norm_rope_fwd / poetx_qk_norm_rope_bwd -- root mean square norms of
+ * the heads of q and k, and the rotary positions of poetx_rope, in one pass:
+ *   r = 1 / sqrt(mean x^2 + eps) over the D elements of a head,
+ *   y = turn(x r w),
+ * with weights wq, wk [D] float32 that all heads of a tensor share (NULL: 1).
+ * Sums are float32 (a head whose squares pass its range, |x| above 2^63, is
+ * not normed); each output is rounded once.  rot = 0: norms alone, pos and
+ * table are not read.
+ *   fwd: q [T][Hq][D] -> qo, k [T][Hk][D] -> ko (Hk = 0: k, ko NULL); qo = q
+ *   and ko = k (same pitch) work in place.  A position outside the table
+ *   reads nothing and writes NaN to the turned part of its row.
+ *   bwd: dqo, dko gradients of the outputs (pitches ldqo, ldko), q and k the
+ *   forward's inputs -> dq, dk (pitches lddq, lddk; dq = dqo and dk = dko work
+ *   in place) and dwq, dwk [D] float32, overwritten (NULL: not wanted; T = 0:
+ *   zero).  A position outside the table gives NaN in its rows and in dwq, dwk.
+ *   The same call gives the same bits (no atomics).
+ *   ws poetx_qk_norm_rope_workspace_bytes(sh) bytes.
+ * D a multiple of 8 up to 512, rot even, 0 <= rot <= D, eps >= 0.
+ * Errors: ERR_ARG, ERR_WORKSPACE, ERR_DEVICE.
+ */
+typedef struct {
+  int32_t T, Hq, Hk, D, rot, P, act, interleaved;
+  float eps;
+  int64_t ldq, ldk, ldqo, ldko, lddq, lddk;
+} poetx_qk_norm_shape;
+size_t poetx_qk_norm_rope_workspace_bytes(const poetx_qk_norm_shape* sh);
+int32_t poetx_qk_norm_rope_fwd(const poetx_qk_norm_shape* sh, const void* q, const void* k, const float* wq,
+                               const float* wk, const int32_t* pos, const float* table, void* qo, void* ko,
+                               poetx_stream_t stream);
+int32_t poetx_qk_norm_rope_bwd(const poetx_qk_norm_shape* sh, const void* dqo, const void* dko, const void* q,
+                               const void* k, const float* wq, const float* wk, const int32_t* pos,
+                               const float* table, void* dq, void* dk, float* dwq, float* dwk, void* ws,
+                               size_t ws_bytes, poetx_stream_t stream);
+
+/*
  * poetx_dropout_fwd / poetx_dropout_bwd -- dropout whose mask is never
  * stored, with the residual sum:
  *   y[i] = residual[i] + (keep(i) ? x[i] * g : 0),   dx[i] = keep(i) ? dy[i] * g : 0

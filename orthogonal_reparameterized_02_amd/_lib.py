@@ -45,6 +45,9 @@ SIGNATURES = {
     "poetx_set_stage_events": (_i, [_p, _i]),
     "poetx_set_fused_gather": (_i, [_i]),
     "poetx_rope": (_i, [_p, _p, _p, _p, _p, _p, _p, _p]),
+    "poetx_qk_norm_rope_workspace_bytes": (_sz, [_p]),
+    "poetx_qk_norm_rope_fwd": (_i, [_p] * 10),
+    "poetx_qk_norm_rope_bwd": (_i, [_p] * 14 + [_sz, _p]),
     "poetx_dropout_fwd": (_i, [_i64, _i, _p, _p, _p, _d, _u64, _u64, _p, _p]),
     "poetx_dropout_bwd": (_i, [_i64, _i, _p, _p, _d, _u64, _u64, _p, _p]),
     "poetx_attn_plan_bytes": (_sz, [_p]),
@@ -74,6 +77,8 @@ def _struct(name: str, ints: str, floats: str, longs: str):
 
 RopeShape = _struct("RopeShape", "T Hq Hk D rot P act interleaved inverse", "",
                     "ldq ldk ldqo ldko")
+QkNormShape = _struct("QkNormShape", "T Hq Hk D rot P act interleaved", "eps",
+                      "ldq ldk ldqo ldko lddq lddk")
 AttnShape = _struct("AttnShape", "Tq Tk ndoc Hq Hkv D act causal", "scale cap",
                     "ldq ldk ldv ldo lddo lddq lddk lddv")
 DecodeShape = _struct("DecodeShape", "B Hq Hkv D act rows", "scale cap",

@@ -197,6 +197,38 @@ int32_t check_dropout(const char* fn, int64_t n, int32_t act, double p, uint64_t
 // p as a threshold for 16-bit draws
 uint32_t cut_of(double p) { return (uint32_t)lrint(p * 65536.0); }
 
+int32_t check_qk_norm(const char* fn, const poetx_qk_norm_shape* sh, bool back) {
+  if (!sh) return fail(POETX_ERR_ARG, "%s: null shape", fn);
+  if (sh->T < 0 || sh->Hq < 1 || sh->Hk < 0 || sh->Hq > H_MAX || sh->Hk > H_MAX)
+    return fail(POETX_ERR_ARG, "%s: T=%d Hq=%d Hk=%d", fn, sh->T, sh->Hq, sh->Hk);
+  if (sh->D < 8 || sh->D % 8 || sh->D > ROPE_D_MAX)
+    return fail(POETX_ERR_ARG, "%s: D=%d must be a multiple of 8, 8..%d", fn, sh->D, ROPE_D_MAX);
+  if (sh->rot < 0 || sh->rot % 2 || sh->rot > sh->D)
+    return fail(POETX_ERR_ARG, "%s: rot=%d must be even, 0..D=%d", fn, sh->rot, sh->D);
+  if (sh->rot && sh->P < 1) return fail(POETX_ERR_ARG, "%s: P=%d positions", fn, sh->P);
+  TRY(check_act(fn, sh->act));
+  if (!(sh->eps >= 0.0f) || !isfinite(sh->eps)) return fail(POETX_ERR_ARG, "%s: eps=%g must be finite and >= 0", fn, sh->eps);
+  const int64_t wq = (int64_t)sh->Hq * sh->D, wk = (int64_t)sh->Hk * sh->D;
+  TRY(check_ld(fn, "ldq", sh->ldq, wq));
+  TRY(check_ld(fn, "ldqo", sh->ldqo, wq));
+  if (back) TRY(check_ld(fn, "lddq", sh->lddq, wq));
+  if (sh->Hk) {
+    TRY(check_ld(fn, "ldk", sh->ldk, wk));
+    TRY(check_ld(fn, "ldko", sh->ldko, wk));
+    if (back) TRY(check_ld(fn, "lddk", sh->lddk, wk));
+  }
+  return POETX_OK;
+}
+
+QkNormArgs qk_norm_args(const poetx_qk_norm_shape* sh) {
+  QkNormArgs a = {};
+  a.T = sh->T, a.Hq = sh->Hq, a.Hk = sh->Hk, a.D = sh->D, a.rot = sh->rot, a.P = sh->P;
+  a.interleaved = sh->interleaved && sh->rot;
+  a.eps = sh->eps, a.inv_d = 1.0f / (float)sh->D;
+  a.ldq = sh->ldq, a.ldk = sh->ldk, a.ldqo = sh->ldqo, a.ldko = sh->ldko, a.lddq = sh->lddq, a.lddk = sh->lddk;
+  return a;
+}
+
 int32_t launched(hipError_t e, const char* fn) { return e == hipSuccess ? ok() : dev_fail(e, fn); }
 
 }  // namespace
@@ -238,6 +270,77 @@ int32_t poetx_rope(const poetx_rope_shape* sh, const void* q, const void* k, con
                       ? launch_rope<bf16>(a, (const bf16*)q, (const bf16*)k, (bf16*)qo, (bf16*)ko, s)
                       : launch_rope<float>(a, (const float*)q, (const float*)k, (float*)qo, (float*)ko, s),
                   fn);
+}
+
+int32_t poetx_qk_norm_rope_fwd(const poetx_qk_norm_shape* sh, const void* q, const void* k, const float* wq,
+                               const float* wk, const int32_t* pos, const float* table, void* qo, void* ko,
+                               poetx_stream_t stream) {
+  const char* fn = "poetx_qk_norm_rope_fwd";
+  TRY(check_qk_norm(fn, sh, false));
+  if (sh->T == 0) return ok();
+  NEED_PTR(q);
+  NEED_PTR(qo);
+  OPT_PTR(wq);
+  if (sh->Hk) {
+    NEED_PTR(k);
+    NEED_PTR(ko);
+    OPT_PTR(wk);
+  }
+  if (sh->rot) {
+    NEED_PTR(pos);
+    NEED_PTR(table);
+  }
+  if ((q == qo && sh->ldq != sh->ldqo) || (sh->Hk && k == ko && sh->ldk != sh->ldko))
+    return fail(POETX_ERR_ARG, "%s: in place needs equal pitches", fn);
+  QkNormArgs a = qk_norm_args(sh);
+  a.q = q, a.k = k, a.wq = wq, a.wk = wk, a.pos = sh->rot ? pos : nullptr, a.table = table, a.qo = qo, a.ko = ko;
+  const hipStream_t s = (hipStream_t)stream;
+  return launched(sh->act == POETX_BF16 ? launch_qk_norm_fwd<bf16>(a, s) : launch_qk_norm_fwd<float>(a, s), fn);
+}
+
+size_t poetx_qk_norm_rope_workspace_bytes(const poetx_qk_norm_shape* sh) {
+  return check_qk_norm("poetx_qk_norm_rope_workspace_bytes", sh, false) == POETX_OK
+             ? align_up(qk_norm_ws_bytes(qk_norm_args(sh))) : 0;
+}
+
+int32_t poetx_qk_norm_rope_bwd(const poetx_qk_norm_shape* sh, const void* dqo, const void* dko, const void* q,
+                               const void* k, const float* wq, const float* wk, const int32_t* pos,
+                               const float* table, void* dq, void* dk, float* dwq, float* dwk, void* ws,
+                               size_t ws_bytes, poetx_stream_t stream) {
+  const char* fn = "poetx_qk_norm_rope_bwd";
+  TRY(check_qk_norm(fn, sh, true));
+  if (sh->T) {
+    NEED_PTR(dqo);
+    NEED_PTR(q);
+    NEED_PTR(dq);
+    if (sh->Hk) {
+      NEED_PTR(dko);
+      NEED_PTR(k);
+      NEED_PTR(dk);
+    }
+    if (sh->rot) {
+      NEED_PTR(pos);
+      NEED_PTR(table);
+    }
+  }
+  OPT_PTR(wq);
+  OPT_PTR(dwq);
+  if (sh->Hk) {
+    OPT_PTR(wk);
+    OPT_PTR(dwk);
+  }
+  if (!sh->T && !dwq && !(sh->Hk && dwk)) return ok();
+  NEED_PTR(ws);
+  if (sh->T && ((dqo == dq && sh->ldqo != sh->lddq) || (sh->Hk && dko == dk && sh->ldko != sh->lddk)))
+    return fail(POETX_ERR_ARG, "%s: in place needs equal pitches", fn);
+  QkNormArgs a = qk_norm_args(sh);
+  const size_t need = align_up(qk_norm_ws_bytes(a));
+  if (ws_bytes < need) return fail(POETX_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, ws_bytes, need);
+  a.q = q, a.k = k, a.wq = wq, a.wk = wk, a.pos = sh->rot ? pos : nullptr, a.table = table;
+  a.gq = dqo, a.gk = dko, a.dq = dq, a.dk = dk, a.dwq = dwq, a.dwk = sh->Hk ? dwk : nullptr;
+  const hipStream_t s = (hipStream_t)stream;
+  return launched(sh->act == POETX_BF16 ? launch_qk_norm_bwd<bf16>(a, (float*)ws, s)
+                                        : launch_qk_norm_bwd<float>(a, (float*)ws, s), fn);
 }
 
 int32_t poetx_dropout_fwd(int64_t n, int32_t act, const void* x, const void* residual, void* y,

@@ -24,6 +24,26 @@ struct RopeArgs {
 template <typename TS>
 hipError_t launch_rope(const RopeArgs& a, const TS* q, const TS* k, TS* qo, TS* ko, hipStream_t s);
 
+// ---- norms of queries and keys with rotary positions (qk_norm.hip) -----------
+struct QkNormArgs {
+  int T, Hq, Hk, D, rot, P, interleaved;
+  float eps, inv_d;
+  long ldq, ldk, ldqo, ldko, lddq, lddk;  // backward: ldqo, ldko of gq, gk
+  const void *q, *k;
+  const float *wq, *wk;  // or null: 1
+  const int* pos;
+  const float* table;
+  void *qo, *ko;
+  // backward
+  const void *gq, *gk;
+  void *dq, *dk;
+  float *dwq, *dwk;      // or null
+};
+// ws: qk_norm_ws_bytes(a) bytes for partial sums of dwq, dwk
+size_t qk_norm_ws_bytes(const QkNormArgs& a);
+template <typename TS> hipError_t launch_qk_norm_fwd(const QkNormArgs& a, hipStream_t s);
+template <typename TS> hipError_t launch_qk_norm_bwd(const QkNormArgs& a, float* ws, hipStream_t s);
+
 // ---- dropout (dropout.hip) --------------------------------------------------
 // out[i] = (res ? res[i] : 0) + (keep(i) ? x[i] * gain : 0)
 template <typename TS>

@@ -13,8 +13,8 @@ from typing import Optional
 
 import torch
 
-from ._lib import (AttnShape, BF16, DecodeShape, F32, I8, PoetxError, RopeShape, Shape,  # noqa: F401
-                   check, lib)
+from ._lib import (AttnShape, BF16, DecodeShape, F32, I8, PoetxError, QkNormShape, RopeShape,  # noqa: F401
+                   Shape, check, lib)
 
 _DT = {F32: torch.float32, BF16: torch.bfloat16}
 
@@ -319,6 +319,69 @@ def poetx_rope(q, k, pos, table, qo, ko, interleaved: bool = False, inverse: boo
     check("poetx_rope", lib().poetx_rope(
         C.byref(sh), qp, kp, _vec(pos, "pos", torch.int32, T),
         _vec(table, "table", torch.float32, table.numel()), qop, kop, _stream(stream)))
+
+
+def qk_norm_shape(q, k, table, eps: float = 1e-6, interleaved: bool = False) -> QkNormShape:
+    """Shape of norms and rotary positions of q [T][Hq][D] and k [T][Hk][D]
+    (k may be None) with table [P][rot/2][2] (None: norms alone); pitches are
+    set by the calls."""
+    T, Hq, D = q.shape
+    if table is not None and (table.dim() != 3 or table.shape[2] != 2):
+        raise ValueError(f"table has shape {tuple(table.shape)}, expected [P][rot/2][2]")
+    rot, positions = (0, 0) if table is None else (2 * table.shape[1], table.shape[0])
+    Hk = 0 if k is None else k.shape[1]
+    wq, wk = Hq * D, Hk * D
+    return QkNormShape(T, Hq, Hk, D, rot, positions, act_of(q.dtype), int(interleaved), eps, wq, wk, wq, wk, wq, wk)
+
+
+def poetx_qk_norm_rope_workspace_bytes(sh: QkNormShape) -> int:
+    return lib().poetx_qk_norm_rope_workspace_bytes(C.byref(sh))
+
+
+def _turned_by(sh: QkNormShape, pos, table):
+    """pos and table of a call that turns; none of one that norms alone."""
+    if table is None:
+        return None, None
+    return _vec(pos, "pos", torch.int32, sh.T), _vec(table, "table", torch.float32, table.numel())
+
+
+def poetx_qk_norm_rope_fwd(q, k, wq, wk, pos, table, qo, ko, eps: float = 1e-6, interleaved: bool = False,
+                           stream=None) -> None:
+    """Norms of the heads of q [T][Hq][D] and k [T][Hk][D] (k, ko may be None)
+    times wq, wk [D] (None: 1), then turned by table [P][rot/2][2] at pos [T]
+    (table None: not turned)."""
+    sh = qk_norm_shape(q, k, table, eps, interleaved)
+    fq, fk = (sh.T, sh.Hq, sh.D), (sh.T, sh.Hk, sh.D)
+    qp, sh.ldq = _rows(q, "q", fq, q.dtype)
+    qop, sh.ldqo = _rows(qo, "qo", fq, q.dtype)
+    kp = kop = None
+    if k is not None:
+        kp, sh.ldk = _rows(k, "k", fk, q.dtype)
+        kop, sh.ldko = _rows(ko, "ko", fk, q.dtype)
+    check("poetx_qk_norm_rope_fwd", lib().poetx_qk_norm_rope_fwd(
+        C.byref(sh), qp, kp, _vec(wq, "wq", torch.float32, sh.D, optional=True),
+        _vec(wk, "wk", torch.float32, sh.D, optional=True), *_turned_by(sh, pos, table), qop, kop, _stream(stream)))
+
+
+def poetx_qk_norm_rope_bwd(dqo, dko, q, k, wq, wk, pos, table, dq, dk, dwq, dwk, ws, eps: float = 1e-6,
+                           interleaved: bool = False, stream=None) -> None:
+    """Gradients of the forward call with the same inputs; dwq, dwk [D]
+    float32 (None: not wanted)."""
+    sh = qk_norm_shape(q, k, table, eps, interleaved)
+    fq, fk = (sh.T, sh.Hq, sh.D), (sh.T, sh.Hk, sh.D)
+    qp, sh.ldq = _rows(q, "q", fq, q.dtype)
+    gqp, sh.ldqo = _rows(dqo, "dqo", fq, q.dtype)
+    dqp, sh.lddq = _rows(dq, "dq", fq, q.dtype)
+    kp = gkp = dkp = None
+    if k is not None:
+        kp, sh.ldk = _rows(k, "k", fk, q.dtype)
+        gkp, sh.ldko = _rows(dko, "dko", fk, q.dtype)
+        dkp, sh.lddk = _rows(dk, "dk", fk, q.dtype)
+    wp, wb = _ws(ws, poetx_qk_norm_rope_workspace_bytes(sh))
+    vec = lambda t, n: _vec(t, n, torch.float32, sh.D, optional=True)
+    check("poetx_qk_norm_rope_bwd", lib().poetx_qk_norm_rope_bwd(
+        C.byref(sh), gqp, gkp, qp, kp, vec(wq, "wq"), vec(wk, "wk"), *_turned_by(sh, pos, table), dqp, dkp,
+        vec(dwq, "dwq"), vec(dwk, "dwk"), wp, wb, _stream(stream)))
 
 
 def poetx_dropout_fwd(x, residual, y, p: float, seed: int, offset: int = 0, offset_dev=None,
