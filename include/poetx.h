@@ -541,6 +541,29 @@ int32_t poetx_attn_bwd(const poetx_attn_shape* sh, const void* dout, const void*
                        poetx_stream_t stream);
 
 /*
+ * Attention with a window and sinks: as above, but a query at position p sees
+ * only keys closer than `window` (causal: p - window < j <= p, otherwise
+ * |p - j| < window) and the first `sinks` keys of its document (causal: those
+ * at j <= p).  There are no prefixes.  window = 0: no window (sinks is then
+ * without meaning), the calls are those above.
+ *   window >= 0; 0 <= sinks <= 128; ndoc sinks Hkv < 2^22.
+ * plan, workspace and calls take the same window; everything else, errors
+ * included, as in poetx_attn_plan, _fwd and _bwd.
+ */
+typedef struct { int32_t window, sinks; } poetx_window;
+size_t poetx_attn_window_plan_bytes(const poetx_attn_shape* sh, const poetx_window* win);
+size_t poetx_attn_window_workspace_bytes(const poetx_attn_shape* sh, const poetx_window* win, int32_t which);
+int32_t poetx_attn_window_plan(const poetx_attn_shape* sh, const poetx_window* win, const int32_t* cu_q,
+                               const int32_t* cu_k, void* plan, size_t plan_bytes, poetx_stream_t stream);
+int32_t poetx_attn_window_fwd(const poetx_attn_shape* sh, const poetx_window* win, const void* q, const void* k,
+                              const void* v, const float* slopes, const void* plan, void* o, float* lse,
+                              void* ws, size_t ws_bytes, poetx_stream_t stream);
+int32_t poetx_attn_window_bwd(const poetx_attn_shape* sh, const poetx_window* win, const void* dout, const void* q,
+                              const void* k, const void* v, const void* o, const float* lse, const float* slopes,
+                              const void* plan, void* dq, void* dk, void* dv, void* ws, size_t ws_bytes,
+                              poetx_stream_t stream);
+
+/*
  * poetx_attn_decode -- the single-token form: one query row per sequence over
  * a cache, same scores as above (bf16: p in two bf16 parts).  Sequence b sees cache rows [start[b],
  * len[b]) (start NULL: 0; both clamped to [0, rows]); its query stands at

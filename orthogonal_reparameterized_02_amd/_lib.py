@@ -55,6 +55,11 @@ SIGNATURES = {
     "poetx_attn_plan": (_i, [_p, _p, _p, _p, _p, _sz, _p]),
     "poetx_attn_fwd": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _p, _sz, _p]),
     "poetx_attn_bwd": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _sz, _p]),
+    "poetx_attn_window_plan_bytes": (_sz, [_p, _p]),
+    "poetx_attn_window_workspace_bytes": (_sz, [_p, _p, _i]),
+    "poetx_attn_window_plan": (_i, [_p, _p, _p, _p, _p, _sz, _p]),
+    "poetx_attn_window_fwd": (_i, [_p] * 10 + [_sz, _p]),
+    "poetx_attn_window_bwd": (_i, [_p] * 14 + [_sz, _p]),
     "poetx_attn_decode_workspace_bytes": (_sz, [_p]),
     "poetx_attn_decode": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _p, _sz, _p]),
 }
@@ -81,6 +86,7 @@ QkNormShape = _struct("QkNormShape", "T Hq Hk D rot P act interleaved", "eps",
                       "ldq ldk ldqo ldko lddq lddk")
 AttnShape = _struct("AttnShape", "Tq Tk ndoc Hq Hkv D act causal", "scale cap",
                     "ldq ldk ldv ldo lddo lddq lddk lddv")
+Window = _struct("Window", "window sinks", "", "")
 DecodeShape = _struct("DecodeShape", "B Hq Hkv D act rows", "scale cap",
                       "ldq ldo ldk ldv bsk bsv")
 

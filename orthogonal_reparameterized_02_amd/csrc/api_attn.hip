@@ -17,6 +17,7 @@ constexpr int D_MAX = 128;       // attention head width
 constexpr int ROPE_D_MAX = 512;
 constexpr int H_MAX = 1024;      // heads
 constexpr int B_MAX = 65535;     // sequences of a decode call
+constexpr int SINKS_MAX = 128;   // first tokens that stay visible past a window
 // packed rows, cache rows: a tile, or a piece of a cut loop, past the last one
 // is still an int
 constexpr int ROWS_MAX = INT32_MAX - 65535;
@@ -91,23 +92,46 @@ constexpr int SORT_TILES = 16;
 
 bool sorts(const poetx_attn_shape* sh) { return attn_tiles(std::max(sh->Tq, sh->Tk)) >= SORT_TILES; }
 
-// Five int32 arrays and the tile tables, each rounded up to 256 bytes.
-struct PlanSizes { size_t q, k, tq, tk, total; };
-PlanSizes plan_sizes(const poetx_attn_shape* sh) {
+// A window that hides something, and its sinks; {0, 0}: none.
+const poetx_window NO_WINDOW = {0, 0};
+int32_t check_window(const char* fn, const poetx_window* w) {
+  if (!w) return fail(POETX_ERR_ARG, "%s: null window", fn);
+  if (w->window < 0) return fail(POETX_ERR_ARG, "%s: window=%d must be >= 0", fn, w->window);
+  if (w->sinks < 0 || w->sinks > SINKS_MAX) return fail(POETX_ERR_ARG, "%s: sinks=%d outside 0..%d", fn, w->sinks, SINKS_MAX);
+  return POETX_OK;
+}
+poetx_window window_of(const poetx_window* w) { return w->window ? *w : NO_WINDOW; }
+
+int32_t check_attn_window(const char* fn, const poetx_attn_shape* sh, const poetx_window* w, bool back) {
+  TRY(check_attn(fn, sh, back));
+  TRY(check_window(fn, w));
+  // a workgroup of 1024 threads a sink, a dispatch 2^32 - 1 of them at most
+  if ((int64_t)sh->ndoc * window_of(w).sinks * sh->Hkv >= 1 << 22)
+    return fail(POETX_ERR_ARG, "%s: ndoc=%d documents of sinks=%d and Hkv=%d heads: 2^22 or more", fn, sh->ndoc, w->sinks, sh->Hkv);
+  return POETX_OK;
+}
+
+// Five int32 arrays and the tile tables, with sinks four arrays more, each
+// rounded up to 256 bytes.
+struct PlanSizes { size_t q, k, tq, tk, sink, far, first, doc, total; };
+PlanSizes plan_sizes(const poetx_attn_shape* sh, const poetx_window& w) {
   PlanSizes z;
   z.q = align_up((size_t)sh->Tq * 4);
   z.k = align_up((size_t)sh->Tk * 4);
   z.tq = align_up((size_t)attn_tiles(sh->Tq) * 16);
   z.tk = align_up((size_t)attn_tiles(sh->Tk) * 16);
-  z.total = 3 * z.q + 2 * z.k + (sorts(sh) ? 2 : 1) * (z.tq + z.tk) + 256;
+  z.sink = w.sinks ? align_up((size_t)sh->Tq * 8) : 0;
+  z.far = w.sinks ? align_up((size_t)attn_tiles(sh->Tq) * 8) : 0;
+  z.first = w.sinks ? align_up((size_t)attn_tiles(sh->Tq) * 4) : 0;
+  z.doc = w.sinks ? align_up((size_t)sh->ndoc * 16) : 0;
+  z.total = 3 * z.q + 2 * z.k + (sorts(sh) ? 2 : 1) * (z.tq + z.tk) + z.sink + z.far + z.first + z.doc + 256;
   return z;
 }
-size_t plan_bytes_of(const poetx_attn_shape* sh) { return plan_sizes(sh).total; }
 
-AttnPlan plan_at(const poetx_attn_shape* sh, const void* plan) {
+AttnPlan plan_at(const poetx_attn_shape* sh, const poetx_window& w, const void* plan) {
   char* p = (char*)const_cast<void*>(plan);
-  const PlanSizes z = plan_sizes(sh);
-  AttnPlan pl;
+  const PlanSizes z = plan_sizes(sh, w);
+  AttnPlan pl = {};
   pl.row_lo = (int*)p;
   pl.row_hi = (int*)(p + z.q);
   pl.row_pos = (int*)(p + 2 * z.q);
@@ -120,11 +144,18 @@ AttnPlan plan_at(const poetx_attn_shape* sh, const void* plan) {
     pl.qtab = (int4*)(t + z.tq + z.tk);
     pl.ktab = (int4*)(t + 2 * z.tq + z.tk);
   }
+  if (w.sinks) {
+    char* u = p + z.total - 256 - z.sink - z.far - z.first - z.doc;
+    pl.row_sink = (int2*)u;
+    pl.qfar = (int2*)(u + z.sink);
+    pl.tile_doc = (int*)(u + z.sink + z.far);
+    pl.doc = (int4*)(u + z.sink + z.far + z.first);
+  }
   return pl;
 }
 
-AttnArgs args_of(const poetx_attn_shape* sh, const void* q, const void* k, const void* v,
-                 const float* slopes, const void* plan) {
+AttnArgs args_of(const poetx_attn_shape* sh, const poetx_window& w, const void* q, const void* k,
+                 const void* v, const float* slopes, const void* plan) {
   AttnArgs a = {};
   a.Tq = sh->Tq, a.Tk = sh->Tk, a.Hq = sh->Hq, a.Hkv = sh->Hkv, a.D = sh->D;
   a.group = sh->Hq / sh->Hkv;
@@ -134,21 +165,23 @@ AttnArgs args_of(const poetx_attn_shape* sh, const void* q, const void* k, const
   a.ldq = sh->ldq, a.ldk = sh->ldk, a.ldv = sh->ldv, a.ldo = sh->ldo;
   a.lddo = sh->lddo, a.lddq = sh->lddq, a.lddk = sh->lddk, a.lddv = sh->lddv;
   a.q = q, a.k = k, a.v = v;
-  a.pl = plan_at(sh, plan);
-  a.ndoc = sh->ndoc;
+  a.pl = plan_at(sh, w, plan);
+  a.ndoc = sh->ndoc, a.causal = sh->causal;
+  a.window = w.window, a.sinks = w.sinks;
   return a;
 }
 
-// backward: delta and lse2, [Hq][Tq] float32 each; then partial sums (its
-// workspace is large enough for the forward pass too)
+// backward: delta and lse2, [Hq][Tq] float32 each; then partial sums, those of
+// the sinks last (its workspace is large enough for the forward pass too)
 size_t row_bytes(const poetx_attn_shape* sh) { return align_up((size_t)sh->Hq * sh->Tq * 4); }
-size_t attn_ws(const poetx_attn_shape* sh, int which) {
-  const AttnArgs a = args_of(sh, nullptr, nullptr, nullptr, nullptr, nullptr);
-  const bool h = sh->act == POETX_BF16;
-  const size_t fwd = align_up(h ? attn_fwd_part_bytes<bf16>(a) : attn_fwd_part_bytes<float>(a));
+size_t sink_at(const poetx_attn_shape* sh, const AttnArgs& a) {
+  return 2 * row_bytes(sh) + align_up(sh->act == POETX_BF16 ? attn_bwd_part_bytes<bf16>(a) : attn_bwd_part_bytes<float>(a));
+}
+size_t attn_ws(const poetx_attn_shape* sh, const poetx_window& w, int which) {
+  const AttnArgs a = args_of(sh, w, nullptr, nullptr, nullptr, nullptr, nullptr);
+  const size_t fwd = align_up(sh->act == POETX_BF16 ? attn_fwd_part_bytes<bf16>(a) : attn_fwd_part_bytes<float>(a));
   if (which == 0) return fwd;
-  const size_t bwd = 2 * row_bytes(sh) + align_up(h ? attn_bwd_part_bytes<bf16>(a) : attn_bwd_part_bytes<float>(a));
-  return std::max(fwd, bwd);
+  return std::max(fwd, sink_at(sh, a) + align_up(attn_sink_part_bytes(a)));
 }
 
 int32_t check_decode(const char* fn, const poetx_decode_shape* sh) {
@@ -375,36 +408,41 @@ int32_t poetx_dropout_bwd(int64_t n, int32_t act, const void* dy, void* dx, doub
                   fn);
 }
 
-size_t poetx_attn_plan_bytes(const poetx_attn_shape* sh) {
-  return check_attn("poetx_attn_plan_bytes", sh, false) == POETX_OK ? plan_bytes_of(sh) : 0;
+}  // extern "C"
+
+namespace {
+
+// The entry points with and without a window: the same but for the window.
+size_t plan_bytes_any(const char* fn, const poetx_attn_shape* sh, const poetx_window* w) {
+  return check_attn_window(fn, sh, w, false) == POETX_OK ? plan_sizes(sh, window_of(w)).total : 0;
 }
 
-size_t poetx_attn_workspace_bytes(const poetx_attn_shape* sh, int32_t which) {
+size_t workspace_any(const char* fn, const poetx_attn_shape* sh, const poetx_window* w, int32_t which) {
   if (which != 0 && which != 1) return 0;
-  return check_attn("poetx_attn_workspace_bytes", sh, false) == POETX_OK ? attn_ws(sh, which) : 0;
+  return check_attn_window(fn, sh, w, false) == POETX_OK ? attn_ws(sh, window_of(w), which) : 0;
 }
 
-int32_t poetx_attn_plan(const poetx_attn_shape* sh, const int32_t* cu_q, const int32_t* cu_k,
-                        const int32_t* prefix, void* plan, size_t plan_bytes,
-                        poetx_stream_t stream) {
-  const char* fn = "poetx_attn_plan";
-  TRY(check_attn(fn, sh, false));
+int32_t plan_any(const char* fn, const poetx_attn_shape* sh, const poetx_window* win, const int32_t* cu_q,
+                 const int32_t* cu_k, const int32_t* prefix, void* plan, size_t plan_bytes, poetx_stream_t stream) {
+  TRY(check_attn_window(fn, sh, win, false));
   NEED_PTR(cu_q);
   NEED_PTR(cu_k);
   OPT_PTR(prefix);
   NEED_PTR(plan);
-  const size_t need = plan_bytes_of(sh);
+  const poetx_window w = window_of(win);
+  const size_t need = plan_sizes(sh, w).total;
   if (plan_bytes < need) return fail(POETX_ERR_WORKSPACE, "%s: plan %zu < %zu bytes", fn, plan_bytes, need);
   if ((int64_t)sh->Tq + sh->Tk == 0) return ok();
-  return launched(launch_attn_plan(sh->Tq, sh->Tk, sh->ndoc, sh->causal, cu_q, cu_k, prefix,
-                                   plan_at(sh, plan), (hipStream_t)stream), fn);
+  const AttnPlan pl = plan_at(sh, w, plan);
+  const hipStream_t s = (hipStream_t)stream;
+  return launched(w.window ? launch_attn_window_plan(sh->Tq, sh->Tk, sh->ndoc, sh->causal, w.window, w.sinks, cu_q, cu_k, pl, s)
+                           : launch_attn_plan(sh->Tq, sh->Tk, sh->ndoc, sh->causal, cu_q, cu_k, prefix, pl, s), fn);
 }
 
-int32_t poetx_attn_fwd(const poetx_attn_shape* sh, const void* q, const void* k, const void* v,
-                       const float* slopes, const void* plan, void* o, float* lse, void* ws,
-                       size_t ws_bytes, poetx_stream_t stream) {
-  const char* fn = "poetx_attn_fwd";
-  TRY(check_attn(fn, sh, false));
+int32_t fwd_any(const char* fn, const poetx_attn_shape* sh, const poetx_window* win, const void* q, const void* k,
+                const void* v, const float* slopes, const void* plan, void* o, float* lse, void* ws,
+                size_t ws_bytes, poetx_stream_t stream) {
+  TRY(check_attn_window(fn, sh, win, false));
   if (sh->Tq == 0) return ok();
   NEED_PTR(q);
   if (sh->Tk) {
@@ -416,9 +454,10 @@ int32_t poetx_attn_fwd(const poetx_attn_shape* sh, const void* q, const void* k,
   NEED_PTR(o);
   NEED_PTR(lse);
   OPT_PTR(ws);
-  const size_t need = attn_ws(sh, 0);
+  const poetx_window w = window_of(win);
+  const size_t need = attn_ws(sh, w, 0);
   if (ws_bytes < need || (need && !ws)) return fail(POETX_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, ws_bytes, need);
-  AttnArgs a = args_of(sh, q, k, v, slopes, plan);
+  AttnArgs a = args_of(sh, w, q, k, v, slopes, plan);
   a.o = o;
   a.lse = lse;
   a.part = (float*)ws;
@@ -426,12 +465,10 @@ int32_t poetx_attn_fwd(const poetx_attn_shape* sh, const void* q, const void* k,
   return launched(sh->act == POETX_BF16 ? launch_attn_fwd<bf16>(a, s) : launch_attn_fwd<float>(a, s), fn);
 }
 
-int32_t poetx_attn_bwd(const poetx_attn_shape* sh, const void* dout, const void* q, const void* k,
-                       const void* v, const void* o, const float* lse, const float* slopes,
-                       const void* plan, void* dq, void* dk, void* dv, void* ws, size_t ws_bytes,
-                       poetx_stream_t stream) {
-  const char* fn = "poetx_attn_bwd";
-  TRY(check_attn(fn, sh, true));
+int32_t bwd_any(const char* fn, const poetx_attn_shape* sh, const poetx_window* win, const void* dout, const void* q,
+                const void* k, const void* v, const void* o, const float* lse, const float* slopes,
+                const void* plan, void* dq, void* dk, void* dv, void* ws, size_t ws_bytes, poetx_stream_t stream) {
+  TRY(check_attn_window(fn, sh, win, true));
   if ((int64_t)sh->Tq + sh->Tk == 0) return ok();
   if (sh->Tq) {
     NEED_PTR(dout);
@@ -449,9 +486,10 @@ int32_t poetx_attn_bwd(const poetx_attn_shape* sh, const void* dout, const void*
   }
   OPT_PTR(slopes);
   NEED_PTR(plan);
-  const size_t need = attn_ws(sh, 1);
+  const poetx_window w = window_of(win);
+  const size_t need = attn_ws(sh, w, 1);
   if (ws_bytes < need) return fail(POETX_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, ws_bytes, need);
-  AttnArgs a = args_of(sh, q, k, v, slopes, plan);
+  AttnArgs a = args_of(sh, w, q, k, v, slopes, plan);
   a.o = const_cast<void*>(o);
   a.lse = const_cast<float*>(lse);
   a.dout = dout;
@@ -459,8 +497,59 @@ int32_t poetx_attn_bwd(const poetx_attn_shape* sh, const void* dout, const void*
   a.delta = (float*)ws;
   a.lse2 = (float*)((char*)ws + row_bytes(sh));
   a.part = (float*)((char*)ws + 2 * row_bytes(sh));
+  a.sink_part = (float*)((char*)ws + sink_at(sh, a));
   const hipStream_t s = (hipStream_t)stream;
   return launched(sh->act == POETX_BF16 ? launch_attn_bwd<bf16>(a, s) : launch_attn_bwd<float>(a, s), fn);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t poetx_attn_plan_bytes(const poetx_attn_shape* sh) { return plan_bytes_any("poetx_attn_plan_bytes", sh, &NO_WINDOW); }
+size_t poetx_attn_window_plan_bytes(const poetx_attn_shape* sh, const poetx_window* win) {
+  return plan_bytes_any("poetx_attn_window_plan_bytes", sh, win);
+}
+
+size_t poetx_attn_workspace_bytes(const poetx_attn_shape* sh, int32_t which) {
+  return workspace_any("poetx_attn_workspace_bytes", sh, &NO_WINDOW, which);
+}
+size_t poetx_attn_window_workspace_bytes(const poetx_attn_shape* sh, const poetx_window* win, int32_t which) {
+  return workspace_any("poetx_attn_window_workspace_bytes", sh, win, which);
+}
+
+int32_t poetx_attn_plan(const poetx_attn_shape* sh, const int32_t* cu_q, const int32_t* cu_k,
+                        const int32_t* prefix, void* plan, size_t plan_bytes,
+                        poetx_stream_t stream) {
+  return plan_any("poetx_attn_plan", sh, &NO_WINDOW, cu_q, cu_k, prefix, plan, plan_bytes, stream);
+}
+int32_t poetx_attn_window_plan(const poetx_attn_shape* sh, const poetx_window* win, const int32_t* cu_q,
+                               const int32_t* cu_k, void* plan, size_t plan_bytes, poetx_stream_t stream) {
+  return plan_any("poetx_attn_window_plan", sh, win, cu_q, cu_k, nullptr, plan, plan_bytes, stream);
+}
+
+int32_t poetx_attn_fwd(const poetx_attn_shape* sh, const void* q, const void* k, const void* v,
+                       const float* slopes, const void* plan, void* o, float* lse, void* ws,
+                       size_t ws_bytes, poetx_stream_t stream) {
+  return fwd_any("poetx_attn_fwd", sh, &NO_WINDOW, q, k, v, slopes, plan, o, lse, ws, ws_bytes, stream);
+}
+int32_t poetx_attn_window_fwd(const poetx_attn_shape* sh, const poetx_window* win, const void* q, const void* k,
+                              const void* v, const float* slopes, const void* plan, void* o, float* lse,
+                              void* ws, size_t ws_bytes, poetx_stream_t stream) {
+  return fwd_any("poetx_attn_window_fwd", sh, win, q, k, v, slopes, plan, o, lse, ws, ws_bytes, stream);
+}
+
+int32_t poetx_attn_bwd(const poetx_attn_shape* sh, const void* dout, const void* q, const void* k,
+                       const void* v, const void* o, const float* lse, const float* slopes,
+                       const void* plan, void* dq, void* dk, void* dv, void* ws, size_t ws_bytes,
+                       poetx_stream_t stream) {
+  return bwd_any("poetx_attn_bwd", sh, &NO_WINDOW, dout, q, k, v, o, lse, slopes, plan, dq, dk, dv, ws, ws_bytes, stream);
+}
+int32_t poetx_attn_window_bwd(const poetx_attn_shape* sh, const poetx_window* win, const void* dout, const void* q,
+                              const void* k, const void* v, const void* o, const float* lse, const float* slopes,
+                              const void* plan, void* dq, void* dk, void* dv, void* ws, size_t ws_bytes,
+                              poetx_stream_t stream) {
+  return bwd_any("poetx_attn_window_bwd", sh, win, dout, q, k, v, o, lse, slopes, plan, dq, dk, dv, ws, ws_bytes, stream);
 }
 
 size_t poetx_attn_decode_workspace_bytes(const poetx_decode_shape* sh) {

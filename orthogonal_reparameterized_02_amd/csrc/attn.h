@@ -54,10 +54,12 @@ hipError_t launch_dropout(long n, const TS* x, const TS* res, TS* out, uint32_t 
 constexpr int ATTN_BM = 128;  // query (key) rows of a tile
 
 // About the rows of the other side that a tile's loop goes through: a
-// document's, and those of the documents that a tile spans.
-inline long loop_rows(int others, int own, int ndoc) {
+// document's, and those of the documents that a tile spans; reach (0: none):
+// no more than a window lets its rows see.
+inline long loop_rows(int others, int own, int ndoc, long reach) {
   const long r = others / (ndoc > 1 ? ndoc : 1) + (long)ATTN_BM * others / (own > 1 ? own : 1);
-  return r < others ? r : others;
+  const long most = reach && reach + ATTN_BM < others ? reach + ATTN_BM : others;
+  return r < most ? r : most;
 }
 
 // Parts that a loop over about `rows` rows is cut into where `groups`
@@ -94,6 +96,13 @@ struct AttnPlan {
   // first, end of the keys (queries) that its rows see, 0}
   int4 *qtab, *ktab;
   int4 *qraw, *kraw;               // the same before sorting
+  // With sinks a query row sees keys [row_sink.x, row_sink.y) besides, which
+  // end at or before row_lo.  Those of a tile lie in its range of qtab, or, of
+  // a document that began before the tile, in [qfar.x, qfar.y) below it.
+  int2* row_sink;                  // [Tq]
+  int2* qfar;                      // [tiles]
+  int* tile_doc;                   // [tiles] first document that ends after the tile's first row
+  int4* doc;                       // [ndoc] {first query row, end, first key row, end}
 };
 inline int attn_tiles(int rows) { return (rows + ATTN_BM - 1) / ATTN_BM; }
 
@@ -111,12 +120,30 @@ struct AttnArgs {
   float *delta, *lse2;  // [Hq][Tq] each
   float* part;          // partial sums (attn_ws_bytes)
   int ndoc;
+  int causal, window, sinks;  // window 0: none; sinks 0: none
+  float* sink_part;           // backward: partial dk and dv of the sinks
   AttnPlan pl;
+  long reach() const { return causal ? window : 2L * window; }
 };
+
+// The sinks of a document are seen past the window where some query stands
+// further than the window from some key.  Their gradients are then summed
+// apart (attn_bwd.hip): such a document takes the next of these numbers, for
+// two of them begin more than a window apart, among the queries or the keys.
+__host__ __device__ inline bool sinks_apart(int lq, int lk, int causal, int window) {
+  return lk > window || (!causal && lq > window);
+}
+__host__ __device__ inline long sink_number(int q0, int k0, int window) {
+  return q0 / ((long)window + 1) + k0 / ((long)window + 1);
+}
 
 // (api.hip) LDS above 64 KB for a kernel on the current device
 hipError_t lds_opt_in(const void* kern, int bytes);
 
+hipError_t launch_attn_window_plan(int Tq, int Tk, int ndoc, int causal, int window, int sinks,
+                                   const int* cu_q, const int* cu_k, const AttnPlan& pl, hipStream_t s);
+// bytes of a.sink_part
+size_t attn_sink_part_bytes(const AttnArgs& a);
 hipError_t launch_attn_plan(int Tq, int Tk, int ndoc, int causal, const int* cu_q, const int* cu_k,
                             const int* prefix, const AttnPlan& pl, hipStream_t s);
 // bytes of a.part for the forward and the backward pass
@@ -133,6 +160,8 @@ struct DecodeArgs {
   const void *q, *k, *v;
   void* o;
   const int *start, *len;
+  int window, sinks, ring;  // window 0: every row
+  const uint8_t *ks, *vs;   // scales of a cache in 4 bits
 };
 // ws: attn_decode_ws_bytes(a) bytes for the pieces' partial results
 size_t attn_decode_ws_bytes(const DecodeArgs& a);

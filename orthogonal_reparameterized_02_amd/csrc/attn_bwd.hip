@@ -77,9 +77,131 @@ __device__ __forceinline__ float dot8(const float*, uint4 a, uint4 b) {
   return fmaf(__uint_as_float(a.w), __uint_as_float(b.w), s);
 }
 
+// What a tile's 128 queries (one head, q and dout in registers) give to dk and
+// dv of the sinks of each document among them whose sinks are seen past the
+// window: the products of the second pass on blocks of 32 sinks, the queries
+// and dout of a wave laid out in LDS for the transposed reads.  The waves' sums
+// join there and go to a.sink_part[tile + number][head][dk, dv][sink][D].
+template <typename T, int DP, int MODE>
+__device__ __forceinline__ void sink_grads(const AttnArgs& a, char* smem, const ScoreArgs& sa,
+                                           const uint4 (&qf)[Tile<T, DP>::KS], const uint4 (&dof)[Tile<T, DP>::KS],
+                                           float delta, float lse2, int q0, int h, int lane, int wave) {
+  using L = Tile<T, DP>;
+  constexpr int ROWS = 32 * L::RB;                     // bytes of a wave's rows
+  float* vals = reinterpret_cast<float*>(smem + 4 * DqCfg<T, DP>::TILE) + wave * 64;
+  float* sums = reinterpret_cast<float*>(smem);        // [NW][32][DP]
+  const int r0 = q0 + 32 * wave, hk = h / a.group, rows = min(a.Tq - q0, BM);
+  const T* kp = (const T*)a.k + (long)hk * a.D;
+  const T* vp = (const T*)a.v + (long)hk * a.D;
+  const uint32_t rlane = L::row_lane(lane) + wave * ROWS, clane = L::col_lane(lane) + wave * ROWS;
+  if (lane < 32) {
+    vals[lane] = lse2;
+    vals[32 + lane] = delta;
+  }
+  for (int d = max(a.pl.tile_doc[q0 / BM], 0); d < a.ndoc; ++d) {
+    const int4 e = a.pl.doc[d];
+    const int dq0 = __builtin_amdgcn_readfirstlane(e.x), dq1 = __builtin_amdgcn_readfirstlane(e.y);
+    const int dk0 = __builtin_amdgcn_readfirstlane(e.z), dk1 = __builtin_amdgcn_readfirstlane(e.w);
+    if (dq0 >= q0 + rows) break;
+    if (dq1 <= q0 || dq0 >= dq1 || !sinks_apart(dq1 - dq0, dk1 - dk0, a.causal, a.window)) continue;
+    const int ns = min(a.sinks, dk1 - dk0);
+    float* out = a.sink_part + ((q0 / BM + sink_number(dq0, dk0, a.window)) * a.Hq + h) * 2 * a.sinks * a.D;
+    for (int b = 0; b < ns; b += 32) {
+      // queries that see this lane's key
+      const int key = b + (lane & 31), t = dk0 + key, off = dq1 - dk1;
+      const int lo = key < ns ? max(a.causal ? t + off : dq0, dq0) : 0, hi = key < ns ? dq1 : 0;
+      uint4 kf[L::KS];
+      rows_to_regs<T>(kf, kp, a.ldk, dk0 + b, dk0 + ns, a.D, lane);
+      f32x16_t s = {}, p;
+#pragma unroll
+      for (int i = 0; i < L::KS; ++i) s = mma16((const T*)nullptr, qf[i], kf[i], s);
+      rows_to_regs<T>(kf, vp, a.ldv, dk0 + b, dk0 + ns, a.D, lane);
+      __syncthreads();  // the sums before, and the loop's tiles, have been read
+      f32x16_t dp;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) dp[i] = -vals[32 + 4 * (lane >> 5) + 8 * (i / 4) + i % 4];
+#pragma unroll
+      for (int i = 0; i < L::KS; ++i) dp = mma16((const T*)nullptr, dof[i], kf[i], dp);
+      const int il = r0 + 4 * (lane >> 5);
+      bool any = false;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int row = il + 8 * (i / 4) + i % 4;
+        const float l2 = vals[4 * (lane >> 5) + 8 * (i / 4) + i % 4];
+        float deriv;
+        if constexpr (MODE == 0) p[i] = exp2_hw(fmaf(s[i], sa.c, -l2));
+        else p[i] = exp2_hw(score2<T, MODE>(s[i], sa, (float)(row - off - t), deriv) - l2);
+        s[i] = p[i] * dp[i];
+        if constexpr (MODE & 1) s[i] *= deriv;
+        const bool seen = row >= lo && row < hi;
+        p[i] = seen ? p[i] : 0.0f;
+        s[i] = seen ? s[i] : 0.0f;
+      }
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {  // dv, then dk
+#pragma unroll
+        for (int i = 0; i < L::KS; ++i)
+          *reinterpret_cast<uint4*>(smem + (rlane ^ (uint32_t)(i << 5))) = which ? qf[i] : dof[i];
+        f32x16_t acc[L::NT];
+#pragma unroll
+        for (int i = 0; i < L::NT; ++i) acc[i] = (f32x16_t){};
+        __builtin_amdgcn_wave_barrier();
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+        for (int u = 0; u < L::CSTEP; ++u) {
+          const uint4 f = L::score_frag(which ? s : p, u);
+#pragma unroll
+          for (int ct = 0; ct < L::NT; ++ct)
+            acc[ct] = mma16((const T*)nullptr, L::col_frag(smem, clane, 0, u, ct), f, acc[ct]);
+        }
+        // rows of other documents enter as 0 times their value; where that left
+        // what is not finite, the sums are formed again from what is seen
+        const bool again = __any(finite_probe<L::NT>(acc) != 0.0f);
+        __syncthreads();
+        float* mine = sums + wave * 32 * DP;
+        if (again) {
+          for (int j = 0; j < min(ns - b, 32); ++j) {
+            const int tj = dk0 + b + j;
+            float2 xk = make_float2(0.0f, 0.0f), xv = xk;
+            attn_row_dkv<T, true>(a, h, tj, max(max(a.causal ? tj + off : dq0, dq0), r0), min(min(dq1, r0 + 32), q0 + rows), lane, xk, xv);
+            if (2 * lane < DP) *reinterpret_cast<float2*>(mine + j * DP + 2 * lane) = which ? xk : xv;
+          }
+        } else if (key < ns) {
+          const float factor = which ? cap_factor<T, MODE> : 1.0f;
+#pragma unroll
+          for (int ct = 0; ct < L::NT; ++ct)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+              *reinterpret_cast<float4*>(mine + (lane & 31) * DP + 32 * ct + 8 * g + 4 * (lane >> 5)) =
+                  make_float4(acc[ct][4 * g] * factor, acc[ct][4 * g + 1] * factor, acc[ct][4 * g + 2] * factor, acc[ct][4 * g + 3] * factor);
+        }
+        __syncthreads();
+        float* to = out + ((which ? 0 : a.sinks) + b) * a.D;
+        for (int x = threadIdx.x; x < min(ns - b, 32) * (DP / 2); x += 64 * NW) {
+          const int j = x / (DP / 2), c = x % (DP / 2) * 2;
+          float2 y = make_float2(0.0f, 0.0f);
+#pragma unroll
+          for (int w = 0; w < NW; ++w) {
+            const float2 z = *reinterpret_cast<const float2*>(sums + (w * 32 + j) * DP + c);
+            y.x += z.x, y.y += z.y;
+          }
+          if (c < a.D) *reinterpret_cast<float2*>(to + (long)j * a.D + c) = y;
+        }
+        __syncthreads();
+      }
+    }
+  }
+}
+
 // dq, and for the second pass delta = dout . o and lse2 = lse log2e of every
 // query (lse2 = +inf where lse = -inf: such a query's p is 0)
-template <typename T, int DP, int MODE>
+//
+// SINK: rows see the first keys of their document besides an interval.  The
+// workgroup then also forms what its queries give to dk and dv of such keys
+// (sink_grads): it has q, dout, lse and delta at hand, and a key that every
+// later query sees would leave one workgroup of the second pass with a loop
+// over the whole document.
+template <typename T, int DP, int MODE, bool SINK>
 __global__ __launch_bounds__(64 * NW, (DqCfg<T, DP>::OCC)) void k_attn_dq(AttnArgs a, int parts) {
   using L = Tile<T, DP>;
   using C = DqCfg<T, DP>;
@@ -99,9 +221,16 @@ __global__ __launch_bounds__(64 * NW, (DqCfg<T, DP>::OCC)) void k_attn_dq(AttnAr
   const T* op = (const T*)a.o + (long)h * a.D;
 
   int jb, je;  // this part's keys; the first tiles are on their way before all else
-  part_of((khi - klo + BN - 1) / BN, parts, part, jb, je);
-  jb = klo + jb * BN;
-  je = min(klo + je * BN, khi);
+  KeyTiles kt;
+  if constexpr (SINK) {
+    kt.init(a.pl.qfar, q0 / BM, klo, khi, a.Tk, BN, parts, part);
+    jb = kt.row(kt.nb, BN);
+    je = kt.nb < kt.ne ? kt.end(kt.nb) : jb;
+  } else {
+    part_of((khi - klo + BN - 1) / BN, parts, part, jb, je);
+    jb = klo + jb * BN;
+    je = min(klo + je * BN, khi);
+  }
   Loader<T, DP, BN, NW> lk, lv;
   lk.init(a.ldk, a.D, wave, lane);
   lv.init(a.ldv, a.D, wave, lane);
@@ -117,6 +246,13 @@ __global__ __launch_bounds__(64 * NW, (DqCfg<T, DP>::OCC)) void k_attn_dq(AttnAr
   const int rlo = a.pl.row_lo[tc], rhi = a.pl.row_hi[tc], rpos = MODE & 2 ? a.pl.row_pos[tc] : 0;
   const int lo = in ? rlo : 0, hi = in ? rhi : 0;
   const Span sp = span_of(lo, hi);
+  int2 sink = make_int2(0, 0);
+  Span ssp = {};
+  if constexpr (SINK) {
+    const int2 rs = a.pl.row_sink[tc];
+    sink = make_int2(in ? rs.x : 0, in ? rs.y : 0);
+    ssp = span_of(sink.x, sink.y);
+  }
 
   uint4 qf[L::KS], dof[L::KS];
   rows_to_regs<T>(dof, dop, a.lddo, r0, a.Tq, a.D, lane);
@@ -144,19 +280,22 @@ __global__ __launch_bounds__(64 * NW, (DqCfg<T, DP>::OCC)) void k_attn_dq(AttnAr
 
   wait_loads();
   int buf = 0;
-  for (int j0 = jb; j0 < je; j0 += BN, buf ^= 1) {
+  for (int j0 = jb, n0 = SINK ? kt.nb : 0; SINK ? n0 < kt.ne : j0 < je; j0 = SINK ? kt.row(n0 + 1, BN) : j0 + BN, ++n0, buf ^= 1) {
     // this tile has landed, and every wave has left the other buffer
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    if (j0 + BN < je) {
-      lk.load(kp, a.ldk, j0 + BN, je, lds0 + (buf ^ 1) * C::TILE);
-      lv.load(vp, a.ldv, j0 + BN, je, lds0 + (2 + (buf ^ 1)) * C::TILE);
+    if (SINK ? n0 + 1 < kt.ne : j0 + BN < je) {
+      const int jnx = SINK ? kt.row(n0 + 1, BN) : j0 + BN, jne = SINK ? kt.end(n0 + 1) : je;
+      lk.load(kp, a.ldk, jnx, jne, lds0 + (buf ^ 1) * C::TILE);
+      lv.load(vp, a.ldv, jnx, jne, lds0 + (2 + (buf ^ 1)) * C::TILE);
     }
+    const bool far = SINK && n0 < kt.far;
     const uint32_t kr = rlane + buf * C::TILE, vr = kr + 2 * C::TILE, kc = clane + buf * C::TILE;
 #pragma unroll
     for (int n = 0; n < NS; ++n) {
       const int jn = j0 + 32 * n;
-      if (sp.lo >= jn + 32 || sp.hi <= jn) continue;  // nothing here for this wave
+      // nothing here for this wave
+      if ((far || sp.lo >= jn + 32 || sp.hi <= jn) && (!SINK || ssp.lo >= jn + 32 || ssp.hi <= jn)) continue;
       f32x16_t s = {}, dp;
 #pragma unroll
       for (int i = 0; i < 16; ++i) dp[i] = -delta;
@@ -183,11 +322,15 @@ __global__ __launch_bounds__(64 * NW, (DqCfg<T, DP>::OCC)) void k_attn_dq(AttnAr
         else s[i] = exp2_hw(score2<T, MODE>(s[i], sa, d0 - (float)(8 * (i / 4) + i % 4), deriv) - lse2) * dp[i];
         if constexpr (MODE & 1) s[i] *= deriv;
       }
-      if (sp.all_lo > jn || sp.all_hi < jn + 32) {  // some pair is hidden
-        const uint32_t width = (uint32_t)(hi - lo);
+      if (far || sp.all_lo > jn || sp.all_hi < jn + 32) {  // some pair is hidden
+        Seen seen = {lo, sink.x, (uint32_t)(hi - lo), (uint32_t)(sink.y - sink.x)};
+        if constexpr (SINK)
+          if (far) seen = {sink.x, 0, sink.x == kt.flo ? (uint32_t)(sink.y - sink.x) : 0, 0};
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          s[i] = (uint32_t)(jl - lo + 8 * (i / 4) + i % 4) < width ? s[i] : 0.0f;
+        for (int i = 0; i < 16; ++i) {
+          const int j = jl + 8 * (i / 4) + i % 4;
+          s[i] = (SINK ? seen.either(j) : seen(j)) ? s[i] : 0.0f;
+        }
       }
       uint4 p;
       cp.run(ldc, [&](int i, uint4 f) {
@@ -210,18 +353,68 @@ __global__ __launch_bounds__(64 * NW, (DqCfg<T, DP>::OCC)) void k_attn_dq(AttnAr
       const int tr = r0 + r;
       if (tr >= a.Tq) break;
       const float2 x = ld2(dop + (long)tr * a.lddo, lane, a.D), y = ld2(op + (long)tr * a.ldo, lane, a.D);
-      const float2 g = attn_row_dq<T>(qp + (long)tr * a.ldq, dop + (long)tr * a.lddo, kp, a.ldk, vp, a.ldv,
-                                      max(a.pl.row_lo[tr], jb), min(a.pl.row_hi[tr], je), a.pl.row_pos[tr],
-                                      a.D, a.scale, a.cap, a.slopes ? a.slopes[h] : 0.0f,
-                                      a.lse[(long)h * a.Tq + tr], wave_sum(x.x * y.x + x.y * y.y), lane);
+      const float dl = wave_sum(x.x * y.x + x.y * y.y);
+      const auto over = [&](int x0, int x1) {
+        return attn_row_dq<T>(qp + (long)tr * a.ldq, dop + (long)tr * a.lddo, kp, a.ldk, vp, a.ldv, x0, x1, a.pl.row_pos[tr],
+                              a.D, a.scale, a.cap, a.slopes ? a.slopes[h] : 0.0f, a.lse[(long)h * a.Tq + tr], dl, lane);
+      };
+      float2 g;
+      if constexpr (SINK) {
+        const int2 f = kt.far_keys(BN), w = kt.near_keys(BN), rs = a.pl.row_sink[tr];
+        const float2 u = rs.x == kt.flo ? over(max(rs.x, f.x), min(rs.y, f.y)) : make_float2(0.0f, 0.0f);
+        const float2 v = over(max(rs.x, w.x), min(rs.y, w.y)), z = over(max(a.pl.row_lo[tr], w.x), min(a.pl.row_hi[tr], w.y));
+        g = make_float2(u.x + v.x + z.x, u.y + v.y + z.y);
+      } else {
+        g = over(max(a.pl.row_lo[tr], jb), min(a.pl.row_hi[tr], je));
+      }
       if (parts > 1) st2(pq + tr * ldp, lane, a.D, g);
       else st2((T*)a.dq + (long)tr * a.lddq + (long)h * a.D, lane, a.D, make_float2(g.x * a.scale, g.y * a.scale));
     }
-    return;
+    if constexpr (!SINK) return;
+  } else {
+    const long tt = in ? t : 0;
+    if (parts > 1) store_rowsT<L::NT>(pq + tt * ldp, dq, FACTOR, a.D, in, lane);
+    else store_rowsT<L::NT>((T*)a.dq + tt * a.lddq + (long)h * a.D, dq, a.scale * FACTOR, a.D, in, lane);
   }
-  const long tt = in ? t : 0;
-  if (parts > 1) store_rowsT<L::NT>(pq + tt * ldp, dq, FACTOR, a.D, in, lane);
-  else store_rowsT<L::NT>((T*)a.dq + tt * a.lddq + (long)h * a.D, dq, a.scale * FACTOR, a.D, in, lane);
+  if constexpr (SINK)
+    if (part == 0) sink_grads<T, DP, MODE>(a, smem, sa, qf, dof, delta, in ? lse2 : INFINITY, q0, h, lane, wave);
+}
+
+// dk and dv of the sinks: what sink_grads left, over the tiles of a document and
+// the query heads of a group.  A workgroup a sink and key head; sixteen waves
+// take every sixteenth partial sum and join in wave order.  The second pass has
+// left zeros in these rows.
+constexpr int SW = 16;
+template <typename T> __global__ __launch_bounds__(64 * SW) void k_attn_sink_join(AttnArgs a) {
+  __shared__ float2 red[SW][2][64];
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, d = blockIdx.x / a.sinks, s = blockIdx.x % a.sinks, hk = blockIdx.y;
+  const int4 e = a.pl.doc[d];
+  const int q0 = e.x, q1 = e.y, k0 = e.z, k1 = e.w;
+  if (s >= k1 - k0 || !sinks_apart(q1 - q0, k1 - k0, a.causal, a.window)) return;
+  const int t0 = q0 / BM, tiles = q1 > q0 ? (q1 - 1) / BM - t0 + 1 : 0;
+  const long slot = t0 + sink_number(q0, k0, a.window), plane = (long)a.sinks * a.D;
+  float2 x[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+  if (2 * lane < a.D) {
+#pragma unroll 4
+    for (int n = wave; n < tiles * a.group; n += SW) {
+      const float* p = a.sink_part + (((slot + n / a.group) * a.Hq + hk * a.group + n % a.group) * 2) * plane + (long)s * a.D + 2 * lane;
+      const float2 u = *reinterpret_cast<const float2*>(p), v = *reinterpret_cast<const float2*>(p + plane);
+      x[0].x += u.x, x[0].y += u.y, x[1].x += v.x, x[1].y += v.y;
+    }
+  }
+  red[wave][0][lane] = x[0];
+  red[wave][1][lane] = x[1];
+  __syncthreads();
+  if (wave > 1) return;
+  float2 y = make_float2(0.0f, 0.0f);
+#pragma unroll
+  for (int w = 0; w < SW; ++w) {
+    const float2 u = red[w][wave][lane];
+    y.x += u.x, y.y += u.y;
+  }
+  const float mul = wave ? 1.0f : a.scale;
+  T* out = wave ? (T*)a.dv + (long)(k0 + s) * a.lddv : (T*)a.dk + (long)(k0 + s) * a.lddk;
+  st2(out + (long)hk * a.D, lane, a.D, make_float2(y.x * mul, y.y * mul));
 }
 
 // dk and dv
@@ -478,12 +671,12 @@ __global__ __launch_bounds__(256) void k_attn_sum_parts(JoinArgs j, int parts, l
 }
 
 template <typename T> int dq_parts(const AttnArgs& a) {
-  return parts_for<T>((long)attn_tiles(a.Tq) * a.Hq, loop_rows(a.Tk, a.Tq, a.ndoc), 64);
+  return parts_for<T>((long)attn_tiles(a.Tq) * a.Hq, loop_rows(a.Tk, a.Tq, a.ndoc, a.reach()), 64);
 }
 template <typename T> int dkv_parts(const AttnArgs& a) {
   // a bf16 workgroup has eight waves: it counts twice
   return parts_for<T>((long)attn_tiles(a.Tk) * a.Hkv * (sizeof(T) == 2 ? 2 : 1),
-                      loop_rows(a.Tq, a.Tk, a.ndoc) * a.group, a.D > 64 ? 32 : 64);
+                      loop_rows(a.Tq, a.Tk, a.ndoc, a.reach()) * a.group, a.D > 64 ? 32 : 64);
 }
 
 // From 1024 workgroups on, two rounds of two a CU, the loops even out by
@@ -502,15 +695,15 @@ template <typename T, int DP, int MODE, int NQ> hipError_t dkv(const AttnArgs& a
   return hipGetLastError();
 }
 
-template <typename T, int DP, int MODE> hipError_t bwd(const AttnArgs& a, hipStream_t s) {
-  constexpr int lds = DqCfg<T, DP>::LDS;
-  hipError_t e = lds_opt_in((const void*)k_attn_dq<T, DP, MODE>, lds);
+template <typename T, int DP, int MODE, bool SINK> hipError_t bwd(const AttnArgs& a, hipStream_t s) {
+  constexpr int lds = DqCfg<T, DP>::LDS + (SINK ? NW * 64 * 4 : 0);
+  hipError_t e = lds_opt_in((const void*)k_attn_dq<T, DP, MODE, SINK>, lds);
   if (e != hipSuccess) return e;
   const int pq = dq_parts<T>(a), pk = dkv_parts<T>(a);
   const int wq = a.Hq * a.D, wk = a.Hkv * a.D;
   const auto blocks = [](long n) { return (unsigned)((n / 8 + 255) / 256); };
   if (a.Tq) {
-    k_attn_dq<T, DP, MODE><<<dim3((unsigned)attn_tiles(a.Tq) * a.Hq * pq), 64 * NW, lds, s>>>(a, pq);
+    k_attn_dq<T, DP, MODE, SINK><<<dim3((unsigned)attn_tiles(a.Tq) * a.Hq * pq), 64 * NW, lds, s>>>(a, pq);
     e = hipGetLastError();
     if (e == hipSuccess && pq > 1) {
       const JoinArgs j = {{a.part}, {a.dq}, {a.lddq}, {a.scale}};
@@ -529,12 +722,19 @@ template <typename T, int DP, int MODE> hipError_t bwd(const AttnArgs& a, hipStr
       k_attn_sum_parts<T><<<dim3(blocks(n), 2), 256, 0, s>>>(j, pk, 2 * n, a.Tk, wk);
       e = hipGetLastError();
     }
+    if (SINK && e == hipSuccess && a.ndoc) {
+      k_attn_sink_join<T><<<dim3(a.ndoc * a.sinks, a.Hkv), 64 * SW, 0, s>>>(a);
+      e = hipGetLastError();
+    }
   }
   return e;
 }
 
 template <typename T, int DP> hipError_t bwd_mode(const AttnArgs& a, hipStream_t s) {
-  return by_mode<T>(a.slopes, a.cap, [&](auto mode) { return bwd<T, DP, decltype(mode)::value>(a, s); });
+  return by_mode<T>(a.slopes, a.cap, [&](auto mode) {
+    constexpr int MODE = decltype(mode)::value;
+    return a.sinks ? bwd<T, DP, MODE, true>(a, s) : bwd<T, DP, MODE, false>(a, s);
+  });
 }
 
 }  // namespace
@@ -545,6 +745,13 @@ template <typename T> size_t attn_bwd_part_bytes(const AttnArgs& a) {
   const size_t q = pq > 1 ? (size_t)pq * a.Tq * a.Hq * a.D * 4 : 0;
   const size_t k = pk > 1 ? (size_t)pk * 2 * a.Tk * a.Hkv * a.D * 4 : 0;
   return std::max(q, k);
+}
+
+// a slot for every query tile of every document whose sinks are summed apart:
+// tile + sink_number grows from one to the next
+size_t attn_sink_part_bytes(const AttnArgs& a) {
+  const size_t slots = attn_tiles(a.Tq) + sink_number(a.Tq, a.Tk, a.window) + 1;
+  return a.sinks ? slots * a.Hq * 2 * a.sinks * a.D * 4 : 0;
 }
 
 template <typename T> hipError_t launch_attn_bwd(const AttnArgs& a, hipStream_t s) {

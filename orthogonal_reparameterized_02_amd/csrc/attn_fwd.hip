@@ -46,7 +46,9 @@ template <typename T, int DP> struct FwdCfg {
   static constexpr int LDS = 4 * TILE;  // two buffers of keys and values
 };
 
-template <typename T, int DP, int MODE>
+// SINK: rows see the first keys of their document besides an interval
+// (KeyTiles); one key tile more a loop.
+template <typename T, int DP, int MODE, bool SINK>
 __global__ __launch_bounds__(64 * NW, 2) void k_attn_fwd(AttnArgs a, int parts) {
   using L = Tile<T, DP>;
   using C = FwdCfg<T, DP>;
@@ -66,9 +68,16 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_fwd(AttnArgs a, int parts) 
   const T* vp = (const T*)a.v + (long)hk * a.D;
 
   int jb, je;  // this part's keys; the first tiles are on their way before all else
-  part_of((khi - klo + BN - 1) / BN, parts, part, jb, je);
-  jb = klo + jb * BN;
-  je = min(klo + je * BN, khi);
+  KeyTiles kt;
+  if constexpr (SINK) {
+    kt.init(a.pl.qfar, q0 / BM, klo, khi, a.Tk, BN, parts, part);
+    jb = kt.row(kt.nb, BN);
+    je = kt.nb < kt.ne ? kt.end(kt.nb) : jb;
+  } else {
+    part_of((khi - klo + BN - 1) / BN, parts, part, jb, je);
+    jb = klo + jb * BN;
+    je = min(klo + je * BN, khi);
+  }
   Loader<T, DP, BN, NW> lk, lv;
   lk.init(a.ldk, a.D, wave, lane);
   lv.init(a.ldv, a.D, wave, lane);
@@ -85,6 +94,13 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_fwd(AttnArgs a, int parts) 
   const int rlo = a.pl.row_lo[tc], rhi = a.pl.row_hi[tc], rpos = MODE & 2 ? a.pl.row_pos[tc] : 0;
   const int lo = in ? rlo : 0, hi = in ? rhi : 0;
   const Span sp = span_of(lo, hi);
+  int2 sink = make_int2(0, 0);
+  Span ssp = {};
+  if constexpr (SINK) {
+    const int2 rs = a.pl.row_sink[tc];
+    sink = make_int2(in ? rs.x : 0, in ? rs.y : 0);
+    ssp = span_of(sink.x, sink.y);
+  }
 
   uint4 qf[L::KS];
   rows_to_regs<T>(qf, qp, a.ldq, q0 + 32 * wave, a.Tq, a.D, lane);
@@ -98,15 +114,18 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_fwd(AttnArgs a, int parts) 
 
   wait_loads();
   int buf = 0;
-  for (int j0 = jb; j0 < je; j0 += BN, buf ^= 1) {
+  for (int j0 = jb, n = SINK ? kt.nb : 0; SINK ? n < kt.ne : j0 < je; j0 = SINK ? kt.row(n + 1, BN) : j0 + BN, ++n, buf ^= 1) {
     // this tile has landed, and every wave has left the other buffer
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    if (j0 + BN < je) {
-      lk.load(kp, a.ldk, j0 + BN, je, lds0 + (buf ^ 1) * C::TILE);
-      lv.load(vp, a.ldv, j0 + BN, je, lds0 + (2 + (buf ^ 1)) * C::TILE);
+    if (SINK ? n + 1 < kt.ne : j0 + BN < je) {
+      const int jn = SINK ? kt.row(n + 1, BN) : j0 + BN, jne = SINK ? kt.end(n + 1) : je;
+      lk.load(kp, a.ldk, jn, jne, lds0 + (buf ^ 1) * C::TILE);
+      lv.load(vp, a.ldv, jn, jne, lds0 + (2 + (buf ^ 1)) * C::TILE);
     }
-    if (sp.lo >= j0 + BN || sp.hi <= j0) continue;  // nothing here for this wave
+    const bool far = SINK && n < kt.far;
+    // nothing here for this wave
+    if ((far || sp.lo >= j0 + BN || sp.hi <= j0) && (!SINK || ssp.lo >= j0 + BN || ssp.hi <= j0)) continue;
     const uint32_t kr = rlane + buf * C::TILE, vc = clane + (2 + buf) * C::TILE;
 
     f32x16_t s[NS];
@@ -135,14 +154,17 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_fwd(AttnArgs a, int parts) 
         for (int i = 0; i < 16; ++i)
           s[n][i] = score2<T, MODE>(s[n][i], sa, d0 - (float)(32 * n + 8 * (i / 4) + i % 4), unused);
     }
-    const bool masked = sp.all_lo > j0 || sp.all_hi < j0 + BN;  // some pair is hidden
-    const uint32_t width = (uint32_t)(hi - lo);
+    const bool masked = far || sp.all_lo > j0 || sp.all_hi < j0 + BN;  // some pair is hidden
+    Seen seen = {lo, sink.x, (uint32_t)(hi - lo), (uint32_t)(sink.y - sink.x)};
+    if constexpr (SINK)
+      if (far) seen = {sink.x, 0, sink.x == kt.flo ? (uint32_t)(sink.y - sink.x) : 0, 0};
+    const auto sees = [&](int j) { return SINK ? seen.either(j) : seen(j); };
     if (masked) {
 #pragma unroll
       for (int n = 0; n < NS; ++n)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          s[n][i] = (uint32_t)(jl - lo + 32 * n + 8 * (i / 4) + i % 4) < width ? s[n][i] : -INFINITY;
+          s[n][i] = sees(jl + 32 * n + 8 * (i / 4) + i % 4) ? s[n][i] : -INFINITY;
     }
 #pragma unroll
     for (int n = 0; n < NS; ++n)
@@ -176,8 +198,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_fwd(AttnArgs a, int parts) 
 #pragma unroll
         for (int n = 0; n < NS; ++n)
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            s[n][i] = (uint32_t)(jl - lo + 32 * n + 8 * (i / 4) + i % 4) < width ? s[n][i] : 0.0f;
+          for (int i = 0; i < 16; ++i) s[n][i] = sees(jl + 32 * n + 8 * (i / 4) + i % 4) ? s[n][i] : 0.0f;
       }
     }
 #pragma unroll
@@ -209,9 +230,22 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_fwd(AttnArgs a, int parts) 
       const int tr = q0 + 32 * wave + r;
       if (tr >= a.Tq) break;
       float mr, lr;
-      const float2 ov = attn_row<T>(qp + (long)tr * a.ldq, kp, a.ldk, vp, a.ldv, max(a.pl.row_lo[tr], jb),
-                                    min(a.pl.row_hi[tr], je), a.pl.row_pos[tr], a.D, a.scale, a.cap,
-                                    a.slopes ? a.slopes[h] : 0.0f, lane, mr, lr);
+      float2 ov;
+      const float slope = a.slopes ? a.slopes[h] : 0.0f;
+      if constexpr (SINK) {
+        mr = -INFINITY, lr = 0.0f, ov = make_float2(0.0f, 0.0f);
+        const int2 f = kt.far_keys(BN), w = kt.near_keys(BN), rs = a.pl.row_sink[tr];
+        const auto more = [&](int x, int y) {
+          attn_row_more<T>(qp + (long)tr * a.ldq, kp, a.ldk, vp, a.ldv, x, y, a.pl.row_pos[tr], a.D, a.scale, a.cap, slope,
+                           lane, mr, lr, ov);
+        };
+        if (rs.x == kt.flo) more(max(rs.x, f.x), min(rs.y, f.y));
+        more(max(rs.x, w.x), min(rs.y, w.y));
+        more(max(a.pl.row_lo[tr], w.x), min(a.pl.row_hi[tr], w.y));
+      } else {
+        ov = attn_row<T>(qp + (long)tr * a.ldq, kp, a.ldk, vp, a.ldv, max(a.pl.row_lo[tr], jb),
+                         min(a.pl.row_hi[tr], je), a.pl.row_pos[tr], a.D, a.scale, a.cap, slope, lane, mr, lr);
+      }
       if (parts == 1) {
         const float inv = lr == 0.0f ? 0.0f : 1.0f / lr;
         st2((T*)a.o + (long)tr * a.ldo + (long)h * a.D, lane, a.D, make_float2(ov.x * inv, ov.y * inv));
@@ -270,15 +304,15 @@ __global__ __launch_bounds__(256) void k_attn_fwd_join(AttnArgs a, int parts) {
 }
 
 template <typename T> int fwd_parts(const AttnArgs& a) {
-  return parts_for<T>((long)attn_tiles(a.Tq) * a.Hq, loop_rows(a.Tk, a.Tq, a.ndoc), 64);
+  return parts_for<T>((long)attn_tiles(a.Tq) * a.Hq, loop_rows(a.Tk, a.Tq, a.ndoc, a.reach()), 64);
 }
 
-template <typename T, int DP, int MODE> hipError_t fwd(const AttnArgs& a, hipStream_t s) {
+template <typename T, int DP, int MODE, bool SINK> hipError_t fwd(const AttnArgs& a, hipStream_t s) {
   constexpr int lds = FwdCfg<T, DP>::LDS;
-  const hipError_t e = lds_opt_in((const void*)k_attn_fwd<T, DP, MODE>, lds);
+  const hipError_t e = lds_opt_in((const void*)k_attn_fwd<T, DP, MODE, SINK>, lds);
   if (e != hipSuccess) return e;
   const int tiles = attn_tiles(a.Tq), parts = fwd_parts<T>(a);
-  k_attn_fwd<T, DP, MODE><<<dim3((unsigned)tiles * a.Hq * parts), 64 * NW, lds, s>>>(a, parts);
+  k_attn_fwd<T, DP, MODE, SINK><<<dim3((unsigned)tiles * a.Hq * parts), 64 * NW, lds, s>>>(a, parts);
   const hipError_t e2 = hipGetLastError();
   if (e2 != hipSuccess || parts == 1) return e2;
   const int rows = 256 / (a.D / 8);
@@ -287,7 +321,10 @@ template <typename T, int DP, int MODE> hipError_t fwd(const AttnArgs& a, hipStr
 }
 
 template <typename T, int DP> hipError_t fwd_mode(const AttnArgs& a, hipStream_t s) {
-  return by_mode<T>(a.slopes, a.cap, [&](auto mode) { return fwd<T, DP, decltype(mode)::value>(a, s); });
+  return by_mode<T>(a.slopes, a.cap, [&](auto mode) {
+    constexpr int MODE = decltype(mode)::value;
+    return a.sinks ? fwd<T, DP, MODE, true>(a, s) : fwd<T, DP, MODE, false>(a, s);
+  });
 }
 
 }  // namespace

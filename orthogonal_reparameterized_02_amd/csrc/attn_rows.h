@@ -44,16 +44,14 @@ __device__ __forceinline__ float pair_score(float qk, float scale, float cap, fl
   return s - slope * (float)abs(dist);
 }
 
-// One query over keys [lo, hi): running maximum m, sum l = sum exp(s - m) and
-// (returned) sum exp(s - m) v.  A maximum of -inf stands for 0, so scores that
-// are all -inf give sums of 0.
+// Adds keys [lo, hi) of one query to a running maximum m, a sum l = sum
+// exp(s - m) and o = sum exp(s - m) v.  A maximum of -inf stands for 0, so
+// scores that are all -inf give sums of 0.
 template <typename TS>
-__device__ __forceinline__ float2 attn_row(const TS* q, const TS* k, long ldk, const TS* v, long ldv,
-                                           int lo, int hi, int pos, int D, float scale, float cap,
-                                           float slope, int lane, float& m, float& l) {
+__device__ __forceinline__ void attn_row_more(const TS* q, const TS* k, long ldk, const TS* v, long ldv,
+                                              int lo, int hi, int pos, int D, float scale, float cap,
+                                              float slope, int lane, float& m, float& l, float2& o) {
   const float2 qv = ld2(q, lane, D);
-  m = -INFINITY, l = 0.0f;
-  float2 o = make_float2(0.0f, 0.0f);
   for (int j = lo; j < hi; ++j) {
     const float2 kv = ld2(k + (long)j * ldk, lane, D), vv = ld2(v + (long)j * ldv, lane, D);
     float unused;
@@ -65,6 +63,16 @@ __device__ __forceinline__ float2 attn_row(const TS* q, const TS* k, long ldk, c
     o.x = o.x * f + p * vv.x;
     o.y = o.y * f + p * vv.y;
   }
+}
+
+// One query over keys [lo, hi) alone: m, l and (returned) o.
+template <typename TS>
+__device__ __forceinline__ float2 attn_row(const TS* q, const TS* k, long ldk, const TS* v, long ldv,
+                                           int lo, int hi, int pos, int D, float scale, float cap,
+                                           float slope, int lane, float& m, float& l) {
+  m = -INFINITY, l = 0.0f;
+  float2 o = make_float2(0.0f, 0.0f);
+  attn_row_more<TS>(q, k, ldk, v, ldv, lo, hi, pos, D, scale, cap, slope, lane, m, l, o);
   return o;
 }
 
@@ -88,7 +96,8 @@ __device__ __forceinline__ float2 attn_row_dq(const TS* q, const TS* dout, const
 }
 
 // adds to dk and dv of one key row what query head h, rows [lo, hi), gives
-template <typename TS>
+// (OWN_DELTA: delta from dout and o instead of a.delta)
+template <typename TS, bool OWN_DELTA = false>
 __device__ __forceinline__ void attn_row_dkv(const AttnArgs& a, int h, int j, int lo, int hi, int lane,
                                              float2& dk, float2& dv) {
   const int hk = h / a.group;
@@ -104,7 +113,14 @@ __device__ __forceinline__ void attn_row_dkv(const AttnArgs& a, int h, int j, in
     const float dp = wave_sum(ov.x * vv.x + ov.y * vv.y);
     const float lse = a.lse[(long)h * a.Tq + i];
     const float p = lse == -INFINITY ? 0.0f : __expf(s - lse);
-    const float ds = p * (dp - a.delta[(long)h * a.Tq + i]) * dsdx;
+    float delta;
+    if constexpr (OWN_DELTA) {
+      const float2 yv = ld2((const TS*)a.o + (long)i * a.ldo + (long)h * a.D, lane, a.D);
+      delta = wave_sum(ov.x * yv.x + ov.y * yv.y);
+    } else {
+      delta = a.delta[(long)h * a.Tq + i];
+    }
+    const float ds = p * (dp - delta) * dsdx;
     dv.x += p * ov.x;
     dv.y += p * ov.y;
     dk.x += ds * qv.x;

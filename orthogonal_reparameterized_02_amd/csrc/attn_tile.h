@@ -432,4 +432,35 @@ __device__ __forceinline__ void part_of(int n, int parts, int part, int& begin, 
   end = min(begin + each, n);
 }
 
+// The key tiles of one part of a query tile's loop: `far` tiles over the sinks
+// of the document that the tile continues, then those of the window.
+struct KeyTiles {
+  int flo, fhi, far, klo, khi;
+  int nb, ne;  // this part's
+  __device__ __forceinline__ void init(const int2* qfar, int tile, int klo_, int khi_, int others, int bn, int parts, int part) {
+    const int2 f = qfar[tile];
+    flo = min(max(__builtin_amdgcn_readfirstlane(f.x), 0), others);
+    fhi = min(max(__builtin_amdgcn_readfirstlane(f.y), flo), others);
+    far = (fhi - flo + bn - 1) / bn;
+    klo = klo_;
+    khi = max(khi_, klo_);
+    part_of(far + (khi - klo + bn - 1) / bn, parts, part, nb, ne);
+  }
+  __device__ __forceinline__ int row(int n, int bn) const { return n < far ? flo + n * bn : klo + (n - far) * bn; }
+  __device__ __forceinline__ int end(int n) const { return n < far ? fhi : khi; }
+  // this part's keys of both ranges
+  __device__ __forceinline__ int2 far_keys(int bn) const { return make_int2(min(flo + min(nb, far) * bn, fhi), min(flo + min(ne, far) * bn, fhi)); }
+  __device__ __forceinline__ int2 near_keys(int bn) const {
+    return make_int2(min(klo + max(nb - far, 0) * bn, khi), min(klo + max(ne - far, 0) * bn, khi));
+  }
+};
+
+// The keys that a lane's query sees in a tile: interval a, and with sinks b
+struct Seen {
+  int alo, blo;
+  uint32_t aw, bw;
+  __device__ __forceinline__ bool operator()(int j) const { return (uint32_t)(j - alo) < aw; }
+  __device__ __forceinline__ bool either(int j) const { return (uint32_t)(j - alo) < aw || (uint32_t)(j - blo) < bw; }
+};
+
 }  // namespace poetx

@@ -14,7 +14,7 @@ from typing import Optional
 import torch
 
 from ._lib import (AttnShape, BF16, DecodeShape, F32, I8, PoetxError, QkNormShape, RopeShape,  # noqa: F401
-                   Shape, check, lib)
+                   Shape, Window, check, lib)
 
 _DT = {F32: torch.float32, BF16: torch.bfloat16}
 
@@ -414,12 +414,39 @@ def attn_shape(q, k, v, ndoc: int, causal: bool = True, scale: float = 0.0,
                      wq, wq, wq, wk, wk)
 
 
+def window(window: int, sinks: int = 0) -> Window:
+    """A window of `window` keys (0: none), the first `sinks` of a document
+    visible past it."""
+    return Window(window, sinks)
+
+
+def _named(name: str, win: Optional[Window]):
+    """An attention entry point (poetx_attn_<name>), its form with a window
+    where there is one, and the arguments that both begin with."""
+    if win is None:
+        return f"poetx_attn_{name}", ()
+    return f"poetx_attn_window_{name}", (C.byref(win),)
+
+
+def _attn_bytes(sh: AttnShape, win: Optional[Window], what: str, *args) -> int:
+    name, w = _named(what, win)
+    return getattr(lib(), name)(C.byref(sh), *w, *args)
+
+
 def poetx_attn_plan_bytes(sh: AttnShape) -> int:
-    return lib().poetx_attn_plan_bytes(C.byref(sh))
+    return _attn_bytes(sh, None, "plan_bytes")
+
+
+def poetx_attn_window_plan_bytes(sh: AttnShape, win: Window) -> int:
+    return _attn_bytes(sh, win, "plan_bytes")
 
 
 def poetx_attn_workspace_bytes(sh: AttnShape, which: int) -> int:
-    return lib().poetx_attn_workspace_bytes(C.byref(sh), which)
+    return _attn_bytes(sh, None, "workspace_bytes", which)
+
+
+def poetx_attn_window_workspace_bytes(sh: AttnShape, win: Window, which: int) -> int:
+    return _attn_bytes(sh, win, "workspace_bytes", which)
 
 
 def poetx_attn_plan(sh: AttnShape, cu_q, cu_k, plan, prefix=None, stream=None) -> None:
@@ -431,7 +458,23 @@ def poetx_attn_plan(sh: AttnShape, cu_q, cu_k, plan, prefix=None, stream=None) -
         plan.numel() * plan.element_size(), _stream(stream)))
 
 
-def poetx_attn_fwd(sh: AttnShape, q, k, v, plan, o, lse, ws=None, slopes=None, stream=None) -> None:
+def poetx_attn_window_plan(sh: AttnShape, win: Window, cu_q, cu_k, plan, stream=None) -> None:
+    """The mask of a packed batch with a window and sinks."""
+    check("poetx_attn_window_plan", lib().poetx_attn_window_plan(
+        C.byref(sh), C.byref(win), _vec(cu_q, "cu_q", torch.int32, sh.ndoc + 1),
+        _vec(cu_k, "cu_k", torch.int32, sh.ndoc + 1), _dev(plan, "plan"),
+        plan.numel() * plan.element_size(), _stream(stream)))
+
+
+def _plan(sh: AttnShape, win: Optional[Window], plan):
+    p = _dev(plan, "plan")
+    need = _attn_bytes(sh, win, "plan_bytes")
+    if plan.numel() * plan.element_size() < need:
+        raise ValueError(f"plan: {need} bytes required")
+    return p
+
+
+def _attn_fwd(sh: AttnShape, win: Optional[Window], q, k, v, plan, o, lse, ws, slopes, stream) -> None:
     sh = AttnShape.from_buffer_copy(sh)
     dt = _DT[sh.act]
     fq, fk = (sh.Tq, sh.Hq, sh.D), (sh.Tk, sh.Hkv, sh.D)
@@ -439,23 +482,24 @@ def poetx_attn_fwd(sh: AttnShape, q, k, v, plan, o, lse, ws=None, slopes=None, s
     kp, sh.ldk = _rows(k, "k", fk, dt)
     vp, sh.ldv = _rows(v, "v", fk, dt)
     op, sh.ldo = _rows(o, "o", fq, dt)
-    wp, wb = _ws(ws, poetx_attn_workspace_bytes(sh, 0))
-    check("poetx_attn_fwd", lib().poetx_attn_fwd(
-        C.byref(sh), qp, kp, vp, _vec(slopes, "slopes", torch.float32, sh.Hq, optional=True),
-        _plan(sh, plan), op, _vec(lse, "lse", torch.float32, sh.Hq * sh.Tq), wp, wb,
+    wp, wb = _ws(ws, _attn_bytes(sh, win, "workspace_bytes", 0))
+    name, w = _named("fwd", win)
+    check(name, getattr(lib(), name)(
+        C.byref(sh), *w, qp, kp, vp, _vec(slopes, "slopes", torch.float32, sh.Hq, optional=True),
+        _plan(sh, win, plan), op, _vec(lse, "lse", torch.float32, sh.Hq * sh.Tq), wp, wb,
         _stream(stream)))
 
 
-def _plan(sh: AttnShape, plan):
-    p = _dev(plan, "plan")
-    need = poetx_attn_plan_bytes(sh)
-    if plan.numel() * plan.element_size() < need:
-        raise ValueError(f"plan: {need} bytes required")
-    return p
+def poetx_attn_fwd(sh: AttnShape, q, k, v, plan, o, lse, ws=None, slopes=None, stream=None) -> None:
+    _attn_fwd(sh, None, q, k, v, plan, o, lse, ws, slopes, stream)
 
 
-def poetx_attn_bwd(sh: AttnShape, dout, q, k, v, o, lse, plan, dq, dk, dv, ws, slopes=None,
-                   stream=None) -> None:
+def poetx_attn_window_fwd(sh: AttnShape, win: Window, q, k, v, plan, o, lse, ws=None, slopes=None, stream=None) -> None:
+    """poetx_attn_fwd under a plan of poetx_attn_window_plan with the same window."""
+    _attn_fwd(sh, win, q, k, v, plan, o, lse, ws, slopes, stream)
+
+
+def _attn_bwd(sh: AttnShape, win: Optional[Window], dout, q, k, v, o, lse, plan, dq, dk, dv, ws, slopes, stream) -> None:
     sh = AttnShape.from_buffer_copy(sh)
     dt = _DT[sh.act]
     fq, fk = (sh.Tq, sh.Hq, sh.D), (sh.Tk, sh.Hkv, sh.D)
@@ -467,11 +511,23 @@ def poetx_attn_bwd(sh: AttnShape, dout, q, k, v, o, lse, plan, dq, dk, dv, ws, s
     dqp, sh.lddq = _rows(dq, "dq", fq, dt)
     dkp, sh.lddk = _rows(dk, "dk", fk, dt)
     dvp, sh.lddv = _rows(dv, "dv", fk, dt)
-    wp, wb = _ws(ws, poetx_attn_workspace_bytes(sh, 1))
-    check("poetx_attn_bwd", lib().poetx_attn_bwd(
-        C.byref(sh), dop, qp, kp, vp, op, _vec(lse, "lse", torch.float32, sh.Hq * sh.Tq),
-        _vec(slopes, "slopes", torch.float32, sh.Hq, optional=True), _plan(sh, plan), dqp, dkp, dvp,
+    wp, wb = _ws(ws, _attn_bytes(sh, win, "workspace_bytes", 1))
+    name, w = _named("bwd", win)
+    check(name, getattr(lib(), name)(
+        C.byref(sh), *w, dop, qp, kp, vp, op, _vec(lse, "lse", torch.float32, sh.Hq * sh.Tq),
+        _vec(slopes, "slopes", torch.float32, sh.Hq, optional=True), _plan(sh, win, plan), dqp, dkp, dvp,
         wp, wb, _stream(stream)))
+
+
+def poetx_attn_bwd(sh: AttnShape, dout, q, k, v, o, lse, plan, dq, dk, dv, ws, slopes=None,
+                   stream=None) -> None:
+    _attn_bwd(sh, None, dout, q, k, v, o, lse, plan, dq, dk, dv, ws, slopes, stream)
+
+
+def poetx_attn_window_bwd(sh: AttnShape, win: Window, dout, q, k, v, o, lse, plan, dq, dk, dv, ws, slopes=None,
+                          stream=None) -> None:
+    """poetx_attn_bwd under a plan of poetx_attn_window_plan with the same window."""
+    _attn_bwd(sh, win, dout, q, k, v, o, lse, plan, dq, dk, dv, ws, slopes, stream)
 
 
 def decode_shape(q, k, v, scale: float = 0.0, cap: float = 0.0) -> DecodeShape:

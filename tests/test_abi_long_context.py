@@ -81,3 +81,64 @@ def test_norm_binding_refusals():
         P.poetx_qk_norm_rope_fwd(q, None, None, None, pos, t[0], q, None)
     with pytest.raises(ValueError, match="unsupported activation"):
         P.qk_norm_shape(q.double(), None, None)
+
+
+# ---- attention with a window and sinks ------------------------------------------------
+def attn_shape(**kw):
+    a = dict(Tq=100, Tk=120, ndoc=3, Hq=8, Hkv=2, D=128, act=1, causal=1, scale=0.0, cap=0.0, ldq=1024,
+             ldk=256, ldv=256, ldo=1024, lddo=1024, lddq=1024, lddk=256, lddv=256)
+    a.update(kw)
+    return _lib.AttnShape(**a)
+
+
+def calls(sh, w, plan_n=1 << 40, ws_n=1 << 40):
+    L, sh, w = _lib.lib(), C.byref(sh), C.byref(w) if w else None
+    return (L.poetx_attn_window_plan(sh, w, FAKE, FAKE, FAKE, plan_n, None),
+            L.poetx_attn_window_fwd(sh, w, FAKE, FAKE, FAKE, None, FAKE, FAKE, FAKE, FAKE, ws_n, None),
+            L.poetx_attn_window_bwd(sh, w, *[FAKE] * 6, None, *[FAKE] * 5, ws_n, None))
+
+
+@pytest.mark.parametrize("window,sinks,word", [(-1, 0, "window"), (16, -1, "sinks"), (16, 129, "sinks"), (0, 200, "sinks")])
+def test_window_errors(window, sinks, word):
+    L, w = _lib.lib(), _lib.Window(window, sinks)
+    assert calls(attn_shape(), w) == (1, 1, 1) and word in _err()
+    assert L.poetx_attn_window_plan_bytes(C.byref(attn_shape()), C.byref(w)) == 0
+    assert L.poetx_attn_window_workspace_bytes(C.byref(attn_shape()), C.byref(w), 1) == 0
+    assert calls(attn_shape(), None) == (1, 1, 1) and "null window" in _err()
+
+
+@pytest.mark.parametrize("kw", [dict(Tq=-1), dict(Hq=7), dict(D=12), dict(act=2), dict(cap=-1.0), dict(ldk=248),
+                                dict(ndoc=1 << 20)])
+def test_window_shape_errors(kw):
+    assert calls(attn_shape(**kw), _lib.Window(16, 4)) == (1, 1, 1)
+
+
+def test_window_sizes_and_nothing_to_do():
+    L = _lib.lib()
+    sh, none, plain, sinks = attn_shape(), _lib.Window(0, 4), _lib.Window(16, 0), _lib.Window(16, 4)
+    size = lambda w: L.poetx_attn_window_plan_bytes(C.byref(sh), C.byref(w))
+    work = lambda w, i: L.poetx_attn_window_workspace_bytes(C.byref(sh), C.byref(w), i)
+    assert size(none) == L.poetx_attn_plan_bytes(C.byref(sh)) and work(none, 1) == L.poetx_attn_workspace_bytes(C.byref(sh), 1)
+    assert size(plain) == size(none) and size(sinks) >= size(none) + 100 * 8 + 3 * 16
+    assert work(sinks, 1) >= work(plain, 1) + 2 * 4 * 128 * 8 * 4 and work(sinks, 2) == 0
+    assert calls(sh, sinks, plan_n=size(sinks) - 1)[0] == 3
+    assert calls(sh, sinks, ws_n=work(sinks, 1) - 1)[2] == 3
+    empty = attn_shape(Tq=0, Tk=0)
+    assert L.poetx_attn_window_fwd(C.byref(empty), C.byref(sinks), *[None] * 7, None, 0, None) == 0
+    assert L.poetx_attn_window_bwd(C.byref(empty), C.byref(sinks), *[None] * 11, None, 0, None) == 0
+
+
+def test_window_pointer_errors():
+    L, sh, w = _lib.lib(), attn_shape(), _lib.Window(16, 4)
+    for i, nm in enumerate(("q", "k", "v", "slopes", "plan", "o", "lse")):
+        args = [FAKE] * 7
+        args[i] = MISALIGNED
+        assert L.poetx_attn_window_fwd(C.byref(sh), C.byref(w), *args, FAKE, 1 << 30, None) == 1 and f"'{nm}'" in _err()
+    for i, nm in enumerate(("dout", "q", "k", "v", "o", "lse", "slopes", "plan", "dq", "dk", "dv")):
+        args = [FAKE] * 11
+        args[i] = MISALIGNED
+        assert L.poetx_attn_window_bwd(C.byref(sh), C.byref(w), *args, FAKE, 1 << 40, None) == 1 and f"'{nm}'" in _err()
+    for i, nm in enumerate(("cu_q", "cu_k", "plan")):
+        args = [FAKE] * 3
+        args[i] = None
+        assert L.poetx_attn_window_plan(C.byref(sh), C.byref(w), *args, 1 << 40, None) == 1 and f"'{nm}'" in _err()
