@@ -585,6 +585,69 @@ int32_t poetx_attn_decode(const poetx_decode_shape* sh, const void* q, const voi
                           const int32_t* start, const int32_t* len, const float* slopes, void* o,
                           void* ws, size_t ws_bytes, poetx_stream_t stream);
 
+/*
+ * poetx_attn_window_decode -- the same with a window and sinks: the query at
+ * position len[b] - 1 sees the last `window` positions and the first `sinks`
+ * ones (window = 0: all).
+ *   ring = 0: position p lies in row p, len is clamped to [0, rows].
+ *   ring != 0: the cache is a ring.  Positions below `sinks` lie in their rows,
+ *   p >= sinks in row sinks + (p - sinks) mod (rows - sinks); len counts every
+ *   token there has been and may pass rows.  1 <= window <= rows - sinks.
+ *   ws poetx_attn_window_decode_workspace_bytes(sh, win) bytes, for either.
+ * Everything else as in poetx_attn_decode.
+ */
+size_t poetx_attn_window_decode_workspace_bytes(const poetx_decode_shape* sh, const poetx_window* win);
+int32_t poetx_attn_window_decode(const poetx_decode_shape* sh, const poetx_window* win, int32_t ring, const void* q,
+                                 const void* k, const void* v, const int32_t* len, const float* slopes, void* o,
+                                 void* ws, size_t ws_bytes, poetx_stream_t stream);
+
+/*
+ * A key/value cache held in 4 bits: blocks of 32 consecutive elements of a head
+ * (the last one filled up with zeros), codes e2m1 (a sign and 0, .5, 1, 1.5, 2,
+ * 3, 4 or 6: codes 0..7, 8 more when negative) and a scale 2^e, held as e + 127:
+ * the microscaling format MXFP4 of the Open Compute Project, 4.25 bits an element.
+ *   kc, vc  [B][Hkv][rows][blocks * 16] bytes, element 2 i of a row in the low
+ *           half of byte i; blocks = (D + 31) / 32
+ *   ks, vs  [B][Hkv][blocks][rows] bytes
+ * rows is a multiple of 64.  A held value is exact in bf16.
+ *
+ * poetx_kv4_write puts token t, row t of k and v [T][Hkv][D] (act), at position
+ * pos[t] of sequence seq[t] (seq NULL: t); nothing is written for a token whose
+ * sequence or position the cache does not have.  e is the least from -127 on with
+ * max |x| < 7 * 2^e, at most 125; a code is the nearest of x / 2^e, ties to the
+ * even code, 6 above that.  A block with NaN or infinity reads as NaN.
+ *   ring and sinks as in poetx_attn_window_decode: without a ring, position p
+ *   lies in row p.  Tokens of one call must have rows of their own.
+ * poetx_kv4_read gives back the values at such places (NaN where the cache has
+ * none; in a ring, what the position's row holds now).
+ *   T Hkv < 2^27; ldk, ldv: pitches of k and v.
+ * Errors: ERR_ARG, ERR_DEVICE.
+ */
+typedef struct {
+  int32_t T, B, rows, Hkv, D, act, sinks, ring;
+  int64_t ldk, ldv;
+} poetx_kv4_shape;
+int32_t poetx_kv4_write(const poetx_kv4_shape* sh, const void* k, const void* v, const int32_t* seq, const int32_t* pos,
+                        void* kc, void* ks, void* vc, void* vs, poetx_stream_t stream);
+int32_t poetx_kv4_read(const poetx_kv4_shape* sh, const int32_t* seq, const int32_t* pos, const void* kc, const void* ks,
+                       const void* vc, const void* vs, void* k, void* v, poetx_stream_t stream);
+
+/*
+ * poetx_attn_kv4_decode -- poetx_attn_decode (window = 0, with start) or
+ * poetx_attn_window_decode (without) over such a cache.  The products of the
+ * held values are exact, sums float32 (bf16: p in two bf16 parts; float32: q and
+ * p in three).  Of the shape ldk, ldv, bsk and bsv have to be valid and are not
+ * used.
+ *   ws poetx_attn_kv4_decode_workspace_bytes(sh, win) bytes, for either kind of
+ *   cache.
+ * Errors: ERR_ARG, ERR_WORKSPACE, ERR_DEVICE.
+ */
+size_t poetx_attn_kv4_decode_workspace_bytes(const poetx_decode_shape* sh, const poetx_window* win);
+int32_t poetx_attn_kv4_decode(const poetx_decode_shape* sh, const poetx_window* win, int32_t ring, const void* q,
+                              const void* kc, const void* ks, const void* vc, const void* vs, const int32_t* start,
+                              const int32_t* len, const float* slopes, void* o, void* ws, size_t ws_bytes,
+                              poetx_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

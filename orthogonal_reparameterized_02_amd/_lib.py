@@ -62,6 +62,12 @@ SIGNATURES = {
     "poetx_attn_window_bwd": (_i, [_p] * 14 + [_sz, _p]),
     "poetx_attn_decode_workspace_bytes": (_sz, [_p]),
     "poetx_attn_decode": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _p, _sz, _p]),
+    "poetx_attn_window_decode_workspace_bytes": (_sz, [_p, _p]),
+    "poetx_attn_window_decode": (_i, [_p, _p, _i] + [_p] * 7 + [_sz, _p]),
+    "poetx_kv4_write": (_i, [_p] * 10),
+    "poetx_kv4_read": (_i, [_p] * 10),
+    "poetx_attn_kv4_decode_workspace_bytes": (_sz, [_p, _p]),
+    "poetx_attn_kv4_decode": (_i, [_p, _p, _i] + [_p] * 10 + [_sz, _p]),
 }
 
 
@@ -86,6 +92,7 @@ QkNormShape = _struct("QkNormShape", "T Hq Hk D rot P act interleaved", "eps",
                       "ldq ldk ldqo ldko lddq lddk")
 AttnShape = _struct("AttnShape", "Tq Tk ndoc Hq Hkv D act causal", "scale cap",
                     "ldq ldk ldv ldo lddo lddq lddk lddv")
+Kv4Shape = _struct("Kv4Shape", "T B rows Hkv D act sinks ring", "", "ldk ldv")
 Window = _struct("Window", "window sinks", "", "")
 DecodeShape = _struct("DecodeShape", "B Hq Hkv D act rows", "scale cap",
                       "ldq ldo ldk ldv bsk bsv")

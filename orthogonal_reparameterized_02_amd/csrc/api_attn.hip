@@ -212,10 +212,6 @@ DecodeArgs decode_args(const poetx_decode_shape* sh) {
   return a;
 }
 
-size_t decode_ws(const poetx_decode_shape* sh) {
-  return sh->B ? align_up(attn_decode_ws_bytes(decode_args(sh))) : 256;
-}
-
 int32_t check_dropout(const char* fn, int64_t n, int32_t act, double p, uint64_t offset,
                       const uint64_t* offset_dev) {
   if (n < 0) return fail(POETX_ERR_ARG, "%s: n=%lld < 0", fn, (long long)n);
@@ -552,15 +548,33 @@ int32_t poetx_attn_window_bwd(const poetx_attn_shape* sh, const poetx_window* wi
   return bwd_any("poetx_attn_window_bwd", sh, win, dout, q, k, v, o, lse, slopes, plan, dq, dk, dv, ws, ws_bytes, stream);
 }
 
-size_t poetx_attn_decode_workspace_bytes(const poetx_decode_shape* sh) {
-  return check_decode("poetx_attn_decode_workspace_bytes", sh) == POETX_OK ? decode_ws(sh) : 0;
+}  // extern "C"
+
+namespace {
+
+// the window of a decoding call; a ring holds one
+int32_t check_decode_window(const char* fn, const poetx_decode_shape* sh, const poetx_window* win, int32_t ring) {
+  TRY(check_decode(fn, sh));
+  TRY(check_window(fn, win));
+  if (ring && win->window < 1) return fail(POETX_ERR_ARG, "%s: a ring needs a window", fn);
+  if (ring && (int64_t)win->window + win->sinks > sh->rows)
+    return fail(POETX_ERR_ARG, "%s: window=%d and sinks=%d in a ring of rows=%d", fn, win->window, win->sinks, sh->rows);
+  return POETX_OK;
 }
 
-int32_t poetx_attn_decode(const poetx_decode_shape* sh, const void* q, const void* k, const void* v,
-                          const int32_t* start, const int32_t* len, const float* slopes, void* o,
-                          void* ws, size_t ws_bytes, poetx_stream_t stream) {
-  const char* fn = "poetx_attn_decode";
-  TRY(check_decode(fn, sh));
+DecodeArgs decode_window_args(const poetx_decode_shape* sh, const poetx_window* win, int32_t ring) {
+  DecodeArgs a = decode_args(sh);
+  const poetx_window w = window_of(win);
+  a.window = w.window, a.sinks = w.sinks, a.ring = ring != 0;
+  return a;
+}
+
+size_t decode_ws(const DecodeArgs& a) { return a.B ? align_up(attn_decode_ws_bytes(a)) : 256; }
+
+int32_t decode_any(const char* fn, const poetx_decode_shape* sh, const poetx_window* win, int32_t ring, const void* q,
+                   const void* k, const void* v, const int32_t* start, const int32_t* len, const float* slopes,
+                   void* o, void* ws, size_t ws_bytes, poetx_stream_t stream) {
+  TRY(check_decode_window(fn, sh, win, ring));
   if (sh->B == 0) return ok();
   NEED_PTR(q);
   if (sh->rows) {
@@ -572,15 +586,157 @@ int32_t poetx_attn_decode(const poetx_decode_shape* sh, const void* q, const voi
   OPT_PTR(slopes);
   NEED_PTR(o);
   NEED_PTR(ws);
-  const size_t need = decode_ws(sh);
+  DecodeArgs a = decode_window_args(sh, win, ring);
+  const size_t need = decode_ws(a);
   if (ws_bytes < need) return fail(POETX_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, ws_bytes, need);
-  DecodeArgs a = decode_args(sh);
   a.q = q, a.k = k, a.v = v, a.o = o;
   a.slopes = slopes;
   a.start = start, a.len = len;
   const hipStream_t s = (hipStream_t)stream;
   return launched(sh->act == POETX_BF16 ? launch_attn_decode<bf16>(a, (float*)ws, s)
                                                : launch_attn_decode<float>(a, (float*)ws, s), fn);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t poetx_attn_decode_workspace_bytes(const poetx_decode_shape* sh) {
+  return check_decode("poetx_attn_decode_workspace_bytes", sh) == POETX_OK ? decode_ws(decode_args(sh)) : 0;
+}
+size_t poetx_attn_window_decode_workspace_bytes(const poetx_decode_shape* sh, const poetx_window* win) {
+  return check_decode_window("poetx_attn_window_decode_workspace_bytes", sh, win, 0) == POETX_OK
+             ? decode_ws(decode_window_args(sh, win, 0)) : 0;
+}
+
+int32_t poetx_attn_decode(const poetx_decode_shape* sh, const void* q, const void* k, const void* v,
+                          const int32_t* start, const int32_t* len, const float* slopes, void* o,
+                          void* ws, size_t ws_bytes, poetx_stream_t stream) {
+  return decode_any("poetx_attn_decode", sh, &NO_WINDOW, 0, q, k, v, start, len, slopes, o, ws, ws_bytes, stream);
+}
+int32_t poetx_attn_window_decode(const poetx_decode_shape* sh, const poetx_window* win, int32_t ring, const void* q,
+                                 const void* k, const void* v, const int32_t* len, const float* slopes, void* o,
+                                 void* ws, size_t ws_bytes, poetx_stream_t stream) {
+  return decode_any("poetx_attn_window_decode", sh, win, ring, q, k, v, nullptr, len, slopes, o, ws, ws_bytes, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+int32_t check_kv4(const char* fn, const poetx_kv4_shape* sh) {
+  if (!sh) return fail(POETX_ERR_ARG, "%s: null shape", fn);
+  if (sh->T < 0 || sh->T > ROWS_MAX || sh->B < 0 || sh->B > B_MAX)
+    return fail(POETX_ERR_ARG, "%s: T=%d (0..%d) B=%d (0..%d)", fn, sh->T, ROWS_MAX, sh->B, B_MAX);
+  if (sh->rows < 0 || sh->rows > ROWS_MAX || sh->rows % 64)
+    return fail(POETX_ERR_ARG, "%s: rows=%d must be a multiple of 64, 0..%d", fn, sh->rows, ROWS_MAX);
+  TRY(check_heads(fn, sh->Hkv, sh->Hkv, sh->D));
+  TRY(check_act(fn, sh->act));
+  if (sh->sinks < 0 || sh->sinks > SINKS_MAX) return fail(POETX_ERR_ARG, "%s: sinks=%d outside 0..%d", fn, sh->sinks, SINKS_MAX);
+  if (sh->ring && sh->rows <= sh->sinks) return fail(POETX_ERR_ARG, "%s: rows=%d of a ring with sinks=%d", fn, sh->rows, sh->sinks);
+  // a workgroup of 256 threads for 16 tokens of a head and more: 2^32 - 1 threads at most
+  if ((int64_t)sh->T * sh->Hkv >= (int64_t)1 << 27)
+    return fail(POETX_ERR_ARG, "%s: T=%d tokens of Hkv=%d heads: 2^27 or more", fn, sh->T, sh->Hkv);
+  TRY(check_ld(fn, "ldk", sh->ldk, (int64_t)sh->Hkv * sh->D));
+  TRY(check_ld(fn, "ldv", sh->ldv, (int64_t)sh->Hkv * sh->D));
+  return POETX_OK;
+}
+
+Kv4Args kv4_args(const poetx_kv4_shape* sh) {
+  Kv4Args a = {};
+  a.T = sh->T, a.B = sh->B, a.rows = sh->rows, a.Hkv = sh->Hkv, a.D = sh->D, a.sinks = sh->sinks, a.ring = sh->ring != 0;
+  a.ldk = sh->ldk, a.ldv = sh->ldv;
+  return a;
+}
+
+int32_t check_kv4_decode(const char* fn, const poetx_decode_shape* sh, const poetx_window* win, int32_t ring) {
+  TRY(check_decode_window(fn, sh, win, ring));
+  if (sh->rows % 64) return fail(POETX_ERR_ARG, "%s: rows=%d must be a multiple of 64", fn, sh->rows);
+  return POETX_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int32_t poetx_kv4_write(const poetx_kv4_shape* sh, const void* k, const void* v, const int32_t* seq, const int32_t* pos,
+                        void* kc, void* ks, void* vc, void* vs, poetx_stream_t stream) {
+  const char* fn = "poetx_kv4_write";
+  TRY(check_kv4(fn, sh));
+  if (sh->T == 0 || sh->B == 0 || sh->rows == 0) return ok();
+  NEED_PTR(k);
+  NEED_PTR(v);
+  OPT_PTR(seq);
+  NEED_PTR(pos);
+  NEED_PTR(kc);
+  NEED_PTR(ks);
+  NEED_PTR(vc);
+  NEED_PTR(vs);
+  Kv4Args a = kv4_args(sh);
+  a.k = const_cast<void*>(k), a.v = const_cast<void*>(v), a.seq = seq, a.pos = pos;
+  a.kc = (uint8_t*)kc, a.ks = (uint8_t*)ks, a.vc = (uint8_t*)vc, a.vs = (uint8_t*)vs;
+  const hipStream_t s = (hipStream_t)stream;
+  return launched(sh->act == POETX_BF16 ? launch_kv4_write<bf16>(a, s) : launch_kv4_write<float>(a, s), fn);
+}
+
+int32_t poetx_kv4_read(const poetx_kv4_shape* sh, const int32_t* seq, const int32_t* pos, const void* kc, const void* ks,
+                       const void* vc, const void* vs, void* k, void* v, poetx_stream_t stream) {
+  const char* fn = "poetx_kv4_read";
+  TRY(check_kv4(fn, sh));
+  if (sh->T == 0) return ok();
+  NEED_PTR(k);
+  NEED_PTR(v);
+  OPT_PTR(seq);
+  NEED_PTR(pos);
+  if (sh->B && sh->rows) {
+    NEED_PTR(kc);
+    NEED_PTR(ks);
+    NEED_PTR(vc);
+    NEED_PTR(vs);
+  }
+  Kv4Args a = kv4_args(sh);
+  if (a.rows == 0) a.B = 0;  // every position is outside
+  a.k = k, a.v = v, a.seq = seq, a.pos = pos;
+  a.kc = (uint8_t*)const_cast<void*>(kc), a.ks = (uint8_t*)const_cast<void*>(ks);
+  a.vc = (uint8_t*)const_cast<void*>(vc), a.vs = (uint8_t*)const_cast<void*>(vs);
+  const hipStream_t s = (hipStream_t)stream;
+  return launched(sh->act == POETX_BF16 ? launch_kv4_read<bf16>(a, s) : launch_kv4_read<float>(a, s), fn);
+}
+
+size_t poetx_attn_kv4_decode_workspace_bytes(const poetx_decode_shape* sh, const poetx_window* win) {
+  if (check_kv4_decode("poetx_attn_kv4_decode_workspace_bytes", sh, win, 0) != POETX_OK) return 0;
+  const DecodeArgs a = decode_window_args(sh, win, 0);
+  return a.B ? align_up(attn_kv4_ws_bytes(a)) : 256;
+}
+
+int32_t poetx_attn_kv4_decode(const poetx_decode_shape* sh, const poetx_window* win, int32_t ring, const void* q,
+                              const void* kc, const void* ks, const void* vc, const void* vs, const int32_t* start,
+                              const int32_t* len, const float* slopes, void* o, void* ws, size_t ws_bytes,
+                              poetx_stream_t stream) {
+  const char* fn = "poetx_attn_kv4_decode";
+  TRY(check_kv4_decode(fn, sh, win, ring));
+  if (sh->B == 0) return ok();
+  NEED_PTR(q);
+  if (sh->rows) {
+    NEED_PTR(kc);
+    NEED_PTR(ks);
+    NEED_PTR(vc);
+    NEED_PTR(vs);
+  }
+  OPT_PTR(start);
+  if (start && win->window) return fail(POETX_ERR_ARG, "%s: 'start' with a window", fn);
+  NEED_PTR(len);
+  OPT_PTR(slopes);
+  NEED_PTR(o);
+  NEED_PTR(ws);
+  DecodeArgs a = decode_window_args(sh, win, ring);
+  const size_t need = align_up(attn_kv4_ws_bytes(a));
+  if (ws_bytes < need) return fail(POETX_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, ws_bytes, need);
+  a.q = q, a.k = kc, a.v = vc, a.ks = (const uint8_t*)ks, a.vs = (const uint8_t*)vs, a.o = o;
+  a.slopes = slopes;
+  a.start = start, a.len = len;
+  const hipStream_t s = (hipStream_t)stream;
+  return launched(sh->act == POETX_BF16 ? launch_attn_kv4<bf16>(a, (float*)ws, s) : launch_attn_kv4<float>(a, (float*)ws, s), fn);
 }
 
 }  // extern "C"

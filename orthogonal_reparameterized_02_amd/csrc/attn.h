@@ -163,6 +163,23 @@ struct DecodeArgs {
   int window, sinks, ring;  // window 0: every row
   const uint8_t *ks, *vs;   // scales of a cache in 4 bits
 };
+// ---- a cache in 4 bits (kv4.hip, attn_kv4.hip) ---------------------------------
+// Blocks of 32 elements: codes [B][Hkv][rows][blocks * 16] bytes, element 2 i
+// in the low half of byte i; scales [B][Hkv][blocks][rows].
+inline __host__ __device__ int kv4_blocks(int D) { return (D + 31) / 32; }
+struct Kv4Args {
+  int T, B, rows, Hkv, D, sinks, ring;
+  long ldk, ldv;
+  const int *seq, *pos;  // seq null: token t is of sequence t
+  void *k, *v;           // read from (write) or written (read)
+  uint8_t *kc, *ks, *vc, *vs;
+};
+template <typename TS> hipError_t launch_kv4_write(const Kv4Args& a, hipStream_t s);
+template <typename TS> hipError_t launch_kv4_read(const Kv4Args& a, hipStream_t s);
+// a.k, a.v: codes
+size_t attn_kv4_ws_bytes(const DecodeArgs& a);
+template <typename T> hipError_t launch_attn_kv4(const DecodeArgs& a, float* ws, hipStream_t s);
+
 // ws: attn_decode_ws_bytes(a) bytes for the pieces' partial results
 size_t attn_decode_ws_bytes(const DecodeArgs& a);
 template <typename TS> hipError_t launch_attn_decode(const DecodeArgs& a, float* ws, hipStream_t s);

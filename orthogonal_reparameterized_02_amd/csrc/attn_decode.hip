@@ -21,6 +21,8 @@
 #include <algorithm>
 
 #include "attn_tile.h"
+#include "decode_join.h"
+#include "decode_view.h"
 
 namespace poetx {
 
@@ -37,8 +39,8 @@ constexpr int MAX_PIECES = 64;
 // to 4096 rows 33.3 us in pieces of 128, 27.3 in 512); but one workgroup a CU
 // from 128 rows on, where latency counts.
 int pieces_of(const DecodeArgs& a) {
-  const int per = a.B * a.Hkv * ((a.group + 31) / 32);
-  const auto cut = [&](int fill, int least) { return std::min((fill + per - 1) / per, (a.rows + least - 1) / least); };
+  const int per = a.B * a.Hkv * ((a.group + 31) / 32), rows = (int)std::min(view_rows(a, BN), (long)INT32_MAX - 65535);
+  const auto cut = [&](int fill, int least) { return std::min((fill + per - 1) / per, (rows + least - 1) / least); };
   return std::max(1, std::min(std::max(cut(2048, 512), cut(256, GRAIN)), MAX_PIECES));
 }
 
@@ -46,11 +48,35 @@ int pieces_of(const DecodeArgs& a) {
 __device__ __forceinline__ void range_of(const DecodeArgs& a, int b, int pieces, int& lo, int& hi, int& piece) {
   hi = min(max(a.len[b], 0), a.rows);
   lo = a.start ? min(max(a.start[b], 0), hi) : 0;
-  const int n = (hi - lo + pieces - 1) / pieces;
-  piece = (n + GRAIN - 1) / GRAIN * GRAIN;
+  piece = piece_of(hi - lo, pieces, GRAIN);
 }
 
-template <typename T, int DP, int MODE>
+// the same with a window: the padded rows of its view
+__device__ __forceinline__ void range_of(const DecodeArgs& a, int b, int pieces, View& v, int& lo, int& hi, int& piece) {
+  v.init<BN, false>(a, b);
+  lo = 0;
+  hi = v.total;
+  piece = piece_of(v.total, pieces, GRAIN);
+}
+
+struct Plain {
+  static __device__ __forceinline__ int rows(const DecodeArgs& a, int b, int pieces, int& piece) {
+    int lo, hi;
+    range_of(a, b, pieces, lo, hi, piece);
+    return hi - lo;
+  }
+};
+struct Windowed {
+  static __device__ __forceinline__ int rows(const DecodeArgs& a, int b, int pieces, int& piece) {
+    View v;
+    int lo, hi;
+    range_of(a, b, pieces, v, lo, hi, piece);
+    return hi;
+  }
+};
+
+// WIN: the rows are those of a View, tile by tile
+template <typename T, int DP, int MODE, bool WIN>
 __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void k_attn_decode(DecodeArgs a, int pieces, float* part, float* ml) {
   using L = Tile<T, DP>;
   constexpr int TILE = BN * L::RB;
@@ -62,9 +88,26 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void 
   const int hk = blockIdx.y / groups, g0 = 32 * (blockIdx.y % groups);
   const int heads = min(a.group - g0, 32), h0 = hk * a.group + g0;
   int lo, hi, piece;
-  range_of(a, b, pieces, lo, hi, piece);
+  View view;
+  if constexpr (WIN) range_of(a, b, pieces, view, lo, hi, piece);
+  else range_of(a, b, pieces, lo, hi, piece);
   const int p0 = lo + s * piece, p1 = min(p0 + piece, hi);
   if (s > 0 && p0 >= hi) return;
+  // rows [row, end) of the tile at j (past the piece: none), and the position
+  // of its first row
+  const auto rows_at = [&](int j, int& row, int& end, int& pos) {
+    if constexpr (WIN) {
+      row = end = pos = 0;
+      if (j < p1) {
+        int begin, shift;
+        view.tile<BN, false>(j, row, begin, end, shift);
+        pos = row + shift;
+      }
+    } else {
+      row = pos = j;
+      end = p1;
+    }
+  };
 
   const T* kp = (const T*)a.k + (long)b * a.bsk + (long)hk * a.D;
   const T* vp = (const T*)a.v + (long)b * a.bsv + (long)hk * a.D;
@@ -87,10 +130,13 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void 
   float m = -INFINITY, l = 0.0f;
   int j0 = p0 + wave * BN;
   wait_loads();  // counts below are of tile loads only
+  int row, end, pos;
+  rows_at(j0, row, end, pos);
   if (j0 < p1) {
-    lk.load(kp, a.ldk, j0, p1, ldsk);
-    lv.load(vp, a.ldv, j0, p1, ldsv);
+    lk.load(kp, a.ldk, row, end, ldsk);
+    lv.load(vp, a.ldv, row, end, ldsv);
   }
+  const int last = WIN ? view.last : hi - 1;
   for (; j0 < p1; j0 += GRAIN) {
     // the key tile has landed when only the value tile's loads are pending
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(NL) : "memory");
@@ -99,15 +145,16 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void 
     for (int ks = 0; ks < L::KS; ++ks) sc = mma16((const T*)nullptr, L::row_frag(smem, kr, 0, ks), qf[ks], sc);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     const int jn = min(j0 + GRAIN, p1);  // a load past the piece has no rows: zeros
-    lk.load(kp, a.ldk, jn, p1, ldsk);
-    const int jl = j0 + 4 * (lane >> 5);
-    const float d0 = (float)(hi - 1 - jl);
+    const int jl = pos + 4 * (lane >> 5), jend = pos + (end - row);
+    rows_at(jn, row, end, pos);
+    lk.load(kp, a.ldk, row, end, ldsk);
+    const float d0 = (float)(last - jl);
     float top = -INFINITY, unused;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const int j = jl + 8 * (i / 4) + i % 4;
       sc[i] = score2<T, MODE>(sc[i], sa, d0 - (float)(8 * (i / 4) + i % 4), unused);
-      sc[i] = j < p1 ? sc[i] : -INFINITY;
+      sc[i] = j < jend ? sc[i] : -INFINITY;
       top = fmaxf(top, sc[i]);
     }
     top = fmaxf(top, other_half(top));
@@ -138,7 +185,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void 
       }
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    lv.load(vp, a.ldv, jn, p1, ldsv);
+    lv.load(vp, a.ldv, row, end, ldsv);
   }
   l += other_half(l);
 
@@ -187,64 +234,26 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void 
   }
 }
 
-// joins the pieces of one query head: lane l of every wave holds elements
-// 2 l, 2 l + 1; wave w takes pieces w, w + NW, ...
-template <typename T>
-__global__ __launch_bounds__(64 * NW) void k_attn_decode_join(DecodeArgs a, int pieces, const float* part, const float* ml) {
-  __shared__ float red[NW][130];
-  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-  const int h = blockIdx.x, b = blockIdx.y;
-  int lo, hi, piece;
-  range_of(a, b, pieces, lo, hi, piece);
-  if (hi - lo <= piece) return;  // written by the first pass
-  const int n = (hi - lo + piece - 1) / piece;
-  const long at = ((long)b * a.Hq + h) * pieces;
-  const float mine = lane < n ? ml[2 * (at + lane)] : -INFINITY;  // n <= 64
-  float M = mine;
-#pragma unroll
-  for (int x = 32; x; x >>= 1) M = fmaxf(M, __shfl_xor(M, x));
-  const float ref = M == -INFINITY ? 0.0f : M;
-  const float f = exp2_hw(mine - ref);
-  float L = lane < n ? f * ml[2 * (at + lane) + 1] : 0.0f;
-#pragma unroll
-  for (int x = 32; x; x >>= 1) L += __shfl_xor(L, x);
-  float2 acc = make_float2(0.0f, 0.0f);
-  const bool in = 2 * lane < a.D;
-  for (int s = wave; s < n; s += NW) {
-    const float w = __shfl(f, s);
-    const float2 v = in ? *reinterpret_cast<const float2*>(part + (at + s) * a.D + 2 * lane) : make_float2(0.0f, 0.0f);
-    acc.x = fmaf(w, v.x, acc.x);
-    acc.y = fmaf(w, v.y, acc.y);
-  }
-  red[wave][2 * lane] = acc.x;
-  red[wave][2 * lane + 1] = acc.y;
-  __syncthreads();
-  const int d = threadIdx.x;
-  if (d < a.D) {
-    float sum = 0.0f;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) sum += red[w][d];
-    St<T>::st((T*)a.o + (long)b * a.ldo + (long)h * a.D + d, L == 0.0f ? 0.0f : sum / L);
-  }
-}
-
 size_t part_floats(const DecodeArgs& a) { return (size_t)a.B * a.Hq * pieces_of(a) * a.D; }
 
-template <typename T, int DP, int MODE> hipError_t decode(const DecodeArgs& a, float* ws, hipStream_t s) {
+template <typename T, int DP, int MODE, bool WIN> hipError_t decode(const DecodeArgs& a, float* ws, hipStream_t s) {
   constexpr int lds = std::max(NW * 2 * BN * Tile<T, DP>::RB, (2 * NW * 32 + NW * 32 * DP) * 4);
-  const hipError_t e = lds_opt_in((const void*)k_attn_decode<T, DP, MODE>, lds);
+  const hipError_t e = lds_opt_in((const void*)k_attn_decode<T, DP, MODE, WIN>, lds);
   if (e != hipSuccess) return e;
   const int pieces = pieces_of(a);
   float* ml = ws + part_floats(a);
-  k_attn_decode<T, DP, MODE><<<dim3(pieces, a.Hkv * ((a.group + 31) / 32), a.B), 64 * NW, lds, s>>>(a, pieces, ws, ml);
+  k_attn_decode<T, DP, MODE, WIN><<<dim3(pieces, a.Hkv * ((a.group + 31) / 32), a.B), 64 * NW, lds, s>>>(a, pieces, ws, ml);
   const hipError_t e2 = hipGetLastError();
   if (e2 != hipSuccess || pieces == 1) return e2;
-  k_attn_decode_join<T><<<dim3(a.Hq, a.B), 64 * NW, 0, s>>>(a, pieces, ws, ml);
+  k_attn_decode_join<T, std::conditional_t<WIN, Windowed, Plain>><<<dim3(a.Hq, a.B), 64 * NW, 0, s>>>(a, pieces, ws, ml);
   return hipGetLastError();
 }
 
 template <typename T, int DP> hipError_t decode_mode(const DecodeArgs& a, float* ws, hipStream_t s) {
-  return by_mode<T>(a.slopes, a.cap, [&](auto mode) { return decode<T, DP, decltype(mode)::value>(a, ws, s); });
+  return by_mode<T>(a.slopes, a.cap, [&](auto mode) {
+    constexpr int MODE = decltype(mode)::value;
+    return a.window ? decode<T, DP, MODE, true>(a, ws, s) : decode<T, DP, MODE, false>(a, ws, s);
+  });
 }
 
 }  // namespace

@@ -1,0 +1,346 @@
+// Attention of one query row per sequence over a cache in 4 bits (kv4.hip for
+// the format), on MFMA tiles.
+//
+// The query heads that share a key head are the columns of 16-wide tiles, up
+// to 16 of them.  A workgroup takes a piece of one sequence's rows for one key
+// head; each of its four waves goes through 64-row tiles of its own without any
+// barrier, the next tile's codes on their way to registers.
+//   Scores: lane (r, g) = (lane % 16, lane / 16) loads block g of rows 4 r + t,
+// t = 0..3: sixteen bytes are 32 codes, which the conversion with a scale turns
+// into exact bf16 numbers in the order of the A operand (K = 8 elements of each
+// of the four blocks; the queries are laid out alike).  The four scales of a
+// block are one dword.  D[row][query] leaves lane (query, h) the rows 16 h +
+// 4 i + t.
+//   Values: sum over rows, so the operand is the transposed tile.  Converted
+// values go through LDS, 32 rows (t, t + 1) at a time, and come back down their
+// columns by ds_read_b64_tr_b16 in just that order of rows; 16-byte chunk c of
+// row r lies at c ^ key(r), which spreads both accesses over the banks.
+//   bf16 queries have probabilities in two bf16 parts, float32 ones both
+// queries and probabilities in three: every product is exact, sums are float32.
+#include <algorithm>
+
+#include "attn_tile.h"
+#include "decode_join.h"
+#include "decode_view.h"
+
+namespace poetx {
+
+namespace {
+
+constexpr int NW = 4;           // waves a workgroup
+constexpr int BN = 64;          // rows a tile
+constexpr int GRAIN = NW * BN;  // a piece is a multiple of this
+constexpr int HEADS = 16;       // query heads a workgroup
+constexpr int MAX_PIECES = 64;
+// The reference of the exponentials moves only when a score passes it by more
+// than this (log2): float32 sums hold probabilities up to 2^8 as well, and
+// without a move no lane has to hear of the others' maxima.
+constexpr float SLACK = 8.0f;
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ f32x4 mma(uint4 a, uint4 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(b), c, 0, 0, 0);
+}
+
+// eight codes times a scale, as bf16
+__device__ __forceinline__ uint4 expand(uint32_t c, float scale) {
+  uint4 u;
+  u.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 0));
+  u.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 1));
+  u.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 2));
+  u.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 3));
+  return u;
+}
+__device__ __forceinline__ float scale_of(uint32_t bytes, int t) {
+  return __uint_as_float((bytes >> (8 * t) & 0xffu) << 23);
+}
+
+// x (>= 0, or any float for queries) as N bf16 parts: pack[n] gets part n of two
+template <int N> __device__ __forceinline__ void parts2(float x, float y, uint32_t (&p)[N]) {
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    p[n] = pack2bf(x, y);
+    x -= __uint_as_float(p[n] << 16);
+    y -= __uint_as_float(p[n] & 0xffff0000u);
+  }
+}
+
+// Pieces that a sequence is cut into at most, as in attn_decode.hip
+int pieces_of(const DecodeArgs& a) {
+  const int per = a.B * a.Hkv * ((a.group + HEADS - 1) / HEADS), rows = (int)std::min(view_rows(a, BN), (long)INT32_MAX - 65535);
+  const auto cut = [&](int fill, int least) { return std::min((fill + per - 1) / per, (rows + least - 1) / least); };
+  return std::max(1, std::min(std::max(cut(2048, 1024), cut(256, GRAIN)), MAX_PIECES));
+}
+
+struct Extent {
+  static __device__ __forceinline__ int rows(const DecodeArgs& a, int b, int pieces, int& piece) {
+    View v;
+    v.init<BN, true>(a, b);
+    piece = piece_of(v.total, pieces, GRAIN);
+    return v.total;
+  }
+};
+
+// NBK: blocks a head, rounded up to 2 or 4; nb of them are there
+template <typename T, int NBK, int MODE>
+__global__ __launch_bounds__(64 * NW, 2) void k_attn_kv4(DecodeArgs a, int nb, int pieces, float* part, float* ml) {
+  constexpr int DP = 32 * NBK, NT = DP / 16, RB = 2 * DP;
+  constexpr int PQ = sizeof(T) == 2 ? 1 : 3, PP = sizeof(T) == 2 ? 2 : 3;
+  constexpr int STAGE = 32 * RB;  // bytes of a wave's 32 rows of values
+  extern __shared__ __align__(16) char smem[];
+  const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int r = lane & 15, g = lane >> 4;
+  const int s = blockIdx.x, b = blockIdx.z;
+  const int groups = (a.group + HEADS - 1) / HEADS;
+  const int hk = blockIdx.y / groups, g0 = HEADS * (blockIdx.y % groups);
+  const int heads = min(a.group - g0, HEADS), h0 = hk * a.group + g0;
+  View view;
+  view.init<BN, true>(a, b);
+  const int piece = piece_of(view.total, pieces, GRAIN);
+  const int p0 = s * piece, p1 = min(p0 + piece, view.total);
+  if (s > 0 && p0 >= view.total) return;
+
+  const int blk = NBK == 4 ? g : g >> 1;  // this lane's block of a row
+  const bool there = blk < nb;
+  const long head = (long)b * a.Hkv + hk;
+  const int rowb = nb * 16;
+  const uint8_t* kc = (const uint8_t*)a.k + head * a.rows * rowb;
+  const uint8_t* vc = (const uint8_t*)a.v + head * a.rows * rowb;
+  const uint8_t* ks = a.ks + (head * nb + (there ? blk : 0)) * a.rows + 4 * r;
+  const uint8_t* vs = a.vs + (head * nb + (there ? blk : 0)) * a.rows + 4 * r;
+  const int off = 4 * r * rowb + (there ? g * (4 * NBK) : 0);
+
+  // queries: column r, elements 8 NBK g + 8 c of step c
+  uint4 qf[PQ][NBK];
+  {
+    const T* q = (const T*)a.q + (long)b * a.ldq + (long)(h0 + min(r, heads - 1)) * a.D;
+#pragma unroll
+    for (int c = 0; c < NBK; ++c) {
+      const int e = 8 * NBK * g + 8 * c;
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = e < a.D && r < heads ? St<T>::ld(q + e + i) : 0.0f;
+      uint32_t p[4][PQ];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) parts2<PQ>(x[2 * i], x[2 * i + 1], p[i]);
+#pragma unroll
+      for (int n = 0; n < PQ; ++n) qf[n][c] = make_uint4(p[0][n], p[1][n], p[2][n], p[3][n]);
+    }
+  }
+  const ScoreArgs sa = score_args<T, MODE>(a.scale, a.cap, MODE & 2 ? a.slopes[h0 + min(r, heads - 1)] : 0.0f);
+
+  struct Codes { uint32_t k[4][NBK], v[4][NBK], ks, vs; };
+  const auto fetch = [&](int j, Codes& c, int& row, int& begin, int& end, int& shift) {
+    view.tile<BN, true>(j, row, begin, end, shift);
+    const uint8_t *kp = kc + (long)row * rowb + off, *vp = vc + (long)row * rowb + off;
+    c.ks = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(ks + row));
+    c.vs = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(vs + row));
+    const auto codes = [&](const uint8_t* p, uint32_t (&o)[NBK]) {
+      if constexpr (NBK == 4) {
+        const u32x4_t u = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p));
+        o[0] = u[0], o[1] = u[1], o[2] = u[2], o[3] = u[3];
+      } else {
+        const u32x2_t u = __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(p));
+        o[0] = u[0], o[1] = u[1];
+      }
+    };
+#pragma unroll
+    for (int t = 0; t < 4; ++t) codes(kp + t * rowb, c.k[t]);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) codes(vp + t * rowb, c.v[t]);
+  };
+
+  // LDS of this wave: row n at n * RB, chunk c of it at c ^ key(n)
+  const auto key = [](int n) { return NBK == 4 ? n & 15 : (n >> 1) & 7; };
+  char* stage = smem + wave * STAGE;
+  const int wr = r * RB + ((NBK * g ^ key(r)) << 4);  // first chunk written; + 16 rows: the same key
+  // transposed read: lane i of 16 gives 4 columns of row 4 g + i / 4
+  const int tr_row = 4 * g + (r >> 2);
+  const int tr = tr_row * RB + ((((r & 3) >> 1) ^ key(tr_row)) << 4) + (r & 1) * 8;
+
+  f32x4 o[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) o[i] = (f32x4){};
+  float m = -INFINITY, l = 0.0f;
+  int j0 = p0 + wave * BN;
+  Codes c;
+  int row, begin, end, shift;
+  if (j0 < p1) fetch(j0, c, row, begin, end, shift);
+  for (; j0 < p1; j0 += GRAIN) {
+    Codes next = c;
+    int nrow = row, nbegin = begin, nend = end, nshift = shift;
+    if (j0 + GRAIN < p1) fetch(j0 + GRAIN, next, nrow, nbegin, nend, nshift);
+    if (!there) {  // no such block: zero
+      c.ks = c.vs = 0x7f7f7f7fu;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int i = 0; i < NBK; ++i) c.k[t][i] = c.v[t][i] = 0;
+    }
+    f32x4 sc[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const float scale = scale_of(c.ks, t);
+      sc[t] = (f32x4){};
+#pragma unroll
+      for (int i = 0; i < NBK; ++i) {
+        const uint4 k = expand(c.k[t][i], scale);
+#pragma unroll
+        for (int n = 0; n < PQ; ++n) sc[t] = mma(k, qf[n][i], sc[t]);
+      }
+    }
+    // this lane's rows: row + 16 g + 4 i + t
+    const float d0 = (float)(view.last - shift - row - 16 * g);
+    float top = -INFINITY, unused;
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sc[t][i] = score2<T, MODE>(sc[t][i], sa, d0 - (float)(4 * i + t), unused);
+    if (begin > row || end < row + BN) {  // some row is not seen: no score, and a value of 0
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = row + 16 * g + 4 * i + t;
+          sc[t][i] = j >= begin && j < end ? sc[t][i] : -INFINITY;
+        }
+        const int jv = row + 4 * r + t;  // row of the codes
+        if (jv < begin || jv >= end) c.vs &= ~(0xffu << (8 * t));
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[t][i]);
+    if (__any(top > m + SLACK)) {
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const float m2 = fmaxf(m, top);
+      const float f = m2 == -INFINITY ? 1.0f : exp2_hw(m - m2);
+      m = m2;
+      l *= f;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) o[i] *= f;
+    }
+    const float ref = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        sc[t][i] = exp2_hw(sc[t][i] - ref);
+        l += sc[t][i];
+      }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float scale = scale_of(c.vs, 2 * u + x);
+#pragma unroll
+        for (int i = 0; i < NBK; ++i)
+          *reinterpret_cast<uint4*>(stage + (wr ^ (i << 4)) + x * 16 * RB) = expand(c.v[2 * u + x][i], scale);
+      }
+      uint4 p[PP];
+      {
+        uint32_t w[4][PP];
+        parts2<PP>(sc[2 * u][0], sc[2 * u][1], w[0]);
+        parts2<PP>(sc[2 * u][2], sc[2 * u][3], w[1]);
+        parts2<PP>(sc[2 * u + 1][0], sc[2 * u + 1][1], w[2]);
+        parts2<PP>(sc[2 * u + 1][2], sc[2 * u + 1][3], w[3]);
+#pragma unroll
+        for (int n = 0; n < PP; ++n) p[n] = make_uint4(w[0][n], w[1][n], w[2][n], w[3][n]);
+      }
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int ct = 0; ct < NT; ++ct) {
+        char* at = stage + (tr ^ (ct << 5));
+        const s16x4_t v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)at);
+        const s16x4_t v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(at + 16 * RB));
+        const uint4 f = __builtin_bit_cast(uint4, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+        for (int n = 0; n < PP; ++n) o[ct] = mma(f, p[n], o[ct]);
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+    c = next;
+    row = nrow, begin = nbegin, end = nend, shift = nshift;
+  }
+  l += __shfl_xor(l, 16);
+  l += __shfl_xor(l, 32);
+
+  // the four waves join: a common maximum, then their sums in wave order
+  __syncthreads();
+  float* wm = reinterpret_cast<float*>(smem);      // [NW][16] maxima, then [NW][16] sums
+  float* wo = wm + 2 * NW * HEADS;                 // [NW][16][DP]
+  if (lane < HEADS) {
+    wm[wave * HEADS + r] = m;
+    wm[(NW + wave) * HEADS + r] = l;
+  }
+  if (r < heads)
+#pragma unroll
+    for (int ct = 0; ct < NT; ++ct)
+      *reinterpret_cast<f32x4*>(wo + (wave * HEADS + r) * DP + 16 * ct + 4 * g) = o[ct];
+  __syncthreads();
+  const bool whole = view.total <= piece;  // one piece: this is the result
+  for (int e = threadIdx.x; e < heads * DP; e += 64 * NW) {
+    const int hh = e / DP, d = e % DP;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) M = fmaxf(M, wm[w * HEADS + hh]);
+    const float ref = M == -INFINITY ? 0.0f : M;
+    float sum = 0.0f, lsum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const float f = exp2_hw(wm[w * HEADS + hh] - ref);
+      lsum += f * wm[(NW + w) * HEADS + hh];
+      sum += f * wo[(w * HEADS + hh) * DP + d];
+    }
+    const int h = h0 + hh;
+    if (whole) {
+      if (d < a.D) St<T>::st((T*)a.o + (long)b * a.ldo + (long)h * a.D + d, lsum == 0.0f ? 0.0f : sum / lsum);
+    } else {
+      const long at = ((long)b * a.Hq + h) * pieces + s;
+      if (d < a.D) part[at * a.D + d] = sum;
+      if (d == 0) {
+        ml[2 * at] = M;
+        ml[2 * at + 1] = lsum;
+      }
+    }
+  }
+}
+
+size_t part_floats(const DecodeArgs& a) { return (size_t)a.B * a.Hq * pieces_of(a) * a.D; }
+
+template <typename T, int NBK, int MODE> hipError_t decode(const DecodeArgs& a, float* ws, hipStream_t s) {
+  constexpr int DP = 32 * NBK, lds = std::max(NW * 32 * 2 * DP, (2 * NW * HEADS + NW * HEADS * DP) * 4);
+  const hipError_t e = lds_opt_in((const void*)k_attn_kv4<T, NBK, MODE>, lds);
+  if (e != hipSuccess) return e;
+  const int pieces = pieces_of(a), nb = kv4_blocks(a.D);
+  float* ml = ws + part_floats(a);
+  k_attn_kv4<T, NBK, MODE><<<dim3(pieces, a.Hkv * ((a.group + HEADS - 1) / HEADS), a.B), 64 * NW, lds, s>>>(a, nb, pieces, ws, ml);
+  const hipError_t e2 = hipGetLastError();
+  if (e2 != hipSuccess || pieces == 1) return e2;
+  k_attn_decode_join<T, Extent><<<dim3(a.Hq, a.B), 64 * JOIN_WAVES, 0, s>>>(a, pieces, ws, ml);
+  return hipGetLastError();
+}
+
+template <typename T, int NBK> hipError_t decode_mode(const DecodeArgs& a, float* ws, hipStream_t s) {
+  return by_mode<T>(a.slopes, a.cap, [&](auto mode) { return decode<T, NBK, decltype(mode)::value>(a, ws, s); });
+}
+
+}  // namespace
+
+size_t attn_kv4_ws_bytes(const DecodeArgs& a) {
+  return (part_floats(a) + (size_t)a.B * a.Hq * pieces_of(a) * 2) * 4;
+}
+
+template <typename T> hipError_t launch_attn_kv4(const DecodeArgs& a, float* ws, hipStream_t s) {
+  return a.D <= 64 ? decode_mode<T, 2>(a, ws, s) : decode_mode<T, 4>(a, ws, s);
+}
+
+template hipError_t launch_attn_kv4<bf16>(const DecodeArgs&, float*, hipStream_t);
+template hipError_t launch_attn_kv4<float>(const DecodeArgs&, float*, hipStream_t);
+
+}  // namespace poetx

@@ -1,0 +1,137 @@
+// Keys and values in 4 bits: blocks of 32 consecutive elements of a head, codes
+// e2m1 (magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6) and a scale 2^e as its exponent
+// byte e + 127 (the microscaling format MXFP4 of the Open Compute Project).
+// e is the least, from -127 on, with max |x| < 7 2^e, at most 125: the largest
+// element then rounds to 6 or less (at e - 1 it would be 8), and every held
+// value is a finite bf16 number.  Codes are the nearest of x / 2^e, ties to the
+// even code, by the conversion instruction.  A block with NaN or infinity gets
+// the byte 255 and reads NaN.
+//
+// Four lanes hold a block, eight elements each; memory-bound.
+#include <algorithm>
+
+#include "attn.h"
+
+namespace poetx {
+
+namespace {
+
+constexpr int NTH = 256;
+
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+
+template <typename TS> struct alignas(16) Pack8 { TS e[8]; };
+
+// row of a position, -1 where there is none
+__device__ __forceinline__ int row_of(const Kv4Args& a, int pos) {
+  if (pos < 0) return -1;
+  if (!a.ring) return pos < a.rows ? pos : -1;
+  return pos < a.sinks ? pos : a.sinks + (pos - a.sinks) % (a.rows - a.sinks);
+}
+
+// This thread's token, head and eighth: a workgroup takes 64 / blocks tokens
+// of one head of one tensor
+struct Place {
+  int t, hk, blk, quarter, seq, row;
+  bool val;  // values
+  __device__ __forceinline__ bool init(const Kv4Args& a, int nb, int t0) {
+    const int per = 4 * nb, u = threadIdx.x / per, w = threadIdx.x - u * per;
+    t = t0 + u;
+    blk = w >> 2;
+    quarter = w & 3;
+    val = (int)blockIdx.y >= a.Hkv;
+    hk = val ? blockIdx.y - a.Hkv : blockIdx.y;
+    if (u >= 64 / nb || t >= a.T) return false;
+    seq = a.seq ? a.seq[t] : t;
+    row = row_of(a, a.pos[t]);
+    if ((unsigned)seq >= (unsigned)a.B) row = -1;
+    return true;
+  }
+  __device__ __forceinline__ long code(const Kv4Args& a, int nb) const {
+    return (((long)seq * a.Hkv + hk) * a.rows + row) * (nb * 16) + blk * 16 + quarter * 4;
+  }
+  __device__ __forceinline__ long scale(const Kv4Args& a, int nb) const {
+    return (((long)seq * a.Hkv + hk) * nb + blk) * a.rows + row;
+  }
+  __device__ __forceinline__ int element() const { return blk * 32 + quarter * 8; }
+};
+
+template <typename TS> __global__ __launch_bounds__(NTH) void k_kv4_write(Kv4Args a, int nb) {
+  Place p;
+  const bool in = p.init(a, nb, blockIdx.x * (64 / nb));
+  float x[8] = {};
+  if (in && p.row >= 0 && p.element() < a.D) {
+    const TS* src = (p.val ? (const TS*)a.v + (long)p.t * a.ldv : (const TS*)a.k + (long)p.t * a.ldk) + (long)p.hk * a.D + p.element();
+    const Pack8<TS> v = *reinterpret_cast<const Pack8<TS>*>(src);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = St<TS>::ld(&v.e[i]);
+  }
+  // magnitudes as integers: NaN above infinity above all numbers
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+  top = max(top, (uint32_t)__shfl_xor((int)top, 1));
+  top = max(top, (uint32_t)__shfl_xor((int)top, 2));
+  if (!in || p.row < 0) return;
+  // 7 / 8 of the next power of two and above carry into the exponent
+  const int e = min(max((int)((top + 0x200000u) >> 23) - 2, 0), 252);
+  const uint32_t byte = top >= 0x7f800000u ? 255u : (uint32_t)e;
+  const float scale = __uint_as_float((uint32_t)e << 23);
+  uint32_t c = 0;
+  if (byte != 255u) {
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[0], x[1], scale, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[2], x[3], scale, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[4], x[5], scale, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[6], x[7], scale, 3);
+  }
+  *reinterpret_cast<uint32_t*>((p.val ? a.vc : a.kc) + p.code(a, nb)) = c;
+  if (p.quarter == 0) (p.val ? a.vs : a.ks)[p.scale(a, nb)] = (uint8_t)byte;
+}
+
+template <typename TS> __global__ __launch_bounds__(NTH) void k_kv4_read(Kv4Args a, int nb) {
+  Place p;
+  if (!p.init(a, nb, blockIdx.x * (64 / nb)) || p.element() >= a.D) return;
+  float x[8];
+  const float nan = __uint_as_float(0x7fc00000u);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = nan;
+  if (p.row >= 0) {
+    const uint32_t c = *reinterpret_cast<const uint32_t*>((p.val ? a.vc : a.kc) + p.code(a, nb));
+    const float scale = __uint_as_float((uint32_t)(p.val ? a.vs : a.ks)[p.scale(a, nb)] << 23);
+    const auto put = [&](int i, auto two) {
+      x[i] = two[0];
+      x[i + 1] = two[1];
+    };
+    put(0, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 0));
+    put(2, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 1));
+    put(4, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 2));
+    put(6, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 3));
+  }
+  Pack8<TS> v;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) St<TS>::st(&v.e[i], x[i]);
+  TS* dst = (p.val ? (TS*)a.v + (long)p.t * a.ldv : (TS*)a.k + (long)p.t * a.ldk) + (long)p.hk * a.D + p.element();
+  *reinterpret_cast<Pack8<TS>*>(dst) = v;
+}
+
+dim3 grid_of(const Kv4Args& a, int nb) { return dim3((a.T + 64 / nb - 1) / (64 / nb), 2 * a.Hkv); }
+
+}  // namespace
+
+template <typename TS> hipError_t launch_kv4_write(const Kv4Args& a, hipStream_t s) {
+  const int nb = kv4_blocks(a.D);
+  k_kv4_write<TS><<<grid_of(a, nb), NTH, 0, s>>>(a, nb);
+  return hipGetLastError();
+}
+template <typename TS> hipError_t launch_kv4_read(const Kv4Args& a, hipStream_t s) {
+  const int nb = kv4_blocks(a.D);
+  k_kv4_read<TS><<<grid_of(a, nb), NTH, 0, s>>>(a, nb);
+  return hipGetLastError();
+}
+
+template hipError_t launch_kv4_write<bf16>(const Kv4Args&, hipStream_t);
+template hipError_t launch_kv4_write<float>(const Kv4Args&, hipStream_t);
+template hipError_t launch_kv4_read<bf16>(const Kv4Args&, hipStream_t);
+template hipError_t launch_kv4_read<float>(const Kv4Args&, hipStream_t);
+
+}  // namespace poetx

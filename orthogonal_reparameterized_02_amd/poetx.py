@@ -13,8 +13,8 @@ from typing import Optional
 
 import torch
 
-from ._lib import (AttnShape, BF16, DecodeShape, F32, I8, PoetxError, QkNormShape, RopeShape,  # noqa: F401
-                   Shape, Window, check, lib)
+from ._lib import (AttnShape, BF16, DecodeShape, F32, I8, Kv4Shape, PoetxError, QkNormShape,  # noqa: F401
+                   RopeShape, Shape, Window, check, lib)
 
 _DT = {F32: torch.float32, BF16: torch.bfloat16}
 
@@ -574,3 +574,100 @@ def poetx_attn_decode(sh: DecodeShape, q, k, v, length, o, ws, start=None, slope
         C.byref(sh), qp, kp, vp, _vec(start, "start", torch.int32, sh.B, optional=True),
         _vec(length, "length", torch.int32, sh.B),
         _vec(slopes, "slopes", torch.float32, sh.Hq, optional=True), op, wp, wb, _stream(stream)))
+
+
+def poetx_attn_window_decode_workspace_bytes(sh: DecodeShape, win: Window) -> int:
+    return lib().poetx_attn_window_decode_workspace_bytes(C.byref(sh), C.byref(win))
+
+
+def poetx_attn_window_decode(sh: DecodeShape, win: Window, q, k, v, length, o, ws, slopes=None, ring: bool = False,
+                             stream=None) -> None:
+    """One query row per sequence over the last `window` positions and the
+    sinks of a cache, or of a ring (length counts all tokens)."""
+    sh = DecodeShape.from_buffer_copy(sh)
+    dt = _DT[sh.act]
+    fq = (sh.B, sh.Hq, sh.D)
+    qp, sh.ldq = _rows(q, "q", fq, dt)
+    op, sh.ldo = _rows(o, "o", fq, dt)
+    kp, sh.ldk, sh.bsk = _cache(k, "k", sh)
+    vp, sh.ldv, sh.bsv = _cache(v, "v", sh)
+    wp, wb = _ws(ws, poetx_attn_window_decode_workspace_bytes(sh, win))
+    check("poetx_attn_window_decode", lib().poetx_attn_window_decode(
+        C.byref(sh), C.byref(win), int(ring), qp, kp, vp, _vec(length, "length", torch.int32, sh.B),
+        _vec(slopes, "slopes", torch.float32, sh.Hq, optional=True), op, wp, wb, _stream(stream)))
+
+
+# ---- a cache in 4 bits ------------------------------------------------------------
+
+
+def kv4_blocks(D: int) -> int:
+    """Blocks of 32 elements of a head: 16 bytes of codes and a scale each."""
+    return (D + 31) // 32
+
+
+def _cache4(kc, ks, vc, vs, D: int):
+    """Pointers, sequences, key heads and rows of a cache in 4 bits: codes
+    [B][Hkv][rows][blocks * 16], scales [B][Hkv][blocks][rows], both uint8."""
+    nb = kv4_blocks(D)
+    if kc.dim() != 4 or kc.shape[3] != nb * 16:
+        raise ValueError(f"kc has shape {tuple(kc.shape)}, expected [B][Hkv][rows][{nb * 16}]")
+    B, H, rows, _ = kc.shape
+    named = ((kc, "kc"), (ks, "ks"), (vc, "vc"), (vs, "vs"))
+    for t, name in named:
+        want = (B, H, rows, nb * 16) if name[1] == "c" else (B, H, nb, rows)
+        if tuple(t.shape) != want:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {want}")
+    return [_dev(t, name, torch.uint8) for t, name in named], B, H, rows
+
+
+def _kv4_call(k, v, seq, pos, cache, sinks: int, ring: bool):
+    ptrs, B, H, rows = _cache4(*cache, k.shape[2])
+    T, D = k.shape[0], k.shape[2]
+    kp, ldk = _rows(k, "k", (T, H, D), k.dtype)
+    vp, ldv = _rows(v, "v", (T, H, D), k.dtype)
+    sh = Kv4Shape(T, B, rows, H, D, act_of(k.dtype), sinks, int(ring), ldk, ldv)
+    return sh, kp, vp, _vec(seq, "seq", torch.int32, T, optional=True), _vec(pos, "pos", torch.int32, T), ptrs
+
+
+def poetx_kv4_write(k, v, seq, pos, kc, ks, vc, vs, sinks: int = 0, ring: bool = False, stream=None) -> None:
+    """Tokens k, v [T][Hkv][D] to positions pos [T] of sequences seq [T]
+    (None: token t to sequence t)."""
+    sh, kp, vp, sp, pp, ptrs = _kv4_call(k, v, seq, pos, (kc, ks, vc, vs), sinks, ring)
+    check("poetx_kv4_write", lib().poetx_kv4_write(C.byref(sh), kp, vp, sp, pp, *ptrs, _stream(stream)))
+
+
+def poetx_kv4_read(seq, pos, kc, ks, vc, vs, k, v, sinks: int = 0, ring: bool = False, stream=None) -> None:
+    """The values at positions pos [T] of sequences seq [T] into k, v [T][Hkv][D]."""
+    sh, kp, vp, sp, pp, ptrs = _kv4_call(k, v, seq, pos, (kc, ks, vc, vs), sinks, ring)
+    check("poetx_kv4_read", lib().poetx_kv4_read(C.byref(sh), sp, pp, *ptrs, kp, vp, _stream(stream)))
+
+
+def kv4_decode_shape(q, kc, scale: float = 0.0, cap: float = 0.0) -> DecodeShape:
+    """Shape of a decode call over a cache in 4 bits, codes kc
+    [B][Hkv][rows][blocks * 16]."""
+    B, Hq, D = q.shape
+    _, Hkv, rows, _ = kc.shape
+    wq, wk = Hq * D, Hkv * D
+    return DecodeShape(B, Hq, Hkv, D, act_of(q.dtype), rows, scale, cap, wq, wq, wk, wk, 0, 0)
+
+
+def poetx_attn_kv4_decode_workspace_bytes(sh: DecodeShape, win: Window) -> int:
+    return lib().poetx_attn_kv4_decode_workspace_bytes(C.byref(sh), C.byref(win))
+
+
+def poetx_attn_kv4_decode(sh: DecodeShape, win: Window, q, kc, ks, vc, vs, length, o, ws, start=None, slopes=None,
+                          ring: bool = False, stream=None) -> None:
+    """One query row per sequence over a cache in 4 bits."""
+    sh = DecodeShape.from_buffer_copy(sh)
+    dt = _DT[sh.act]
+    fq = (sh.B, sh.Hq, sh.D)
+    qp, sh.ldq = _rows(q, "q", fq, dt)
+    op, sh.ldo = _rows(o, "o", fq, dt)
+    ptrs, B, H, rows = _cache4(kc, ks, vc, vs, sh.D)
+    if (B, H, rows) != (sh.B, sh.Hkv, sh.rows):
+        raise ValueError(f"a cache of {B} sequences, {H} heads and {rows} rows, expected {sh.B}, {sh.Hkv}, {sh.rows}")
+    wp, wb = _ws(ws, poetx_attn_kv4_decode_workspace_bytes(sh, win))
+    check("poetx_attn_kv4_decode", lib().poetx_attn_kv4_decode(
+        C.byref(sh), C.byref(win), int(ring), qp, *ptrs, _vec(start, "start", torch.int32, sh.B, optional=True),
+        _vec(length, "length", torch.int32, sh.B), _vec(slopes, "slopes", torch.float32, sh.Hq, optional=True), op, wp, wb,
+        _stream(stream)))

@@ -142,3 +142,105 @@ def test_window_pointer_errors():
         args = [FAKE] * 3
         args[i] = None
         assert L.poetx_attn_window_plan(C.byref(sh), C.byref(w), *args, 1 << 40, None) == 1 and f"'{nm}'" in _err()
+
+
+# ---- decoding with a window, and a cache in 4 bits -----------------------------------------
+def decode_shape(**kw):
+    a = dict(B=2, Hq=8, Hkv=2, D=128, act=1, rows=64, scale=0.0, cap=0.0, ldq=1024, ldo=1024, ldk=256, ldv=256,
+             bsk=64 * 256, bsv=64 * 256)
+    a.update(kw)
+    return _lib.DecodeShape(**a)
+
+
+WDEC = ("q", "k", "v", "len", "slopes", "o", "ws")
+KDEC = ("q", "kc", "ks", "vc", "vs", "start", "len", "slopes", "o", "ws")
+
+
+def wdec(sh, w, ring=0, n=1 << 40, **kw):
+    a = {x: FAKE for x in WDEC} | kw
+    return _lib.lib().poetx_attn_window_decode(C.byref(sh), C.byref(w) if w else None, ring, *[a[x] for x in WDEC], n, None)
+
+
+def kdec(sh, w, ring=0, n=1 << 40, **kw):
+    a = {x: FAKE for x in KDEC} | (dict(start=None) if w and w.window else {}) | kw
+    return _lib.lib().poetx_attn_kv4_decode(C.byref(sh), C.byref(w) if w else None, ring, *[a[x] for x in KDEC], n, None)
+
+
+@pytest.mark.parametrize("kw", [dict(B=-1), dict(B=70000), dict(rows=-64), dict(Hq=9), dict(D=4), dict(D=136), dict(act=2),
+                                dict(cap=-2.0), dict(ldq=8), dict(ldo=1)])
+def test_decode_shape_errors(kw):
+    L, sh, w = _lib.lib(), decode_shape(**kw), _lib.Window(16, 4)
+    assert L.poetx_attn_window_decode_workspace_bytes(C.byref(sh), C.byref(w)) == 0
+    assert L.poetx_attn_kv4_decode_workspace_bytes(C.byref(sh), C.byref(w)) == 0
+    assert wdec(sh, w) == 1 and kdec(sh, w) == 1
+
+
+def test_decode_window_errors():
+    for call in (wdec, kdec):
+        for w in (_lib.Window(-1, 0), _lib.Window(8, 129), _lib.Window(8, -1)):
+            assert call(decode_shape(), w) == 1
+        assert call(decode_shape(), None) == 1 and "null window" in _err()
+        assert call(decode_shape(), _lib.Window(0, 4), ring=1) == 1 and "ring" in _err()
+        assert call(decode_shape(), _lib.Window(61, 4), ring=1) == 1 and "ring" in _err()
+        assert call(decode_shape(), _lib.Window(2 ** 31 - 1, 4), ring=1) == 1 and "ring" in _err()
+        assert call(decode_shape(B=0), _lib.Window(61, 4)) == 0
+    assert kdec(decode_shape(rows=96), _lib.Window(8, 0)) == 1 and "multiple of 64" in _err()
+    assert kdec(decode_shape(), _lib.Window(8, 0), start=FAKE) == 1 and "start" in _err()
+
+
+def test_decode_pointer_and_workspace_errors():
+    L, sh, w = _lib.lib(), decode_shape(), _lib.Window(16, 4)
+    for call, names, need in ((wdec, WDEC, L.poetx_attn_window_decode_workspace_bytes(C.byref(sh), C.byref(w))),
+                              (kdec, KDEC, L.poetx_attn_kv4_decode_workspace_bytes(C.byref(sh), C.byref(w)))):
+        assert need > 0 and call(sh, w, n=need - 1) == 3
+        for n in names:
+            assert call(sh, w, **{n: MISALIGNED}) == 1 and f"'{n}'" in _err()
+            if n not in ("slopes", "start"):
+                assert call(sh, w, **{n: None}) == 1 and f"'{n}'" in _err()
+
+
+def kv4_shape(**kw):
+    a = dict(T=3, B=2, rows=64, Hkv=2, D=64, act=1, sinks=0, ring=0, ldk=128, ldv=128)
+    a.update(kw)
+    return _lib.Kv4Shape(**a)
+
+
+def kv4(sh, read, **kw):
+    names = ("seq", "pos", "kc", "ks", "vc", "vs", "k", "v") if read else ("k", "v", "seq", "pos", "kc", "ks", "vc", "vs")
+    a = {x: FAKE for x in names} | kw
+    return getattr(_lib.lib(), "poetx_kv4_read" if read else "poetx_kv4_write")(C.byref(sh) if sh else None, *[a[x] for x in names], None)
+
+
+@pytest.mark.parametrize("read", [False, True])
+@pytest.mark.parametrize("kw,word", [
+    (dict(T=-1), "T="), (dict(B=-1), "B="), (dict(B=70000), "B="), (dict(rows=-64), "rows"), (dict(rows=100), "rows"), (dict(Hkv=0), "Hkv"),
+    (dict(D=12), "D="), (dict(D=136), "D="), (dict(act=2), "dtype"), (dict(sinks=-1), "sinks"), (dict(sinks=129), "sinks"),
+    (dict(sinks=64, ring=1), "ring"), (dict(ldk=64), "ldk"), (dict(ldv=129), "ldv"), (dict(T=1 << 30), "2^27")])
+def test_kv4_shape_errors(read, kw, word):
+    assert kv4(kv4_shape(**kw), read) == 1 and word in _err()
+
+
+@pytest.mark.parametrize("read", [False, True])
+def test_kv4_pointer_errors_and_nothing_to_do(read):
+    assert kv4(None, read) == 1
+    for n in ("k", "v", "seq", "pos", "kc", "ks", "vc", "vs"):
+        assert kv4(kv4_shape(), read, **{n: MISALIGNED}) == 1 and f"'{n}'" in _err()
+        if n != "seq":
+            assert kv4(kv4_shape(), read, **{n: None}) == 1 and f"'{n}'" in _err()
+    assert kv4(kv4_shape(T=0), read, k=None, kc=None) == 0
+    if not read:
+        assert kv4(kv4_shape(B=0), read, k=None) == 0 and kv4(kv4_shape(rows=0), read, k=None) == 0
+
+
+def test_kv4_binding_refusals():
+    t = lambda *s: torch.zeros(*s, dtype=torch.uint8)
+    q, k, n = torch.zeros(2, 4, 64), torch.zeros(3, 2, 64), torch.zeros(3, dtype=torch.int32)
+    good = (t(2, 2, 64, 32), t(2, 2, 2, 64), t(2, 2, 64, 32), t(2, 2, 2, 64))
+    for i, bad in ((0, t(2, 2, 64, 16)), (1, t(2, 2, 64, 2)), (2, t(2, 2, 128, 32)), (3, t(2, 2, 1, 64))):
+        cache = [bad if i == j else c for j, c in enumerate(good)]
+        with pytest.raises(ValueError, match="shape"):
+            P.poetx_kv4_write(k, k, None, n, *cache)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        P.poetx_kv4_write(k, k, None, n, *good)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        P.poetx_attn_kv4_decode(P.kv4_decode_shape(q, good[0]), P.window(0), q, *good, n, q, None)

@@ -1,0 +1,294 @@
+"""GPU parity of the cache in 4 bits, and of decoding with a window, sinks and
+rings over both kinds of cache, against the float64 oracle.
+
+Tolerances.  Held values are equal bit for bit: the scale and the nearest code
+have no rounding of their own.  Decoding: float32 1e-5 relative (2-norm), sums of
+float32 products; bf16: the output is rounded once, 2^-8 at most and 2^-8 /
+sqrt(3) in the 2-norm, and p in two bf16 parts adds 2^-16: bounded by 2^-8, the
+largest difference by 2e-2 of the largest value."""
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import bits, to_dev, to_f64
+from orthogonal_reparameterized_02_amd import poetx as P
+from oracle import long_context_oracle as L
+
+pytestmark = pytest.mark.gpu
+
+FRO = {"f32": 1e-5, "bf16": 2.0 ** -8}
+MAX = {"f32": 1e-4, "bf16": 2e-2}
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    P.lib()
+
+
+def normal(rng, shape, dt, scale=1.0):
+    return torch.from_numpy((rng.standard_normal(shape) * scale).astype(np.float32)).to(DT[dt]).cuda()
+
+
+def close(name, got, ref, dt):
+    got = to_f64(got)
+    np.testing.assert_array_equal(np.isnan(got), np.isnan(ref), err_msg=name)
+    g, r = got[~np.isnan(ref)], ref[~np.isnan(ref)]
+    if not np.abs(r).max(initial=0):
+        assert not np.abs(g).max(initial=0), name
+        return
+    fro, mx = np.linalg.norm(g - r) / np.linalg.norm(r), np.abs(g - r).max() / np.abs(r).max()
+    print(f"  {name}: fro={fro:.2e} max={mx:.2e}", file=sys.stderr, flush=True)
+    assert fro <= FRO[dt] and mx <= MAX[dt], (name, fro, mx)
+
+
+def cache4(B, rows, H, D, fill=0xFF):
+    nb = P.kv4_blocks(D)
+    e = lambda *s: torch.full(s, fill, dtype=torch.uint8, device="cuda")
+    return e(B, H, rows, nb * 16), e(B, H, nb, rows), e(B, H, rows, nb * 16), e(B, H, nb, rows)
+
+
+# ---- writing and reading ----------------------------------------------------------------
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("T,B,rows,H,D", [(1, 1, 64, 1, 8), (3, 3, 64, 2, 64), (70, 2, 128, 3, 128), (33, 1, 64, 1, 104),
+                                          (20, 4, 64, 8, 40), (100, 3, 192, 2, 72)])
+def test_written_values(dt, T, B, rows, H, D):
+    rng = np.random.default_rng(T + D)
+    # magnitudes over many powers of two, grid points and their middles, zeros of both signs
+    k = normal(rng, (T, H, D), "f32") * torch.from_numpy(2.0 ** rng.integers(-20, 20, (T, H, 1))).float().cuda()
+    v = torch.from_numpy((rng.integers(-28, 29, (T, H, D)) / 4.0).astype(np.float32)).cuda()
+    v[0, 0, :8] = torch.tensor([0.0, -0.0, 6.99, -7.0, 0.25, 0.75, 2.5, 5.0])
+    k, v = k.to(DT[dt]), v.to(DT[dt])
+    places = rng.choice(B * rows, T, replace=False)
+    seq, pos = to_dev((places // rows).astype(np.int32)), to_dev((places % rows).astype(np.int32))
+    cache = cache4(B, rows, H, D, 0xA5)
+    P.poetx_kv4_write(k, v, seq, pos, *cache)
+    for x, c, s in ((k, cache[0], cache[1]), (v, cache[2], cache[3])):
+        codes, scales = L.kv4_encode(to_f64(x))
+        c, s, at = c.cpu().numpy(), s.cpu().numpy(), (places // rows, slice(None), places % rows)
+        np.testing.assert_array_equal(c[places // rows, :, places % rows], codes)
+        np.testing.assert_array_equal(s[places // rows, :, :, places % rows], scales)
+        rest = np.ones((B, rows), bool)
+        rest[places // rows, places % rows] = False
+        assert (c.transpose(0, 2, 1, 3)[rest] == 0xA5).all() and (s.transpose(0, 3, 1, 2)[rest] == 0xA5).all()
+    ko, vo = torch.full_like(k, 7), torch.full_like(v, 7)
+    P.poetx_kv4_read(seq, pos, *cache, ko, vo)
+    for x, y in ((k, ko), (v, vo)):
+        want = L.kv4_decode(*L.kv4_encode(to_f64(x)), D)
+        np.testing.assert_array_equal(to_f64(y), want)
+        np.testing.assert_array_equal(np.signbit(to_f64(y)), np.signbit(want))
+    # what was read is held as it is
+    again = cache4(B, rows, H, D, 0xA5)
+    P.poetx_kv4_write(ko, vo, seq, pos, *again)
+    P.poetx_kv4_read(seq, pos, *again, k, v)
+    assert torch.equal(k, ko) and torch.equal(v, vo)
+
+
+def test_extremes():
+    x = torch.zeros(6, 1, 32, device="cuda")
+    x[0, 0, 0] = float("inf")
+    x[1, 0, 3] = float("nan")
+    x[2, 0, :3] = torch.tensor([3.4e38, -3.4e38, 1e37])
+    x[3, 0, :2] = torch.tensor([1e-38, 1e-45])
+    x[4, 0, 0] = 1.75 * 2.0 ** 127
+    cache = cache4(6, 64, 1, 32)
+    pos = torch.zeros(6, dtype=torch.int32, device="cuda")
+    P.poetx_kv4_write(x, x, None, pos, *cache)
+    y, z = torch.empty_like(x), torch.empty_like(x)
+    P.poetx_kv4_read(None, pos, *cache, y, z)
+    np.testing.assert_array_equal(to_f64(y), L.kv4_decode(*L.kv4_encode(to_f64(x)), 32))
+    assert torch.isnan(y[:2]).all() and torch.isfinite(y[2:]).all() and y[2, 0, 0] == 6 * 2.0 ** 125
+
+
+def test_places_that_the_cache_does_not_have():
+    rng = np.random.default_rng(1)
+    k, v = normal(rng, (6, 2, 64), "bf16"), normal(rng, (6, 2, 64), "bf16")
+    seq = torch.tensor([0, -1, 2, 1, 1, 1], dtype=torch.int32, device="cuda")
+    pos = torch.tensor([0, 5, 5, -1, 64, 63], dtype=torch.int32, device="cuda")
+    cache = cache4(2, 64, 2, 64, 0x11)
+    P.poetx_kv4_write(k, v, seq, pos, *cache)
+    assert (cache[0][0, :, 1:] == 0x11).all() and (cache[0][1, :, :63] == 0x11).all() and not (cache[1][1, :, :, 63] == 0x11).all()
+    ko, vo = torch.zeros_like(k), torch.zeros_like(v)
+    P.poetx_kv4_read(seq, pos, *cache, ko, vo)
+    bad = torch.tensor([False, True, True, True, True, False])
+    assert torch.isnan(ko[bad]).all() and torch.isnan(vo[bad]).all() and not torch.isnan(ko[~bad]).any()
+
+
+def test_ring_places_and_columns_of_a_projection():
+    rng = np.random.default_rng(2)
+    fused = normal(rng, (100, 6, 32), "bf16")
+    k, v = fused[:, 1:3], fused[:, 4:6]
+    cache, pos = cache4(1, 64, 2, 32), torch.arange(100, dtype=torch.int32, device="cuda")
+    seq = torch.zeros(100, dtype=torch.int32, device="cuda")
+    for at in (slice(0, 60), slice(60, 100)):  # a call's tokens have rows of their own
+        P.poetx_kv4_write(k[at], v[at], seq[at], pos[at].contiguous(), *cache, sinks=4, ring=True)
+    held = [0, 1, 2, 3, *range(40, 100)]
+    ko, vo = torch.zeros(64, 2, 32, dtype=torch.bfloat16, device="cuda"), torch.zeros(64, 2, 32, dtype=torch.bfloat16, device="cuda")
+    P.poetx_kv4_read(seq[:64], to_dev(np.array(held, np.int32)), *cache, ko, vo, sinks=4, ring=True)
+    np.testing.assert_array_equal(to_f64(ko), L.kv4_decode(*L.kv4_encode(to_f64(k[held])), 32))
+    np.testing.assert_array_equal(to_f64(vo), L.kv4_decode(*L.kv4_encode(to_f64(v[held])), 32))
+
+
+# ---- decoding ----------------------------------------------------------------------------
+CASES = [  # lengths, rows, Hq, Hkv, D, window, sinks, ring, cap, bias
+    dict(len=[1], rows=64, Hq=1, Hkv=1, D=64),
+    dict(len=[0, 64, 63, 5], rows=64, Hq=4, Hkv=2, D=128),
+    dict(len=[700, 1, 1000], rows=1024, Hq=8, Hkv=2, D=128, bias=True),
+    dict(len=[300, 129], rows=320, Hq=6, Hkv=2, D=104, cap=5.0),
+    dict(len=[300, 257], rows=320, Hq=20, Hkv=1, D=40, cap=200.0, bias=True),      # more heads than a tile has columns
+    dict(len=[77], rows=128, Hq=2, Hkv=2, D=8),
+    dict(len=[100, 3, 900], rows=960, Hq=4, Hkv=1, D=72, w=50, s=4),
+    dict(len=[100, 3, 900, 130], rows=960, Hq=4, Hkv=4, D=128, w=64, s=0, bias=True),
+    dict(len=[100, 900, 20], rows=960, Hq=4, Hkv=2, D=64, w=1, s=3),
+    dict(len=[100, 900, 500], rows=960, Hq=4, Hkv=2, D=64, w=300, s=100, cap=3.0),
+    # rings: not yet full, full to the row, gone round, far round
+    dict(len=[0, 1, 4, 5, 64, 65, 100, 129, 4000], rows=64, Hq=4, Hkv=2, D=64, w=60, s=4, ring=True, bias=True),
+    dict(len=[50, 128, 190, 333, 100000], rows=128, Hq=8, Hkv=2, D=128, w=100, s=2, ring=True),
+    dict(len=[700, 3000, 5000], rows=1024, Hq=8, Hkv=1, D=128, w=1000, s=17, ring=True, cap=20.0, bias=True),
+    dict(len=[7, 3000], rows=64, Hq=3, Hkv=1, D=32, w=5, s=0, ring=True),
+    dict(len=[2 ** 31 - 1, 2 ** 30], rows=192, Hq=2, Hkv=1, D=64, w=190, s=2, ring=True, host=False),
+    # cut into pieces and joined
+    dict(len=[6000, 2500, 300], rows=6016, Hq=4, Hkv=1, D=64),
+    dict(len=[9000, 4000, 300], rows=9024, Hq=2, Hkv=1, D=128, w=5000, s=4, bias=True),
+]
+
+
+def setup(c, dt, four):
+    rng = np.random.default_rng(len(c["len"]) + c["rows"] + c["D"])
+    B, rows, Hq, Hkv, D = len(c["len"]), c["rows"], c["Hq"], c["Hkv"], c["D"]
+    st = dict(c=c, q=normal(rng, (B, Hq, D), dt, 1.5), len=torch.tensor(c["len"], dtype=torch.int32, device="cuda"),
+              slopes=to_dev((2.0 ** -np.arange(1, Hq + 1)).astype(np.float32)) if c.get("bias") else None)
+    k, v = normal(rng, (B, rows, Hkv, D), dt), normal(rng, (B, rows, Hkv, D), dt)
+    if four:
+        st["cache"] = cache4(B, rows, Hkv, D)
+        seq = torch.arange(B, dtype=torch.int32, device="cuda").repeat_interleave(rows)
+        pos = torch.arange(rows, dtype=torch.int32, device="cuda").repeat(B)
+        P.poetx_kv4_write(k.flatten(0, 1), v.flatten(0, 1), seq, pos, *st["cache"])
+        P.poetx_kv4_read(seq, pos, *st["cache"], k.flatten(0, 1), v.flatten(0, 1))
+    st["k"], st["v"] = k, v
+    return st
+
+
+def run(st, four, ws=None, o=None, **kw):
+    c = st["c"]
+    w = P.window(c.get("w", 0), c.get("s", 0))
+    o = torch.full_like(st["q"], 7) if o is None else o
+    raw = lambda n: torch.full((n,), 255, dtype=torch.uint8, device="cuda")  # unwritten is NaN
+    if four:
+        sh = P.kv4_decode_shape(st["q"], st["cache"][0], cap=c.get("cap", 0.0))
+        ws = raw(P.poetx_attn_kv4_decode_workspace_bytes(sh, w)) if ws is None else ws
+        P.poetx_attn_kv4_decode(sh, w, st["q"], *st["cache"], st["len"], o, ws, slopes=st["slopes"], ring=c.get("ring", False), **kw)
+    else:
+        sh = P.decode_shape(st["q"], st["k"], st["v"], cap=c.get("cap", 0.0))
+        ws = raw(P.poetx_attn_window_decode_workspace_bytes(sh, w)) if ws is None else ws
+        P.poetx_attn_window_decode(sh, w, st["q"], st["k"], st["v"], st["len"], o, ws, slopes=st["slopes"], ring=c.get("ring", False), **kw)
+    return o
+
+
+def reference(st):
+    c = st["c"]
+    lens = c["len"]
+    if not c.get("host", True):  # the same rows at positions that a host array can hold
+        R = c["rows"] - c["s"]
+        lens = [c["s"] + (n - c["s"]) % R + 4 * R for n in lens]
+    return L.window_decode(to_f64(st["q"]), to_f64(st["k"]), to_f64(st["v"]), lens, c.get("w", 0), c.get("s", 0), c.get("ring", False),
+                           None, c.get("cap", 0.0), None if st["slopes"] is None else to_f64(st["slopes"]))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("i", range(len(CASES)))
+def test_decode(i, four, dt):
+    st = setup(CASES[i], dt, four)
+    close("o", run(st, four), reference(st), dt)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_window_that_hides_nothing_is_plain_decoding(dt):
+    st = setup(dict(len=[100, 600, 3], rows=640, Hq=4, Hkv=2, D=64, bias=True), dt, False)
+    sh = P.decode_shape(st["q"], st["k"], st["v"])
+    ws, o = torch.empty(P.poetx_attn_decode_workspace_bytes(sh), dtype=torch.uint8, device="cuda"), torch.empty_like(st["q"])
+    P.poetx_attn_decode(sh, st["q"], st["k"], st["v"], st["len"], o, ws, slopes=st["slopes"])
+    np.testing.assert_array_equal(bits(run(st, False)), bits(o))
+    st["c"] = dict(st["c"], w=640, s=3)
+    close("wide", run(st, False), to_f64(o), dt)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_start_over_a_cache_in_four_bits(dt):
+    st = setup(dict(len=[100, 300, 50, 10], rows=320, Hq=4, Hkv=2, D=64), dt, True)
+    start = [7, 299, 50, 60]
+    got = run(st, True, start=torch.tensor(start, dtype=torch.int32, device="cuda"))
+    from oracle import block_oracle as B
+    close("o", got, B.decode(to_f64(st["q"]), to_f64(st["k"]), to_f64(st["v"]), start, [100, 300, 50, 10]), dt)
+
+
+@pytest.mark.parametrize("four", [False, True])
+def test_rows_that_are_not_seen_have_no_influence(four):
+    c = dict(len=[200, 90, 30], rows=256, Hq=4, Hkv=2, D=64, w=40, s=3)
+    st = setup(c, "bf16", four)
+    want = run(st, four)
+    for b, n in enumerate(c["len"]):
+        hidden = [p for p in range(256) if p >= n or 3 <= p < n - 40]
+        if four:
+            for i in (1, 3):
+                st["cache"][i][b, :, :, hidden] = 255
+        else:
+            st["k"][b, hidden], st["v"][b, hidden] = float("nan"), float("inf")
+    np.testing.assert_array_equal(bits(run(st, four)), bits(want))
+    assert torch.isfinite(want).all()
+    if four:  # and a seen one that is NaN has
+        st["cache"][3][0, 1, 1, 190] = 255
+        got = to_f64(run(st, four))
+        assert np.isnan(got[0, 2:, 32:]).all() and np.isfinite(got[0, :2]).all() and np.isfinite(got[0, 2:, :32]).all() and np.isfinite(got[1:]).all()
+
+
+@pytest.mark.parametrize("four", [False, True])
+def test_same_bits_on_another_stream_and_in_a_graph(four):
+    c = dict(len=[900, 2000, 40], rows=1024, Hq=8, Hkv=2, D=128, w=900, s=4, ring=True, bias=True)
+    st = setup(c, "bf16", four)
+    want = bits(run(st, four))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = run(st, four)
+    np.testing.assert_array_equal(bits(got), want)
+    ws, o = torch.empty(1 << 24, dtype=torch.uint8, device="cuda"), torch.empty_like(st["q"])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run(st, four, ws, o)
+        st["len"].add_(1)
+    lens = c["len"]
+    for i in range(3):
+        o.fill_(float("nan"))
+        ws.fill_(255)
+        g.replay()
+        torch.cuda.synchronize()
+        st["c"] = dict(c, len=[n + i for n in lens])
+        close(f"replay {i}", o, reference(st), "bf16")
+
+
+def test_caches_of_more_than_two_to_the_32_bytes():
+    """The last sequence of a cache whose codes pass 32 bits."""
+    B, rows, H, D = 9, 2 ** 20, 8, 128
+    nb = P.kv4_blocks(D)
+    kc = torch.zeros(B, H, rows, nb * 16, dtype=torch.uint8, device="cuda")
+    ks = torch.full((B, H, nb, rows), 127, dtype=torch.uint8, device="cuda")
+    assert kc.numel() > 2 ** 32
+    rng = np.random.default_rng(4)
+    q, k, v = normal(rng, (B, H, D), "f32"), normal(rng, (200, H, D), "f32"), normal(rng, (200, H, D), "f32")
+    seq, pos = torch.full((200,), B - 1, dtype=torch.int32, device="cuda"), torch.arange(rows - 200, rows, dtype=torch.int32, device="cuda")
+    vc, vs = kc.clone(), ks.clone()
+    P.poetx_kv4_write(k, v, seq, pos, kc, ks, vc, vs)
+    P.poetx_kv4_read(seq, pos, kc, ks, vc, vs, k, v)
+    sh, w = P.kv4_decode_shape(q, kc), P.window(200)
+    ws, o = torch.empty(P.poetx_attn_kv4_decode_workspace_bytes(sh, w), dtype=torch.uint8, device="cuda"), torch.empty_like(q)
+    length = torch.tensor([0] * (B - 1) + [rows], dtype=torch.int32, device="cuda")
+    P.poetx_attn_kv4_decode(sh, w, q, kc, ks, vc, vs, length, o, ws)
+    ref = L.window_decode(to_f64(q[-1:]), to_f64(k)[None], to_f64(v)[None], [200], 0, 0)
+    close("o", o[-1:], ref, "f32")
+    assert not o[:-1].any()
