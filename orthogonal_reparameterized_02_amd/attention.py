@@ -1,10 +1,10 @@
 """An attention block around POET-X projections.
 
-`rope_table`, `apply_rope`, `dropout_add`, `AttentionPlan` / `attention` and
-`KVCache` / `attention_decode` are the library's attention-block operators
-(include/poetx.h) with autograd and their workspaces; `POETXAttention` puts
-them between four `POETXLinear` projections: packed documents for training,
-single tokens over a cache for serving.  PyTorch supplies device memory,
+`rope_table`, `apply_rope`, `qk_norm_rope`, `dropout_add`, `AttentionPlan` /
+`attention` and `KVCache`, `KVCache4` / `attention_decode` are the library's
+attention-block operators (include/poetx.h) with autograd and their workspaces;
+`POETXAttention` puts them between four `POETXLinear` projections: packed
+documents for training, single tokens over a cache for serving.  PyTorch supplies device memory,
 streams and autograd only.  The gradients have no gradients of their own:
 differentiating them raises.
 """
@@ -94,6 +94,41 @@ def apply_rope(q: torch.Tensor, k: Optional[torch.Tensor], pos: torch.Tensor, ta
     return out[0] if k is None else out
 
 
+class _QkNormRope(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, wq, wk, pos, table, eps, interleaved):
+        qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        ko = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        P.poetx_qk_norm_rope_fwd(q, k, wq, wk, pos, table, qo, ko, eps, interleaved)
+        ctx.save_for_backward(q, k, wq, wk, pos, table)
+        ctx.args = (eps, interleaved)
+        return (qo,) if k is None else (qo, ko)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, *grads):
+        q, k, wq, wk, pos, table = ctx.saved_tensors
+        eps, interleaved = ctx.args
+        new = lambda t, want=True: torch.empty(t.shape, dtype=t.dtype, device=t.device) if t is not None and want else None
+        dq, dk = new(q), new(k)
+        dwq, dwk = new(wq, ctx.needs_input_grad[2]), new(wk, ctx.needs_input_grad[3])
+        ws = _bytes(P.poetx_qk_norm_rope_workspace_bytes(P.qk_norm_shape(q, k, table, eps, interleaved)), q.device)
+        P.poetx_qk_norm_rope_bwd(grads[0].contiguous(), None if k is None else grads[1].contiguous(), q, k, wq, wk, pos, table,
+                                 dq, dk, dwq, dwk, ws, eps, interleaved)
+        return dq, dk, dwq, dwk, None, None, None, None
+
+
+def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], wq: Optional[torch.Tensor], wk: Optional[torch.Tensor],
+                 pos: Optional[torch.Tensor], table: Optional[torch.Tensor], eps: float = 1e-6, interleaved: bool = False):
+    """Root mean square norms of the heads of q [T][Hq][D] (and k [T][Hk][D])
+    times wq, wk [D] float32 (None: 1), then apply_rope (table None: norms
+    alone), in one pass; returns the pair, or q alone without k."""
+    if k is None and wk is not None:
+        raise ValueError("wk without k")
+    out = _QkNormRope.apply(q, k, wq, wk, pos, table, eps, interleaved)
+    return out[0] if k is None else out
+
+
 # ---- dropout ------------------------------------------------------------------------
 class _DropoutAdd(torch.autograd.Function):
     @staticmethod
@@ -129,22 +164,41 @@ def dropout_add(x: torch.Tensor, residual: Optional[torch.Tensor], p: float, see
 
 
 # ---- attention ------------------------------------------------------------------------
+def _window(window: int, sinks: int):
+    """A window and its sinks; sinks alone would have no meaning."""
+    if window < 0 or sinks < 0 or (sinks and not window):
+        raise ValueError(f"window={window} and sinks={sinks}: both at least 0, sinks with a window only")
+    return window, sinks
+
+
 class AttentionPlan:
     """The mask of one packed batch, shared by every layer, head and
     direction: document offsets cu_q (and cu_k where the keys have other
-    lengths) as int32 GPU tensors, prefix lengths, causal or not."""
+    lengths) as int32 GPU tensors, prefix lengths, causal or not; or, without
+    prefixes, a window: keys less than `window` away, and the first `sinks` of
+    the document from wherever they lie behind."""
 
     def __init__(self, cu_q: torch.Tensor, Tq: int, cu_k: Optional[torch.Tensor] = None,
-                 Tk: Optional[int] = None, prefix: Optional[torch.Tensor] = None, causal: bool = True):
+                 Tk: Optional[int] = None, prefix: Optional[torch.Tensor] = None, causal: bool = True,
+                 window: int = 0, sinks: int = 0):
         if (cu_k is None) != (Tk is None):
             raise ValueError("cu_k and Tk go together")
+        if window and prefix is not None:
+            raise ValueError("a window has no prefixes")
+        self.window, self.sinks = _window(window, sinks)
+        self.win = P.window(window, sinks) if window else None
         self.Tq, self.Tk = Tq, Tq if Tk is None else Tk
         self.ndoc, self.causal = cu_q.numel() - 1, causal
         if self.ndoc < 0 or (cu_k is not None and cu_k.numel() != cu_q.numel()):
             raise ValueError("cu_q and cu_k hold one offset more than there are documents")
         sh = self.shape(1, 1, 8, P.F32)
-        self.data = _bytes(P.poetx_attn_plan_bytes(sh), cu_q.device)
-        P.poetx_attn_plan(sh, cu_q, cu_q if cu_k is None else cu_k, self.data, prefix)
+        cu_k = cu_q if cu_k is None else cu_k
+        if self.win is None:
+            self.data = _bytes(P.poetx_attn_plan_bytes(sh), cu_q.device)
+            P.poetx_attn_plan(sh, cu_q, cu_k, self.data, prefix)
+        else:
+            self.data = _bytes(P.poetx_attn_window_plan_bytes(sh, self.win), cu_q.device)
+            P.poetx_attn_window_plan(sh, self.win, cu_q, cu_k, self.data)
 
     def shape(self, Hq: int, Hkv: int, D: int, act: int, scale: float = 0.0, cap: float = 0.0) -> P.AttnShape:
         wq, wk = Hq * D, Hkv * D
@@ -159,8 +213,12 @@ class _Attention(torch.autograd.Function):
         sh = plan.shape(Hq, Hkv, D, P.act_of(q.dtype), scale, cap)
         o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         lse = torch.empty(Hq, plan.Tq, dtype=torch.float32, device=q.device)
-        ws = _bytes(P.poetx_attn_workspace_bytes(sh, 0), q.device)
-        P.poetx_attn_fwd(sh, q, k, v, plan.data, o, lse, ws, slopes)
+        if plan.win is None:
+            ws = _bytes(P.poetx_attn_workspace_bytes(sh, 0), q.device)
+            P.poetx_attn_fwd(sh, q, k, v, plan.data, o, lse, ws, slopes)
+        else:
+            ws = _bytes(P.poetx_attn_window_workspace_bytes(sh, plan.win, 0), q.device)
+            P.poetx_attn_window_fwd(sh, plan.win, q, k, v, plan.data, o, lse, ws, slopes)
         ctx.save_for_backward(q, k, v, o, lse, slopes)
         ctx.plan, ctx.sh = plan, sh
         return o
@@ -170,8 +228,13 @@ class _Attention(torch.autograd.Function):
     def backward(ctx, dout):
         q, k, v, o, lse, slopes = ctx.saved_tensors
         dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
-        ws = _bytes(P.poetx_attn_workspace_bytes(ctx.sh, 1), q.device)
-        P.poetx_attn_bwd(ctx.sh, dout.contiguous(), q, k, v, o, lse, ctx.plan.data, dq, dk, dv, ws, slopes)
+        sh, plan, dout = ctx.sh, ctx.plan, dout.contiguous()
+        if plan.win is None:
+            ws = _bytes(P.poetx_attn_workspace_bytes(sh, 1), q.device)
+            P.poetx_attn_bwd(sh, dout, q, k, v, o, lse, plan.data, dq, dk, dv, ws, slopes)
+        else:
+            ws = _bytes(P.poetx_attn_window_workspace_bytes(sh, plan.win, 1), q.device)
+            P.poetx_attn_window_bwd(sh, plan.win, dout, q, k, v, o, lse, plan.data, dq, dk, dv, ws, slopes)
         return dq, dk, dv, None, None, None, None
 
 
@@ -197,24 +260,79 @@ class KVCache:
     """Keys and values of B sequences, up to `rows` tokens each.  An idle slot
     counts tokens like the others; fill it with none of them to empty it.
 
+    With a window the cache is a ring: it keeps the first `sinks` tokens of a
+    sequence and the rows - sinks (at least `window`) newest ones, and is never
+    full; its queries see the last `window` tokens and the sinks.
+
     append refuses a full cache from a count on the host.  A replayed graph
     appends without the host: there a sequence without room keeps its rows and
     its length, and from the first captured call on the count is read from the
     GPU."""
 
-    def __init__(self, B: int, rows: int, Hkv: int, D: int, dtype=torch.bfloat16, device="cuda"):
-        self.k = torch.empty(B, rows, Hkv, D, dtype=dtype, device=device)
-        self.v = torch.empty_like(self.k)
+    def __init__(self, B: int, rows: int, Hkv: int, D: int, dtype=torch.bfloat16, device="cuda", window: int = 0,
+                 sinks: int = 0):
+        self.B, self.rows, self.Hkv, self.D, self.dtype = B, rows, Hkv, D, dtype
+        self.window, self.sinks = _window(window, sinks)
+        self.ring = window > 0
+        if self.ring and rows < window + sinks:
+            raise ValueError(f"{rows} rows do not hold a window of {window} and {sinks} sinks")
+        self._storage(device)
         self.length = torch.zeros(B, dtype=torch.int32, device=device)
-        self.B, self.rows = B, rows
         # the same on the host, so that no token waits for the GPU: each length less the tokens appended
         # to all, and the largest of them.  None: replays may have changed it
         self._filled: Optional[list] = [0] * B
         self._most, self._appended = 0, 0
         self._at = torch.arange(B, device=device)
 
+    # -- where rows lie: what a cache of another form has of its own ------------------
+    def _storage(self, device) -> None:
+        self.k = torch.empty(self.B, self.rows, self.Hkv, self.D, dtype=self.dtype, device=device)
+        self.v = torch.empty_like(self.k)
+
+    def _row(self, pos: torch.Tensor) -> torch.Tensor:
+        """Rows of positions."""
+        pos = pos.long()
+        if not self.ring:
+            return pos
+        return torch.where(pos < self.sinks, pos, self.sinks + (pos - self.sinks) % (self.rows - self.sinks))
+
+    def _positions(self, spans) -> torch.Tensor:
+        """Ranges of positions as one int32 tensor."""
+        return torch.cat([torch.arange(a, b, dtype=torch.int32, device=self.length.device) for a, b in spans])
+
+    def _write(self, b: int, spans, k: torch.Tensor, v: torch.Tensor) -> None:
+        """k, v to the positions of spans, a list of ranges."""
+        rows = self._row(self._positions(spans)) if self.ring else slice(*spans[0])
+        self.k[b, rows], self.v[b, rows] = k, v
+
+    def _read(self, b: int, spans):
+        rows = self._row(self._positions(spans))
+        return self.k[b, rows], self.v[b, rows]
+
+    def _next(self, k: torch.Tensor, v: torch.Tensor) -> None:
+        """Every sequence's token at its length."""
+        at = self._row(self.length)
+        self.k[self._at, at], self.v[self._at, at] = k, v
+
+    def _next_where_room(self, k: torch.Tensor, v: torch.Tensor) -> None:
+        """The same for a graph: what a replay finds full is written back as it
+        was, so no replay writes outside the cache."""
+        at, full = self.length.clamp(0, self.rows - 1).long(), (self.length >= self.rows)[:, None, None]
+        for rows, new in ((self.k, k), (self.v, v)):
+            rows[self._at, at] = torch.where(full, rows[self._at, at], new)
+
+    def _decode(self, q, o, scale, cap, slopes, start, win) -> None:
+        sh = P.decode_shape(q, self.k, self.v, scale, cap)
+        if win is None:
+            ws = _bytes(P.poetx_attn_decode_workspace_bytes(sh), q.device)
+            P.poetx_attn_decode(sh, q, self.k, self.v, self.length, o, ws, start, slopes)
+        else:
+            ws = _bytes(P.poetx_attn_window_decode_workspace_bytes(sh, win), q.device)
+            P.poetx_attn_window_decode(sh, win, q, self.k, self.v, self.length, o, ws, slopes, self.ring)
+
+    # -- tokens ---------------------------------------------------------------------------
     def _captured(self) -> bool:
-        return self.k.is_cuda and torch.cuda.is_current_stream_capturing()
+        return self.length.is_cuda and torch.cuda.is_current_stream_capturing()
 
     def longest(self) -> Optional[int]:
         """Tokens of the longest sequence; None while a graph is captured."""
@@ -224,12 +342,39 @@ class KVCache:
             return max(self.length.tolist(), default=0)
         return self._most + self._appended
 
+    def tokens(self, b: int) -> int:
+        """Tokens of sequence b (also those that a ring no longer holds)."""
+        return int(self.length[b]) if self._filled is None else self._filled[b] + self._appended
+
+    def held(self, b: int):
+        """k, v [n][Hkv][D] of sequence b: every token in order, or of a ring
+        the sinks and the newest ones."""
+        return self._read(b, self._held(self.tokens(b)))
+
+    def _held(self, n: int, at: int = 0):
+        """The positions from `at` on that n tokens leave in the cache, as
+        ranges: all, or of a ring the sinks' and the newest."""
+        if not self.ring or n <= self.rows:
+            return [(at, n)]
+        return [(min(at, self.sinks), self.sinks), (max(at, n - (self.rows - self.sinks)), n)]
+
     def fill(self, b: int, k: torch.Tensor, v: torch.Tensor) -> None:
         """Sequence b becomes k, v [n][Hkv][D] (a prompt's)."""
-        n = k.shape[0]
-        if n > self.rows:
+        self._put(b, 0, k, v)
+
+    def extend(self, b: int, k: torch.Tensor, v: torch.Tensor) -> None:
+        """n tokens k, v [n][Hkv][D] more for sequence b (a prompt's later part)."""
+        self._put(b, self.tokens(b), k, v)
+
+    def _put(self, b: int, at: int, k: torch.Tensor, v: torch.Tensor) -> None:
+        n = at + k.shape[0]
+        if not self.ring and n > self.rows:
             raise ValueError(f"{n} tokens do not fit a cache of {self.rows} rows")
-        self.k[b, :n], self.v[b, :n] = k, v
+        if k.shape[0]:
+            spans = self._held(n, at)
+            if len(spans) > 1:  # a ring that these tokens go round
+                k, v = (torch.cat([t[x - at:y - at] for x, y in spans]) for t in (k, v))
+            self._write(b, spans, k, v)
         self.length[b] = n
         if self._captured():
             self._filled = None
@@ -240,34 +385,75 @@ class KVCache:
     def append(self, k: torch.Tensor, v: torch.Tensor) -> None:
         """One token more for every sequence: k, v [B][Hkv][D]."""
         n = self.longest()
-        if self.rows == 0 or (n is not None and n >= self.rows):
+        if self.rows == 0 or (not self.ring and n is not None and n >= self.rows):
             raise ValueError(f"the cache is full ({self.rows} rows)")
         if n is None:
-            self._append_where_room(k, v)
-            return
-        at = self.length.long()
-        self.k[self._at, at], self.v[self._at, at] = k, v
-        self.length += 1
-        self._appended += 1
+            self._filled = None
+        if n is not None or self.ring:
+            self._next(k, v)
+            self.length += 1
+            self._appended += n is not None
+        else:
+            self._next_where_room(k, v)
+            self.length.add_(1).clamp_(max=self.rows)
 
-    def _append_where_room(self, k: torch.Tensor, v: torch.Tensor) -> None:
-        """append for a graph: what a replay finds full is written back as it
-        was, so no replay writes outside the cache."""
-        self._filled = None
-        at, full = self.length.clamp(0, self.rows - 1).long(), (self.length >= self.rows)[:, None, None]
-        for rows, new in ((self.k, k), (self.v, v)):
-            rows[self._at, at] = torch.where(full, rows[self._at, at], new)
-        self.length.add_(1).clamp_(max=self.rows)
+
+class KVCache4(KVCache):
+    """The same in 4 bits: keys and values are held in blocks of 32 elements of
+    a head (include/poetx.h, poetx_kv4_write), 17 bytes a block.  rows is rounded
+    up to a multiple of 64.  On a GPU only."""
+
+    def __init__(self, B: int, rows: int, Hkv: int, D: int, dtype=torch.bfloat16, device="cuda", window: int = 0,
+                 sinks: int = 0):
+        super().__init__(B, (rows + 63) // 64 * 64, Hkv, D, dtype, device, window, sinks)
+
+    def _storage(self, device) -> None:
+        nb = P.kv4_blocks(self.D)
+        new = lambda *s: torch.empty(*s, dtype=torch.uint8, device=device)
+        self.kc, self.ks = new(self.B, self.Hkv, self.rows, nb * 16), new(self.B, self.Hkv, nb, self.rows)
+        self.vc, self.vs = torch.empty_like(self.kc), torch.empty_like(self.ks)
+
+    @property
+    def _cache(self):
+        return self.kc, self.ks, self.vc, self.vs
+
+    def _write(self, b, spans, k, v) -> None:
+        pos = self._positions(spans)
+        P.poetx_kv4_write(k, v, torch.full_like(pos, b), pos, *self._cache, sinks=self.sinks, ring=self.ring)
+
+    def _read(self, b, spans):
+        pos = self._positions(spans)
+        k = torch.empty(pos.numel(), self.Hkv, self.D, dtype=self.dtype, device=pos.device)
+        v = torch.empty_like(k)
+        P.poetx_kv4_read(torch.full_like(pos, b), pos, *self._cache, k, v, sinks=self.sinks, ring=self.ring)
+        return k, v
+
+    def _next(self, k, v) -> None:
+        P.poetx_kv4_write(k, v, None, self.length, *self._cache, sinks=self.sinks, ring=self.ring)
+
+    _next_where_room = _next  # a position past the last row writes nothing
+
+    def _decode(self, q, o, scale, cap, slopes, start, win) -> None:
+        sh, win = P.kv4_decode_shape(q, self.kc, scale, cap), win or P.window(0)
+        ws = _bytes(P.poetx_attn_kv4_decode_workspace_bytes(sh, win), q.device)
+        P.poetx_attn_kv4_decode(sh, win, q, *self._cache, self.length, o, ws, start, slopes, self.ring)
 
 
 def attention_decode(q: torch.Tensor, cache: KVCache, scale: float = 0.0, cap: float = 0.0,
-                     slopes: Optional[torch.Tensor] = None, start: Optional[torch.Tensor] = None) -> torch.Tensor:
+                     slopes: Optional[torch.Tensor] = None, start: Optional[torch.Tensor] = None, window: int = 0,
+                     sinks: int = 0) -> torch.Tensor:
     """One query per sequence, q [B][Hq][D], over the cache's rows
-    [start[b], length[b])."""
-    sh = P.decode_shape(q, cache.k, cache.v, scale, cap)
-    ws = _bytes(P.poetx_attn_decode_workspace_bytes(sh), q.device)
+    [start[b], length[b]); or over the last `window` tokens and the first
+    `sinks` (a ring's own, unless given)."""
+    window, sinks = _window(window, sinks)
+    if cache.ring:
+        if (window or sinks) and (window, sinks) != (cache.window, cache.sinks):
+            raise ValueError(f"a ring of window={cache.window} and sinks={cache.sinks}, called with {window} and {sinks}")
+        window, sinks = cache.window, cache.sinks
+    if window and start is not None:
+        raise ValueError("start with a window")
     o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    P.poetx_attn_decode(sh, q, cache.k, cache.v, cache.length, o, ws, start, slopes)
+    cache._decode(q, o, scale, cap, slopes, start, P.window(window, sinks) if window else None)
     return o
 
 
@@ -275,9 +461,12 @@ def attention_decode(q: torch.Tensor, cache: KVCache, scale: float = 0.0, cap: f
 class POETXAttention(torch.nn.Module):
     """x + dropout(Wo attention(rope(Wq x), rope(Wk x), Wv x)) with POET-X
     projections of block size b and Neumann order k.
+    qk_norm: the heads of Wq x and Wk x are normed before they turn, with
+    weights of their own (q_norm, k_norm).  window, sinks: a token sees the last
+    `window` ones and the first `sinks` of its document.
 
-    forward(x, plan, pos, at): x [T][n] packed tokens, plan their AttentionPlan,
-    pos [T] int32 positions (of each token in its document; one outside the
+    forward(x, plan, pos, at): x [T][n] packed tokens, plan their AttentionPlan
+    (self.plan makes one with the block's window), pos [T] int32 positions (of each token in its document; one outside the
     table gives NaN), at the place of the dropout mask (draw; by default the
     next one, which a recomputed pass could not find again).  prefill and
     decode serve: no dropout, no gradients, and no token past the table."""
@@ -285,8 +474,11 @@ class POETXAttention(torch.nn.Module):
     def __init__(self, n: int, heads: int, kv_heads: int, b: int, k: int, head_dim: Optional[int] = None,
                  positions: int = 8192, rot: Optional[int] = None, base: float = 10000.0, scaling=None,
                  interleaved: bool = False, cap: float = 0.0, bias: bool = False, dropout: float = 0.0,
-                 dtype=torch.bfloat16, seed: int = 0, device="cuda"):
+                 dtype=torch.bfloat16, seed: int = 0, device="cuda", qk_norm: bool = False, eps: float = 1e-6,
+                 window: int = 0, sinks: int = 0):
         super().__init__()
+        self.window, self.sinks = _window(window, sinks)
+        self.eps = eps
         self.n, self.Hq, self.Hkv = n, heads, kv_heads
         self.D = head_dim or n // heads
         self.cap, self.p, self.interleaved, self.dtype = cap, dropout, interleaved, dtype
@@ -295,6 +487,8 @@ class POETXAttention(torch.nn.Module):
         self.v, self.o = lin(n, kv_heads * self.D, 2), lin(heads * self.D, n, 3)
         self.register_buffer("table", rope_table(positions, rot or self.D, base, scaling, device=device))
         self.register_buffer("slopes", alibi_slopes(heads, device) if bias else None)
+        one = lambda: torch.nn.Parameter(torch.ones(self.D, device=device)) if qk_norm else None
+        self.q_norm, self.k_norm = one(), one()
         # place in the mask's sequence, on the GPU: a captured step moves on too
         self.seed = seed
         self.register_buffer("drawn", torch.zeros(1, dtype=torch.int64, device=device))
@@ -302,8 +496,23 @@ class POETXAttention(torch.nn.Module):
     def _heads(self, x, pos):
         T = x.shape[0]
         q, k = self.q(x).view(T, self.Hq, self.D), self.k(x).view(T, self.Hkv, self.D)
-        q, k = apply_rope(q, k, pos, self.table, self.interleaved)
+        if self.q_norm is None:
+            q, k = apply_rope(q, k, pos, self.table, self.interleaved)
+        else:
+            q, k = qk_norm_rope(q, k, self.q_norm, self.k_norm, pos, self.table, self.eps, self.interleaved)
         return q, k, self.v(x).view(T, self.Hkv, self.D)
+
+    def plan(self, cu_q: torch.Tensor, Tq: int, cu_k: Optional[torch.Tensor] = None, Tk: Optional[int] = None) -> AttentionPlan:
+        """The AttentionPlan of a packed batch under the block's window."""
+        return AttentionPlan(cu_q, Tq, cu_k, Tk, window=self.window, sinks=self.sinks)
+
+    def cache(self, B: int, rows: int, four_bits: bool = False) -> KVCache:
+        """A cache for B sequences of up to `rows` tokens, in the block's type
+        or held in 4 bits; a ring where the window and sinks are fewer."""
+        form, need = KVCache4 if four_bits else KVCache, self.window + self.sinks
+        if self.window and need < rows:
+            return form(B, need, self.Hkv, self.D, self.dtype, self.table.device, self.window, self.sinks)
+        return form(B, rows, self.Hkv, self.D, self.dtype, self.table.device)
 
     def _check_positions(self, n: int) -> None:
         if n > self.table.shape[0]:
@@ -320,6 +529,8 @@ class POETXAttention(torch.nn.Module):
 
     def forward(self, x: torch.Tensor, plan: AttentionPlan, pos: torch.Tensor,
                 at: Optional[torch.Tensor] = None) -> torch.Tensor:
+        if (plan.window, plan.sinks) != (self.window, self.sinks):
+            raise ValueError(f"a plan of window={plan.window} and sinks={plan.sinks} for a block of {self.window} and {self.sinks}")
         q, k, v = self._heads(x, pos)
         y = self.o(attention(q, k, v, plan, cap=self.cap, slopes=self.slopes).view(x.shape[0], -1))
         if not (self.training and self.p > 0):
@@ -333,29 +544,49 @@ class POETXAttention(torch.nn.Module):
         return dropout_add(y, x, self.p, self.seed, 0, at)
 
     @torch.no_grad()
-    def prefill(self, x: torch.Tensor, cache: KVCache, b: int = 0) -> torch.Tensor:
+    def prefill(self, x: torch.Tensor, cache: KVCache, b: int = 0, follow: bool = False) -> torch.Tensor:
         """A prompt x [n tokens][n] of sequence b from position 0; fills its
-        cache rows."""
-        T = x.shape[0]
-        self._check_positions(T)
-        pos = torch.arange(T, dtype=torch.int32, device=x.device)
+        cache rows.  follow: a later part of one, behind the tokens that the
+        cache has of the sequence, which it reads from there."""
+        T, at = x.shape[0], cache.tokens(b) if follow else 0
+        self._check_cache(cache)
+        self._check_positions(at + T)
+        pos = torch.arange(at, at + T, dtype=torch.int32, device=x.device)
         q, k, v = self._heads(x, pos)
-        cache.fill(b, k, v)
-        plan = AttentionPlan(torch.tensor([0, T], dtype=torch.int32, device=x.device), T)
+        cu = lambda n: torch.tensor([0, n], dtype=torch.int32, device=x.device)
+        if at == 0:
+            cache.fill(b, k, v)
+            plan = self.plan(cu(T), T)
+        else:
+            # a ring's newest rows stand right behind its sinks here: the mask is
+            # the same, for it counts from the ends, a bias is not
+            if self.slopes is not None and cache.ring and at > cache.rows:
+                raise ValueError("a later part of a prompt over a ring that has dropped tokens has no distances for a bias")
+            if not cache.ring and at + T > cache.rows:
+                raise ValueError(f"{at + T} tokens do not fit a cache of {cache.rows} rows")
+            before = cache.held(b)
+            cache.extend(b, k, v)
+            k, v = torch.cat([before[0], k]), torch.cat([before[1], v])
+            plan = self.plan(cu(T), T, cu(k.shape[0]), k.shape[0])
         return x + self.o(attention(q, k, v, plan, cap=self.cap, slopes=self.slopes).view(T, -1))
+
+    def _check_cache(self, cache: KVCache) -> None:
+        if cache.ring and (cache.window, cache.sinks) != (self.window, self.sinks):
+            raise ValueError(f"a ring of window={cache.window} and sinks={cache.sinks} for a block of {self.window} and {self.sinks}")
 
     @torch.no_grad()
     def decode(self, x: torch.Tensor, cache: KVCache) -> torch.Tensor:
         """The next token of every sequence, x [B][n].  In a captured graph a
         sequence without room for it, or without a position in the rotary
         table, answers NaN."""
+        self._check_cache(cache)
         n = cache.longest()
-        full = cache.length >= cache.rows if n is None else None
+        full = cache.length >= cache.rows if n is None and not cache.ring else None
         if n is not None:
             self._check_positions(n + 1)
         q, k, v = self._heads(x, cache.length)
         cache.append(k, v)
-        o = attention_decode(q, cache, cap=self.cap, slopes=self.slopes)
+        o = attention_decode(q, cache, cap=self.cap, slopes=self.slopes, window=self.window, sinks=self.sinks)
         if full is not None:
             o.masked_fill_(full[:, None, None], math.nan)
         return x + self.o(o.view(x.shape[0], -1))
