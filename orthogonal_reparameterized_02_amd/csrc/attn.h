@@ -98,7 +98,7 @@ struct AttnPlan {
   int4 *qraw, *kraw;               // the same before sorting
   // With sinks a query row sees keys [row_sink.x, row_sink.y) besides, which
   // end at or before row_lo.  Those of a tile lie in its range of qtab, or, of
-  // a document that began before the tile, in [qfar.x, qfar.y) below it.
+  // its first document, in [qfar.x, qfar.y) below it.
   int2* row_sink;                  // [Tq]
   int2* qfar;                      // [tiles]
   int* tile_doc;                   // [tiles] first document that ends after the tile's first row

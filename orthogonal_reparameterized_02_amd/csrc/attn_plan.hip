@@ -87,9 +87,9 @@ __global__ __launch_bounds__(NTH) void k_attn_plan(int Tq, int Tk, int ndoc, int
 // The same with a window and sinks (window >= 1).  A query at position p sees
 // [p - window + 1, p] (or to p + window - 1) and the first `sinks` keys of its
 // document; where the two touch they are one interval.
-//   Query tiles: the sinks of documents that begin inside a tile lie less than
-// a tile below their rows' windows, so the tile's range takes them in; only the
-// document that a tile continues has sinks far away, and its rows have the same.
+//   Query tiles: a tile's range runs from the first document's windows to the
+// last one's, so all sinks but those of its first document lie in it; the rows
+// of that document that see sinks apart from their window see the same.
 //   Keys: every key but a sink that is seen past the window has one interval of
 // queries; those sinks get none here.
 __global__ __launch_bounds__(NTH) void k_attn_window_plan(int Tq, int Tk, int ndoc, int causal, int window, int sinks,
@@ -134,8 +134,12 @@ __global__ __launch_bounds__(NTH) void k_attn_window_plan(int Tq, int Tk, int nd
         sink = make_int2(k0, s1);
       }
       if (hi <= lo) lo = hi = 0;
-      near = sink.x < sink.y && q0 >= t / ATTN_BM * ATTN_BM ? k0 : lo;
-      if (sink.x < sink.y && q0 < t / ATTN_BM * ATTN_BM) away = sink;
+      near = lo;
+      if (sink.x < sink.y) {
+        // the first document with rows in this tile
+        if (q0 <= max(t / ATTN_BM * ATTN_BM, min(max(cu_q[0], 0), Tq))) away = sink;
+        else near = k0;
+      }
     } else if (t >= first || !sinks_apart(q1 - q0, k1 - k0, causal, window)) {
       const long off = (long)q1 - k1;  // query row of position p: p + off
       lo = within(causal ? t + off : t - window + 1L + off, q0, q1);

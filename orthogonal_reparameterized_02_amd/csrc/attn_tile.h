@@ -433,7 +433,7 @@ __device__ __forceinline__ void part_of(int n, int parts, int part, int& begin, 
 }
 
 // The key tiles of one part of a query tile's loop: `far` tiles over the sinks
-// of the document that the tile continues, then those of the window.
+// of the tile's first document, then those of the window.
 struct KeyTiles {
   int flo, fhi, far, klo, khi;
   int nb, ne;  // this part's
