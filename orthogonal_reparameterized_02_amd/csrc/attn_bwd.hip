@@ -77,130 +77,10 @@ __device__ __forceinline__ float dot8(const float*, uint4 a, uint4 b) {
   return fmaf(__uint_as_float(a.w), __uint_as_float(b.w), s);
 }
 
-// What a tile's 128 queries (one head, q and dout in registers) give to dk and
-// dv of the sinks of each document among them whose sinks are seen past the
-// window: the products of the second pass on blocks of 32 sinks, the queries
-// and dout of a wave laid out in LDS for the transposed reads.  The waves' sums
-// join there and go to a.sink_part[tile + number][head][dk, dv][sink][D].
-template <typename T, int DP, int MODE>
-__device__ __forceinline__ void sink_grads(const AttnArgs& a, char* smem, const ScoreArgs& sa,
-                                           const uint4 (&qf)[Tile<T, DP>::KS], const uint4 (&dof)[Tile<T, DP>::KS],
-                                           float delta, float lse2, int q0, int h, int lane, int wave) {
-  using L = Tile<T, DP>;
-  constexpr int ROWS = 32 * L::RB;                     // bytes of a wave's rows
-  float* vals = reinterpret_cast<float*>(smem + 4 * DqCfg<T, DP>::TILE) + wave * 64;
-  float* sums = reinterpret_cast<float*>(smem);        // [NW][32][DP]
-  const int r0 = q0 + 32 * wave, hk = h / a.group, rows = min(a.Tq - q0, BM);
-  const T* kp = (const T*)a.k + (long)hk * a.D;
-  const T* vp = (const T*)a.v + (long)hk * a.D;
-  const uint32_t rlane = L::row_lane(lane) + wave * ROWS, clane = L::col_lane(lane) + wave * ROWS;
-  if (lane < 32) {
-    vals[lane] = lse2;
-    vals[32 + lane] = delta;
-  }
-  for (int d = max(a.pl.tile_doc[q0 / BM], 0); d < a.ndoc; ++d) {
-    const int4 e = a.pl.doc[d];
-    const int dq0 = __builtin_amdgcn_readfirstlane(e.x), dq1 = __builtin_amdgcn_readfirstlane(e.y);
-    const int dk0 = __builtin_amdgcn_readfirstlane(e.z), dk1 = __builtin_amdgcn_readfirstlane(e.w);
-    if (dq0 >= q0 + rows) break;
-    if (dq1 <= q0 || dq0 >= dq1 || !sinks_apart(dq1 - dq0, dk1 - dk0, a.causal, a.window)) continue;
-    const int ns = min(a.sinks, dk1 - dk0);
-    float* out = a.sink_part + ((q0 / BM + sink_number(dq0, dk0, a.window)) * a.Hq + h) * 2 * a.sinks * a.D;
-    for (int b = 0; b < ns; b += 32) {
-      // queries that see this lane's key
-      const int key = b + (lane & 31), t = dk0 + key, off = dq1 - dk1;
-      const int lo = key < ns ? max(a.causal ? t + off : dq0, dq0) : 0, hi = key < ns ? dq1 : 0;
-      uint4 kf[L::KS];
-      rows_to_regs<T>(kf, kp, a.ldk, dk0 + b, dk0 + ns, a.D, lane);
-      f32x16_t s = {}, p;
-#pragma unroll
-      for (int i = 0; i < L::KS; ++i) s = mma16((const T*)nullptr, qf[i], kf[i], s);
-      rows_to_regs<T>(kf, vp, a.ldv, dk0 + b, dk0 + ns, a.D, lane);
-      __syncthreads();  // the sums before, and the loop's tiles, have been read
-      f32x16_t dp;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) dp[i] = -vals[32 + 4 * (lane >> 5) + 8 * (i / 4) + i % 4];
-#pragma unroll
-      for (int i = 0; i < L::KS; ++i) dp = mma16((const T*)nullptr, dof[i], kf[i], dp);
-      const int il = r0 + 4 * (lane >> 5);
-      bool any = false;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int row = il + 8 * (i / 4) + i % 4;
-        const float l2 = vals[4 * (lane >> 5) + 8 * (i / 4) + i % 4];
-        float deriv;
-        if constexpr (MODE == 0) p[i] = exp2_hw(fmaf(s[i], sa.c, -l2));
-        else p[i] = exp2_hw(score2<T, MODE>(s[i], sa, (float)(row - off - t), deriv) - l2);
-        s[i] = p[i] * dp[i];
-        if constexpr (MODE & 1) s[i] *= deriv;
-        const bool seen = row >= lo && row < hi;
-        p[i] = seen ? p[i] : 0.0f;
-        s[i] = seen ? s[i] : 0.0f;
-      }
-#pragma unroll
-      for (int which = 0; which < 2; ++which) {  // dv, then dk
-#pragma unroll
-        for (int i = 0; i < L::KS; ++i)
-          *reinterpret_cast<uint4*>(smem + (rlane ^ (uint32_t)(i << 5))) = which ? qf[i] : dof[i];
-        f32x16_t acc[L::NT];
-#pragma unroll
-        for (int i = 0; i < L::NT; ++i) acc[i] = (f32x16_t){};
-        __builtin_amdgcn_wave_barrier();
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-#pragma unroll
-        for (int u = 0; u < L::CSTEP; ++u) {
-          const uint4 f = L::score_frag(which ? s : p, u);
-#pragma unroll
-          for (int ct = 0; ct < L::NT; ++ct)
-            acc[ct] = mma16((const T*)nullptr, L::col_frag(smem, clane, 0, u, ct), f, acc[ct]);
-        }
-        // rows of other documents enter as 0 times their value; where that left
-        // what is not finite, the sums are formed again from what is seen
-        const bool again = __any(finite_probe<L::NT>(acc) != 0.0f);
-        __syncthreads();
-        float* mine = sums + wave * 32 * DP;
-        if (again) {
-          for (int j = 0; j < min(ns - b, 32); ++j) {
-            const int tj = dk0 + b + j;
-            float2 xk = make_float2(0.0f, 0.0f), xv = xk;
-            attn_row_dkv<T, true>(a, h, tj, max(max(a.causal ? tj + off : dq0, dq0), r0), min(min(dq1, r0 + 32), q0 + rows), lane, xk, xv);
-            if (2 * lane < DP) *reinterpret_cast<float2*>(mine + j * DP + 2 * lane) = which ? xk : xv;
-          }
-        } else if (key < ns) {
-          const float factor = which ? cap_factor<T, MODE> : 1.0f;
-#pragma unroll
-          for (int ct = 0; ct < L::NT; ++ct)
-#pragma unroll
-            for (int g = 0; g < 4; ++g)
-              *reinterpret_cast<float4*>(mine + (lane & 31) * DP + 32 * ct + 8 * g + 4 * (lane >> 5)) =
-                  make_float4(acc[ct][4 * g] * factor, acc[ct][4 * g + 1] * factor, acc[ct][4 * g + 2] * factor, acc[ct][4 * g + 3] * factor);
-        }
-        __syncthreads();
-        float* to = out + ((which ? 0 : a.sinks) + b) * a.D;
-        for (int x = threadIdx.x; x < min(ns - b, 32) * (DP / 2); x += 64 * NW) {
-          const int j = x / (DP / 2), c = x % (DP / 2) * 2;
-          float2 y = make_float2(0.0f, 0.0f);
-#pragma unroll
-          for (int w = 0; w < NW; ++w) {
-            const float2 z = *reinterpret_cast<const float2*>(sums + (w * 32 + j) * DP + c);
-            y.x += z.x, y.y += z.y;
-          }
-          if (c < a.D) *reinterpret_cast<float2*>(to + (long)j * a.D + c) = y;
-        }
-        __syncthreads();
-      }
-    }
-  }
-}
-
 // dq, and for the second pass delta = dout . o and lse2 = lse log2e of every
 // query (lse2 = +inf where lse = -inf: such a query's p is 0)
 //
-// SINK: rows see the first keys of their document besides an interval.  The
-// workgroup then also forms what its queries give to dk and dv of such keys
-// (sink_grads): it has q, dout, lse and delta at hand, and a key that every
-// later query sees would leave one workgroup of the second pass with a loop
-// over the whole document.
+// SINK: rows see the first keys of their document besides an interval.
 template <typename T, int DP, int MODE, bool SINK>
 __global__ __launch_bounds__(64 * NW, (DqCfg<T, DP>::OCC)) void k_attn_dq(AttnArgs a, int parts) {
   using L = Tile<T, DP>;
@@ -370,18 +250,224 @@ __global__ __launch_bounds__(64 * NW, (DqCfg<T, DP>::OCC)) void k_attn_dq(AttnAr
       if (parts > 1) st2(pq + tr * ldp, lane, a.D, g);
       else st2((T*)a.dq + (long)tr * a.lddq + (long)h * a.D, lane, a.D, make_float2(g.x * a.scale, g.y * a.scale));
     }
-    if constexpr (!SINK) return;
-  } else {
-    const long tt = in ? t : 0;
-    if (parts > 1) store_rowsT<L::NT>(pq + tt * ldp, dq, FACTOR, a.D, in, lane);
-    else store_rowsT<L::NT>((T*)a.dq + tt * a.lddq + (long)h * a.D, dq, a.scale * FACTOR, a.D, in, lane);
+    return;
   }
-  if constexpr (SINK)
-    if (part == 0) sink_grads<T, DP, MODE>(a, smem, sa, qf, dof, delta, in ? lse2 : INFINITY, q0, h, lane, wave);
+  const long tt = in ? t : 0;
+  if (parts > 1) store_rowsT<L::NT>(pq + tt * ldp, dq, FACTOR, a.D, in, lane);
+  else store_rowsT<L::NT>((T*)a.dq + tt * a.lddq + (long)h * a.D, dq, a.scale * FACTOR, a.D, in, lane);
 }
 
-// dk and dv of the sinks: what sink_grads left, over the tiles of a document and
-// the query heads of a group.  A workgroup a sink and key head; sixteen waves
+// dk and dv of the sinks that are seen past the window.  Such a key is seen by
+// every later query, and would leave one workgroup of the second pass with a
+// loop over the whole document; here a workgroup takes 128 queries and all query
+// heads of one key head, a wave 32 of the queries, with blocks of 16 sinks of
+// each document among them.  The sums, without those of other tiles, go to
+// a.sink_part[tile + number][key head][dk, dv][sink][D].
+//
+// Bound by reading q and dout once more, from the last-level cache where they
+// fit.  Measured (8192 tokens in 3 documents, window 1024, 4 sinks, 32 heads on
+// 8, D 128, bf16): SINKUS us; as a part of k_attn_dq, whose registers it fills,
+// 52 us.
+// On 16 x 16 tiles: of 32 columns four sinks leave 28 idle, and the sums would
+// take 128 registers (57 spilled, 50 us).
+template <typename T, int DP> struct SinkCfg {
+  using L = Tile<T, DP>;
+  static constexpr int NS = 16;                      // sinks a block
+  static constexpr int KS = L::RB / 64;              // row fragments: 64 bytes of a row over four lanes
+  static constexpr int NT = DP / 16;                 // column tiles
+  static constexpr int ROWS = 32 * L::RB;            // bytes of a wave's rows of q, of dout
+  static constexpr int VAL = NW * 2 * ROWS;          // lse2 and delta of a wave's rows begin here
+  static constexpr int LDS = VAL + NW * 256;
+  static constexpr int OCC = sizeof(T) == 4 && DP == 128 ? 1 : 2;
+  static_assert(VAL >= 2 * NW * NS * DP * 4, "room for the waves' sums");
+
+  static __device__ __forceinline__ f32x4_t mma(uint4 x, uint4 y, f32x4_t c) {
+    if constexpr (sizeof(T) == 2) return __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(x), as_bf16x8(y), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(x.x), __uint_as_float(y.x), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(x.y), __uint_as_float(y.y), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(x.z), __uint_as_float(y.z), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(x.w), __uint_as_float(y.w), c, 0, 0, 0);
+  }
+  // rows of a Tile as operands: lane l holds row l % 16, chunk 4 ks + l / 16
+  static __device__ __forceinline__ uint32_t row_lane(int lane) {
+    const int r = lane & 15;
+    return r * L::RB + (((lane >> 4) ^ L::key(r)) << 4);
+  }
+  static __device__ __forceinline__ uint4 row_frag(const char* lds, uint32_t at, int m, int ks) {
+    return *reinterpret_cast<const uint4*>(lds + ((at ^ (uint32_t)(ks << 6)) + 16 * m * L::RB));
+  }
+  // columns 16 ct + 0..15 as rows of the operand, K in the order that the
+  // accumulators of 32 score rows have in a lane: 16 m + 4 (l / 16) + i
+  static __device__ __forceinline__ uint32_t col_lane(int lane) {
+    if constexpr (sizeof(T) == 2) {
+      const int r = 4 * (lane >> 4) + ((lane & 15) >> 2);
+      return r * L::RB + ((((lane & 3) >> 1) ^ L::key(r)) << 4) + (lane & 1) * 8;
+    } else {
+      const int r = 4 * (lane >> 4);
+      return r * L::RB + ((((lane & 15) >> 2) ^ L::key(r)) << 4) + (lane & 3) * 4;
+    }
+  }
+  // acc += columns^T x, x the scores' accumulators
+  static __device__ __forceinline__ f32x4_t mma_cols(const char* lds, uint32_t at, int ct, const f32x4_t (&x)[2], uint4 frag, f32x4_t acc) {
+    if constexpr (sizeof(T) == 2) {
+      char* p = const_cast<char*>(lds) + (at ^ (uint32_t)(ct << 5));
+      const s16x4_t h0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)p);
+      const s16x4_t h1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(p + 16 * L::RB));
+      return mma(__builtin_bit_cast(uint4, __builtin_shufflevector(h0, h1, 0, 1, 2, 3, 4, 5, 6, 7)), frag, acc);
+    } else {
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)  // i enters the key of row 4 (l / 16) + i as it stands
+          acc = __builtin_amdgcn_mfma_f32_16x16x4f32(
+              *reinterpret_cast<const float*>(lds + ((at ^ (uint32_t)(ct << 6 | i << 4)) + (16 * m + i) * L::RB)), x[m][i], acc, 0, 0, 0);
+      return acc;
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const f32x4_t (&x)[2]) {
+    return make_uint4(pack2bf(x[0][0], x[0][1]), pack2bf(x[0][2], x[0][3]), pack2bf(x[1][0], x[1][1]), pack2bf(x[1][2], x[1][3]));
+  }
+};
+template <typename T, int DP, int MODE>
+__global__ __launch_bounds__(64 * NW, (SinkCfg<T, DP>::OCC)) void k_attn_sink(AttnArgs a) {
+  using C = SinkCfg<T, DP>;
+  constexpr int NS = C::NS;
+  extern __shared__ __align__(16) char smem[];
+  const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), g = lane >> 4;
+  const int hk = blockIdx.x % a.Hkv, tile = blockIdx.x / a.Hkv, q0 = tile * BM, rows = min(a.Tq - q0, BM);
+  const int r0 = q0 + 32 * wave, rend = min(r0 + 32, a.Tq);
+  const T* kp = (const T*)a.k + (long)hk * a.D;
+  const T* vp = (const T*)a.v + (long)hk * a.D;
+  Loader<T, DP, 32, 1> lq, ld;
+  lq.init(a.ldq, a.D, 0, lane);
+  ld.init(a.lddo, a.D, 0, lane);
+  const uint32_t at = wave * 2 * C::ROWS;
+  const uint32_t ldsq = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem + at;
+  float* vals = reinterpret_cast<float*>(smem + C::VAL + wave * 256);
+  float* sums = reinterpret_cast<float*>(smem);  // [dk, dv][NW][NS][DP]
+  for (int d = max(a.pl.tile_doc[tile], 0); d < a.ndoc; ++d) {
+    const int4 e = a.pl.doc[d];
+    const int dq0 = __builtin_amdgcn_readfirstlane(e.x), dq1 = __builtin_amdgcn_readfirstlane(e.y);
+    const int dk0 = __builtin_amdgcn_readfirstlane(e.z), dk1 = __builtin_amdgcn_readfirstlane(e.w);
+    if (dq0 >= q0 + rows) break;
+    if (dq1 <= q0 || dq0 >= dq1 || !sinks_apart(dq1 - dq0, dk1 - dk0, a.causal, a.window)) continue;
+    const int ns = min(a.sinks, dk1 - dk0), off = dq1 - dk1;
+    float* out = a.sink_part + ((tile + sink_number(dq0, dk0, a.window)) * a.Hkv + hk) * 2 * a.sinks * a.D;
+    for (int b = 0; b < ns; b += NS) {
+      // queries that see this lane's key
+      const int key = b + (lane & 15), t = dk0 + key;
+      const int lo = key < ns ? max(a.causal ? t + off : dq0, dq0) : 0, hi = key < ns ? dq1 : 0;
+      uint4 kf[C::KS], vf[C::KS];
+      {
+        const int r = dk0 + min(key, ns - 1);
+        const T *pk = kp + (long)r * a.ldk, *pv = vp + (long)r * a.ldv;
+#pragma unroll
+        for (int i = 0; i < C::KS; ++i) {
+          const int el = (64 * i + 16 * g) / (int)sizeof(T);
+          kf[i] = *reinterpret_cast<const uint4*>(pk + (el < a.D ? el : 0));
+          vf[i] = *reinterpret_cast<const uint4*>(pv + (el < a.D ? el : 0));
+          if (el >= a.D) kf[i] = vf[i] = make_uint4(0, 0, 0, 0);
+        }
+      }
+      f32x4_t dk[C::NT], dv[C::NT];
+#pragma unroll
+      for (int i = 0; i < C::NT; ++i) dk[i] = dv[i] = (f32x4_t){};
+      // rows past the last one are zeros, and seen by none
+      if (rend > r0 && r0 < dq1 && rend > dq0)
+        for (int h = hk * a.group; h < (hk + 1) * a.group; ++h) {
+          lq.load((const T*)a.q + (long)h * a.D, a.ldq, r0, rend, ldsq);
+          ld.load((const T*)a.dout + (long)h * a.D, a.lddo, r0, rend, ldsq + C::ROWS);
+          const long row = (long)h * a.Tq + min(r0 + (lane & 31), a.Tq - 1);
+          const float own = lane < 32 ? a.lse2[row] : a.delta[row];
+          wait_loads();
+          vals[lane] = own;
+          const ScoreArgs sa = score_args<T, MODE>(a, h);
+          // a new value to the compiler: kept over the loop, the addresses of
+          // the fragments would fill registers
+          uint32_t rl = C::row_lane(lane), cl = C::col_lane(lane);
+          asm volatile("" : "+v"(rl), "+v"(cl));
+          const uint32_t qr = rl + at, dr = qr + C::ROWS, qc = cl + at, dc = qc + C::ROWS;
+          f32x4_t s[2], dp[2], p[2];
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            s[m] = (f32x4_t){};
+            dp[m] = -*reinterpret_cast<const f32x4_t*>(vals + 32 + 16 * m + 4 * g);
+#pragma unroll
+            for (int i = 0; i < C::KS; ++i) {
+              s[m] = C::mma(C::row_frag(smem, qr, m, i), kf[i], s[m]);
+              dp[m] = C::mma(C::row_frag(smem, dr, m, i), vf[i], dp[m]);
+            }
+          }
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            const f32x4_t l2 = *reinterpret_cast<const f32x4_t*>(vals + 16 * m + 4 * g);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int qrow = r0 + 16 * m + 4 * g + i;
+              float deriv;
+              if constexpr (MODE == 0) p[m][i] = exp2_hw(fmaf(s[m][i], sa.c, -l2[i]));
+              else p[m][i] = exp2_hw(score2<T, MODE>(s[m][i], sa, (float)(qrow - off - t), deriv) - l2[i]);
+              s[m][i] = p[m][i] * dp[m][i];
+              if constexpr (MODE & 1) s[m][i] *= deriv;
+              const bool seen = qrow >= lo && qrow < hi;
+              p[m][i] = seen ? p[m][i] : 0.0f;
+              s[m][i] = seen ? s[m][i] : 0.0f;
+            }
+          }
+          const uint4 fp = C::pack(p), fs = C::pack(s);
+#pragma unroll
+          for (int ct = 0; ct < C::NT; ++ct) {
+            dv[ct] = C::mma_cols(smem, dc, ct, p, fp, dv[ct]);
+            dk[ct] = C::mma_cols(smem, qc, ct, s, fs, dk[ct]);
+          }
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the next rows may land
+        }
+      // rows of other documents enter as 0 times their value; where that left
+      // what is not finite, the sums are formed again from what is seen
+      float probe = 0.0f;
+#pragma unroll
+      for (int ct = 0; ct < C::NT; ++ct)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) probe = fmaf(dk[ct][i], 0.0f, fmaf(dv[ct][i], 0.0f, probe));
+      const int n = min(ns - b, NS);
+      __syncthreads();  // the rows, or the sums before, have been read
+      if (__any(probe != 0.0f)) {
+        for (int j = 0; j < n; ++j) {
+          const int tj = dk0 + b + j;
+          float2 xk = make_float2(0.0f, 0.0f), xv = xk;
+          for (int h = hk * a.group; h < (hk + 1) * a.group; ++h)
+            attn_row_dkv<T>(a, h, tj, max(max(a.causal ? tj + off : dq0, dq0), r0), min(dq1, rend), lane, xk, xv);
+          if (2 * lane < DP) {
+            *reinterpret_cast<float2*>(sums + (wave * NS + j) * DP + 2 * lane) = xk;
+            *reinterpret_cast<float2*>(sums + ((NW + wave) * NS + j) * DP + 2 * lane) = xv;
+          }
+        }
+      } else if (key < ns) {
+        float* mine = sums + (wave * NS + (lane & 15)) * DP + 4 * g;
+#pragma unroll
+        for (int ct = 0; ct < C::NT; ++ct) {
+          *reinterpret_cast<f32x4_t*>(mine + 16 * ct) = dk[ct] * cap_factor<T, MODE>;
+          *reinterpret_cast<f32x4_t*>(mine + NW * NS * DP + 16 * ct) = dv[ct];
+        }
+      }
+      __syncthreads();
+      for (int x = threadIdx.x; x < 2 * n * (DP / 2); x += 64 * NW) {
+        const int which = x / (n * (DP / 2)), y = x - which * (n * (DP / 2)), j = y / (DP / 2), c = y % (DP / 2) * 2;
+        float2 z = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          const float2 v = *reinterpret_cast<const float2*>(sums + ((which * NW + w) * NS + j) * DP + c);
+          z.x += v.x, z.y += v.y;
+        }
+        if (c < a.D) *reinterpret_cast<float2*>(out + (long)(which * a.sinks + b + j) * a.D + c) = z;
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// dk and dv of the sinks: what k_attn_sink left, over the tiles of a document.  A
+// workgroup a sink and key head; sixteen waves
 // take every sixteenth partial sum and join in wave order.  The second pass has
 // left zeros in these rows.
 constexpr int SW = 16;
@@ -396,8 +482,8 @@ template <typename T> __global__ __launch_bounds__(64 * SW) void k_attn_sink_joi
   float2 x[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
   if (2 * lane < a.D) {
 #pragma unroll 4
-    for (int n = wave; n < tiles * a.group; n += SW) {
-      const float* p = a.sink_part + (((slot + n / a.group) * a.Hq + hk * a.group + n % a.group) * 2) * plane + (long)s * a.D + 2 * lane;
+    for (int n = wave; n < tiles; n += SW) {
+      const float* p = a.sink_part + (((slot + n) * a.Hkv + hk) * 2) * plane + (long)s * a.D + 2 * lane;
       const float2 u = *reinterpret_cast<const float2*>(p), v = *reinterpret_cast<const float2*>(p + plane);
       x[0].x += u.x, x[0].y += u.y, x[1].x += v.x, x[1].y += v.y;
     }
@@ -696,7 +782,7 @@ template <typename T, int DP, int MODE, int NQ> hipError_t dkv(const AttnArgs& a
 }
 
 template <typename T, int DP, int MODE, bool SINK> hipError_t bwd(const AttnArgs& a, hipStream_t s) {
-  constexpr int lds = DqCfg<T, DP>::LDS + (SINK ? NW * 64 * 4 : 0);
+  constexpr int lds = DqCfg<T, DP>::LDS;
   hipError_t e = lds_opt_in((const void*)k_attn_dq<T, DP, MODE, SINK>, lds);
   if (e != hipSuccess) return e;
   const int pq = dq_parts<T>(a), pk = dkv_parts<T>(a);
@@ -720,6 +806,13 @@ template <typename T, int DP, int MODE, bool SINK> hipError_t bwd(const AttnArgs
       const long n = (long)a.Tk * wk;
       const JoinArgs j = {{a.part, a.part + n}, {a.dk, a.dv}, {a.lddk, a.lddv}, {a.scale, 1.0f}};
       k_attn_sum_parts<T><<<dim3(blocks(n), 2), 256, 0, s>>>(j, pk, 2 * n, a.Tk, wk);
+      e = hipGetLastError();
+    }
+    if (SINK && e == hipSuccess && a.ndoc && a.Tq) {
+      constexpr int lds_s = SinkCfg<T, DP>::LDS;
+      e = lds_opt_in((const void*)k_attn_sink<T, DP, MODE>, lds_s);
+      if (e != hipSuccess) return e;
+      k_attn_sink<T, DP, MODE><<<dim3((unsigned)attn_tiles(a.Tq) * a.Hkv), 64 * NW, lds_s, s>>>(a);
       e = hipGetLastError();
     }
     if (SINK && e == hipSuccess && a.ndoc) {
@@ -751,7 +844,7 @@ template <typename T> size_t attn_bwd_part_bytes(const AttnArgs& a) {
 // tile + sink_number grows from one to the next
 size_t attn_sink_part_bytes(const AttnArgs& a) {
   const size_t slots = attn_tiles(a.Tq) + sink_number(a.Tq, a.Tk, a.window) + 1;
-  return a.sinks ? slots * a.Hq * 2 * a.sinks * a.D * 4 : 0;
+  return a.sinks ? slots * a.Hkv * 2 * a.sinks * a.D * 4 : 0;
 }
 
 template <typename T> hipError_t launch_attn_bwd(const AttnArgs& a, hipStream_t s) {

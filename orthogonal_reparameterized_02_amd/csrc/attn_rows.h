@@ -96,8 +96,7 @@ __device__ __forceinline__ float2 attn_row_dq(const TS* q, const TS* dout, const
 }
 
 // adds to dk and dv of one key row what query head h, rows [lo, hi), gives
-// (OWN_DELTA: delta from dout and o instead of a.delta)
-template <typename TS, bool OWN_DELTA = false>
+template <typename TS>
 __device__ __forceinline__ void attn_row_dkv(const AttnArgs& a, int h, int j, int lo, int hi, int lane,
                                              float2& dk, float2& dv) {
   const int hk = h / a.group;
@@ -113,14 +112,7 @@ __device__ __forceinline__ void attn_row_dkv(const AttnArgs& a, int h, int j, in
     const float dp = wave_sum(ov.x * vv.x + ov.y * vv.y);
     const float lse = a.lse[(long)h * a.Tq + i];
     const float p = lse == -INFINITY ? 0.0f : __expf(s - lse);
-    float delta;
-    if constexpr (OWN_DELTA) {
-      const float2 yv = ld2((const TS*)a.o + (long)i * a.ldo + (long)h * a.D, lane, a.D);
-      delta = wave_sum(ov.x * yv.x + ov.y * yv.y);
-    } else {
-      delta = a.delta[(long)h * a.Tq + i];
-    }
-    const float ds = p * (dp - delta) * dsdx;
+    const float ds = p * (dp - a.delta[(long)h * a.Tq + i]) * dsdx;
     dv.x += p * ov.x;
     dv.y += p * ov.y;
     dk.x += ds * qv.x;

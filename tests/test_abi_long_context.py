@@ -120,7 +120,7 @@ def test_window_sizes_and_nothing_to_do():
     work = lambda w, i: L.poetx_attn_window_workspace_bytes(C.byref(sh), C.byref(w), i)
     assert size(none) == L.poetx_attn_plan_bytes(C.byref(sh)) and work(none, 1) == L.poetx_attn_workspace_bytes(C.byref(sh), 1)
     assert size(plain) == size(none) and size(sinks) >= size(none) + 100 * 8 + 3 * 16
-    assert work(sinks, 1) >= work(plain, 1) + 2 * 4 * 128 * 8 * 4 and work(sinks, 2) == 0
+    assert work(sinks, 1) >= work(plain, 1) + 2 * 4 * 128 * 2 * 4 and work(sinks, 2) == 0
     assert calls(sh, sinks, plan_n=size(sinks) - 1)[0] == 3
     assert calls(sh, sinks, ws_n=work(sinks, 1) - 1)[2] == 3
     empty = attn_shape(Tq=0, Tk=0)

@@ -70,6 +70,7 @@ CASES = [  # q lengths, k lengths, rows before and after, Hq, Hkv, D, window, si
     dict(q=[257], k=[257], Hq=8, Hkv=1, D=64, w=1000, s=4),                 # a window past the document
     dict(q=[257, 100], k=[257, 100], Hq=2, Hkv=1, D=64, w=0, s=4),          # none
     dict(q=[200, 90], k=[200, 90], Hq=4, Hkv=2, D=128, w=60, s=0, bias=True, cap=30.0),
+    dict(q=[20, 30, 90], k=[400, 300, 350], Hq=2, Hkv=1, D=64, w=40, s=5),  # chunks of several prompts in one tile
     # the loops are cut into parts and joined
     dict(q=[64, 3], k=[1500, 1100], Hq=2, Hkv=1, D=64, w=900, s=4),
     dict(q=[33], k=[2049], pad=(1, 2), Hq=4, Hkv=1, D=128, w=1500, s=7, cap=6.0, bias=True),
