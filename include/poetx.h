@@ -571,7 +571,7 @@ int32_t poetx_attn_window_bwd(const poetx_attn_shape* sh, const poetx_window* wi
  *   q, o [B][Hq][D] (pitches ldq, ldo); row j of sequence b of the caches
  *   at b * bsk + j * ldk, b * bsv + j * ldv (offsets are 64-bit), heads of
  *   D values side by side; rows: cache capacity per sequence, at most
- *   2^31 - 2^16.
+ *   2^31 - 2^16; B Hq below 2^24.
  *   ws poetx_attn_decode_workspace_bytes(sh) bytes.
  * Errors: ERR_ARG, ERR_WORKSPACE, ERR_DEVICE.
  */

@@ -190,6 +190,8 @@ int32_t check_decode(const char* fn, const poetx_decode_shape* sh) {
     return fail(POETX_ERR_ARG, "%s: B=%d (0..%d) rows=%d (>= 0)", fn, sh->B, B_MAX, sh->rows);
   if (sh->rows > ROWS_MAX) return fail(POETX_ERR_ARG, "%s: rows=%d above %d", fn, sh->rows, ROWS_MAX);
   TRY(check_heads(fn, sh->Hq, sh->Hkv, sh->D));
+  // a workgroup of 256 threads a sequence and head, a dispatch 2^32 - 1 of them at most
+  if ((int64_t)sh->B * sh->Hq >= 1 << 24) return fail(POETX_ERR_ARG, "%s: B=%d sequences of Hq=%d heads: 2^24 or more", fn, sh->B, sh->Hq);
   TRY(check_act(fn, sh->act));
   TRY(check_scores(fn, sh->scale, sh->cap));
   const int64_t wq = (int64_t)sh->Hq * sh->D, wk = (int64_t)sh->Hkv * sh->D;

@@ -53,25 +53,21 @@ __device__ __forceinline__ void range_of(const DecodeArgs& a, int b, int pieces,
 
 // the same with a window: the padded rows of its view
 __device__ __forceinline__ void range_of(const DecodeArgs& a, int b, int pieces, View& v, int& lo, int& hi, int& piece) {
-  v.init<BN, false>(a, b);
+  v.init<BN, false>(a, a.len[b], 0);
   lo = 0;
   hi = v.total;
   piece = piece_of(v.total, pieces, GRAIN);
 }
 
-struct Plain {
-  static __device__ __forceinline__ int rows(const DecodeArgs& a, int b, int pieces, int& piece) {
-    int lo, hi;
-    range_of(a, b, pieces, lo, hi, piece);
-    return hi - lo;
-  }
-};
-struct Windowed {
-  static __device__ __forceinline__ int rows(const DecodeArgs& a, int b, int pieces, int& piece) {
+template <bool WIN> struct Pieces {
+  int pieces;
+  __device__ __forceinline__ int find(const DecodeArgs& a, int b, int h, long& at) const {
+    int lo, hi, piece;
     View v;
-    int lo, hi;
-    range_of(a, b, pieces, v, lo, hi, piece);
-    return hi;
+    if constexpr (WIN) range_of(a, b, pieces, v, lo, hi, piece);
+    else range_of(a, b, pieces, lo, hi, piece);
+    at = ((long)b * a.Hq + h) * pieces;
+    return hi - lo <= piece ? 1 : (hi - lo + piece - 1) / piece;
   }
 };
 
@@ -245,7 +241,7 @@ template <typename T, int DP, int MODE, bool WIN> hipError_t decode(const Decode
   k_attn_decode<T, DP, MODE, WIN><<<dim3(pieces, a.Hkv * ((a.group + 31) / 32), a.B), 64 * NW, lds, s>>>(a, pieces, ws, ml);
   const hipError_t e2 = hipGetLastError();
   if (e2 != hipSuccess || pieces == 1) return e2;
-  k_attn_decode_join<T, std::conditional_t<WIN, Windowed, Plain>><<<dim3(a.Hq, a.B), 64 * NW, 0, s>>>(a, pieces, ws, ml);
+  k_attn_decode_join<T><<<dim3(a.Hq, a.B), 64 * NW, 0, s>>>(a, Pieces<WIN>{pieces}, ws, ml);
   return hipGetLastError();
 }
 

@@ -1,8 +1,11 @@
 // Attention of one query row per sequence over a cache in 4 bits (kv4.hip for
 // the format), on MFMA tiles.
 //
-// The query heads that share a key head are the columns of 16-wide tiles, up
-// to 16 of them.  A workgroup takes a piece of one sequence's rows for one key
+// The query heads that share a key head are the columns of 16-wide tiles: up to
+// 16 of them, or copies of up to 8 or 4, so that every column works: a column of
+// copy c keeps the scores of its part of the rows, and has a maximum and sums of
+// its own until the end.  Softmax would else be formed in all 64 lanes for 4
+// heads' worth of scores.  A workgroup takes a piece of one sequence's rows for one key
 // head; each of its four waves goes through 64-row tiles of its own without any
 // barrier, the next tile's codes on their way to registers.
 //   Scores: lane (r, g) = (lane % 16, lane / 16) loads block g of rows 4 r + t,
@@ -30,7 +33,7 @@ namespace {
 constexpr int NW = 4;           // waves a workgroup
 constexpr int BN = 64;          // rows a tile
 constexpr int GRAIN = NW * BN;  // a piece is a multiple of this
-constexpr int HEADS = 16;       // query heads a workgroup
+constexpr int COLS = 16;        // columns of a tile: copies times heads
 constexpr int MAX_PIECES = 64;
 // The reference of the exponentials moves only when a score passes it by more
 // than this (log2): float32 sums hold probabilities up to 2^8 as well, and
@@ -68,69 +71,60 @@ template <int N> __device__ __forceinline__ void parts2(float x, float y, uint32
   }
 }
 
+// copies of the heads among the columns
+int copies_of(const DecodeArgs& a) { return a.group <= 4 ? 4 : a.group <= 8 ? 2 : 1; }
+int groups_of(const DecodeArgs& a) { return (a.group + COLS / copies_of(a) - 1) / (COLS / copies_of(a)); }
+
 // Pieces that a sequence is cut into at most, as in attn_decode.hip
 int pieces_of(const DecodeArgs& a) {
-  const int per = a.B * a.Hkv * ((a.group + HEADS - 1) / HEADS), rows = (int)std::min(view_rows(a, BN), (long)INT32_MAX - 65535);
+  const int per = a.B * a.Hkv * groups_of(a), rows = (int)std::min(view_rows(a, BN), (long)INT32_MAX - 65535);
   const auto cut = [&](int fill, int least) { return std::min((fill + per - 1) / per, (rows + least - 1) / least); };
   return std::max(1, std::min(std::max(cut(2048, 1024), cut(256, GRAIN)), MAX_PIECES));
 }
 
-struct Extent {
-  static __device__ __forceinline__ int rows(const DecodeArgs& a, int b, int pieces, int& piece) {
+struct Pieces {
+  int pieces;
+  __device__ __forceinline__ int find(const DecodeArgs& a, int b, int h, long& at) const {
     View v;
-    v.init<BN, true>(a, b);
-    piece = piece_of(v.total, pieces, GRAIN);
-    return v.total;
+    v.init<BN, true>(a, a.len[b], a.start ? a.start[b] : 0);
+    const int piece = piece_of(v.total, pieces, GRAIN);
+    at = ((long)b * a.Hq + h) * pieces;
+    return v.total <= piece ? 1 : (v.total + piece - 1) / piece;
   }
 };
 
 // NBK: blocks a head, rounded up to 2 or 4; nb of them are there
-template <typename T, int NBK, int MODE>
+template <typename T, int NBK, int MODE, int COPIES>
 __global__ __launch_bounds__(64 * NW, 2) void k_attn_kv4(DecodeArgs a, int nb, int pieces, float* part, float* ml) {
   constexpr int DP = 32 * NBK, NT = DP / 16, RB = 2 * DP;
   constexpr int PQ = sizeof(T) == 2 ? 1 : 3, PP = sizeof(T) == 2 ? 2 : 3;
   constexpr int STAGE = 32 * RB;  // bytes of a wave's 32 rows of values
+  constexpr int HEADS = COLS / COPIES, TPL = 4 / COPIES;  // heads a workgroup; tiles whose scores a lane keeps
   extern __shared__ __align__(16) char smem[];
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int r = lane & 15, g = lane >> 4;
+  const int copy = r / HEADS, head_r = r % HEADS;  // of column r
   const int s = blockIdx.x, b = blockIdx.z;
   const int groups = (a.group + HEADS - 1) / HEADS;
   const int hk = blockIdx.y / groups, g0 = HEADS * (blockIdx.y % groups);
   const int heads = min(a.group - g0, HEADS), h0 = hk * a.group + g0;
   View view;
-  view.init<BN, true>(a, b);
+  view.init<BN, true>(a, a.len[b], a.start ? a.start[b] : 0);
   const int piece = piece_of(view.total, pieces, GRAIN);
   const int p0 = s * piece, p1 = min(p0 + piece, view.total);
   if (s > 0 && p0 >= view.total) return;
 
   const int blk = NBK == 4 ? g : g >> 1;  // this lane's block of a row
   const bool there = blk < nb;
-  const long head = (long)b * a.Hkv + hk;
+  const long plane = (long)b * a.Hkv + hk;
   const int rowb = nb * 16;
-  const uint8_t* kc = (const uint8_t*)a.k + head * a.rows * rowb;
-  const uint8_t* vc = (const uint8_t*)a.v + head * a.rows * rowb;
-  const uint8_t* ks = a.ks + (head * nb + (there ? blk : 0)) * a.rows + 4 * r;
-  const uint8_t* vs = a.vs + (head * nb + (there ? blk : 0)) * a.rows + 4 * r;
+  const uint8_t* kc = (const uint8_t*)a.k + plane * a.rows * rowb;
+  const uint8_t* vc = (const uint8_t*)a.v + plane * a.rows * rowb;
+  const uint8_t* ks = a.ks + (plane * nb + (there ? blk : 0)) * a.rows + 4 * r;
+  const uint8_t* vs = a.vs + (plane * nb + (there ? blk : 0)) * a.rows + 4 * r;
   const int off = 4 * r * rowb + (there ? g * (4 * NBK) : 0);
 
-  // queries: column r, elements 8 NBK g + 8 c of step c
-  uint4 qf[PQ][NBK];
-  {
-    const T* q = (const T*)a.q + (long)b * a.ldq + (long)(h0 + min(r, heads - 1)) * a.D;
-#pragma unroll
-    for (int c = 0; c < NBK; ++c) {
-      const int e = 8 * NBK * g + 8 * c;
-      float x[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = e < a.D && r < heads ? St<T>::ld(q + e + i) : 0.0f;
-      uint32_t p[4][PQ];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) parts2<PQ>(x[2 * i], x[2 * i + 1], p[i]);
-#pragma unroll
-      for (int n = 0; n < PQ; ++n) qf[n][c] = make_uint4(p[0][n], p[1][n], p[2][n], p[3][n]);
-    }
-  }
-  const ScoreArgs sa = score_args<T, MODE>(a.scale, a.cap, MODE & 2 ? a.slopes[h0 + min(r, heads - 1)] : 0.0f);
+  const ScoreArgs sa = score_args<T, MODE>(a.scale, a.cap, MODE & 2 ? a.slopes[h0 + min(head_r, heads - 1)] : 0.0f);
 
   struct Codes { uint32_t k[4][NBK], v[4][NBK], ks, vs; };
   const auto fetch = [&](int j, Codes& c, int& row, int& begin, int& end, int& shift) {
@@ -140,10 +134,10 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_kv4(DecodeArgs a, int nb, i
     c.vs = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(vs + row));
     const auto codes = [&](const uint8_t* p, uint32_t (&o)[NBK]) {
       if constexpr (NBK == 4) {
-        const u32x4_t u = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p));
+        const u32x4_t u = *reinterpret_cast<const u32x4_t*>(p);
         o[0] = u[0], o[1] = u[1], o[2] = u[2], o[3] = u[3];
       } else {
-        const u32x2_t u = __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(p));
+        const u32x2_t u = *reinterpret_cast<const u32x2_t*>(p);
         o[0] = u[0], o[1] = u[1];
       }
     };
@@ -169,6 +163,27 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_kv4(DecodeArgs a, int nb, i
   Codes c;
   int row, begin, end, shift;
   if (j0 < p1) fetch(j0, c, row, begin, end, shift);
+  // queries: column r, elements 8 NBK g + 8 c of step c
+  uint4 qf[PQ][NBK];
+  {
+    const T* q = (const T*)a.q + (long)b * a.ldq + (long)(h0 + min(head_r, heads - 1)) * a.D;
+    struct alignas(16) Eight { T e[8]; } x[NBK];
+#pragma unroll
+    for (int c = 0; c < NBK; ++c) {
+      const int e = 8 * NBK * g + 8 * c;
+      x[c] = *reinterpret_cast<const Eight*>(q + (e < a.D ? e : 0));
+    }
+#pragma unroll
+    for (int c = 0; c < NBK; ++c) {
+      const bool in = 8 * NBK * g + 8 * c < a.D && head_r < heads;
+      uint32_t p[4][PQ];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        parts2<PQ>(in ? St<T>::ld(&x[c].e[2 * i]) : 0.0f, in ? St<T>::ld(&x[c].e[2 * i + 1]) : 0.0f, p[i]);
+#pragma unroll
+      for (int n = 0; n < PQ; ++n) qf[n][c] = make_uint4(p[0][n], p[1][n], p[2][n], p[3][n]);
+    }
+  }
   for (; j0 < p1; j0 += GRAIN) {
     Codes next = c;
     int nrow = row, nbegin = begin, nend = end, nshift = shift;
@@ -180,41 +195,53 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_kv4(DecodeArgs a, int nb, i
 #pragma unroll
         for (int i = 0; i < NBK; ++i) c.k[t][i] = c.v[t][i] = 0;
     }
-    f32x4 sc[4];
+    f32x4 all[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const float scale = scale_of(c.ks, t);
-      sc[t] = (f32x4){};
+      all[t] = (f32x4){};
 #pragma unroll
       for (int i = 0; i < NBK; ++i) {
         const uint4 k = expand(c.k[t][i], scale);
 #pragma unroll
-        for (int n = 0; n < PQ; ++n) sc[t] = mma(k, qf[n][i], sc[t]);
+        for (int n = 0; n < PQ; ++n) all[t] = mma(k, qf[n][i], all[t]);
       }
     }
-    // this lane's rows: row + 16 g + 4 i + t
-    const float d0 = (float)(view.last - shift - row - 16 * g);
+    // this lane's scores: rows row + 16 g + 4 i + TPL copy + x
+    f32x4 sc[TPL];
+#pragma unroll
+    for (int x = 0; x < TPL; ++x) {
+      sc[x] = all[x];
+#pragma unroll
+      for (int n = 1; n < COPIES; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[x][i] = copy == n ? all[n * TPL + x][i] : sc[x][i];
+    }
+    const int first = row + 16 * g + TPL * copy;
+    const float d0 = (float)(view.last - shift - first);
     float top = -INFINITY, unused;
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
+    for (int x = 0; x < TPL; ++x)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sc[t][i] = score2<T, MODE>(sc[t][i], sa, d0 - (float)(4 * i + t), unused);
+      for (int i = 0; i < 4; ++i) sc[x][i] = score2<T, MODE>(sc[x][i], sa, d0 - (float)(4 * i + x), unused);
     if (begin > row || end < row + BN) {  // some row is not seen: no score, and a value of 0
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
+      for (int x = 0; x < TPL; ++x)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int j = row + 16 * g + 4 * i + t;
-          sc[t][i] = j >= begin && j < end ? sc[t][i] : -INFINITY;
+          const int j = first + 4 * i + x;
+          sc[x][i] = j >= begin && j < end ? sc[x][i] : -INFINITY;
         }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
         const int jv = row + 4 * r + t;  // row of the codes
         if (jv < begin || jv >= end) c.vs &= ~(0xffu << (8 * t));
       }
     }
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
+    for (int x = 0; x < TPL; ++x)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[t][i]);
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[x][i]);
     if (__any(top > m + SLACK)) {
       top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32));
@@ -226,13 +253,17 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_kv4(DecodeArgs a, int nb, i
       for (int i = 0; i < NT; ++i) o[i] *= f;
     }
     const float ref = m == -INFINITY ? 0.0f : m;
+    uint32_t pk[TPL][2][PP];  // probabilities as operands
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
+    for (int x = 0; x < TPL; ++x) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        sc[t][i] = exp2_hw(sc[t][i] - ref);
-        l += sc[t][i];
+        sc[x][i] = exp2_hw(sc[x][i] - ref);
+        l += sc[x][i];
       }
+      parts2<PP>(sc[x][0], sc[x][1], pk[x][0]);
+      parts2<PP>(sc[x][2], sc[x][3], pk[x][1]);
+    }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
 #pragma unroll
@@ -242,15 +273,19 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_kv4(DecodeArgs a, int nb, i
         for (int i = 0; i < NBK; ++i)
           *reinterpret_cast<uint4*>(stage + (wr ^ (i << 4)) + x * 16 * RB) = expand(c.v[2 * u + x][i], scale);
       }
+      // rows (2 u, 2 u + 1): a column has those of its copy, zeros elsewhere
       uint4 p[PP];
-      {
-        uint32_t w[4][PP];
-        parts2<PP>(sc[2 * u][0], sc[2 * u][1], w[0]);
-        parts2<PP>(sc[2 * u][2], sc[2 * u][3], w[1]);
-        parts2<PP>(sc[2 * u + 1][0], sc[2 * u + 1][1], w[2]);
-        parts2<PP>(sc[2 * u + 1][2], sc[2 * u + 1][3], w[3]);
 #pragma unroll
-        for (int n = 0; n < PP; ++n) p[n] = make_uint4(w[0][n], w[1][n], w[2][n], w[3][n]);
+      for (int n = 0; n < PP; ++n) {
+        if constexpr (COPIES == 1) {
+          p[n] = make_uint4(pk[2 * u][0][n], pk[2 * u][1][n], pk[2 * u + 1][0][n], pk[2 * u + 1][1][n]);
+        } else if constexpr (COPIES == 2) {
+          const bool on = copy == u;
+          p[n] = make_uint4(on ? pk[0][0][n] : 0, on ? pk[0][1][n] : 0, on ? pk[1][0][n] : 0, on ? pk[1][1][n] : 0);
+        } else {
+          const bool on0 = copy == 2 * u, on1 = copy == 2 * u + 1;
+          p[n] = make_uint4(on0 ? pk[0][0][n] : 0, on0 ? pk[0][1][n] : 0, on1 ? pk[0][0][n] : 0, on1 ? pk[0][1][n] : 0);
+        }
       }
       __builtin_amdgcn_wave_barrier();
 #pragma unroll
@@ -270,33 +305,46 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_kv4(DecodeArgs a, int nb, i
   l += __shfl_xor(l, 16);
   l += __shfl_xor(l, 32);
 
-  // the four waves join: a common maximum, then their sums in wave order
+  // the waves' columns join: a common maximum, then their sums in order
   __syncthreads();
-  float* wm = reinterpret_cast<float*>(smem);      // [NW][16] maxima, then [NW][16] sums
-  float* wo = wm + 2 * NW * HEADS;                 // [NW][16][DP]
-  if (lane < HEADS) {
-    wm[wave * HEADS + r] = m;
-    wm[(NW + wave) * HEADS + r] = l;
+  float* wm = reinterpret_cast<float*>(smem);     // [NW][COLS] maxima, then [NW][COLS] sums
+  float* wo = wm + 2 * NW * COLS;                 // [NW][COLS][DP]
+  if (lane < COLS) {
+    wm[wave * COLS + r] = m;
+    wm[(NW + wave) * COLS + r] = l;
   }
-  if (r < heads)
 #pragma unroll
-    for (int ct = 0; ct < NT; ++ct)
-      *reinterpret_cast<f32x4*>(wo + (wave * HEADS + r) * DP + 16 * ct + 4 * g) = o[ct];
+  for (int ct = 0; ct < NT; ++ct)
+    *reinterpret_cast<f32x4*>(wo + (wave * COLS + r) * DP + 16 * ct + 4 * g) = o[ct];
   __syncthreads();
   const bool whole = view.total <= piece;  // one piece: this is the result
-  for (int e = threadIdx.x; e < heads * DP; e += 64 * NW) {
-    const int hh = e / DP, d = e % DP;
+  if (threadIdx.x < COLS) {  // the factors of a head's columns, and its sum
+    const int hh = threadIdx.x % HEADS;
     float M = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) M = fmaxf(M, wm[w * HEADS + hh]);
+    for (int w = 0; w < NW * COPIES; ++w) M = fmaxf(M, wm[w * HEADS + hh]);
     const float ref = M == -INFINITY ? 0.0f : M;
-    float sum = 0.0f, lsum = 0.0f;
+    float lsum = 0.0f, f[NW];
 #pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      const float f = exp2_hw(wm[w * HEADS + hh] - ref);
-      lsum += f * wm[(NW + w) * HEADS + hh];
-      sum += f * wo[(w * HEADS + hh) * DP + d];
+    for (int w = 0; w < NW * COPIES; ++w) {
+      const float x = exp2_hw(wm[w * HEADS + hh] - ref);
+      lsum += x * wm[NW * COLS + w * HEADS + hh];
+      if (w % COPIES == threadIdx.x / HEADS) f[w / COPIES] = x;
     }
+    float* wf = wo + NW * COLS * DP;  // [NW][COLS] factors, [COLS] maxima, [COLS] sums
+#pragma unroll
+    for (int w = 0; w < NW; ++w) wf[w * COLS + threadIdx.x] = f[w];
+    wf[NW * COLS + threadIdx.x] = M;
+    wf[(NW + 1) * COLS + threadIdx.x] = lsum;
+  }
+  __syncthreads();
+  const float* wf = wo + NW * COLS * DP;
+  for (int e = threadIdx.x; e < heads * DP; e += 64 * NW) {
+    const int hh = e / DP, d = e % DP;
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < NW * COPIES; ++w) sum = fmaf(wf[w * HEADS + hh], wo[(w * HEADS + hh) * DP + d], sum);
+    const float M = wf[NW * COLS + hh], lsum = wf[(NW + 1) * COLS + hh];
     const int h = h0 + hh;
     if (whole) {
       if (d < a.D) St<T>::st((T*)a.o + (long)b * a.ldo + (long)h * a.D + d, lsum == 0.0f ? 0.0f : sum / lsum);
@@ -313,21 +361,25 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_kv4(DecodeArgs a, int nb, i
 
 size_t part_floats(const DecodeArgs& a) { return (size_t)a.B * a.Hq * pieces_of(a) * a.D; }
 
-template <typename T, int NBK, int MODE> hipError_t decode(const DecodeArgs& a, float* ws, hipStream_t s) {
-  constexpr int DP = 32 * NBK, lds = std::max(NW * 32 * 2 * DP, (2 * NW * HEADS + NW * HEADS * DP) * 4);
-  const hipError_t e = lds_opt_in((const void*)k_attn_kv4<T, NBK, MODE>, lds);
+template <typename T, int NBK, int MODE, int COPIES> hipError_t decode(const DecodeArgs& a, float* ws, hipStream_t s) {
+  constexpr int DP = 32 * NBK, lds = std::max(NW * 32 * 2 * DP, (2 * NW * COLS + NW * COLS * DP + (NW + 2) * COLS) * 4);
+  const hipError_t e = lds_opt_in((const void*)k_attn_kv4<T, NBK, MODE, COPIES>, lds);
   if (e != hipSuccess) return e;
   const int pieces = pieces_of(a), nb = kv4_blocks(a.D);
   float* ml = ws + part_floats(a);
-  k_attn_kv4<T, NBK, MODE><<<dim3(pieces, a.Hkv * ((a.group + HEADS - 1) / HEADS), a.B), 64 * NW, lds, s>>>(a, nb, pieces, ws, ml);
+  k_attn_kv4<T, NBK, MODE, COPIES><<<dim3(pieces, a.Hkv * groups_of(a), a.B), 64 * NW, lds, s>>>(a, nb, pieces, ws, ml);
   const hipError_t e2 = hipGetLastError();
   if (e2 != hipSuccess || pieces == 1) return e2;
-  k_attn_decode_join<T, Extent><<<dim3(a.Hq, a.B), 64 * JOIN_WAVES, 0, s>>>(a, pieces, ws, ml);
+  k_attn_decode_join<T><<<dim3(a.Hq, a.B), 64 * JOIN_WAVES, 0, s>>>(a, Pieces{pieces}, ws, ml);
   return hipGetLastError();
 }
 
 template <typename T, int NBK> hipError_t decode_mode(const DecodeArgs& a, float* ws, hipStream_t s) {
-  return by_mode<T>(a.slopes, a.cap, [&](auto mode) { return decode<T, NBK, decltype(mode)::value>(a, ws, s); });
+  return by_mode<T>(a.slopes, a.cap, [&](auto mode) {
+    constexpr int MODE = decltype(mode)::value;
+    const int n = copies_of(a);
+    return n == 4 ? decode<T, NBK, MODE, 4>(a, ws, s) : n == 2 ? decode<T, NBK, MODE, 2>(a, ws, s) : decode<T, NBK, MODE, 1>(a, ws, s);
+  });
 }
 
 }  // namespace

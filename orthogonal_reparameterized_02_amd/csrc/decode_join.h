@@ -15,19 +15,18 @@ __device__ __forceinline__ int piece_of(int rows, int pieces, int grain) {
   return (n + grain - 1) / grain * grain;
 }
 
-// One query head.  Extent::rows gives the rows of sequence b and of a piece.  Lane l of every wave holds elements
+// One query head.  pieces.find gives the number of a sequence's pieces, at most
+// 64, and the first one's place.  Lane l of every wave holds elements
 // 2 l, 2 l + 1; wave w takes pieces w, w + NW, ...
-template <typename T, class Extent>
-__global__ __launch_bounds__(64 * JOIN_WAVES) void k_attn_decode_join(DecodeArgs a, int pieces, const float* part, const float* ml) {
+template <typename T, class Pieces>
+__global__ __launch_bounds__(64 * JOIN_WAVES) void k_attn_decode_join(DecodeArgs a, Pieces pieces, const float* part, const float* ml) {
   constexpr int NW = JOIN_WAVES;
   __shared__ float red[NW][130];
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
   const int h = blockIdx.x, b = blockIdx.y;
-  int piece;
-  const int rows = Extent::rows(a, b, pieces, piece);
-  if (rows <= piece) return;  // written by the first pass
-  const int n = (rows + piece - 1) / piece;
-  const long at = ((long)b * a.Hq + h) * pieces;
+  long at;
+  const int n = pieces.find(a, b, h, at);
+  if (n <= 1) return;  // written by the first pass
   const float mine = lane < n ? ml[2 * (at + lane)] : -INFINITY;  // n <= 64
   float M = mine;
 #pragma unroll

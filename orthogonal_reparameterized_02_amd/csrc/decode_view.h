@@ -19,9 +19,9 @@ struct View {
   int t0, t1, total;   // padded rows: sinks, window, all
 
   // TILE rows a tile; ALIGN: tiles begin at multiples of TILE in the cache
-  template <int TILE, bool ALIGN> __device__ __forceinline__ void init(const DecodeArgs& a, int b) {
-    const int hi = a.ring ? max(a.len[b], 0) : min(max(a.len[b], 0), a.rows);
-    lo = a.start ? min(max(a.start[b], 0), hi) : 0;
+  template <int TILE, bool ALIGN> __device__ __forceinline__ void init(const DecodeArgs& a, int len, int start) {
+    const int hi = a.ring ? max(len, 0) : min(max(len, 0), a.rows);
+    lo = min(max(start, 0), hi);
     if (a.window) lo = max(hi - a.window, 0);
     last = hi - 1;
     n0 = a.window ? min(a.sinks, lo) : 0;

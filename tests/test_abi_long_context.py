@@ -167,7 +167,7 @@ def kdec(sh, w, ring=0, n=1 << 40, **kw):
 
 
 @pytest.mark.parametrize("kw", [dict(B=-1), dict(B=70000), dict(rows=-64), dict(Hq=9), dict(D=4), dict(D=136), dict(act=2),
-                                dict(cap=-2.0), dict(ldq=8), dict(ldo=1)])
+                                dict(B=65535, Hq=1024, ldq=1 << 17, ldo=1 << 17), dict(cap=-2.0), dict(ldq=8), dict(ldo=1)])
 def test_decode_shape_errors(kw):
     L, sh, w = _lib.lib(), decode_shape(**kw), _lib.Window(16, 4)
     assert L.poetx_attn_window_decode_workspace_bytes(C.byref(sh), C.byref(w)) == 0

@@ -151,6 +151,10 @@ CASES = [  # lengths, rows, Hq, Hkv, D, window, sinks, ring, cap, bias
     dict(len=[700, 3000, 5000], rows=1024, Hq=8, Hkv=1, D=128, w=1000, s=17, ring=True, cap=20.0, bias=True),
     dict(len=[7, 3000], rows=64, Hq=3, Hkv=1, D=32, w=5, s=0, ring=True),
     dict(len=[2 ** 31 - 1, 2 ** 30], rows=192, Hq=2, Hkv=1, D=64, w=190, s=2, ring=True, host=False),
+    # many sequences, one long one among empty ones
+    dict(len=[(37 * i) % 130 for i in range(300)], rows=192, Hq=2, Hkv=1, D=32),
+    dict(len=[(37 * i) % 130 for i in range(257)], rows=64, Hq=2, Hkv=2, D=64, w=50, s=3, ring=True),
+    dict(len=[0] * 70 + [9000] + [1] * 80, rows=9024, Hq=2, Hkv=1, D=8),
     # cut into pieces and joined
     dict(len=[6000, 2500, 300], rows=6016, Hq=4, Hkv=1, D=64),
     dict(len=[9000, 4000, 300], rows=9024, Hq=2, Hkv=1, D=128, w=5000, s=4, bias=True),
