@@ -651,6 +651,10 @@ Kv4Args kv4_args(const poetx_kv4_shape* sh) {
   return a;
 }
 
+size_t kv4_ws(const DecodeArgs& a, int32_t act) {
+  return align_up(act == POETX_BF16 ? attn_kv4_ws_bytes<bf16>(a) : attn_kv4_ws_bytes<float>(a));
+}
+
 int32_t check_kv4_decode(const char* fn, const poetx_decode_shape* sh, const poetx_window* win, int32_t ring) {
   TRY(check_decode_window(fn, sh, win, ring));
   if (sh->rows % 64) return fail(POETX_ERR_ARG, "%s: rows=%d must be a multiple of 64", fn, sh->rows);
@@ -708,7 +712,7 @@ int32_t poetx_kv4_read(const poetx_kv4_shape* sh, const int32_t* seq, const int3
 size_t poetx_attn_kv4_decode_workspace_bytes(const poetx_decode_shape* sh, const poetx_window* win) {
   if (check_kv4_decode("poetx_attn_kv4_decode_workspace_bytes", sh, win, 0) != POETX_OK) return 0;
   const DecodeArgs a = decode_window_args(sh, win, 0);
-  return a.B ? align_up(attn_kv4_ws_bytes(a)) : 256;
+  return a.B ? kv4_ws(a, sh->act) : 256;
 }
 
 int32_t poetx_attn_kv4_decode(const poetx_decode_shape* sh, const poetx_window* win, int32_t ring, const void* q,
@@ -732,7 +736,7 @@ int32_t poetx_attn_kv4_decode(const poetx_decode_shape* sh, const poetx_window* 
   NEED_PTR(o);
   NEED_PTR(ws);
   DecodeArgs a = decode_window_args(sh, win, ring);
-  const size_t need = align_up(attn_kv4_ws_bytes(a));
+  const size_t need = kv4_ws(a, sh->act);
   if (ws_bytes < need) return fail(POETX_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, ws_bytes, need);
   a.q = q, a.k = kc, a.v = vc, a.ks = (const uint8_t*)ks, a.vs = (const uint8_t*)vs, a.o = o;
   a.slopes = slopes;

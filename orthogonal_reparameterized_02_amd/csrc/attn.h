@@ -177,7 +177,7 @@ struct Kv4Args {
 template <typename TS> hipError_t launch_kv4_write(const Kv4Args& a, hipStream_t s);
 template <typename TS> hipError_t launch_kv4_read(const Kv4Args& a, hipStream_t s);
 // a.k, a.v: codes
-size_t attn_kv4_ws_bytes(const DecodeArgs& a);
+template <typename T> size_t attn_kv4_ws_bytes(const DecodeArgs& a);
 template <typename T> hipError_t launch_attn_kv4(const DecodeArgs& a, float* ws, hipStream_t s);
 
 // ws: attn_decode_ws_bytes(a) bytes for the pieces' partial results

@@ -8,14 +8,18 @@
 // heads' worth of scores.  A workgroup takes a piece of one sequence's rows for one key
 // head; each of its four waves goes through 64-row tiles of its own without any
 // barrier, the next tile's codes on their way to registers.
-//   Scores: lane (r, g) = (lane % 16, lane / 16) loads block g of rows 4 r + t,
-// t = 0..3: sixteen bytes are 32 codes, which the conversion with a scale turns
-// into exact bf16 numbers in the order of the A operand (K = 8 elements of each
-// of the four blocks; the queries are laid out alike).  The four scales of a
-// block are one dword.  D[row][query] leaves lane (query, h) the rows 16 h +
-// 4 i + t.
+//   Scores: lane (r, g) = (lane % 16, lane / 16) loads block g of row 16 t +
+// 4 (r % 4) + r / 4, t = 0..3: sixteen bytes are 32 codes, which the conversion
+// with a scale turns into exact bf16 numbers in the order of the A operand (K = 8
+// elements of each of the four blocks; the queries are laid out alike).  Four
+// neighbouring rows' scales of a block are one dword; this order of rows leaves
+// every quad of lanes the same four dwords to take a byte of.  D[row][query]
+// leaves lane (query, h) the rows 16 t + 4 i + h.
+//   Each load takes a whole KB.  In rows 4 r + t, whose scales would need no
+// exchange, two loads share every 128 bytes, and a cache that is read past the
+// others (non-temporal) twice: 91 us for the 16 sequences below.
 //   Values: sum over rows, so the operand is the transposed tile.  Converted
-// values go through LDS, 32 rows (t, t + 1) at a time, and come back down their
+// values go through LDS, 32 rows of t and t + 1 at a time, and come back down their
 // columns by ds_read_b64_tr_b16 in just that order of rows; 16-byte chunk c of
 // row r lies at c ^ key(r), which spreads both accesses over the banks.
 //   bf16 queries have probabilities in two bf16 parts, float32 ones both
@@ -57,8 +61,11 @@ __device__ __forceinline__ uint4 expand(uint32_t c, float scale) {
   u.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 3));
   return u;
 }
-__device__ __forceinline__ float scale_of(uint32_t bytes, int t) {
-  return __uint_as_float((bytes >> (8 * t) & 0xffu) << 23);
+// scale of this lane's row of tile t: byte `shift` / 8 of lane 4 t + lane % 4 of
+// these 16
+template <int t> __device__ __forceinline__ float scale_of(uint32_t bytes, int shift) {
+  const uint32_t d = (uint32_t)__builtin_amdgcn_ds_swizzle((int)bytes, t << 7 | 0x13);
+  return __uint_as_float((d >> shift & 0xffu) << 23);
 }
 
 // x (>= 0, or any float for queries) as N bf16 parts: pack[n] gets part n of two
@@ -75,11 +82,17 @@ template <int N> __device__ __forceinline__ void parts2(float x, float y, uint32
 int copies_of(const DecodeArgs& a) { return a.group <= 4 ? 4 : a.group <= 8 ? 2 : 1; }
 int groups_of(const DecodeArgs& a) { return (a.group + COLS / copies_of(a) - 1) / (COLS / copies_of(a)); }
 
-// Pieces that a sequence is cut into at most, as in attn_decode.hip
-int pieces_of(const DecodeArgs& a) {
+// Pieces that a sequence is cut into at most: two rounds of the workgroups that
+// run at once, 2 to 4 a CU by their registers, in pieces of 1024 rows at least (16
+// sequences of 8000 to 32768 rows: 82 us with two rounds, 84 to 98 with 1024, 2048
+// or 4096 workgroups; 8 in float32 57, and 64 to 68); but one workgroup a CU from
+// 256 rows on, where latency counts.  Pieces of one length over all sequences,
+// found from the lengths by every wave, were slower: 100 us.
+template <typename T> int pieces_of(const DecodeArgs& a) {
   const int per = a.B * a.Hkv * groups_of(a), rows = (int)std::min(view_rows(a, BN), (long)INT32_MAX - 65535);
+  const int resident = 256 * (a.D <= 64 ? 4 : sizeof(T) == 2 ? 3 : 2);
   const auto cut = [&](int fill, int least) { return std::min((fill + per - 1) / per, (rows + least - 1) / least); };
-  return std::max(1, std::min(std::max(cut(2048, 1024), cut(256, GRAIN)), MAX_PIECES));
+  return std::max(1, std::min(std::max(cut(2 * resident, 1024), cut(256, GRAIN)), MAX_PIECES));
 }
 
 struct Pieces {
@@ -122,33 +135,39 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_kv4(DecodeArgs a, int nb, i
   const uint8_t* vc = (const uint8_t*)a.v + plane * a.rows * rowb;
   const uint8_t* ks = a.ks + (plane * nb + (there ? blk : 0)) * a.rows + 4 * r;
   const uint8_t* vs = a.vs + (plane * nb + (there ? blk : 0)) * a.rows + 4 * r;
-  const int off = 4 * r * rowb + (there ? g * (4 * NBK) : 0);
+  const int off = (4 * (r & 3) + (r >> 2)) * rowb + (there ? g * (4 * NBK) : 0), byte = 8 * (r >> 2);
 
   const ScoreArgs sa = score_args<T, MODE>(a.scale, a.cap, MODE & 2 ? a.slopes[h0 + min(head_r, heads - 1)] : 0.0f);
 
-  struct Codes { uint32_t k[4][NBK], v[4][NBK], ks, vs; };
-  const auto fetch = [&](int j, Codes& c, int& row, int& begin, int& end, int& shift) {
-    view.tile<BN, true>(j, row, begin, end, shift);
-    const uint8_t *kp = kc + (long)row * rowb + off, *vp = vc + (long)row * rowb + off;
-    c.ks = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(ks + row));
-    c.vs = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(vs + row));
-    const auto codes = [&](const uint8_t* p, uint32_t (&o)[NBK]) {
+  // The next tile's keys are asked for as soon as the scores are formed, its
+  // values as soon as this tile's are in LDS: in the registers that these leave.
+  struct Codes { uint32_t c[4][NBK], scales; };
+  const auto fetch = [&](const uint8_t* codes, const uint8_t* scales, int row, Codes& o) {
+    o.scales = *reinterpret_cast<const uint32_t*>(scales + row);
+    const uint8_t* p = codes + (long)row * rowb + off;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
       if constexpr (NBK == 4) {
-        const u32x4_t u = *reinterpret_cast<const u32x4_t*>(p);
-        o[0] = u[0], o[1] = u[1], o[2] = u[2], o[3] = u[3];
+        const u32x4_t u = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p + 16 * t * rowb));
+        o.c[t][0] = u[0], o.c[t][1] = u[1], o.c[t][2] = u[2], o.c[t][3] = u[3];
       } else {
-        const u32x2_t u = *reinterpret_cast<const u32x2_t*>(p);
-        o[0] = u[0], o[1] = u[1];
+        const u32x2_t u = __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(p + 16 * t * rowb));
+        o.c[t][0] = u[0], o.c[t][1] = u[1];
       }
-    };
+    }
+  };
+  const auto blank = [&](Codes& o) {  // no such block: zero
+    if (there) return;
+    o.scales = 0x7f7f7f7fu;
 #pragma unroll
-    for (int t = 0; t < 4; ++t) codes(kp + t * rowb, c.k[t]);
+    for (int t = 0; t < 4; ++t)
 #pragma unroll
-    for (int t = 0; t < 4; ++t) codes(vp + t * rowb, c.v[t]);
+      for (int i = 0; i < NBK; ++i) o.c[t][i] = 0;
   };
 
   // LDS of this wave: row n at n * RB, chunk c of it at c ^ key(n)
-  const auto key = [](int n) { return NBK == 4 ? n & 15 : (n >> 1) & 7; };
+  // (eight rows that are read together lie in eight pairs of chunks)
+  const auto key = [](int n) { return NBK == 4 ? (n & 7) << 1 | (n >> 3 & 1) : (n >> 1 & 3) << 1 | (n >> 3 & 1); };
   char* stage = smem + wave * STAGE;
   const int wr = r * RB + ((NBK * g ^ key(r)) << 4);  // first chunk written; + 16 rows: the same key
   // transposed read: lane i of 16 gives 4 columns of row 4 g + i / 4
@@ -160,9 +179,13 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_kv4(DecodeArgs a, int nb, i
   for (int i = 0; i < NT; ++i) o[i] = (f32x4){};
   float m = -INFINITY, l = 0.0f;
   int j0 = p0 + wave * BN;
-  Codes c;
-  int row, begin, end, shift;
-  if (j0 < p1) fetch(j0, c, row, begin, end, shift);
+  Codes k, v;
+  int row = 0, begin = 0, end = 0, shift = 0;
+  if (j0 < p1) {
+    view.tile<BN, true>(j0, row, begin, end, shift);
+    fetch(kc, ks, row, k);
+    fetch(vc, vs, row, v);
+  }
   // queries: column r, elements 8 NBK g + 8 c of step c
   uint4 qf[PQ][NBK];
   {
@@ -185,29 +208,28 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_kv4(DecodeArgs a, int nb, i
     }
   }
   for (; j0 < p1; j0 += GRAIN) {
-    Codes next = c;
-    int nrow = row, nbegin = begin, nend = end, nshift = shift;
-    if (j0 + GRAIN < p1) fetch(j0 + GRAIN, next, nrow, nbegin, nend, nshift);
-    if (!there) {  // no such block: zero
-      c.ks = c.vs = 0x7f7f7f7fu;
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int i = 0; i < NBK; ++i) c.k[t][i] = c.v[t][i] = 0;
-    }
+    blank(k);
     f32x4 all[4];
+    const float kscale[4] = {scale_of<0>(k.scales, byte), scale_of<1>(k.scales, byte), scale_of<2>(k.scales, byte),
+                             scale_of<3>(k.scales, byte)};
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      const float scale = scale_of(c.ks, t);
+      const float scale = kscale[t];
       all[t] = (f32x4){};
 #pragma unroll
       for (int i = 0; i < NBK; ++i) {
-        const uint4 k = expand(c.k[t][i], scale);
+        const uint4 f = expand(k.c[t][i], scale);
 #pragma unroll
-        for (int n = 0; n < PQ; ++n) all[t] = mma(k, qf[n][i], all[t]);
+        for (int n = 0; n < PQ; ++n) all[t] = mma(f, qf[n][i], all[t]);
       }
     }
-    // this lane's scores: rows row + 16 g + 4 i + TPL copy + x
+    const bool more = j0 + GRAIN < p1;
+    int nrow = 0, nbegin = 0, nend = 0, nshift = 0;
+    if (more) {
+      view.tile<BN, true>(j0 + GRAIN, nrow, nbegin, nend, nshift);
+      fetch(kc, ks, nrow, k);
+    }
+    // this lane's scores: rows row + 16 (TPL copy + x) + 4 i + g
     f32x4 sc[TPL];
 #pragma unroll
     for (int x = 0; x < TPL; ++x) {
@@ -217,25 +239,26 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_kv4(DecodeArgs a, int nb, i
 #pragma unroll
         for (int i = 0; i < 4; ++i) sc[x][i] = copy == n ? all[n * TPL + x][i] : sc[x][i];
     }
-    const int first = row + 16 * g + TPL * copy;
+    const int first = row + 16 * TPL * copy + g;
     const float d0 = (float)(view.last - shift - first);
     float top = -INFINITY, unused;
 #pragma unroll
     for (int x = 0; x < TPL; ++x)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sc[x][i] = score2<T, MODE>(sc[x][i], sa, d0 - (float)(4 * i + x), unused);
+      for (int i = 0; i < 4; ++i) sc[x][i] = score2<T, MODE>(sc[x][i], sa, d0 - (float)(16 * x + 4 * i), unused);
+    blank(v);
     if (begin > row || end < row + BN) {  // some row is not seen: no score, and a value of 0
 #pragma unroll
       for (int x = 0; x < TPL; ++x)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int j = first + 4 * i + x;
+          const int j = first + 16 * x + 4 * i;
           sc[x][i] = j >= begin && j < end ? sc[x][i] : -INFINITY;
         }
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const int jv = row + 4 * r + t;  // row of the codes
-        if (jv < begin || jv >= end) c.vs &= ~(0xffu << (8 * t));
+        const int jv = row + 4 * r + t;  // row of the scale
+        if (jv < begin || jv >= end) v.scales &= ~(0xffu << (8 * t));
       }
     }
 #pragma unroll
@@ -264,15 +287,18 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_kv4(DecodeArgs a, int nb, i
       parts2<PP>(sc[x][0], sc[x][1], pk[x][0]);
       parts2<PP>(sc[x][2], sc[x][3], pk[x][1]);
     }
+    const float vscale[4] = {scale_of<0>(v.scales, byte), scale_of<1>(v.scales, byte), scale_of<2>(v.scales, byte),
+                             scale_of<3>(v.scales, byte)};
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const float scale = scale_of(c.vs, 2 * u + x);
+        const float scale = vscale[2 * u + x];
 #pragma unroll
         for (int i = 0; i < NBK; ++i)
-          *reinterpret_cast<uint4*>(stage + (wr ^ (i << 4)) + x * 16 * RB) = expand(c.v[2 * u + x][i], scale);
+          *reinterpret_cast<uint4*>(stage + (wr ^ (i << 4)) + x * 16 * RB) = expand(v.c[2 * u + x][i], scale);
       }
+      if (u == 1 && more) fetch(vc, vs, nrow, v);
       // rows (2 u, 2 u + 1): a column has those of its copy, zeros elsewhere
       uint4 p[PP];
 #pragma unroll
@@ -299,7 +325,6 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_kv4(DecodeArgs a, int nb, i
       }
       __builtin_amdgcn_wave_barrier();
     }
-    c = next;
     row = nrow, begin = nbegin, end = nend, shift = nshift;
   }
   l += __shfl_xor(l, 16);
@@ -359,14 +384,14 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_kv4(DecodeArgs a, int nb, i
   }
 }
 
-size_t part_floats(const DecodeArgs& a) { return (size_t)a.B * a.Hq * pieces_of(a) * a.D; }
+template <typename T> size_t part_floats(const DecodeArgs& a) { return (size_t)a.B * a.Hq * pieces_of<T>(a) * a.D; }
 
 template <typename T, int NBK, int MODE, int COPIES> hipError_t decode(const DecodeArgs& a, float* ws, hipStream_t s) {
   constexpr int DP = 32 * NBK, lds = std::max(NW * 32 * 2 * DP, (2 * NW * COLS + NW * COLS * DP + (NW + 2) * COLS) * 4);
   const hipError_t e = lds_opt_in((const void*)k_attn_kv4<T, NBK, MODE, COPIES>, lds);
   if (e != hipSuccess) return e;
-  const int pieces = pieces_of(a), nb = kv4_blocks(a.D);
-  float* ml = ws + part_floats(a);
+  const int pieces = pieces_of<T>(a), nb = kv4_blocks(a.D);
+  float* ml = ws + part_floats<T>(a);
   k_attn_kv4<T, NBK, MODE, COPIES><<<dim3(pieces, a.Hkv * groups_of(a), a.B), 64 * NW, lds, s>>>(a, nb, pieces, ws, ml);
   const hipError_t e2 = hipGetLastError();
   if (e2 != hipSuccess || pieces == 1) return e2;
@@ -384,14 +409,16 @@ template <typename T, int NBK> hipError_t decode_mode(const DecodeArgs& a, float
 
 }  // namespace
 
-size_t attn_kv4_ws_bytes(const DecodeArgs& a) {
-  return (part_floats(a) + (size_t)a.B * a.Hq * pieces_of(a) * 2) * 4;
+template <typename T> size_t attn_kv4_ws_bytes(const DecodeArgs& a) {
+  return (part_floats<T>(a) + (size_t)a.B * a.Hq * pieces_of<T>(a) * 2) * 4;
 }
 
 template <typename T> hipError_t launch_attn_kv4(const DecodeArgs& a, float* ws, hipStream_t s) {
   return a.D <= 64 ? decode_mode<T, 2>(a, ws, s) : decode_mode<T, 4>(a, ws, s);
 }
 
+template size_t attn_kv4_ws_bytes<bf16>(const DecodeArgs&);
+template size_t attn_kv4_ws_bytes<float>(const DecodeArgs&);
 template hipError_t launch_attn_kv4<bf16>(const DecodeArgs&, float*, hipStream_t);
 template hipError_t launch_attn_kv4<float>(const DecodeArgs&, float*, hipStream_t);
 
