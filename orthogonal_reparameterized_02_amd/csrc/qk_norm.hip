@@ -10,6 +10,11 @@
 // of the rotary kernel (W elements of the first half with their partners, W
 // consecutive elements of pairs, or W elements that are not turned); its mean
 // takes n exchanges.
+//
+// Measured, 16384 tokens, 32 + 8 heads of 128, bf16: forward 67 us (336 MB, 5.0
+// TB/s, what a large copy reaches), backward 137 us (503 MB, 3.7 TB/s: three
+// streams and 104 to 158 registers a lane for the sums of dw, three or four
+// waves on a SIMD) and 8 us for the join of its rows; 211 us a training pass.
 #include <algorithm>
 #include <type_traits>
 
@@ -22,7 +27,10 @@ namespace {
 template <typename TS, int W> struct alignas(sizeof(TS) * W < 16 ? sizeof(TS) * W : 16) Pack { TS e[W]; };
 
 constexpr int NTH = 256;
-constexpr int MOST_ROWS = 2048;  // workgroups of the backward pass, each a row of partial sums
+// Workgroups of the backward pass at most, each a row of partial sums.  16384
+// tokens of 32 + 8 heads of 128, bf16, a training pass: 512 rows 251 us, 1024 230,
+// 2048 211, 4096 219 (the join takes longer than the balance wins).
+constexpr int MOST_ROWS = 2048;
 
 // How a head's units lie in its lanes
 struct Lanes {
@@ -49,17 +57,32 @@ template <typename TS, int W, bool PAIRS> struct Head {
   }
   static __device__ __forceinline__ bool has(int u, int p, const Lanes& l) { return u < (p ? l.turn : l.units); }
 
-  template <typename T> __device__ __forceinline__ void load(const T* x, int lane, const Lanes& l, int rot) {
+  // the elements as they are stored
+  template <typename T> struct Raw {
+    Pack<T, W> k[U][P];
+    __device__ __forceinline__ void load(const T* x, int lane, const Lanes& l, int rot) {
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          const int u = lane + (i << l.lg);
+          k[i][p] = {};
+          if (has(u, p, l)) k[i][p] = *reinterpret_cast<const Pack<T, W>*>(x + at(u, p, l, rot));
+        }
+    }
+  };
+  template <typename T> __device__ __forceinline__ void set(const Raw<T>& r) {
 #pragma unroll
     for (int i = 0; i < U; ++i)
 #pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const int u = lane + (i << l.lg);
-        Pack<T, W> k = {};
-        if (has(u, p, l)) k = *reinterpret_cast<const Pack<T, W>*>(x + at(u, p, l, rot));
+      for (int p = 0; p < P; ++p)
 #pragma unroll
-        for (int e = 0; e < W; ++e) v[i][p][e] = St<T>::ld(&k.e[e]);
-      }
+        for (int e = 0; e < W; ++e) v[i][p][e] = St<T>::ld(&r.k[i][p].e[e]);
+  }
+  template <typename T> __device__ __forceinline__ void load(const T* x, int lane, const Lanes& l, int rot) {
+    Raw<T> r;
+    r.load(x, lane, l, rot);
+    set(r);
   }
   __device__ __forceinline__ void store(TS* y, int lane, const Lanes& l, int rot) const {
 #pragma unroll
@@ -155,17 +178,18 @@ __global__ __launch_bounds__(NTH) void k_qk_norm_fwd(QkNormArgs a, Lanes l, int 
   }
 }
 
-// A group goes through every (tokens, heads of one tensor) chunk that is its
-// own in turn; the sum of dw over them stays in its registers.  The first
-// rows_q workgroups take the queries.
-template <typename TS, int W, bool PAIRS, int HPG>
-__global__ __launch_bounds__(NTH) void k_qk_norm_bwd(QkNormArgs a, Lanes l, int rows_q, int rows_k, float* part) {
+// A group takes `run` heads of one token, whose weights and angles it loads once,
+// while the next head is on its way; then the next such run that is its own.
+// The sum of dw stays in its registers.  The first rows_q workgroups take the
+// queries.
+template <typename TS, int W, bool PAIRS>
+__global__ __launch_bounds__(NTH) void k_qk_norm_bwd(QkNormArgs a, Lanes l, int rows_q, int rows_k, int run, float* part) {
   using H = Head<TS, W, PAIRS>;
   __shared__ float red[NTH * 16];
   const int lane = threadIdx.x & ((1 << l.lg) - 1), group = threadIdx.x >> l.lg, groups = NTH >> l.lg;
   const bool isq = (int)blockIdx.x < rows_q;
   const int row = isq ? blockIdx.x : blockIdx.x - rows_q, rows = isq ? rows_q : rows_k;
-  const int heads = isq ? a.Hq : a.Hk, chunks = (heads + HPG - 1) / HPG;
+  const int heads = isq ? a.Hq : a.Hk, chunks = (heads + run - 1) / run;
   const TS* x0 = isq ? (const TS*)a.q : (const TS*)a.k;
   const TS* g0 = isq ? (const TS*)a.gq : (const TS*)a.gk;
   TS* d0 = isq ? (TS*)a.dq : (TS*)a.dk;
@@ -178,34 +202,36 @@ __global__ __launch_bounds__(NTH) void k_qk_norm_bwd(QkNormArgs a, Lanes l, int 
   const long step = (long)rows * groups, items = (long)a.T * chunks;
   for (long it = (long)row * groups + group; it < items; it += step) {
     const long t = it / chunks;
-    const int h0 = (int)(it - t * chunks) * HPG, n = min(HPG, heads - h0);
-    H xs[HPG], gs[HPG];
-#pragma unroll
-    for (int i = 0; i < HPG; ++i)
-      if (i < n) {
-        xs[i].load(x0 + t * ldx + (long)(h0 + i) * a.D, lane, l, a.rot);
-        gs[i].load(g0 + t * ldg + (long)(h0 + i) * a.D, lane, l, a.rot);
-      }
+    const int h0 = (int)(it - t * chunks) * run, h1 = min(h0 + run, heads);
+    const TS *xp = x0 + t * ldx, *gp = g0 + t * ldg;
+    TS* dp = d0 + t * ldd;
+    typename H::template Raw<TS> rx, rg;
+    rx.load(xp + (long)h0 * a.D, lane, l, a.rot);
+    rg.load(gp + (long)h0 * a.D, lane, l, a.rot);
     Angles<TS, W, PAIRS> ang;
     ang.load(a, t, lane, l);
-#pragma unroll
-    for (int i = 0; i < HPG; ++i) {
-      if (i >= n) break;
+    for (int h = h0; h < h1; ++h) {
+      H x, g;
+      x.set(rx);
+      g.set(rg);
+      if (h + 1 < h1) {
+        rx.load(xp + (long)(h + 1) * a.D, lane, l, a.rot);
+        rg.load(gp + (long)(h + 1) * a.D, lane, l, a.rot);
+      }
       float ss = 0.0f, un = 0.0f;
-      ang.template turn<true>(gs[i], lane, l);
+      ang.template turn<true>(g, lane, l);
       H::each([&](int j, int p, int e) {
-        const float x = xs[i].v[j][p][e];
-        ss = fmaf(x, x, ss);
-        un = fmaf(gs[i].v[j][p][e] * w.v[j][p][e], x, un);
+        ss = fmaf(x.v[j][p][e], x.v[j][p][e], ss);
+        un = fmaf(g.v[j][p][e] * w.v[j][p][e], x.v[j][p][e], un);
       });
       const float r = rsqrtf(fmaf(group_sum(ss, l.lg), a.inv_d, a.eps));
       const float m = group_sum(un, l.lg) * r * a.inv_d;  // mean of u n
       H::each([&](int j, int p, int e) {
-        const float nrm = xs[i].v[j][p][e] * r, g = gs[i].v[j][p][e];
-        dw.v[j][p][e] = fmaf(g, nrm, dw.v[j][p][e]);
-        xs[i].v[j][p][e] = r * fmaf(-nrm, m, g * w.v[j][p][e]);
+        const float nrm = x.v[j][p][e] * r, gv = g.v[j][p][e];
+        dw.v[j][p][e] = fmaf(gv, nrm, dw.v[j][p][e]);
+        x.v[j][p][e] = r * fmaf(-nrm, m, gv * w.v[j][p][e]);
       });
-      xs[i].store(d0 + t * ldd + (long)(h0 + i) * a.D, lane, l, a.rot);
+      x.store(dp + (long)h * a.D, lane, l, a.rot);
     }
   }
   if (!(isq ? a.dwq : a.dwk)) return;
@@ -227,42 +253,55 @@ __global__ __launch_bounds__(NTH) void k_qk_norm_bwd(QkNormArgs a, Lanes l, int 
   }
 }
 
-// dw[d] = sum of the rows: 64 columns a workgroup, sixteen waves that take
-// every sixteenth row and join in wave order
+// dw[d] = sum of the rows: 64 columns a workgroup, four rows a wave's load, sixteen
+// waves; a thread's rows, then four lanes, then the waves in order
 constexpr int JW = 16;
 __global__ __launch_bounds__(64 * JW) void k_qk_norm_join(int D, int rows_q, int rows_k, const float* part,
                                                           float* dwq, float* dwk) {
-  __shared__ float red[JW][64];
-  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, d = blockIdx.x * 64 + lane;
+  __shared__ float4 red[JW][16];
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, d = blockIdx.x * 64 + 4 * (lane & 15);
   float* out = blockIdx.y ? dwk : dwq;
   if (!out) return;
-  const float* p = part + (blockIdx.y ? (long)rows_q * D : 0) + min(d, D - 1);
+  const float* p = part + (blockIdx.y ? (long)rows_q * D : 0) + min(d, D - 4);
   const int rows = blockIdx.y ? rows_k : rows_q;
-  float s = 0.0f;
+  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
-  for (int r = wave; r < rows; r += JW) s += p[(long)r * D];
-  red[wave][lane] = s;
+  for (int r = 4 * wave + (lane >> 4); r < rows; r += 4 * JW) {
+    const float4 x = *reinterpret_cast<const float4*>(p + (long)r * D);
+    s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
+  }
+#pragma unroll
+  for (int m = 16; m < 64; m <<= 1) {
+    s.x += __shfl_xor(s.x, m);
+    s.y += __shfl_xor(s.y, m);
+    s.z += __shfl_xor(s.z, m);
+    s.w += __shfl_xor(s.w, m);
+  }
+  if (lane < 16) red[wave][lane] = s;
   __syncthreads();
-  if (wave == 0 && d < D) {
+  if (threadIdx.x < 64 && blockIdx.x * 64 + threadIdx.x < D) {
     float t = 0.0f;
 #pragma unroll
-    for (int w = 0; w < JW; ++w) t += red[w][lane];
-    out[d] = t;
+    for (int w = 0; w < JW; ++w) t += reinterpret_cast<const float*>(red[w])[threadIdx.x];
+    out[blockIdx.x * 64 + threadIdx.x] = t;
   }
 }
 
 struct Rows { int q, k; };
-// rows of partial sums for the queries and for the keys: as their work, at
-// least one each
+// Rows of partial sums for the queries and for the keys: as their work, at
+// least one each, and 32 heads a row (as many as a workgroup holds at a time if
+// they have 128 bf16; 1000 tokens of 40 heads: 2048 rows 31 us, 1024 27 us).
 Rows rows_of(const QkNormArgs& a) {
-  const long most = std::min((long)MOST_ROWS, ((long)a.T * (a.Hq + a.Hk) + 7) / 8);
+  const long most = std::min((long)MOST_ROWS, ((long)a.T * (a.Hq + a.Hk) + 31) / 32);
   Rows r;
   r.q = (int)std::max(1L, most * a.Hq / (a.Hq + a.Hk));
   r.k = a.Hk ? (int)std::max(1L, most * a.Hk / (a.Hq + a.Hk)) : 0;
   return r;
 }
 
-constexpr int HPG_F = 4, HPG_B = 2;
+// Heads of one token a group takes, one after another with the next on its way:
+// the weights and angles are loaded once for them.
+constexpr int HPG_F = 4;
 
 template <typename TS, int W, bool PAIRS> hipError_t norm_fwd(const QkNormArgs& a, const Lanes& l, hipStream_t s) {
   const int cq = (a.Hq + HPG_F - 1) / HPG_F, per_token = cq + (a.Hk + HPG_F - 1) / HPG_F;
@@ -284,7 +323,10 @@ template <typename TS, int W, bool PAIRS> hipError_t norm_fwd(const QkNormArgs& 
 
 template <typename TS, int W, bool PAIRS> hipError_t norm_bwd(const QkNormArgs& a, const Lanes& l, float* ws, hipStream_t s) {
   const Rows r = rows_of(a);
-  k_qk_norm_bwd<TS, W, PAIRS, HPG_B><<<dim3(r.q + r.k), NTH, 0, s>>>(a, l, r.q, r.k, ws);
+  // as many heads as a group has to take anyway
+  const long groups = (long)(r.q + r.k) * (NTH >> l.lg), all = (long)a.T * (a.Hq + a.Hk);
+  const int run = (int)std::max(1L, std::min((all + groups - 1) / groups, (long)std::max(a.Hq, a.Hk)));
+  k_qk_norm_bwd<TS, W, PAIRS><<<dim3(r.q + r.k), NTH, 0, s>>>(a, l, r.q, r.k, run, ws);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || (!a.dwq && !a.dwk)) return e;
   k_qk_norm_join<<<dim3((a.D + 63) / 64, 2), 64 * JW, 0, s>>>(a.D, r.q, r.k, ws, a.dwq, a.dwk);
