@@ -20,6 +20,9 @@
 // they form, at the power limit; in 9 documents 320 us, a fifth of the wave
 // slots empty as in the forward pass.  float32, D 64, two documents of 1024,
 // 16 heads on 4, capped: 225 us, a third of the float32 matrix rate.
+// With a window (8192 tokens in 3 documents, window 1024, 4 sinks) 185 us for dq,
+// 270 to 285 for dk, dv and 38 for the sinks, 0.56 PFLOP/s of the products that are
+// seen; a tenth more are formed at the edges of the window, and the loops are short.
 #include <algorithm>
 
 #include "attn_rows.h"
@@ -203,12 +206,12 @@ __global__ __launch_bounds__(64 * NW, (DqCfg<T, DP>::OCC)) void k_attn_dq(AttnAr
         if constexpr (MODE & 1) s[i] *= deriv;
       }
       if (far || sp.all_lo > jn || sp.all_hi < jn + 32) {  // some pair is hidden
-        Seen seen = {lo, sink.x, (uint32_t)(hi - lo), (uint32_t)(sink.y - sink.x)};
+        Seen seen = {jl - lo, jl - sink.x, (uint32_t)(hi - lo), (uint32_t)(sink.y - sink.x)};
         if constexpr (SINK)
-          if (far) seen = {sink.x, 0, sink.x == kt.flo ? (uint32_t)(sink.y - sink.x) : 0, 0};
+          if (far) seen = {jl - sink.x, 0, sink.x == kt.flo ? (uint32_t)(sink.y - sink.x) : 0, 0};
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const int j = jl + 8 * (i / 4) + i % 4;
+          const int j = 8 * (i / 4) + i % 4;
           s[i] = (SINK ? seen.either(j) : seen(j)) ? s[i] : 0.0f;
         }
       }
@@ -266,9 +269,8 @@ __global__ __launch_bounds__(64 * NW, (DqCfg<T, DP>::OCC)) void k_attn_dq(AttnAr
 //
 // Bound by reading q and dout once more, from the last-level cache where they
 // fit.  Measured (8192 tokens in 3 documents, window 1024, 4 sinks, 32 heads on
-// 8, D 128, bf16): SINKUS us; as a part of k_attn_dq, whose registers it fills,
-// 52 us.
-// On 16 x 16 tiles: of 32 columns four sinks leave 28 idle, and the sums would
+// 8, D 128, bf16): 33 us and 5 for the join; as a part of k_attn_dq, whose
+// registers it fills, 52 us.  On 16 x 16 tiles: of 32 columns four sinks leave 28 idle, and the sums would
 // take 128 registers (57 spilled, 50 us).
 template <typename T, int DP> struct SinkCfg {
   using L = Tile<T, DP>;

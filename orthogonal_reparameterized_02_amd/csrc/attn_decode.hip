@@ -18,6 +18,7 @@
 // 233 us = 6.1 TB/s (a copy of 1 GiB moves 5.0, reading alone 6.5); one
 // sequence of up to 1024 rows 13 us, two launches.  float32 with a group of 4
 // is bound by its products (one column in eight is used): 220 MB in 61 us.
+// 64 sequences on rings, window 4096 with 4 sinks: 183 us = 5.8 TB/s.
 #include <algorithm>
 
 #include "attn_tile.h"

@@ -22,6 +22,12 @@
 // values go through LDS, 32 rows of t and t + 1 at a time, and come back down their
 // columns by ds_read_b64_tr_b16 in just that order of rows; 16-byte chunk c of
 // row r lies at c ^ key(r), which spreads both accesses over the banks.
+//
+// Measured (bf16, 32 heads on 8, D 128): 16 sequences of 8000 to 32768 rows 82 us
+// with the join, 4.6 TB/s, 5.8 to 6.3 where all are equally long (the bf16 cache
+// 233 us); bound by the read, and by the longest sequences' pieces at the end.  One
+// sequence of up to 1024 rows 13.5 us, two launches.
+//
 //   bf16 queries have probabilities in two bf16 parts, float32 ones both
 // queries and probabilities in three: every product is exact, sums are float32.
 #include <algorithm>

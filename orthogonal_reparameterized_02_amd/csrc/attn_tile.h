@@ -455,12 +455,13 @@ struct KeyTiles {
   }
 };
 
-// The keys that a lane's query sees in a tile: interval a, and with sinks b
+// The keys that a lane's query sees in a tile: interval a, and with sinks b,
+// from where they begin up to the lane's first key, with their widths
 struct Seen {
-  int alo, blo;
+  int a, b;
   uint32_t aw, bw;
-  __device__ __forceinline__ bool operator()(int j) const { return (uint32_t)(j - alo) < aw; }
-  __device__ __forceinline__ bool either(int j) const { return (uint32_t)(j - alo) < aw || (uint32_t)(j - blo) < bw; }
+  __device__ __forceinline__ bool operator()(int j) const { return (uint32_t)(a + j) < aw; }
+  __device__ __forceinline__ bool either(int j) const { return (uint32_t)(a + j) < aw || (uint32_t)(b + j) < bw; }
 };
 
 }  // namespace poetx
