@@ -6,7 +6,9 @@ attention-block operators (include/poetx.h) with autograd and their workspaces;
 `POETXAttention` puts them between four `POETXLinear` projections: packed
 documents for training, single tokens over a cache for serving.  PyTorch supplies device memory,
 streams and autograd only.  The gradients have no gradients of their own:
-differentiating them raises.
+differentiating them raises.  Capture a backward pass into a graph only where
+no eager autograd graph of the same parameters is alive: PyTorch's accumulation
+then waits across streams, which a capture does not survive.
 """
 from __future__ import annotations
 
@@ -344,6 +346,8 @@ class KVCache:
 
     def tokens(self, b: int) -> int:
         """Tokens of sequence b (also those that a ring no longer holds)."""
+        if self._captured():  # a replay would take the count of now
+            raise RuntimeError("the tokens of a sequence are not known while a graph is captured")
         return int(self.length[b]) if self._filled is None else self._filled[b] + self._appended
 
     def held(self, b: int):

@@ -128,13 +128,17 @@ struct AttnArgs {
 
 // The sinks of a document are seen past the window where some query stands
 // further than the window from some key.  Their gradients are then summed
-// apart (attn_bwd.hip): such a document takes the next of these numbers, for
-// two of them begin more than a window apart, among the queries or the keys.
+// apart (attn_bwd.hip).  Each such document has a number that grows from one to
+// the next: its index, or, where there are fewer of those, its place in windows: two
+// of them begin more than a window apart, among the queries or the keys.
 __host__ __device__ inline bool sinks_apart(int lq, int lk, int causal, int window) {
   return lk > window || (!causal && lq > window);
 }
-__host__ __device__ inline long sink_number(int q0, int k0, int window) {
+__host__ __device__ inline long sink_place(int q0, int k0, int window) {
   return q0 / ((long)window + 1) + k0 / ((long)window + 1);
+}
+__host__ __device__ inline long sink_number(const AttnArgs& a, int d, int q0, int k0) {
+  return a.ndoc <= sink_place(a.Tq, a.Tk, a.window) ? d : sink_place(q0, k0, a.window);
 }
 
 // (api.hip) LDS above 64 KB for a kernel on the current device

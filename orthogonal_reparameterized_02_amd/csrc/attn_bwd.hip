@@ -270,8 +270,8 @@ __global__ __launch_bounds__(64 * NW, (DqCfg<T, DP>::OCC)) void k_attn_dq(AttnAr
 // Bound by reading q and dout once more, from the last-level cache where they
 // fit.  Measured (8192 tokens in 3 documents, window 1024, 4 sinks, 32 heads on
 // 8, D 128, bf16): 33 us and 5 for the join; as a part of k_attn_dq, whose
-// registers it fills, 52 us.  On 16 x 16 tiles: of 32 columns four sinks leave 28 idle, and the sums would
-// take 128 registers (57 spilled, 50 us).
+// registers it fills, 52 us.  On 16 x 16 tiles: of 32 columns four sinks leave
+// 28 idle, and the sums would take 128 registers (57 spilled, 50 us).
 template <typename T, int DP> struct SinkCfg {
   using L = Tile<T, DP>;
   static constexpr int NS = 16;                      // sinks a block
@@ -354,7 +354,7 @@ __global__ __launch_bounds__(64 * NW, (SinkCfg<T, DP>::OCC)) void k_attn_sink(At
     if (dq0 >= q0 + rows) break;
     if (dq1 <= q0 || dq0 >= dq1 || !sinks_apart(dq1 - dq0, dk1 - dk0, a.causal, a.window)) continue;
     const int ns = min(a.sinks, dk1 - dk0), off = dq1 - dk1;
-    float* out = a.sink_part + ((tile + sink_number(dq0, dk0, a.window)) * a.Hkv + hk) * 2 * a.sinks * a.D;
+    float* out = a.sink_part + ((tile + sink_number(a, d, dq0, dk0)) * a.Hkv + hk) * 2 * a.sinks * a.D;
     for (int b = 0; b < ns; b += NS) {
       // queries that see this lane's key
       const int key = b + (lane & 15), t = dk0 + key;
@@ -469,9 +469,8 @@ __global__ __launch_bounds__(64 * NW, (SinkCfg<T, DP>::OCC)) void k_attn_sink(At
 }
 
 // dk and dv of the sinks: what k_attn_sink left, over the tiles of a document.  A
-// workgroup a sink and key head; sixteen waves
-// take every sixteenth partial sum and join in wave order.  The second pass has
-// left zeros in these rows.
+// workgroup a sink and key head; sixteen waves take every sixteenth partial sum
+// and join in wave order.  The second pass has left zeros in these rows.
 constexpr int SW = 16;
 template <typename T> __global__ __launch_bounds__(64 * SW) void k_attn_sink_join(AttnArgs a) {
   __shared__ float2 red[SW][2][64];
@@ -480,7 +479,7 @@ template <typename T> __global__ __launch_bounds__(64 * SW) void k_attn_sink_joi
   const int q0 = e.x, q1 = e.y, k0 = e.z, k1 = e.w;
   if (s >= k1 - k0 || !sinks_apart(q1 - q0, k1 - k0, a.causal, a.window)) return;
   const int t0 = q0 / BM, tiles = q1 > q0 ? (q1 - 1) / BM - t0 + 1 : 0;
-  const long slot = t0 + sink_number(q0, k0, a.window), plane = (long)a.sinks * a.D;
+  const long slot = t0 + sink_number(a, d, q0, k0), plane = (long)a.sinks * a.D;
   float2 x[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
   if (2 * lane < a.D) {
 #pragma unroll 4
@@ -845,7 +844,7 @@ template <typename T> size_t attn_bwd_part_bytes(const AttnArgs& a) {
 // a slot for every query tile of every document whose sinks are summed apart:
 // tile + sink_number grows from one to the next
 size_t attn_sink_part_bytes(const AttnArgs& a) {
-  const size_t slots = attn_tiles(a.Tq) + sink_number(a.Tq, a.Tk, a.window) + 1;
+  const size_t slots = attn_tiles(a.Tq) + std::min((long)a.ndoc, sink_place(a.Tq, a.Tk, a.window)) + 1;
   return a.sinks ? slots * a.Hkv * 2 * a.sinks * a.D * 4 : 0;
 }
 

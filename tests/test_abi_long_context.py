@@ -244,3 +244,13 @@ def test_kv4_binding_refusals():
         P.poetx_kv4_write(k, k, None, n, *good)
     with pytest.raises(ValueError, match="GPU tensor"):
         P.poetx_attn_kv4_decode(P.kv4_decode_shape(q, good[0]), P.window(0), q, *good, n, q, None)
+
+
+def test_workspace_of_a_short_window():
+    """Partial sums of sinks: a slot a query tile and document, however short
+    the window is."""
+    L, w = _lib.lib(), P.window(1, 128)
+    sh = attn_shape(Tq=8192, Tk=8192, ndoc=1)
+    plain = L.poetx_attn_window_workspace_bytes(C.byref(sh), C.byref(P.window(1, 0)), 1)
+    slots = 8192 // 128 + 1 + 1  # query tiles, documents, one behind
+    assert L.poetx_attn_window_workspace_bytes(C.byref(sh), C.byref(w), 1) <= plain + slots * sh.Hkv * 2 * 128 * sh.D * 4 + 256

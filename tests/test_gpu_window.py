@@ -240,3 +240,24 @@ def test_many_short_documents():
     st = dict(q=normal(rng, (T, 1, 64), "f32"), k=normal(rng, (T, 1, 64), "f32"), v=normal(rng, (T, 1, 64), "f32"),
               dout=normal(rng, (T, 1, 64), "f32"), cu_q=cu, cu_k=cu, window=2, sinks=1, slopes=None, causal=True, cap=0.0, ndoc=1500)
     compare(st, run(st), "f32")
+
+
+def test_few_documents_among_many_have_sinks_apart():
+    """Partial sums are numbered by documents, or by windows where those are
+    fewer: here 202 documents, of which two pass the window."""
+    lens = [3] * 100 + [400] + [1] * 60 + [350] + [2] * 40
+    compare_lens(lens, 300, 3)
+
+
+def test_a_short_window_under_one_document():
+    compare_lens([700], 1, 20)
+
+
+def compare_lens(lens, window, sinks):
+    rng = np.random.default_rng(window)
+    cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    T = int(cu[-1])
+    st = dict(q=normal(rng, (T, 2, 64), "bf16"), k=normal(rng, (T, 1, 64), "bf16"), v=normal(rng, (T, 1, 64), "bf16"),
+              dout=normal(rng, (T, 2, 64), "bf16"), cu_q=cu, cu_k=cu, window=window, sinks=sinks, slopes=None, causal=True,
+              cap=0.0, ndoc=len(lens))
+    compare(st, run(st), "bf16")

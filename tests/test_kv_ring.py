@@ -71,3 +71,15 @@ def test_plan_refusals():
         AttentionPlan(cu, 4, prefix=cu[:1], window=2)
     with pytest.raises(ValueError, match="sinks"):
         AttentionPlan(cu, 4, sinks=2)
+
+
+def test_counts_are_refused_while_a_graph_is_captured(monkeypatch):
+    """A replay would take the count of now: nothing that reads one on the host
+    is captured, and the cache stays as it was."""
+    cache = ring()
+    cache.fill(0, tokens(5), tokens(5))
+    monkeypatch.setattr(cache, "_captured", lambda: True)
+    for call in (lambda: cache.tokens(0), lambda: cache.held(0), lambda: cache.extend(0, tokens(1), tokens(1))):
+        with pytest.raises(RuntimeError, match="captured"):
+            call()
+    assert cache.length.tolist() == [5, 0]
