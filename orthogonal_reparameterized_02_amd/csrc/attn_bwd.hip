@@ -13,7 +13,10 @@
 // of the result itself makes 1.7e-3, that of ds as much again, delta 1.1e-3.
 // ds in two bf16 parts would leave 1.9e-3 (with a bias 2.3e-3), for two products
 // more beside seven: a training pass of 9 documents 414 -> 462 us, of one 2235
-// -> 2591 us.
+// -> 2591 us.  With a window (below) dq is off by 2.5e-3 and dk by 2.4e-3; dq from
+// two parts by 1.8e-3, for 644 -> 683 us, and dk, dv has no registers for them.
+// Rows of a few keys, where dp and delta are alike, 3e-3, and 4e-3 where
+// documents have four of them: delta's share, of o as it is stored.
 //
 // Measured (bf16, D 128, 32 heads on 8): 8192 causal tokens in one document
 // 1.75 ms for both passes, dq at 1.19 and dk, dv at 1.06 PFLOP/s of the products
