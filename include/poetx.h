@@ -620,7 +620,7 @@ int32_t poetx_attn_window_decode(const poetx_decode_shape* sh, const poetx_windo
  *   lies in row p.  Tokens of one call must have rows of their own.
  * poetx_kv4_read gives back the values at such places (NaN where the cache has
  * none; in a ring, what the position's row holds now).
- *   T Hkv < 2^27; ldk, ldv: pitches of k and v.
+ *   T Hkv < 2^27, T rounded up to a multiple of 16; ldk, ldv: pitches of k and v.
  * Errors: ERR_ARG, ERR_DEVICE.
  */
 typedef struct {

@@ -637,7 +637,7 @@ int32_t check_kv4(const char* fn, const poetx_kv4_shape* sh) {
   if (sh->sinks < 0 || sh->sinks > SINKS_MAX) return fail(POETX_ERR_ARG, "%s: sinks=%d outside 0..%d", fn, sh->sinks, SINKS_MAX);
   if (sh->ring && sh->rows <= sh->sinks) return fail(POETX_ERR_ARG, "%s: rows=%d of a ring with sinks=%d", fn, sh->rows, sh->sinks);
   // a workgroup of 256 threads for 16 tokens of a head and more: 2^32 - 1 threads at most
-  if ((int64_t)sh->T * sh->Hkv >= (int64_t)1 << 27)
+  if (((int64_t)sh->T + 15) / 16 * 16 * sh->Hkv >= (int64_t)1 << 27)
     return fail(POETX_ERR_ARG, "%s: T=%d tokens of Hkv=%d heads: 2^27 or more", fn, sh->T, sh->Hkv);
   TRY(check_ld(fn, "ldk", sh->ldk, (int64_t)sh->Hkv * sh->D));
   TRY(check_ld(fn, "ldv", sh->ldv, (int64_t)sh->Hkv * sh->D));

@@ -254,3 +254,12 @@ def test_workspace_of_a_short_window():
     plain = L.poetx_attn_window_workspace_bytes(C.byref(sh), C.byref(P.window(1, 0)), 1)
     slots = 8192 // 128 + 1 + 1  # query tiles, documents, one behind
     assert L.poetx_attn_window_workspace_bytes(C.byref(sh), C.byref(w), 1) <= plain + slots * sh.Hkv * 2 * 128 * sh.D * 4 + 256
+
+
+@pytest.mark.parametrize("read", [False, True])
+@pytest.mark.parametrize("T,Hkv", [(2 ** 27 - 1, 1), (2 ** 24 - 15, 8)])
+def test_a_grid_of_all_of_two_to_the_32_threads_is_refused(T, Hkv, read):
+    """A workgroup takes 16 tokens of 128 elements: the last one counts whole."""
+    sh = kv4_shape(T=T, Hkv=Hkv, D=128, ldk=128 * Hkv, ldv=128 * Hkv)
+    assert T * Hkv < 2 ** 27 and kv4(sh, read) == 1
+    assert "2^27" in _lib.lib().poetx_last_error().decode()
