@@ -13,6 +13,7 @@ then waits across streams, which a capture does not survive.
 from __future__ import annotations
 
 import math
+import operator
 from typing import Optional, Sequence
 
 import torch
@@ -344,8 +345,16 @@ class KVCache:
             return max(self.length.tolist(), default=0)
         return self._most + self._appended
 
+    def _sequence(self, b: int) -> int:
+        """b counted from the front: below 0 it counts from the end."""
+        b = operator.index(b)
+        if not -self.B <= b < self.B:
+            raise IndexError(f"sequence {b} of a cache of {self.B}")
+        return b % self.B
+
     def tokens(self, b: int) -> int:
         """Tokens of sequence b (also those that a ring no longer holds)."""
+        b = self._sequence(b)
         if self._captured():  # a replay would take the count of now
             raise RuntimeError("the tokens of a sequence are not known while a graph is captured")
         return int(self.length[b]) if self._filled is None else self._filled[b] + self._appended
@@ -353,7 +362,7 @@ class KVCache:
     def held(self, b: int):
         """k, v [n][Hkv][D] of sequence b: every token in order, or of a ring
         the sinks and the newest ones."""
-        return self._read(b, self._held(self.tokens(b)))
+        return self._read(self._sequence(b), self._held(self.tokens(b)))
 
     def _held(self, n: int, at: int = 0):
         """The positions from `at` on that n tokens leave in the cache, as
@@ -371,7 +380,7 @@ class KVCache:
         self._put(b, self.tokens(b), k, v)
 
     def _put(self, b: int, at: int, k: torch.Tensor, v: torch.Tensor) -> None:
-        n = at + k.shape[0]
+        b, n = self._sequence(b), at + k.shape[0]
         if not self.ring and n > self.rows:
             raise ValueError(f"{n} tokens do not fit a cache of {self.rows} rows")
         if k.shape[0]:
