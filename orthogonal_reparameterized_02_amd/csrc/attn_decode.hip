@@ -142,10 +142,11 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 4 && DP == 128 ? 1 : 2) void 
     for (int ks = 0; ks < L::KS; ++ks) sc = mma16((const T*)nullptr, L::row_frag(smem, kr, 0, ks), qf[ks], sc);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     const int jn = min(j0 + GRAIN, p1);  // a load past the piece has no rows: zeros
-    const int jl = pos + 4 * (lane >> 5), jend = pos + (end - row);
+    // counted from the tile's first row: a position behind the query may pass 2^31
+    const int jl = 4 * (lane >> 5), jend = end - row;
+    const float d0 = (float)(last - pos - jl);
     rows_at(jn, row, end, pos);
     lk.load(kp, a.ldk, row, end, ldsk);
-    const float d0 = (float)(last - jl);
     float top = -INFINITY, unused;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
