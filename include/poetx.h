@@ -571,7 +571,7 @@ int32_t poetx_attn_window_bwd(const poetx_attn_shape* sh, const poetx_window* wi
  *   q, o [B][Hq][D] (pitches ldq, ldo); row j of sequence b of the caches
  *   at b * bsk + j * ldk, b * bsv + j * ldv (offsets are 64-bit), heads of
  *   D values side by side; rows: cache capacity per sequence, at most
- *   2^31 - 2^16; B Hq below 2^24.
+ *   2^31 - 2^16; B Hkv ceil(Hq / Hkv / 32) below 2^24.
  *   ws poetx_attn_decode_workspace_bytes(sh) bytes.
  * Errors: ERR_ARG, ERR_WORKSPACE, ERR_DEVICE.
  */
@@ -593,6 +593,7 @@ int32_t poetx_attn_decode(const poetx_decode_shape* sh, const void* q, const voi
  *   ring != 0: the cache is a ring.  Positions below `sinks` lie in their rows,
  *   p >= sinks in row sinks + (p - sinks) mod (rows - sinks); len counts every
  *   token there has been and may pass rows.  1 <= window <= rows - sinks.
+ *   B Hq below 2^24.
  *   ws poetx_attn_window_decode_workspace_bytes(sh, win) bytes, for either.
  * Everything else as in poetx_attn_decode.
  */
@@ -634,7 +635,7 @@ int32_t poetx_kv4_read(const poetx_kv4_shape* sh, const int32_t* seq, const int3
 
 /*
  * poetx_attn_kv4_decode -- poetx_attn_decode (window = 0, with start) or
- * poetx_attn_window_decode (without) over such a cache.  The products of the
+ * poetx_attn_window_decode (without) over such a cache, B Hq below 2^24.  The products of the
  * held values are exact, sums float32 (bf16: p in two bf16 parts; float32: q and
  * p in three).  Of the shape ldk, ldv, bsk and bsv have to be valid and are not
  * used.

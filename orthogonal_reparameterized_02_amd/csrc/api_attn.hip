@@ -190,8 +190,10 @@ int32_t check_decode(const char* fn, const poetx_decode_shape* sh) {
     return fail(POETX_ERR_ARG, "%s: B=%d (0..%d) rows=%d (>= 0)", fn, sh->B, B_MAX, sh->rows);
   if (sh->rows > ROWS_MAX) return fail(POETX_ERR_ARG, "%s: rows=%d above %d", fn, sh->rows, ROWS_MAX);
   TRY(check_heads(fn, sh->Hq, sh->Hkv, sh->D));
-  // a workgroup of 256 threads a sequence and head, a dispatch 2^32 - 1 of them at most
-  if ((int64_t)sh->B * sh->Hq >= 1 << 24) return fail(POETX_ERR_ARG, "%s: B=%d sequences of Hq=%d heads: 2^24 or more", fn, sh->B, sh->Hq);
+  // a workgroup of 256 threads for 32 heads of a key head and sequence, a dispatch
+  // 2^32 - 1 of them at most (pieces, and their join, are of far fewer workgroups)
+  if ((int64_t)sh->B * sh->Hkv * ((sh->Hq / sh->Hkv + 31) / 32) >= 1 << 24)
+    return fail(POETX_ERR_ARG, "%s: B=%d sequences of Hq=%d heads on Hkv=%d: 2^24 workgroups or more", fn, sh->B, sh->Hq, sh->Hkv);
   TRY(check_act(fn, sh->act));
   TRY(check_scores(fn, sh->scale, sh->cap));
   const int64_t wq = (int64_t)sh->Hq * sh->D, wk = (int64_t)sh->Hkv * sh->D;
@@ -554,9 +556,11 @@ int32_t poetx_attn_window_bwd(const poetx_attn_shape* sh, const poetx_window* wi
 
 namespace {
 
-// the window of a decoding call; a ring holds one
+// the window of a decoding call; a ring holds one.  These calls take fewer
+// sequences and heads than the one without.
 int32_t check_decode_window(const char* fn, const poetx_decode_shape* sh, const poetx_window* win, int32_t ring) {
   TRY(check_decode(fn, sh));
+  if ((int64_t)sh->B * sh->Hq >= 1 << 24) return fail(POETX_ERR_ARG, "%s: B=%d sequences of Hq=%d heads: 2^24 or more", fn, sh->B, sh->Hq);
   TRY(check_window(fn, win));
   if (ring && win->window < 1) return fail(POETX_ERR_ARG, "%s: a ring needs a window", fn);
   if (ring && (int64_t)win->window + win->sinks > sh->rows)
@@ -576,7 +580,7 @@ size_t decode_ws(const DecodeArgs& a) { return a.B ? align_up(attn_decode_ws_byt
 int32_t decode_any(const char* fn, const poetx_decode_shape* sh, const poetx_window* win, int32_t ring, const void* q,
                    const void* k, const void* v, const int32_t* start, const int32_t* len, const float* slopes,
                    void* o, void* ws, size_t ws_bytes, poetx_stream_t stream) {
-  TRY(check_decode_window(fn, sh, win, ring));
+  TRY(win == &NO_WINDOW ? check_decode(fn, sh) : check_decode_window(fn, sh, win, ring));
   if (sh->B == 0) return ok();
   NEED_PTR(q);
   if (sh->rows) {
