@@ -345,6 +345,14 @@ def _turned_by(sh: QkNormShape, pos, table):
     return _vec(pos, "pos", torch.int32, sh.T), _vec(table, "table", torch.float32, table.numel())
 
 
+def _weights(D: int, **named) -> list:
+    """Pointers of weights or their gradients that all heads share (None: none)."""
+    for name, t in named.items():
+        if t is not None and t.numel() != D:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({D},)")
+    return [_vec(t, name, torch.float32, D, optional=True) for name, t in named.items()]
+
+
 def poetx_qk_norm_rope_fwd(q, k, wq, wk, pos, table, qo, ko, eps: float = 1e-6, interleaved: bool = False,
                            stream=None) -> None:
     """Norms of the heads of q [T][Hq][D] and k [T][Hk][D] (k, ko may be None)
@@ -352,6 +360,7 @@ def poetx_qk_norm_rope_fwd(q, k, wq, wk, pos, table, qo, ko, eps: float = 1e-6, 
     (table None: not turned)."""
     sh = qk_norm_shape(q, k, table, eps, interleaved)
     fq, fk = (sh.T, sh.Hq, sh.D), (sh.T, sh.Hk, sh.D)
+    wqp, wkp = _weights(sh.D, wq=wq, wk=wk)
     qp, sh.ldq = _rows(q, "q", fq, q.dtype)
     qop, sh.ldqo = _rows(qo, "qo", fq, q.dtype)
     kp = kop = None
@@ -359,8 +368,7 @@ def poetx_qk_norm_rope_fwd(q, k, wq, wk, pos, table, qo, ko, eps: float = 1e-6, 
         kp, sh.ldk = _rows(k, "k", fk, q.dtype)
         kop, sh.ldko = _rows(ko, "ko", fk, q.dtype)
     check("poetx_qk_norm_rope_fwd", lib().poetx_qk_norm_rope_fwd(
-        C.byref(sh), qp, kp, _vec(wq, "wq", torch.float32, sh.D, optional=True),
-        _vec(wk, "wk", torch.float32, sh.D, optional=True), *_turned_by(sh, pos, table), qop, kop, _stream(stream)))
+        C.byref(sh), qp, kp, wqp, wkp, *_turned_by(sh, pos, table), qop, kop, _stream(stream)))
 
 
 def poetx_qk_norm_rope_bwd(dqo, dko, q, k, wq, wk, pos, table, dq, dk, dwq, dwk, ws, eps: float = 1e-6,
@@ -369,6 +377,7 @@ def poetx_qk_norm_rope_bwd(dqo, dko, q, k, wq, wk, pos, table, dq, dk, dwq, dwk,
     float32 (None: not wanted)."""
     sh = qk_norm_shape(q, k, table, eps, interleaved)
     fq, fk = (sh.T, sh.Hq, sh.D), (sh.T, sh.Hk, sh.D)
+    wqp, wkp, dwqp, dwkp = _weights(sh.D, wq=wq, wk=wk, dwq=dwq, dwk=dwk)
     qp, sh.ldq = _rows(q, "q", fq, q.dtype)
     gqp, sh.ldqo = _rows(dqo, "dqo", fq, q.dtype)
     dqp, sh.lddq = _rows(dq, "dq", fq, q.dtype)
@@ -378,10 +387,8 @@ def poetx_qk_norm_rope_bwd(dqo, dko, q, k, wq, wk, pos, table, dq, dk, dwq, dwk,
         gkp, sh.ldko = _rows(dko, "dko", fk, q.dtype)
         dkp, sh.lddk = _rows(dk, "dk", fk, q.dtype)
     wp, wb = _ws(ws, poetx_qk_norm_rope_workspace_bytes(sh))
-    vec = lambda t, n: _vec(t, n, torch.float32, sh.D, optional=True)
     check("poetx_qk_norm_rope_bwd", lib().poetx_qk_norm_rope_bwd(
-        C.byref(sh), gqp, gkp, qp, kp, vec(wq, "wq"), vec(wk, "wk"), *_turned_by(sh, pos, table), dqp, dkp,
-        vec(dwq, "dwq"), vec(dwk, "dwk"), wp, wb, _stream(stream)))
+        C.byref(sh), gqp, gkp, qp, kp, wqp, wkp, *_turned_by(sh, pos, table), dqp, dkp, dwqp, dwkp, wp, wb, _stream(stream)))
 
 
 def poetx_dropout_fwd(x, residual, y, p: float, seed: int, offset: int = 0, offset_dev=None,
