@@ -441,6 +441,12 @@ class KVCache4(KVCache):
         P.poetx_kv4_read(torch.full_like(pos, b), pos, *self._cache, k, v, sinks=self.sinks, ring=self.ring)
         return k, v
 
+    def append(self, k: torch.Tensor, v: torch.Tensor) -> None:
+        # the kernel writes the tokens that there are: fewer would leave sequences without theirs
+        if k.shape[0] != self.B or v.shape[0] != self.B:
+            raise ValueError(f"tokens of {k.shape[0]} and {v.shape[0]} sequences for a cache of {self.B} sequences")
+        super().append(k, v)
+
     def _next(self, k, v) -> None:
         P.poetx_kv4_write(k, v, None, self.length, *self._cache, sinks=self.sinks, ring=self.ring)
 
