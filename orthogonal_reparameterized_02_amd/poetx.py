@@ -421,10 +421,16 @@ def attn_shape(q, k, v, ndoc: int, causal: bool = True, scale: float = 0.0,
                      wq, wq, wq, wk, wk)
 
 
+def _int32(n: int) -> int:
+    """n, or the 32-bit integer next to it (ctypes would take its low 32 bits):
+    positions have no more, so a window hides as much."""
+    return min(max(n, -2 ** 31), 2 ** 31 - 1)
+
+
 def window(window: int, sinks: int = 0) -> Window:
     """A window of `window` keys (0: none), the first `sinks` of a document
     visible past it."""
-    return Window(window, sinks)
+    return Window(_int32(window), _int32(sinks))
 
 
 def _named(name: str, win: Optional[Window]):
@@ -632,7 +638,7 @@ def _kv4_call(k, v, seq, pos, cache, sinks: int, ring: bool):
     T, D = k.shape[0], k.shape[2]
     kp, ldk = _rows(k, "k", (T, H, D), k.dtype)
     vp, ldv = _rows(v, "v", (T, H, D), k.dtype)
-    sh = Kv4Shape(T, B, rows, H, D, act_of(k.dtype), sinks, int(ring), ldk, ldv)
+    sh = Kv4Shape(T, B, rows, H, D, act_of(k.dtype), _int32(sinks), int(ring), ldk, ldv)
     return sh, kp, vp, _vec(seq, "seq", torch.int32, T, optional=True), _vec(pos, "pos", torch.int32, T), ptrs
 
 
