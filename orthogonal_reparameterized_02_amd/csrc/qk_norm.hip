@@ -300,8 +300,8 @@ Rows rows_of(const QkNormArgs& a) {
   return r;
 }
 
-// Heads of one token a group takes, one after another with the next on its way:
-// the weights and angles are loaded once for them.
+// Heads of one token that a group of the forward kernel loads together: the
+// weights and angles are loaded once for them.
 constexpr int HPG_F = 4;
 
 template <typename TS, int W, bool PAIRS> hipError_t norm_fwd(const QkNormArgs& a, const Lanes& l, hipStream_t s) {
