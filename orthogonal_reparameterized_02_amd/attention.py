@@ -261,11 +261,13 @@ def alibi_slopes(heads: int, device="cuda") -> torch.Tensor:
 # ---- single tokens over a cache -----------------------------------------------------------
 class KVCache:
     """Keys and values of B sequences, up to `rows` tokens each.  An idle slot
-    counts tokens like the others; fill it with none of them to empty it.
+    counts tokens like the others; fill it with none of them to empty it, before
+    it is full or at the end of a block's rotary table.
 
     With a window the cache is a ring: it keeps the first `sinks` tokens of a
     sequence and the rows - sinks (at least `window`) newest ones, and is never
-    full; its queries see the last `window` tokens and the sinks.
+    full (a block's rotary table still ends); its queries see the last `window`
+    tokens and the sinks.
 
     append refuses a full cache from a count on the host.  A replayed graph
     appends without the host: there a sequence without room keeps its rows and
@@ -488,7 +490,8 @@ class POETXAttention(torch.nn.Module):
     (self.plan makes one with the block's window), pos [T] int32 positions (of each token in its document; one outside the
     table gives NaN), at the place of the dropout mask (draw; by default the
     next one, which a recomputed pass could not find again).  prefill and
-    decode serve: no dropout, no gradients, and no token past the table."""
+    decode serve: no dropout, no gradients, and no token past the table's
+    `positions`, over a ring as over any cache."""
 
     def __init__(self, n: int, heads: int, kv_heads: int, b: int, k: int, head_dim: Optional[int] = None,
                  positions: int = 8192, rot: Optional[int] = None, base: float = 10000.0, scaling=None,
@@ -566,7 +569,7 @@ class POETXAttention(torch.nn.Module):
     def prefill(self, x: torch.Tensor, cache: KVCache, b: int = 0, follow: bool = False) -> torch.Tensor:
         """A prompt x [n tokens][n] of sequence b from position 0; fills its
         cache rows.  follow: a later part of one, behind the tokens that the
-        cache has of the sequence, which it reads from there."""
+        cache has of the sequence, all of which it reads from there."""
         T, at = x.shape[0], cache.tokens(b) if follow else 0
         self._check_cache(cache)
         self._check_positions(at + T)
@@ -597,7 +600,8 @@ class POETXAttention(torch.nn.Module):
     def decode(self, x: torch.Tensor, cache: KVCache) -> torch.Tensor:
         """The next token of every sequence, x [B][n].  In a captured graph a
         sequence without room for it, or without a position in the rotary
-        table, answers NaN."""
+        table, answers NaN (and so does a ring from then on: such a token's key
+        is NaN in it until the sequence is filled again)."""
         self._check_cache(cache)
         n = cache.longest()
         full = cache.length >= cache.rows if n is None and not cache.ring else None
