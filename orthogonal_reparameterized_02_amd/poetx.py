@@ -1,6 +1,6 @@
 """Python binding of libpoetx.so with the C ABI's names.
 
-Argument marshalling only: every tensor must already live on the GPU,
+Argument marshalling only: every tensor must already live on the current GPU,
 contiguous, in the storage type the call expects; the functions check that on
 the host (so no host pointer ever reaches a kernel), pass raw pointers and the
 current HIP stream, and raise PoetxError on a non-OK status.  No arithmetic of
@@ -27,13 +27,17 @@ def act_of(dtype: torch.dtype) -> int:
     raise ValueError(f"unsupported activation dtype {dtype}")
 
 
-def _stream(stream) -> int:
+def _stream(stream, t: torch.Tensor) -> int:
     """The hipStream_t of `stream`, or of the current stream of the current
     device (read directly: a torch.cuda.Stream object for it costs 3 us a
-    call, as much as a launch)."""
+    call, as much as a launch), which has to be that of t, the call's first
+    tensor."""
     if stream is not None:
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    device = torch._C._cuda_getDevice()
+    if t.get_device() != device:
+        raise ValueError(f"tensors on GPU {t.get_device()}, but the current one is {device} (torch.cuda.device sets it)")
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def _dev(t: Optional[torch.Tensor], name: str, dtype=None, numel=None, optional=False):
@@ -97,7 +101,7 @@ def poetx_cnp_fwd(theta: torch.Tensor, b: int, k: int, G: torch.Tensor,
     wp, wb = _ws(ws, need)
     check("poetx_cnp_fwd", lib().poetx_cnp_fwd(
         nblk, b, k, _dev(theta, "theta", torch.float32, nblk * tb), _dev(G, "G", None, nblk * b * b),
-        _dev(GT, "GT", G.dtype, nblk * b * b, optional=True), act, wp, wb, _stream(stream)))
+        _dev(GT, "GT", G.dtype, nblk * b * b, optional=True), act, wp, wb, _stream(stream, theta)))
 
 
 def poetx_cnp_fwd_noalloc(theta: torch.Tensor, b: int, k: int, G: torch.Tensor,
@@ -109,7 +113,7 @@ def poetx_cnp_fwd_noalloc(theta: torch.Tensor, b: int, k: int, G: torch.Tensor,
     tb = b * (b - 1) // 2
     check("poetx_cnp_fwd_noalloc", lib().poetx_cnp_fwd_noalloc(
         nblk, b, k, _dev(theta, "theta", torch.float32, nblk * tb), _dev(G, "G", None, nblk * b * b),
-        _dev(GT, "GT", G.dtype, nblk * b * b, optional=True), act, _stream(stream)))
+        _dev(GT, "GT", G.dtype, nblk * b * b, optional=True), act, _stream(stream, theta)))
 
 
 def poetx_cnp_bwd(theta: torch.Tensor, dG: torch.Tensor, b: int, k: int, dtheta: torch.Tensor,
@@ -125,7 +129,7 @@ def poetx_cnp_bwd(theta: torch.Tensor, dG: torch.Tensor, b: int, k: int, dtheta:
     check(name, getattr(lib(), name)(
         nblk, b, k, _dev(theta, "theta", torch.float32, nblk * tb),
         _dev(dG, "dG", torch.float32, nblk * b * b), _dev(dtheta, "dtheta", torch.float32, nblk * tb),
-        int(bool(accumulate)), prec, wp, wb, _stream(stream)))
+        int(bool(accumulate)), prec, wp, wb, _stream(stream, theta)))
 
 
 def poetx_fold_perm(W0: torch.Tensor, perm_R: torch.Tensor, perm_P: torch.Tensor,
@@ -139,7 +143,7 @@ def poetx_fold_perm(W0: torch.Tensor, perm_R: torch.Tensor, perm_P: torch.Tensor
         _dev(perm_P, "perm_P", torch.int32, n), _dev(W0f, "W0f", W0.dtype, m * n),
         _dev(W0fT, "W0fT", W0.dtype, m * n, optional=True),
         _dev(perm_R_inv, "perm_R_inv", torch.int32, m, optional=True),
-        _dev(perm_P_inv, "perm_P_inv", torch.int32, n, optional=True), _stream(stream)))
+        _dev(perm_P_inv, "perm_P_inv", torch.int32, n, optional=True), _stream(stream, W0)))
 
 
 def poetx_layer_fwd(sh: Shape, x, G_P, G_R, W0f, perm_P, perm_R_inv, y, saved, ws,
@@ -154,7 +158,7 @@ def poetx_layer_fwd(sh: Shape, x, G_P, G_R, W0f, perm_P, perm_R_inv, y, saved, w
         C.byref(sh), _dev(x, "x", dt, T * n), _dev(G_P, "G_P", dt, n * b),
         _dev(G_R, "G_R", dt, m * b), _dev(W0f, "W0f", dt, m * n),
         _dev(perm_P, "perm_P", torch.int32, n), _dev(perm_R_inv, "perm_R_inv", torch.int32, m),
-        _dev(y, "y", dt, T * m), _dev(saved, "saved"), wp, wb, _stream(stream)))
+        _dev(y, "y", dt, T * m), _dev(saved, "saved"), wp, wb, _stream(stream, x)))
 
 
 def poetx_layer_bwd(sh: Shape, dy, GT_P, GT_R, W0f, W0fT, perm_P_inv, perm_R, saved, dx, dG_P,
@@ -172,7 +176,7 @@ def poetx_layer_bwd(sh: Shape, dy, GT_P, GT_R, W0f, W0fT, perm_P_inv, perm_R, sa
         _dev(W0fT, "W0fT", dt, m * n, optional=True),
         _dev(perm_P_inv, "perm_P_inv", torch.int32, n), _dev(perm_R, "perm_R", torch.int32, m),
         _dev(saved, "saved"), _dev(dx, "dx", dt, T * n), _dev(dG_P, "dG_P", torch.float32, n * b),
-        _dev(dG_R, "dG_R", torch.float32, m * b), wp, wb, _stream(stream)))
+        _dev(dG_R, "dG_R", torch.float32, m * b), wp, wb, _stream(stream, dy)))
 
 
 def poetx_layer_fwd_xmem(sh: Shape, x, G_P, G_R, W0f, perm_P, perm_R_inv, y, saved, ws,
@@ -187,7 +191,7 @@ def poetx_layer_fwd_xmem(sh: Shape, x, G_P, G_R, W0f, perm_P, perm_R_inv, y, sav
         C.byref(sh), _dev(x, "x", dt, T * n), _dev(G_P, "G_P", dt, n * b),
         _dev(G_R, "G_R", dt, m * b), _dev(W0f, "W0f", dt, m * n),
         _dev(perm_P, "perm_P", torch.int32, n), _dev(perm_R_inv, "perm_R_inv", torch.int32, m),
-        _dev(y, "y", dt, T * m), _dev(saved, "saved"), wp, wb, _stream(stream)))
+        _dev(y, "y", dt, T * m), _dev(saved, "saved"), wp, wb, _stream(stream, x)))
 
 
 def poetx_layer_bwd_xmem(sh: Shape, dy, G_P, GT_P, GT_R, W0f, W0fT, perm_P_inv, perm_R, saved,
@@ -204,7 +208,7 @@ def poetx_layer_bwd_xmem(sh: Shape, dy, G_P, GT_P, GT_R, W0f, W0fT, perm_P_inv, 
         _dev(W0f, "W0f", dt, m * n), _dev(W0fT, "W0fT", dt, m * n, optional=True),
         _dev(perm_P_inv, "perm_P_inv", torch.int32, n), _dev(perm_R, "perm_R", torch.int32, m),
         _dev(saved, "saved"), _dev(dx, "dx", dt, T * n), _dev(dG_P, "dG_P", torch.float32, n * b),
-        _dev(dG_R, "dG_R", torch.float32, m * b), wp, wb, _stream(stream)))
+        _dev(dG_R, "dG_R", torch.float32, m * b), wp, wb, _stream(stream, dy)))
 
 
 def poetx_layer_fwd_q(sh: Shape, x, G_P, G_R, q_f, s_f, perm_P, perm_R_inv, y, saved, ws,
@@ -222,7 +226,7 @@ def poetx_layer_fwd_q(sh: Shape, x, G_P, G_R, q_f, s_f, perm_P, perm_R_inv, y, s
         _dev(G_R, "G_R", dt, m * b), _dev(q_f, "q_f", torch.int8, m * n),
         _dev(s_f, "s_f", torch.float32, m), _dev(perm_P, "perm_P", torch.int32, n),
         _dev(perm_R_inv, "perm_R_inv", torch.int32, m), _dev(y, "y", dt, T * m),
-        _dev(saved, "saved"), wp, wb, int(bool(xmem)), _stream(stream)))
+        _dev(saved, "saved"), wp, wb, int(bool(xmem)), _stream(stream, x)))
 
 
 def poetx_layer_bwd_q(sh: Shape, dy, G_P, GT_P, GT_R, q_f, q_fT, s_f, perm_P_inv, perm_R, saved,
@@ -243,7 +247,7 @@ def poetx_layer_bwd_q(sh: Shape, dy, G_P, GT_P, GT_R, q_f, q_fT, s_f, perm_P_inv
         _dev(q_fT, "q_fT", torch.int8, m * n), _dev(s_f, "s_f", torch.float32, m),
         _dev(perm_P_inv, "perm_P_inv", torch.int32, n), _dev(perm_R, "perm_R", torch.int32, m),
         _dev(saved, "saved"), _dev(dx, "dx", dt, T * n), _dev(dG_P, "dG_P", torch.float32, n * b),
-        _dev(dG_R, "dG_R", torch.float32, m * b), wp, wb, int(bool(xmem)), _stream(stream)))
+        _dev(dG_R, "dG_R", torch.float32, m * b), wp, wb, int(bool(xmem)), _stream(stream, dy)))
 
 
 def poetx_merge(sh: Shape, W0f, G_R, GT_P, perm_R_inv, perm_P_inv, W0_out, ws,
@@ -256,7 +260,7 @@ def poetx_merge(sh: Shape, W0f, G_R, GT_P, perm_R_inv, perm_P_inv, W0_out, ws,
         C.byref(sh), _dev(W0f, "W0f", dt, m * n), _dev(G_R, "G_R", dt, m * b),
         _dev(GT_P, "GT_P", dt, n * b), _dev(perm_R_inv, "perm_R_inv", torch.int32, m),
         _dev(perm_P_inv, "perm_P_inv", torch.int32, n), _dev(W0_out, "W0_out", dt, m * n),
-        wp, wb, _stream(stream)))
+        wp, wb, _stream(stream, W0f)))
 
 
 def poetx_fold_scale(s, perm_R, s_f, stream=None) -> None:
@@ -264,7 +268,7 @@ def poetx_fold_scale(s, perm_R, s_f, stream=None) -> None:
     m = perm_R.numel()
     check("poetx_fold_scale", lib().poetx_fold_scale(
         m, _dev(s, "s", torch.float32, m), _dev(perm_R, "perm_R", torch.int32, m),
-        _dev(s_f, "s_f", torch.float32, m), _stream(stream)))
+        _dev(s_f, "s_f", torch.float32, m), _stream(stream, s)))
 
 
 def poetx_dequant(q, scale, per_row: bool, out, stream=None) -> None:
@@ -273,7 +277,7 @@ def poetx_dequant(q, scale, per_row: bool, out, stream=None) -> None:
     check("poetx_dequant", lib().poetx_dequant(
         rows, cols, _dev(q, "q", torch.int8, rows * cols),
         _dev(scale, "scale", torch.float32, rows if per_row else cols), int(bool(per_row)),
-        _dev(out, "out", torch.bfloat16, rows * cols), _stream(stream)))
+        _dev(out, "out", torch.bfloat16, rows * cols), _stream(stream, q)))
 
 
 # ---- attention-block operators ------------------------------------------------
@@ -318,7 +322,7 @@ def poetx_rope(q, k, pos, table, qo, ko, interleaved: bool = False, inverse: boo
                    int(interleaved), int(inverse), ldq, ldk, ldqo, ldko)
     check("poetx_rope", lib().poetx_rope(
         C.byref(sh), qp, kp, _vec(pos, "pos", torch.int32, T),
-        _vec(table, "table", torch.float32, table.numel()), qop, kop, _stream(stream)))
+        _vec(table, "table", torch.float32, table.numel()), qop, kop, _stream(stream, q)))
 
 
 def qk_norm_shape(q, k, table, eps: float = 1e-6, interleaved: bool = False) -> QkNormShape:
@@ -368,7 +372,7 @@ def poetx_qk_norm_rope_fwd(q, k, wq, wk, pos, table, qo, ko, eps: float = 1e-6, 
         kp, sh.ldk = _rows(k, "k", fk, q.dtype)
         kop, sh.ldko = _rows(ko, "ko", fk, q.dtype)
     check("poetx_qk_norm_rope_fwd", lib().poetx_qk_norm_rope_fwd(
-        C.byref(sh), qp, kp, wqp, wkp, *_turned_by(sh, pos, table), qop, kop, _stream(stream)))
+        C.byref(sh), qp, kp, wqp, wkp, *_turned_by(sh, pos, table), qop, kop, _stream(stream, q)))
 
 
 def poetx_qk_norm_rope_bwd(dqo, dko, q, k, wq, wk, pos, table, dq, dk, dwq, dwk, ws, eps: float = 1e-6,
@@ -388,7 +392,7 @@ def poetx_qk_norm_rope_bwd(dqo, dko, q, k, wq, wk, pos, table, dq, dk, dwq, dwk,
         dkp, sh.lddk = _rows(dk, "dk", fk, q.dtype)
     wp, wb = _ws(ws, poetx_qk_norm_rope_workspace_bytes(sh))
     check("poetx_qk_norm_rope_bwd", lib().poetx_qk_norm_rope_bwd(
-        C.byref(sh), gqp, gkp, qp, kp, wqp, wkp, *_turned_by(sh, pos, table), dqp, dkp, dwqp, dwkp, wp, wb, _stream(stream)))
+        C.byref(sh), gqp, gkp, qp, kp, wqp, wkp, *_turned_by(sh, pos, table), dqp, dkp, dwqp, dwkp, wp, wb, _stream(stream, dqo)))
 
 
 def poetx_dropout_fwd(x, residual, y, p: float, seed: int, offset: int = 0, offset_dev=None,
@@ -398,7 +402,7 @@ def poetx_dropout_fwd(x, residual, y, p: float, seed: int, offset: int = 0, offs
     check("poetx_dropout_fwd", lib().poetx_dropout_fwd(
         n, act_of(x.dtype), _dev(x, "x"), _dev(residual, "residual", x.dtype, n, optional=True),
         _dev(y, "y", x.dtype, n), p, seed, offset,
-        _dev(offset_dev, "offset_dev", torch.int64, 1, optional=True), _stream(stream)))
+        _dev(offset_dev, "offset_dev", torch.int64, 1, optional=True), _stream(stream, x)))
 
 
 def poetx_dropout_bwd(dy, dx, p: float, seed: int, offset: int = 0, offset_dev=None,
@@ -407,7 +411,7 @@ def poetx_dropout_bwd(dy, dx, p: float, seed: int, offset: int = 0, offset_dev=N
     n = dy.numel()
     check("poetx_dropout_bwd", lib().poetx_dropout_bwd(
         n, act_of(dy.dtype), _dev(dy, "dy"), _dev(dx, "dx", dy.dtype, n), p, seed, offset,
-        _dev(offset_dev, "offset_dev", torch.int64, 1, optional=True), _stream(stream)))
+        _dev(offset_dev, "offset_dev", torch.int64, 1, optional=True), _stream(stream, dy)))
 
 
 def attn_shape(q, k, v, ndoc: int, causal: bool = True, scale: float = 0.0,
@@ -468,7 +472,7 @@ def poetx_attn_plan(sh: AttnShape, cu_q, cu_k, plan, prefix=None, stream=None) -
         C.byref(sh), _vec(cu_q, "cu_q", torch.int32, sh.ndoc + 1),
         _vec(cu_k, "cu_k", torch.int32, sh.ndoc + 1),
         _vec(prefix, "prefix", torch.int32, sh.ndoc, optional=True), _dev(plan, "plan"),
-        plan.numel() * plan.element_size(), _stream(stream)))
+        plan.numel() * plan.element_size(), _stream(stream, cu_q)))
 
 
 def poetx_attn_window_plan(sh: AttnShape, win: Window, cu_q, cu_k, plan, stream=None) -> None:
@@ -476,7 +480,7 @@ def poetx_attn_window_plan(sh: AttnShape, win: Window, cu_q, cu_k, plan, stream=
     check("poetx_attn_window_plan", lib().poetx_attn_window_plan(
         C.byref(sh), C.byref(win), _vec(cu_q, "cu_q", torch.int32, sh.ndoc + 1),
         _vec(cu_k, "cu_k", torch.int32, sh.ndoc + 1), _dev(plan, "plan"),
-        plan.numel() * plan.element_size(), _stream(stream)))
+        plan.numel() * plan.element_size(), _stream(stream, cu_q)))
 
 
 def _plan(sh: AttnShape, win: Optional[Window], plan):
@@ -500,7 +504,7 @@ def _attn_fwd(sh: AttnShape, win: Optional[Window], q, k, v, plan, o, lse, ws, s
     check(name, getattr(lib(), name)(
         C.byref(sh), *w, qp, kp, vp, _vec(slopes, "slopes", torch.float32, sh.Hq, optional=True),
         _plan(sh, win, plan), op, _vec(lse, "lse", torch.float32, sh.Hq * sh.Tq), wp, wb,
-        _stream(stream)))
+        _stream(stream, q)))
 
 
 def poetx_attn_fwd(sh: AttnShape, q, k, v, plan, o, lse, ws=None, slopes=None, stream=None) -> None:
@@ -529,7 +533,7 @@ def _attn_bwd(sh: AttnShape, win: Optional[Window], dout, q, k, v, o, lse, plan,
     check(name, getattr(lib(), name)(
         C.byref(sh), *w, dop, qp, kp, vp, op, _vec(lse, "lse", torch.float32, sh.Hq * sh.Tq),
         _vec(slopes, "slopes", torch.float32, sh.Hq, optional=True), _plan(sh, win, plan), dqp, dkp, dvp,
-        wp, wb, _stream(stream)))
+        wp, wb, _stream(stream, dout)))
 
 
 def poetx_attn_bwd(sh: AttnShape, dout, q, k, v, o, lse, plan, dq, dk, dv, ws, slopes=None,
@@ -586,7 +590,7 @@ def poetx_attn_decode(sh: DecodeShape, q, k, v, length, o, ws, start=None, slope
     check("poetx_attn_decode", lib().poetx_attn_decode(
         C.byref(sh), qp, kp, vp, _vec(start, "start", torch.int32, sh.B, optional=True),
         _vec(length, "length", torch.int32, sh.B),
-        _vec(slopes, "slopes", torch.float32, sh.Hq, optional=True), op, wp, wb, _stream(stream)))
+        _vec(slopes, "slopes", torch.float32, sh.Hq, optional=True), op, wp, wb, _stream(stream, q)))
 
 
 def poetx_attn_window_decode_workspace_bytes(sh: DecodeShape, win: Window) -> int:
@@ -607,7 +611,7 @@ def poetx_attn_window_decode(sh: DecodeShape, win: Window, q, k, v, length, o, w
     wp, wb = _ws(ws, poetx_attn_window_decode_workspace_bytes(sh, win))
     check("poetx_attn_window_decode", lib().poetx_attn_window_decode(
         C.byref(sh), C.byref(win), int(ring), qp, kp, vp, _vec(length, "length", torch.int32, sh.B),
-        _vec(slopes, "slopes", torch.float32, sh.Hq, optional=True), op, wp, wb, _stream(stream)))
+        _vec(slopes, "slopes", torch.float32, sh.Hq, optional=True), op, wp, wb, _stream(stream, q)))
 
 
 # ---- a cache in 4 bits ------------------------------------------------------------
@@ -646,13 +650,13 @@ def poetx_kv4_write(k, v, seq, pos, kc, ks, vc, vs, sinks: int = 0, ring: bool =
     """Tokens k, v [T][Hkv][D] to positions pos [T] of sequences seq [T]
     (None: token t to sequence t)."""
     sh, kp, vp, sp, pp, ptrs = _kv4_call(k, v, seq, pos, (kc, ks, vc, vs), sinks, ring)
-    check("poetx_kv4_write", lib().poetx_kv4_write(C.byref(sh), kp, vp, sp, pp, *ptrs, _stream(stream)))
+    check("poetx_kv4_write", lib().poetx_kv4_write(C.byref(sh), kp, vp, sp, pp, *ptrs, _stream(stream, k)))
 
 
 def poetx_kv4_read(seq, pos, kc, ks, vc, vs, k, v, sinks: int = 0, ring: bool = False, stream=None) -> None:
     """The values at positions pos [T] of sequences seq [T] into k, v [T][Hkv][D]."""
     sh, kp, vp, sp, pp, ptrs = _kv4_call(k, v, seq, pos, (kc, ks, vc, vs), sinks, ring)
-    check("poetx_kv4_read", lib().poetx_kv4_read(C.byref(sh), sp, pp, *ptrs, kp, vp, _stream(stream)))
+    check("poetx_kv4_read", lib().poetx_kv4_read(C.byref(sh), sp, pp, *ptrs, kp, vp, _stream(stream, k)))
 
 
 def kv4_decode_shape(q, kc, scale: float = 0.0, cap: float = 0.0) -> DecodeShape:
@@ -683,4 +687,4 @@ def poetx_attn_kv4_decode(sh: DecodeShape, win: Window, q, kc, ks, vc, vs, lengt
     check("poetx_attn_kv4_decode", lib().poetx_attn_kv4_decode(
         C.byref(sh), C.byref(win), int(ring), qp, *ptrs, _vec(start, "start", torch.int32, sh.B, optional=True),
         _vec(length, "length", torch.int32, sh.B), _vec(slopes, "slopes", torch.float32, sh.Hq, optional=True), op, wp, wb,
-        _stream(stream)))
+        _stream(stream, q)))
