@@ -23,9 +23,12 @@
 // they form, at the power limit; in 9 documents 320 us, a fifth of the wave
 // slots empty as in the forward pass.  float32, D 64, two documents of 1024,
 // 16 heads on 4, capped: 225 us, a third of the float32 matrix rate.
-// With a window (8192 tokens in 3 documents, window 1024, 4 sinks) 185 us for dq,
-// 270 to 285 for dk, dv and 38 for the sinks, 0.56 PFLOP/s of the products that are
-// seen; a tenth more are formed at the edges of the window, and the loops are short.
+// With a window (8192 tokens in 3 documents, window 1024, 4 sinks) 477 us for both
+// passes: 180 to 190 for dq, 268 to 290 for dk, dv, 33 for the sinks and 5 for
+// their join, 0.59 PFLOP/s of the products that are seen.  A tenth more are formed
+// at the edges of the window, the loops are short, and dk, dv's 512 workgroups of
+// unequal loops are two rounds: matrix pipes busy in 0.42 (dq) and 0.35 (dk, dv) of
+// the cycles.
 #include <algorithm>
 
 #include "attn_rows.h"

@@ -25,7 +25,9 @@
 // With a window, 8192 tokens in 3 documents, window 1024, 4 sinks: 142 us = 0.79
 // PFLOP/s of the products that are seen, 0.9 of those formed (a tile at either
 // edge of the window is half hidden, the sinks' tile nearly); capped, 2048
-// queries on 16384 keys, window 4096: 181 us = 0.76 PFLOP/s.
+// queries on 16384 keys, window 4096: 177 us = 0.78 PFLOP/s (207 us under the
+// profiler: vector instructions issue in 0.56 of the cycles, matrix pipes are busy
+// in 0.31, and the two hardly overlap), o off by 2.3e-3.
 #include <algorithm>
 
 #include "attn_rows.h"
