@@ -420,8 +420,9 @@ int32_t poetx_rope(const poetx_rope_shape* sh, const void* q, const void* k, con
  *   y = turn(x r w),
  * with weights wq, wk [D] float32 that all heads of a tensor share (NULL: 1).
  * Sums are float32; each output is rounded once.  A head whose squares sum to
- * 2^128 or more (128 elements of 2^60.5) has r = 0: its outputs and gradients are
- * zeros.  With eps = 0 a head's root mean square is to be above 2^-63.
+ * 2^128 or more (128 elements of 2^60.5) has r = 0: its outputs are zeros, and
+ * its gradients too (NaN in dq, dk where the sum of dy w x passes 2^128 as well).
+ * With eps = 0 a head's root mean square is to be above 2^-63.
  * rot = 0: norms alone, pos and table are not read.
  *   fwd: q [T][Hq][D] -> qo, k [T][Hk][D] -> ko (Hk = 0: k, ko NULL); qo = q
  *   and ko = k (same pitch) work in place.  A position outside the table

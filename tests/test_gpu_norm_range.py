@@ -41,3 +41,16 @@ def test_large_and_small_heads(dt):
             want = 2.0 ** -p * ((torch.arange(128, device="cuda") == 0).float() + sign / 128)
             assert ((q.grad[0, i].float() - want).abs() <= tol * 2.0 ** -p).all(), p
     assert abs(w.grad[0].item() + (~big).sum().item()) <= 2.0 ** -18 and not w.grad[1:].any()
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_gradients_whose_products_pass_the_range(dt):
+    """The sum of dy w x is 2^6 * 2^125 * 128: NaN in that head alone."""
+    q = torch.full((1, 3, 128), 1.0, device="cuda", dtype=dt)
+    q[0, 1] = 2.0 ** 125
+    q.requires_grad_()
+    w = torch.ones(128, device="cuda", requires_grad=True)
+    y = A.qk_norm_rope(q, None, w, None, None, None)
+    y.backward(torch.full_like(y, 64.0))
+    assert (y[0, 1] == 0).all() and torch.isnan(q.grad[0, 1]).all()
+    assert torch.isfinite(q.grad[0, [0, 2]]).all() and torch.isfinite(w.grad).all()
